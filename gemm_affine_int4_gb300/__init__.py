@@ -13,7 +13,9 @@ with T = torch.bfloat16, torch.float16 or torch.float32.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -58,6 +60,12 @@ SIGNATURES = {
     "gai4_check_bounded_wait": ([_I, _I64, _P, _P], _I),
     "gai4_q8_0_34b_gemv": ([_P, _P, _P, _I64, _I64, _P], _I),
     "gai4_q6_k_gemv": ([_P, _P, _P, _I64, _I64, _P], _I),
+    "gai4_kv_plan": ([_P, _P, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P, _P, _P, _I64, _I, _P], _I),
+    "gai4_kv_append": ([_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I64, _I64, _I, _I64, _I, _P], _I),
+    "gai4_kv_read": ([_P, _P, _P, _P, _P, _I, _I, _I64, _I64, _I, _I64, _I, _P], _I),
+    "gai4_kv_attention": ([_P, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _P, _I64, _P, _I, _I, _I64, _I64, _I64,
+                           _I64, _I64, _I, _I64, _I, ctypes.c_float, _I64, _P, ctypes.c_size_t, _P], _I),
+    "gai4_kv_attention_workspace_bytes": ([_I64, _I64, _I, _I], ctypes.c_size_t),
 }
 
 
@@ -325,6 +333,157 @@ def gai4_q6_k_gemv(blocks, x, out=None, stream=None):
     if out is None:
         out = torch.empty((N,), dtype=torch.float32, device=x.device)
     _check("gai4_q6_k_gemv", lib().gai4_q6_k_gemv(_ptr(blocks), _ptr(x), _ptr(out), N, K, _stream(stream)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# paged key/value cache held in 4 bits. A cache is a tuple (packed, scales,
+# biases): packed int32 [num_blocks, kv_heads, page_size, head_dim / 8],
+# scales and biases T [num_blocks, kv_heads, page_size, head_dim / group_size].
+# ---------------------------------------------------------------------------
+class KvPlan(NamedTuple):
+    """What gai4_kv_plan returns beside the updated block table and free list."""
+    slots: torch.Tensor        # [num_tokens] int64, -1 in the rows after the last new token
+    positions: torch.Tensor    # [num_tokens] int32
+    cu_q: torch.Tensor         # [batch + 1] int32, first row of each request
+    kv_lens: torch.Tensor      # [batch] int32, lengths after the step
+    free_count: torch.Tensor   # [1] int32
+    info: torch.Tensor         # [4] int32, all zero unless the step was refused
+
+
+def gai4_kv_cache(num_blocks: int, kv_heads: int, page_size: int, head_dim: int, group_size: int = 64,
+                  dtype=torch.bfloat16, device="cuda"):
+    """An empty (zeroed) cache for keys or for values: (packed, scales, biases)."""
+    rows = (num_blocks, kv_heads, page_size)
+    return (torch.zeros(rows + (head_dim // 8,), dtype=torch.int32, device=device),
+            torch.zeros(rows + (head_dim // group_size,), dtype=dtype, device=device),
+            torch.zeros(rows + (head_dim // group_size,), dtype=dtype, device=device))
+
+
+def _need(cond: bool, what: str):
+    if not cond:
+        raise ValueError("gai4: " + what)
+
+
+def _kv_shape(cache, group_size: int):
+    """(num_blocks, kv_heads, page_size, head_dim, dtype number) of a cache."""
+    packed, scales, biases = cache
+    _need(packed.dim() == 4 and packed.element_size() == 4, "a cache's packed tensor is 32-bit [blocks, heads, page, D/8]")
+    nb, h, page, words = packed.shape
+    _need(scales.shape == (nb, h, page, words * 8 // group_size) and biases.shape == scales.shape and
+          biases.dtype == scales.dtype, "scales and biases are [blocks, heads, page, D/group_size] of one type")
+    return nb, h, page, words * 8, _dtype(scales)
+
+
+def _i32(t: torch.Tensor, what: str):
+    _need(t.dtype == torch.int32, f"{what} must be int32")
+    return _ptr(t)
+
+
+def _slots(t: torch.Tensor, n: int):
+    _need(t.dtype == torch.int64 and t.dim() == 1 and t.shape[0] == n, "slots must be int64, one per row")
+    return _ptr(t)
+
+
+def _rows(t: torch.Tensor, heads: int, d: int, dtype, what: str):
+    """(address, token stride) of [tokens, heads, d] rows with contiguous heads."""
+    _need(t.dim() == 3 and t.shape[1] == heads and t.shape[2] == d and t.dtype == dtype,
+          f"{what} must be [tokens, {heads}, {d}] of the cache's type")
+    _need(t.stride(2) == 1 and (heads == 1 or t.stride(1) == d), f"{what}: heads must be contiguous within a token")
+    return _ptr_strided(t), (t.stride(0) if t.shape[0] > 1 else heads * d)
+
+
+def gai4_kv_plan(kv_lens, q_lens, block_table, free_blocks, free_count, page_size: int, num_tokens: int,
+                 out: KvPlan | None = None, stream=None) -> KvPlan:
+    """Block tables, slot map, positions and query offsets of one step, built
+    on the device. kv_lens, q_lens [B], block_table [B, max_blocks],
+    free_blocks [capacity] and free_count [1] are int32 and contiguous;
+    block_table and free_blocks are updated in place. A negative q_lens frees
+    the request's pages. `out` gives tensors to write into."""
+    B = kv_lens.shape[0]
+    _need(q_lens.shape == (B,) and block_table.dim() == 2 and block_table.shape[0] == B and free_count.numel() == 1,
+          "kv_lens, q_lens [B], block_table [B, max_blocks], free_count [1]")
+    if out is None:
+        dev = kv_lens.device
+        # one allocation for the 32-bit outputs
+        a = torch.empty(num_tokens + 2 * B + 6, dtype=torch.int32, device=dev)
+        positions, cu_q, lens, count, info = a.split([num_tokens, B + 1, B, 1, 4])
+        out = KvPlan(torch.empty(num_tokens, dtype=torch.int64, device=dev), positions, cu_q, lens, count, info)
+    else:
+        _need(out.positions.shape == (num_tokens,) and out.cu_q.shape == (B + 1,) and out.kv_lens.shape == (B,) and
+              out.free_count.numel() == 1 and out.info.numel() == 4, "out: wrong shapes")
+    _check("gai4_kv_plan", lib().gai4_kv_plan(
+        _i32(kv_lens, "kv_lens"), _i32(q_lens, "q_lens"), _i32(block_table, "block_table"), block_table.shape[1],
+        _i32(free_blocks, "free_blocks"), free_blocks.numel(), _i32(free_count, "free_count"),
+        _slots(out.slots, num_tokens), _i32(out.positions, "positions"), num_tokens, _i32(out.cu_q, "cu_q"),
+        _i32(out.kv_lens, "kv_lens"), _i32(out.free_count, "free_count"), _i32(out.info, "info"), B, page_size,
+        _stream(stream)))
+    return out
+
+
+def gai4_kv_append(k, v, slots, k_cache, v_cache, group_size: int = 64, stream=None):
+    """Quantize key and value rows k, v [tokens, kv_heads, head_dim] (any token
+    stride) into the caches' slots; rows with a slot outside the pool (such as
+    -1) are skipped."""
+    nb, h, page, d, dt = _kv_shape(k_cache, group_size)
+    _need(_kv_shape(v_cache, group_size) == (nb, h, page, d, dt), "key and value caches differ in shape or type")
+    n = k.shape[0]
+    _need(v.shape[0] == n, "k and v differ in length")
+    kp, ks = _rows(k, h, d, k_cache[1].dtype, "k")
+    vp, vs = _rows(v, h, d, k_cache[1].dtype, "v")
+    _check("gai4_kv_append", lib().gai4_kv_append(kp, ks, vp, vs, _slots(slots, n), *map(_ptr, k_cache),
+                                                  *map(_ptr, v_cache), dt, group_size, n, h, d, nb, page,
+                                                  _stream(stream)))
+
+
+def gai4_kv_read(cache, slots, group_size: int = 64, out=None, stream=None) -> torch.Tensor:
+    """Values of cached rows, float32 [tokens, kv_heads, head_dim]; zeros where
+    the slot is outside the pool."""
+    nb, h, page, d, dt = _kv_shape(cache, group_size)
+    n = slots.shape[0]
+    if out is None:
+        out = torch.empty((n, h, d), dtype=torch.float32, device=slots.device)
+    _need(out.shape == (n, h, d) and out.dtype == torch.float32, "out must be float32 [tokens, kv_heads, head_dim]")
+    _check("gai4_kv_read", lib().gai4_kv_read(*map(_ptr, cache), _slots(slots, n), _ptr(out), dt, group_size, n, h, d,
+                                              nb, page, _stream(stream)))
+    return out
+
+
+def gai4_kv_attention_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int, dtype) -> int:
+    return int(lib().gai4_kv_attention_workspace_bytes(q_heads, kv_heads, head_dim, _DTYPE[dtype]))
+
+
+def gai4_kv_attention(q, k_cache, v_cache, block_table, kv_lens, cu_q, group_size: int = 64, scale=None,
+                      window: int = 0, max_q_len: int = 1, out=None, lse=None, workspace=None, stream=None):
+    """Causal attention of q [tokens, q_heads, head_dim] (rows of one request
+    after another, offsets cu_q [B + 1]) over each request's kv_lens[r] cached
+    tokens, the new ones among them. scale defaults to head_dim ** -0.5;
+    window > 0 keeps the last `window` positions; max_q_len, the most rows of a
+    request, guides the choice of kernel. lse, when given, float32 [tokens,
+    q_heads], takes the logarithms of the softmax sums. A workspace is
+    allocated here when none is given."""
+    nb, h, page, d, dt = _kv_shape(k_cache, group_size)
+    _need(_kv_shape(v_cache, group_size) == (nb, h, page, d, dt), "key and value caches differ in shape or type")
+    n, hq = q.shape[0], q.shape[1]
+    B = kv_lens.shape[0]
+    T = k_cache[1].dtype
+    qp, qs = _rows(q, hq, d, T, "q")
+    _need(block_table.dim() == 2 and block_table.shape[0] == B and cu_q.shape == (B + 1,),
+          "block_table [B, max_blocks], cu_q [B + 1]")
+    if out is None:
+        out = torch.empty((n, hq, d), dtype=T, device=q.device)
+    _need(out.shape[0] == n, "out must have a row for each row of q")
+    op, os_ = _rows(out, hq, d, T, "out")
+    if lse is not None:
+        _need(lse.shape == (n, hq) and lse.dtype == torch.float32, "lse must be float32 [tokens, q_heads]")
+    if workspace is None:
+        nbytes = gai4_kv_attention_workspace_bytes(hq, h, d, T)
+        workspace = torch.empty(nbytes // 4, dtype=torch.float32, device=q.device) if nbytes else None
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check("gai4_kv_attention", lib().gai4_kv_attention(
+        qp, qs, *map(_ptr, k_cache), *map(_ptr, v_cache), _i32(block_table, "block_table"), block_table.shape[1],
+        _i32(kv_lens, "kv_lens"), _i32(cu_q, "cu_q"), op, os_, _ptr(lse), dt, group_size, B, n, max_q_len, hq, h, d,
+        nb, page, 1.0 / math.sqrt(d) if scale is None else scale, window, _ptr(workspace), ws_bytes, _stream(stream)))
     return out
 
 

@@ -13,7 +13,7 @@ namespace gai4 {
 // Device status word: kernels with bounded waits record GAI4_ERR_TIMEOUT here.
 __device__ int g_device_status;
 
-static int* status_ptr() {
+int* status_ptr() {
     static int* ptrs[64] = {nullptr};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return nullptr;

@@ -119,6 +119,69 @@ cudaError_t launch_q8_0_gemv(const uint32_t* blocks, const float* x, float* out,
 cudaError_t launch_q4_k_gemv(const uint8_t* blocks, const float* x, float* out, int64_t N,
                              int64_t K, cudaStream_t s);
 
+// paged 4-bit key/value cache (kv_cache.cu)
+struct KvPlanLaunch {
+    const int32_t* kv_lens;
+    const int32_t* q_lens;
+    int32_t* table;
+    int64_t max_blocks;
+    int32_t* free_blocks;
+    int64_t free_capacity;
+    const int32_t* free_count;
+    int64_t* slots;
+    int32_t* positions;
+    int64_t num_tokens;
+    int32_t* cu_q;
+    int32_t* kv_lens_out;
+    int32_t* free_count_out;
+    int32_t* info;
+    int batch;
+    int page_log2;
+};
+constexpr int kKvPlanMaxBatch = 8192;
+cudaError_t launch_kv_plan(const KvPlanLaunch& L, cudaStream_t s);
+
+// one of the two caches; rows (block, head, slot) as in gai4.h
+struct KvCache {
+    const uint32_t* packed;
+    const void* scales;
+    const void* biases;
+};
+struct KvShape {
+    int dtype, gs, hkv, d, page_log2;
+    int64_t num_blocks;
+};
+cudaError_t launch_kv_append(const void* k, int64_t ks, const void* v, int64_t vs, const int64_t* slots, KvCache kc,
+                             KvCache vc, const KvShape& sh, int64_t num_tokens, cudaStream_t s);
+cudaError_t launch_kv_read(KvCache c, const int64_t* slots, float* out, const KvShape& sh, int64_t num_tokens,
+                           cudaStream_t s);
+
+// attention over the cache (kv_attention.cu)
+struct KvAttnLaunch {
+    const void* q;
+    int64_t q_stride;
+    KvCache k, v;
+    const int32_t* table;
+    int64_t max_blocks;
+    const int32_t* kv_lens;
+    const int32_t* cu_q;
+    void* out;
+    int64_t out_stride;
+    float* lse;
+    KvShape sh;
+    int batch;
+    int64_t num_tokens, max_q_len;
+    int group;          // query heads per key/value head
+    float scale;
+    int64_t window;
+    void* workspace;
+    int* status;
+    long long spin_limit;
+};
+cudaError_t launch_kv_attention(const KvAttnLaunch& L, cudaStream_t s);
+size_t kv_attention_workspace(int group, int d);
+
+int* status_ptr();  // device status word of the current device
 int num_sms();  // SM count of the current device (cached)
 
 }  // namespace gai4

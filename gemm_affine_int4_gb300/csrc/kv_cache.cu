@@ -1,0 +1,364 @@
+// kv_cache.cu -- bookkeeping and rows of the paged 4-bit key/value cache
+// (gai4_kv_plan, gai4_kv_append, gai4_kv_read).
+#include "common.cuh"
+#include "internal.h"
+
+namespace gai4 {
+namespace {
+
+// ---------------------------------------------------------------------------
+// plan: with old length l, n new tokens and page size P, request r needs
+// ceil((l + n) / P) - ceil(l / P) new pages; exclusive prefix sums over the
+// requests of n, of the pages taken and of the pages given back say where its
+// rows, its pops and its pushes are. Every block computes the sums over all
+// requests for itself (8 bytes a request, from L2) and then does its share of
+// the tokens, so no block waits for another. Reads and writes do not meet:
+// pushed pages are written at or above free_count and read only below it (a
+// popped page that was pushed in this step is taken from the finished
+// request's row), and table columns are written only from ceil(l / P) on.
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024;
+
+struct Sum3 {
+    long long q, took, gave;
+};
+
+__device__ __forceinline__ Sum3 add3(Sum3 a, Sum3 b) { return {a.q + b.q, a.took + b.took, a.gave + b.gave}; }
+
+__device__ __forceinline__ Sum3 shfl_up3(Sum3 v, int o) {
+    return {__shfl_up_sync(0xffffffffu, v.q, o), __shfl_up_sync(0xffffffffu, v.took, o),
+            __shfl_up_sync(0xffffffffu, v.gave, o)};
+}
+
+// largest i in [0, n) with a[i] <= x, for ascending a with a[0] <= x
+__device__ __forceinline__ int last_not_above(const int* a, int n, int x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPlanLaunch p) {
+    extern __shared__ int plan_smem[];
+    __shared__ Sum3 warp_sums[32];
+    __shared__ int bad_rows, bad_len;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.batch, pl = p.page_log2;
+    const long long pm = (1ll << pl) - 1;
+    int* cu = plan_smem;           // [B + 1] first row of each request
+    int* tk = cu + B + 1;          // [B + 1] pages popped before it
+    int* gv = tk + B + 1;          // [B + 1] pages pushed before it
+    if (tid == 0) bad_rows = bad_len = 0;
+    __syncthreads();
+
+    // each thread takes `per` consecutive requests
+    const int per = (B + kPlanThreads - 1) / kPlanThreads;
+    const int r0 = min(tid * per, B), r1 = min(r0 + per, B);
+    auto one = [&](int r, int& rows_bad, int& len_bad) {
+        const long long l = p.kv_lens[r], n = p.q_lens[r];
+        const long long had = (l + pm) >> pl, need = n < 0 ? had : (l + n + pm) >> pl;
+        len_bad |= l < 0;
+        rows_bad += need > p.max_blocks;
+        return n < 0 ? Sum3{0, 0, had} : Sum3{n, need - had, 0};
+    };
+    Sum3 mine{0, 0, 0};
+    int rows_bad = 0, len_bad = 0;
+    for (int r = r0; r < r1; ++r) mine = add3(mine, one(r, rows_bad, len_bad));
+    if (rows_bad) atomicAdd(&bad_rows, rows_bad);
+    if (len_bad) bad_len = 1;
+    Sum3 inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Sum3 u = shfl_up3(inc, o);
+        if (lane >= o) inc = add3(inc, u);
+    }
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+        Sum3 w = warp_sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const Sum3 u = shfl_up3(w, o);
+            if (lane >= o) w = add3(w, u);
+        }
+        warp_sums[lane] = w;
+    }
+    __syncthreads();
+    const Sum3 total = warp_sums[31];
+    Sum3 at = {inc.q - mine.q, inc.took - mine.took, inc.gave - mine.gave};
+    if (warp > 0) at = add3(at, warp_sums[warp - 1]);
+
+    const long long count = p.free_count[0];
+    const long long missing = total.took - (count + total.gave);
+    const long long over = total.q - p.num_tokens;
+    const bool wrong = bad_len || count < 0 || count + total.gave > p.free_capacity;
+    const bool refused = missing > 0 || bad_rows > 0 || over > 0 || wrong;
+    const long long top = refused ? count : count + total.gave;
+    if (blockIdx.x == 0 && tid == 0) {
+        const long long most = 0x7fffffff;
+        p.info[0] = wrong ? 0 : (int)min(max(missing, 0ll), most);
+        p.info[1] = bad_rows;
+        p.info[2] = (int)min(max(over, 0ll), most);
+        p.info[3] = wrong;
+        p.free_count_out[0] = (int)(refused ? count : top - total.took);
+        p.cu_q[B] = refused ? 0 : (int)total.q;
+    }
+    if (tid == 0) {
+        cu[B] = (int)total.q;
+        tk[B] = (int)total.took;
+        gv[B] = (int)total.gave;
+    }
+    int unused = 0;
+    for (int r = r0; r < r1; ++r) {
+        cu[r] = (int)at.q;
+        tk[r] = (int)at.took;
+        gv[r] = (int)at.gave;
+        at = add3(at, one(r, unused, unused));
+        if (blockIdx.x == 0) {
+            const int l = p.kv_lens[r], n = p.q_lens[r];
+            p.cu_q[r] = refused ? 0 : cu[r];
+            p.kv_lens_out[r] = refused ? l : (n < 0 ? 0 : l + n);
+        }
+    }
+    __syncthreads();
+
+    const long long stride = (long long)gridDim.x * kPlanThreads, first = (long long)blockIdx.x * kPlanThreads + tid;
+    if (refused) {
+        for (long long t = first; t < p.num_tokens; t += stride) {
+            p.slots[t] = -1;
+            p.positions[t] = 0;
+        }
+        return;
+    }
+    // page number `i` from the bottom of the stack after the pushes
+    auto stack = [&](int i) {
+        if (i < count) return p.free_blocks[i];
+        const int j = i - (int)count;
+        const int r = last_not_above(gv, B, j);
+        return p.table[(long long)r * p.max_blocks + (j - gv[r])];
+    };
+    // tokens
+    for (long long t = first; t < p.num_tokens; t += stride) {
+        long long slot = -1;
+        int pos = 0;
+        if (t < total.q) {
+            const int r = last_not_above(cu, B, (int)t);
+            const int l = p.kv_lens[r];
+            const int had = (int)((l + pm) >> pl);
+            pos = l + ((int)t - cu[r]);
+            const int blk = pos >> pl;
+            const int page = blk < had ? p.table[(long long)r * p.max_blocks + blk]
+                                       : stack((int)top - 1 - (tk[r] + blk - had));
+            slot = ((long long)page << pl) + (pos & pm);
+        }
+        p.slots[t] = slot;
+        p.positions[t] = pos;
+    }
+    // pushes and new table entries, one request per warp
+    const int nwarps = gridDim.x * (kPlanThreads / 32);
+    for (int r = blockIdx.x * (kPlanThreads / 32) + warp; r < B; r += nwarps) {
+        const int gave = gv[r + 1] - gv[r], took = tk[r + 1] - tk[r];
+        int* row = p.table + (long long)r * p.max_blocks;
+        for (int j = lane; j < gave; j += 32) p.free_blocks[count + gv[r] + j] = row[j];
+        if (took > 0) {
+            const int had = (int)((p.kv_lens[r] + pm) >> pl);
+            for (int j = lane; j < took; j += 32) row[had + j] = stack((int)top - 1 - (tk[r] + j));
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// rows: lane-sized pieces of 8 elements = one word of codes
+// ---------------------------------------------------------------------------
+// slot -> first row index of (page, head, offset), or -1 outside the pool
+__device__ __forceinline__ long long cache_row(long long slot, int h, const KvShape& sh) {
+    if (slot < 0 || slot >= (sh.num_blocks << sh.page_log2)) return -1;
+    const long long page = slot >> sh.page_log2;
+    return (((page * sh.hkv + h) << sh.page_log2) + (slot & ((1ll << sh.page_log2) - 1)));
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const void* p, long long at, float (&x)[8]) {
+    const typename T::storage* s = static_cast<const typename T::storage*>(p) + at;
+    if constexpr (!VEC) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = T::to_f32(s[i]);
+    } else if constexpr (T::kBytes == 4) {
+        const float4 a = *reinterpret_cast<const float4*>(s), b = *reinterpret_cast<const float4*>(s + 4);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+        const uint4 a = *reinterpret_cast<const uint4*>(s);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = T::to_f32((uint16_t)w[i]);
+            x[2 * i + 1] = T::to_f32((uint16_t)(w[i] >> 16));
+        }
+    }
+}
+
+// One group is GS / 8 neighbouring lanes; its extremes come from a butterfly
+// over them. Scale, bias and codes are those of gai4_quantize: the same
+// binary32 steps, each rounded once.
+template <typename T, int D, int GS, bool VEC>
+__global__ void __launch_bounds__(256) kv_append_kernel(const void* k, long long ks, const void* v, long long vs,
+                                                        const int64_t* __restrict__ slots, KvCache kc, KvCache vc,
+                                                        KvShape sh, int rows) {
+    constexpr int LPR = D / 8, LPG = GS / 8;   // lanes per row and per group
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int sub = lane / LPR, li = lane % LPR;
+    const int row = (blockIdx.x * 8 + (threadIdx.x >> 5)) * (32 / LPR) + sub;   // (token, k or v, head)
+    const bool live = row < rows;
+    const int per_token = 2 * sh.hkv;
+    const int token = live ? row / per_token : 0;
+    int h = live ? row - token * per_token : 0;
+    const bool is_v = h >= sh.hkv;
+    if (is_v) h -= sh.hkv;
+    const long long dst = live ? cache_row(slots[token], h, sh) : -1;
+    float x[8];
+    load8<T, VEC>(is_v ? v : k, token * (is_v ? vs : ks) + (long long)h * D + li * 8, x);
+    float mn = x[0], mx = x[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        mn = fminf(mn, x[i]);
+        mx = fmaxf(mx, x[i]);
+    }
+#pragma unroll
+    for (int o = 1; o < LPG; o <<= 1) {
+        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    }
+    const typename T::storage s_h = T::from_f32(__fdiv_rn(__fsub_rn(mx, mn), 15.0f)), b_h = T::from_f32(mn);
+    const float s = T::to_f32(s_h), b = T::to_f32(b_h);
+    uint32_t word = 0;
+    if (s != 0.0f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float r = rintf(__fdiv_rn(__fsub_rn(x[i], b), s));
+            const uint32_t q = r <= 0.0f ? 0u : (r >= 15.0f ? 15u : (uint32_t)r);
+            word |= q << (4 * i);
+        }
+    }
+    if (dst < 0) return;
+    const KvCache& c = is_v ? vc : kc;
+    const_cast<uint32_t*>(c.packed)[dst * LPR + li] = word;
+    if (li % LPG == 0) {
+        const long long g = dst * (D / GS) + li / LPG;
+        static_cast<typename T::storage*>(const_cast<void*>(c.scales))[g] = s_h;
+        static_cast<typename T::storage*>(const_cast<void*>(c.biases))[g] = b_h;
+    }
+}
+
+template <typename T, int D, int GS>
+__global__ void __launch_bounds__(256) kv_read_kernel(KvCache c, const int64_t* __restrict__ slots, float* out,
+                                                      KvShape sh, long long words) {
+    constexpr int LPR = D / 8;
+    pdl_launch_dependents();
+    pdl_wait();
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;   // word (token, head, li)
+    if (i >= words) return;
+    const long long row = i / LPR;
+    const int li = (int)(i % LPR);
+    const long long token = row / sh.hkv;
+    const long long src = cache_row(slots[token], (int)(row - token * sh.hkv), sh);
+    float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (src >= 0) {
+        const uint32_t w = c.packed[src * LPR + li];
+        const long long g = src * (D / GS) + li / (GS / 8);
+        const float s = T::to_f32(static_cast<const typename T::storage*>(c.scales)[g]);
+        const float b = T::to_f32(static_cast<const typename T::storage*>(c.biases)[g]);
+        float* f = reinterpret_cast<float*>(o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = fmaf(s, (float)((w >> (4 * j)) & 15u), b);
+    }
+    reinterpret_cast<float4*>(out)[2 * i] = o[0];
+    reinterpret_cast<float4*>(out)[2 * i + 1] = o[1];
+}
+
+// calls f<T, D, GS>() for the runtime type, head size and group size
+template <typename F>
+cudaError_t by_type(int dtype, F&& f) {
+    switch (dtype) {
+    case GAI4_F32: return f(F32{});
+    case GAI4_F16: return f(F16{});
+    default: return f(BF16{});
+    }
+}
+
+template <int D_, int GS_>
+struct Sizes {
+    static constexpr int D = D_, GS = GS_;
+};
+template <typename F>
+cudaError_t by_sizes(int d, int gs, F&& f) {
+    if (d == 64) return gs == 32 ? f(Sizes<64, 32>{}) : f(Sizes<64, 64>{});
+    return gs == 32 ? f(Sizes<128, 32>{}) : gs == 64 ? f(Sizes<128, 64>{}) : f(Sizes<128, 128>{});
+}
+
+}  // namespace
+
+cudaError_t launch_kv_plan(const KvPlanLaunch& L, cudaStream_t s) {
+    const size_t smem = 3 * sizeof(int) * (size_t)(L.batch + 1);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   3 * sizeof(int) * (kKvPlanMaxBatch + 1));
+        if (e != cudaSuccess) return e;
+    }
+    int64_t blocks = (L.num_tokens + 2 * kPlanThreads - 1) / (2 * kPlanThreads);
+    const int64_t by_rows = (L.batch + 255) / 256;
+    if (blocks < by_rows) blocks = by_rows;
+    if (blocks > num_sms()) blocks = num_sms();
+    return launch_pdl(kv_plan_kernel, dim3((unsigned)blocks), dim3(kPlanThreads), smem, s, L);
+}
+
+cudaError_t launch_kv_append(const void* k, int64_t ks, const void* v, int64_t vs, const int64_t* slots, KvCache kc,
+                             KvCache vc, const KvShape& sh, int64_t num_tokens, cudaStream_t s) {
+    return by_type(sh.dtype, [&](auto t) {
+        using T = decltype(t);
+        return by_sizes(sh.d, sh.gs, [&](auto z) {
+            using Z = decltype(z);
+            const bool vec = ((uintptr_t)k & 15) == 0 && ((uintptr_t)v & 15) == 0 && ks * T::kBytes % 16 == 0 &&
+                             vs * T::kBytes % 16 == 0;
+            // row numbers of one launch stay below 2^31
+            const int64_t chunk = (1ll << 30) / (2 * sh.hkv);
+            for (int64_t t0 = 0; t0 < num_tokens; t0 += chunk) {
+                const int64_t n = num_tokens - t0 < chunk ? num_tokens - t0 : chunk;
+                const int rows = (int)(n * 2 * sh.hkv), per_block = 8 * (32 / (Z::D / 8));
+                const dim3 grid((unsigned)((rows + per_block - 1) / per_block));
+                const void* kp = static_cast<const char*>(k) + t0 * ks * T::kBytes;
+                const void* vp = static_cast<const char*>(v) + t0 * vs * T::kBytes;
+                const cudaError_t e =
+                    vec ? launch_pdl(kv_append_kernel<T, Z::D, Z::GS, true>, grid, dim3(256), 0, s, kp, (long long)ks,
+                                     vp, (long long)vs, slots + t0, kc, vc, sh, rows)
+                        : launch_pdl(kv_append_kernel<T, Z::D, Z::GS, false>, grid, dim3(256), 0, s, kp, (long long)ks,
+                                     vp, (long long)vs, slots + t0, kc, vc, sh, rows);
+                if (e != cudaSuccess) return e;
+            }
+            return cudaSuccess;
+        });
+    });
+}
+
+cudaError_t launch_kv_read(KvCache c, const int64_t* slots, float* out, const KvShape& sh, int64_t num_tokens,
+                           cudaStream_t s) {
+    return by_type(sh.dtype, [&](auto t) {
+        using T = decltype(t);
+        return by_sizes(sh.d, sh.gs, [&](auto z) {
+            using Z = decltype(z);
+            const long long words = num_tokens * sh.hkv * (Z::D / 8);
+            const long long blocks = (words + 255) / 256;
+            if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+            return launch_pdl(kv_read_kernel<T, Z::D, Z::GS>, dim3((unsigned)blocks), dim3(256), 0, s, c, slots, out,
+                              sh, words);
+        });
+    });
+}
+
+}  // namespace gai4

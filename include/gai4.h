@@ -346,6 +346,125 @@ gai4_status gai4_last_device_status(void* stream);
  */
 gai4_status gai4_check_bounded_wait(int arrive, int64_t limit_cycles, int* status, void* stream);
 
+/* ===========================================================================
+ * Paged key/value cache held in 4 bits
+ *
+ * A cache of keys (and one of values) is a pool of `num_blocks` pages of
+ * `page_size` token slots each, in the affine group format above with 4-bit
+ * codes; a row is one slot of one key/value head:
+ *   packed          u32 [num_blocks, kv_heads, page_size, head_dim / 8]
+ *   scales, biases  T   [num_blocks, kv_heads, page_size, head_dim / group_size]
+ * so row (b, h, o) stands for s * q + b per group, and the arrays can be given
+ * to gai4_dequantize as N = num_blocks * kv_heads * page_size rows of
+ * K = head_dim. Slot numbers are b * page_size + o. A request's token at
+ * position j is in slot block_table[r, j / page_size] * page_size +
+ * j % page_size of every layer's cache.
+ * Supported: head_dim 64 or 128, group_size 32, 64 or 128 and at most
+ * head_dim, page_size 16, 32, 64, 128 or 256. The cache arrays are 16-byte
+ * aligned. (No counterpart on the pages; an addition of this library.)
+ * These calls read and write caches only after the preceding kernels of the
+ * stream have completed.
+ * ======================================================================== */
+
+/*
+ * gai4_kv_plan -- block tables, slot map, positions and query offsets of one
+ * step, from the requests' lengths, on the device.
+ *   kv_lens [batch] i32   tokens each request has in the cache
+ *   q_lens  [batch] i32   new tokens of each request in this step (0: none);
+ *                         negative: the request has finished
+ *   block_table [batch, max_blocks] i32, updated in place: the new pages of
+ *                         request r in columns ceil(kv_lens[r] / page_size) on;
+ *                         nothing else is written (a finished request's row
+ *                         stays as it is)
+ *   free_blocks [free_capacity] i32, free_count [1] i32   the stack of free
+ *                         pages. Finished requests' pages are pushed first (in
+ *                         request order, first page first), then the new pages
+ *                         are popped (in request order, first page first).
+ *                         free_blocks is updated in place.
+ *   Outputs: slots [num_tokens] i64 and positions [num_tokens] i32, the
+ *   requests' new tokens one request after the other (the rows after the last:
+ *   slot -1, position 0); cu_q [batch + 1] i32, the first row of each request;
+ *   kv_lens_out [batch] i32, the lengths after the step (0: finished);
+ *   free_count_out [1] i32; info [4] i32.
+ *   A step that does not fit is refused as a whole: info then says why, and
+ *   the outputs are those of a step in which every q_lens is 0.
+ *     info[0] pages missing           info[1] requests with more than max_blocks pages
+ *     info[2] tokens over num_tokens  info[3] 1 if a length is negative, or free_count
+ *                                     or the pages pushed do not fit free_capacity
+ * No page may be in two requests' rows. kv_lens_out and free_count_out must
+ * not alias kv_lens and free_count. 1 <= batch <= 8192; num_tokens >= 0.
+ * slots 8-byte aligned, the others 4-byte aligned. Nothing is read on the host.
+ */
+gai4_status gai4_kv_plan(const int32_t* kv_lens, const int32_t* q_lens, int32_t* block_table, int64_t max_blocks,
+                         int32_t* free_blocks, int64_t free_capacity, const int32_t* free_count, int64_t* slots,
+                         int32_t* positions, int64_t num_tokens, int32_t* cu_q, int32_t* kv_lens_out,
+                         int32_t* free_count_out, int32_t* info, int64_t batch, int page_size, void* stream);
+
+/*
+ * gai4_kv_append -- quantizes new key and value rows into their slots, by the
+ * rule of gai4_quantize (bit for bit, for finite inputs).
+ *   k, v  T, row (token i, head h) at k + i * k_token_stride + h * head_dim
+ *         (strides in elements, >= kv_heads * head_dim; aligned to their
+ *         element size)
+ *   slots [num_tokens] i64; rows whose slot is outside
+ *         [0, num_blocks * page_size) are skipped. Slots are distinct.
+ */
+gai4_status gai4_kv_append(const void* k, int64_t k_token_stride, const void* v, int64_t v_token_stride,
+                           const int64_t* slots, uint32_t* k_packed, void* k_scales, void* k_biases,
+                           uint32_t* v_packed, void* v_scales, void* v_biases, gai4_dtype dtype, int group_size,
+                           int64_t num_tokens, int64_t kv_heads, int head_dim, int64_t num_blocks, int page_size,
+                           void* stream);
+
+/*
+ * gai4_kv_read -- the values of cached rows:
+ *   out [num_tokens, kv_heads, head_dim] f32, out[i, h] = s * q + b (one
+ *   rounding) of slot slots[i], head h; zeros where the slot is outside
+ *   [0, num_blocks * page_size). out 16-byte aligned.
+ */
+gai4_status gai4_kv_read(const uint32_t* packed, const void* scales, const void* biases, const int64_t* slots,
+                         float* out, gai4_dtype dtype, int group_size, int64_t num_tokens, int64_t kv_heads,
+                         int head_dim, int64_t num_blocks, int page_size, void* stream);
+
+/*
+ * gai4_kv_attention -- causal attention of a step's queries over the cache.
+ *   Request r has the query rows [cu_q[r], cu_q[r + 1]) and kv_lens[r] cached
+ *   tokens, its own new ones among them: query i of n is at position
+ *   p = kv_lens[r] - n + i and sees the positions j <= p, and with window > 0
+ *   only j > p - window. Query head h reads key/value head
+ *   h / (q_heads / kv_heads):
+ *     out[row, h] = sum_j softmax_j(scale * q[row, h] . k_j) v_j
+ *     lse[row, h] = log sum_j exp(scale * q[row, h] . k_j)      (natural log)
+ *   A row that sees nothing gives zeros and lse -inf, and so do the rows from
+ *   cu_q[batch] to num_tokens.
+ *   q    T, row i, head h at q + i * q_token_stride + h * head_dim (strides in
+ *        elements, >= q_heads * head_dim; aligned to the element size)
+ *   out  T, likewise with out_token_stride; lse [num_tokens, q_heads] f32 or NULL
+ *   block_table [batch, max_blocks] i32; entries outside [0, num_blocks) are
+ *        never read from, and their tokens are left out.
+ *   max_q_len: the largest number of query rows of a request as far as the
+ *        host knows; it only guides the choice of kernel.
+ * bf16 / f16: with few rows per key/value head the codes enter the matrix unit
+ * as they are and scales and biases are applied in binary32; with many rows
+ * (max_q_len * q_heads / kv_heads above 32) keys and values are rounded once
+ * to T and multiplied on the tensor cores as in gai4_qmm_t. Softmax and sums
+ * are binary32; scores, probabilities and lse in the f32 form are as exact as
+ * binary32 sums are. Results do not depend on the contents of the workspace,
+ * and repeat bit for bit.
+ * workspace: 16-byte aligned, >= gai4_kv_attention_workspace_bytes(...).
+ */
+gai4_status gai4_kv_attention(const void* q, int64_t q_token_stride, const uint32_t* k_packed, const void* k_scales,
+                              const void* k_biases, const uint32_t* v_packed, const void* v_scales,
+                              const void* v_biases, const int32_t* block_table, int64_t max_blocks,
+                              const int32_t* kv_lens, const int32_t* cu_q, void* out, int64_t out_token_stride,
+                              float* lse, gai4_dtype dtype, int group_size, int64_t batch, int64_t num_tokens,
+                              int64_t max_q_len, int64_t q_heads, int64_t kv_heads, int head_dim, int64_t num_blocks,
+                              int page_size, float scale, int64_t window, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Workspace of gai4_kv_attention; it does not depend on the lengths. 0 for
+ * arguments that gai4_kv_attention refuses. */
+size_t gai4_kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int head_dim, gai4_dtype dtype);
+
 #ifdef __cplusplus
 }
 #endif
