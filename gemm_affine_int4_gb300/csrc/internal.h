@@ -156,7 +156,7 @@ cudaError_t launch_kv_append(const void* k, int64_t ks, const void* v, int64_t v
 cudaError_t launch_kv_read(KvCache c, const int64_t* slots, float* out, const KvShape& sh, int64_t num_tokens,
                            cudaStream_t s);
 
-// attention over the cache (kv_attention.cu)
+// attention over the cache (kv_attention.cuh, one file per type)
 struct KvAttnLaunch {
     const void* q;
     int64_t q_stride;
@@ -178,8 +178,9 @@ struct KvAttnLaunch {
     int* status;
     long long spin_limit;
 };
-cudaError_t launch_kv_attention(const KvAttnLaunch& L, cudaStream_t s);
-size_t kv_attention_workspace(int group, int d);
+cudaError_t launch_kv_attention_bf16(const KvAttnLaunch& L, cudaStream_t s);
+cudaError_t launch_kv_attention_f16(const KvAttnLaunch& L, cudaStream_t s);
+cudaError_t launch_kv_attention_f32(const KvAttnLaunch& L, cudaStream_t s);
 
 int* status_ptr();  // device status word of the current device
 int num_sms();  // SM count of the current device (cached)

@@ -37,6 +37,13 @@ gai4_status check_cache(const KvCache& c) {
     return GAI4_OK;
 }
 
+// two records of 16 query rows (32-bit O, m, l) for each of two CTAs per SM,
+// and a line of 16 bytes per CTA
+size_t attention_workspace(int d) {
+    const size_t ctas = 2 * (size_t)num_sms();
+    return (ctas * 16 + 255) / 256 * 256 + ctas * 2 * 16 * (size_t)(d + 2) * 4;
+}
+
 gai4_status done(cudaError_t e) { return e == cudaSuccess ? GAI4_OK : GAI4_ERR_CUDA; }
 
 }  // namespace
@@ -105,7 +112,7 @@ size_t gai4_kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int 
     KvShape sh;
     if (check_shape(dtype, 32, kv_heads, head_dim, 1, 16, &sh) != GAI4_OK) return 0;
     if (q_heads < 1 || q_heads % kv_heads != 0 || q_heads / kv_heads > 65535) return 0;
-    return kv_attention_workspace((int)(q_heads / kv_heads), head_dim);
+    return attention_workspace(head_dim);
 }
 
 gai4_status gai4_kv_attention(const void* q, int64_t q_token_stride, const uint32_t* k_packed, const void* k_scales,
@@ -134,8 +141,7 @@ gai4_status gai4_kv_attention(const void* q, int64_t q_token_stride, const uint3
         !aligned_to(cu_q, 4) || !aligned_to(lse, 4))
         return GAI4_ERR_MISALIGNED;
     L.group = (int)(q_heads / kv_heads);
-    const size_t need = kv_attention_workspace(L.group, head_dim);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return GAI4_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < attention_workspace(head_dim)) return GAI4_ERR_WORKSPACE;
     if (!aligned_to(workspace, 16)) return GAI4_ERR_MISALIGNED;
     L.q = q;
     L.q_stride = q_token_stride;
@@ -155,7 +161,11 @@ gai4_status gai4_kv_attention(const void* q, int64_t q_token_stride, const uint3
     L.status = status_ptr();
     L.spin_limit = 2000000000LL;   // ~1 s of SM clock per wait
     if (!L.status) return GAI4_ERR_CUDA;
-    return done(launch_kv_attention(L, (cudaStream_t)stream));
+    switch (dtype) {
+    case GAI4_F32: return done(launch_kv_attention_f32(L, (cudaStream_t)stream));
+    case GAI4_F16: return done(launch_kv_attention_f16(L, (cudaStream_t)stream));
+    default: return done(launch_kv_attention_bf16(L, (cudaStream_t)stream));
+    }
 }
 
 }  // extern "C"

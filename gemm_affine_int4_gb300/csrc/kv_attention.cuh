@@ -1,0 +1,1022 @@
+// kv_attention.cuh -- causal attention over the paged 4-bit key/value cache
+// for few query rows per key/value head (one token or a few per request), and
+// for f32 activations at any length.
+//
+// Mathematics. With k_j = s q_j + b per group of a key row, q . k_j =
+// sum_g s_g (q_g . c_g) + b_g (sum of q_g): the 4-bit codes go into the matrix
+// unit as they are (exact in binary16) and scale and bias are applied to the
+// products in binary32. For values, p_j s_j is rounded to binary16 and
+// multiplied with the codes, and sum_j p_j b_j is kept in binary32. So no key
+// or value is ever rounded; softmax maximum and sum run over the keys once.
+//
+//  * A code masked out of its word is a binary16 subnormal, c * 2^-24 (bits
+//    0..3 of a half) or c * 2^-20 (bits 4..7): no conversion at all. The query
+//    operand is scaled by a power of two per row so that its largest element
+//    is near 2^13 (queries keep all their bits; 2^-4 more for the elements
+//    that meet bits 4..7); the powers of two leave in the score's factor.
+//  * The value side's p s is scaled by a power of two R that follows the
+//    largest |s| seen (accumulators are rescaled when it grows), so any range
+//    of scales works and binary16 has 38 bits of room.
+//  * f32 queries and f32 p s are split in two binary16 parts (22 bits).
+//
+// Shape of the products (mma m16n8k16, tokens or value channels along M, query
+// rows along N): S^T = K Q^T and O^T = V^T P^T. One N tile is 8 query rows
+// (tokens x query heads of one key/value head), so the usual 4 to 8 query
+// heads per key head waste little. The matrix rate is no limit here: at 8
+// rows a cached row of 144 bytes takes 4096 multiply-adds, a fifth of the rate
+// that mma.sync reaches at the memory's speed; tcgen05 would need the codes
+// expanded through shared memory first.
+//
+// Work split. Tokens are cut into 64-token tiles; a unit is (request,
+// key/value head, block of 8 NT query rows), and all units' tiles form one
+// line that is cut evenly over the CTAs: ragged lengths and few long requests
+// alike fill the GPU. In a CTA a producer warp streams tiles through a ring of
+// shared-memory stages (one bulk copy per page and array), consumer warps take
+// tiles in turn with accumulators of their own and join them at the end of
+// the unit. A unit that is cut leaves (m, l, O) records in the workspace,
+// which a second kernel joins in order; its launch overlaps the first.
+#pragma once
+
+#include <math.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "pipeline.cuh"
+
+namespace gai4 {
+namespace kvs {
+
+using namespace pipe;
+
+constexpr int kTile = 64;
+constexpr int kWarps = 7;                       // consumer warps: with the producer 8, so that the registers divide well
+constexpr int kThreads = 32 * (kWarps + 1);     // and one producer warp
+
+template <typename T_, int D_, int GS_, int NT_>
+struct Cfg {
+    using T = T_;
+    static constexpr int D = D_, GS = GS_, NT = NT_;
+    static constexpr int NG = D / GS;                       // groups of a row
+    static constexpr int NC = 8 * NT;                       // query rows (columns of the products)
+    static constexpr int E = T::kBytes;
+    static constexpr bool kSplit = E == 4;                  // two binary16 parts
+    static constexpr uint32_t kCodes = kTile * D / 2, kSb = kTile * NG * E;
+    static constexpr uint32_t kStage = 2 * kCodes + 4 * kSb;
+    static constexpr int DP = D + 4;                        // padded row of the join buffer
+    static constexpr uint32_t kJoin = kWarps * NC * DP * 4 + 2 * kWarps * NC * 4;
+    static constexpr int kCtas = NT == 1 && !kSplit ? 2 : 1;   // resident CTAs per SM
+    static constexpr uint32_t kBudget = (kCtas == 2 ? 112 : 225) * 1024 - kJoin - 1024;
+    static constexpr int kStages = kBudget / (kStage + 24) < 24 ? kBudget / (kStage + 24) : 24;
+    static constexpr uint32_t kSmem = kStages * kStage + kJoin + kStages * 24 + 256;
+    static_assert(kStages >= 4, "ring too short");
+};
+
+// records of cut units in the workspace: per CTA two of (O [NC][D], m [NC],
+// l [NC]), number 0 for the end (or a middle) of a unit, 1 for its beginning,
+// and one int4 {request or -1, unit of the request, last CTA of the unit, 0}
+__host__ __device__ constexpr size_t rec_floats(int nc, int d) { return (size_t)nc * (d + 2); }
+__host__ __device__ constexpr size_t meta_bytes(int ctas) { return ((size_t)ctas * 16 + 255) / 256 * 256; }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+
+// token of row r (0..7) of a product's 8-row block: the P operand's rows 2t
+// and 2t + 1 are tokens t and t + 4, so that neighbouring lanes of the value
+// loads read neighbouring tokens
+__device__ __forceinline__ int row_token(int r) { return (r >> 1) + 4 * (r & 1); }
+
+// NG neighbouring scales or biases
+template <typename T, int NG>
+__device__ __forceinline__ void load_groups(const uint8_t* p, float (&v)[NG]) {
+    if constexpr (T::kBytes == 4) {
+        if constexpr (NG == 1) v[0] = *reinterpret_cast<const float*>(p);
+        else
+#pragma unroll
+            for (int i = 0; i < NG; i += 2) {
+                const float2 f = *reinterpret_cast<const float2*>(p + 4 * i);
+                v[i] = f.x;
+                v[i + 1] = f.y;
+            }
+    } else if constexpr (NG == 1) {
+        v[0] = T::to_f32(*reinterpret_cast<const uint16_t*>(p));
+    } else {
+#pragma unroll
+        for (int i = 0; i < NG; i += 2) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(p + 2 * i);
+            v[i] = T::to_f32((uint16_t)w);
+            v[i + 1] = T::to_f32((uint16_t)(w >> 16));
+        }
+    }
+}
+
+struct Req {
+    int q0, qn, kv, tile0, ntile;   // first query row, rows, cached tokens, first tile, tiles of each unit
+};
+
+// units of request r: all rows of a request share the range of tiles that any
+// of them sees (at least one tile, so that every unit writes its output)
+__device__ __forceinline__ Req request(const KvAttnLaunch& p, int r) {
+    Req q;
+    const int n = (int)p.num_tokens;
+    q.q0 = min(max(p.cu_q[r], 0), n);
+    q.qn = max(min(p.cu_q[r + 1], n) - q.q0, 0);
+    const long long cap = p.max_blocks << p.sh.page_log2;
+    q.kv = (int)min((long long)max(p.kv_lens[r], 0), cap);
+    const long long lo = p.window > 0 ? max((long long)q.kv - q.qn - p.window + 1, 0ll) : 0;
+    q.tile0 = (int)(min(lo, (long long)q.kv) / kTile);
+    q.ntile = max((q.kv + kTile - 1) / kTile - q.tile0, 1);
+    return q;
+}
+__device__ __forceinline__ int row_blocks(const Req& q, int group, int nc) {
+    return (int)(((long long)q.qn * group + nc - 1) / nc);
+}
+
+// A warp's walk along the line of tiles: the requests' sizes are held by the
+// lanes, 32 at a time.
+template <int NC>
+struct Walk {
+    const KvAttnLaunch& p;
+    int base, lane;
+    Req mine;
+    long long c, c1;
+    int r, unit, tile;    // current request, unit within it, tile within the unit
+    Req q;
+    int nrb, units;
+
+    __device__ Walk(const KvAttnLaunch& p_, int lane_, int r0, long long off, long long c0, long long c1_)
+        : p(p_), base(-1), lane(lane_), c(c0), c1(c1_), r(r0) {
+        load();
+        unit = (int)(off / q.ntile);
+        tile = (int)(off - (long long)unit * q.ntile);
+    }
+    __device__ void load() {
+        if (base < 0 || r - base >= 32) {
+            base = r;
+            mine = Req{0, 0, 0, 0, 1};
+            if (r + lane < p.batch) mine = request(p, r + lane);
+        }
+        const int s = r - base;
+        q.q0 = __shfl_sync(0xffffffffu, mine.q0, s);
+        q.qn = __shfl_sync(0xffffffffu, mine.qn, s);
+        q.kv = __shfl_sync(0xffffffffu, mine.kv, s);
+        q.tile0 = __shfl_sync(0xffffffffu, mine.tile0, s);
+        q.ntile = __shfl_sync(0xffffffffu, mine.ntile, s);
+        nrb = row_blocks(q, p.group, NC);
+        units = nrb * p.sh.hkv;
+    }
+    __device__ bool more() const { return c < c1; }
+    __device__ int here() const { return (int)min((long long)(q.ntile - tile), c1 - c); }   // tiles of this segment
+    __device__ int head() const { return unit / nrb; }
+    __device__ int block() const { return unit % nrb; }
+    // tiles [a, b) of the segment that some row of the unit can see
+    __device__ void clip(int& a, int& b) const {
+        const int rb = block();
+        const int i0 = (int)((long long)rb * NC / p.group);
+        const int i1 = min((int)(((long long)rb * NC + NC - 1) / p.group), q.qn - 1);
+        const long long end = (long long)q.kv - q.qn + i1 + 1;      // keys below it
+        const long long lo = p.window > 0 ? max((long long)q.kv - q.qn + i0 - p.window + 1, 0ll) : 0;
+        a = max(tile, (int)(lo / kTile) - q.tile0);
+        b = min(tile + here(), (int)((max(end, 0ll) + kTile - 1) / kTile) - q.tile0);
+    }
+    __device__ void advance() {
+        const int n = here();
+        c += n;
+        tile += n;
+        if (tile == q.ntile) {
+            tile = 0;
+            if (++unit == units) {
+                unit = 0;
+                if (c < c1) {
+                    do {
+                        ++r;
+                        load();
+                    } while (units == 0 && r + 1 < p.batch);
+                }
+            }
+        }
+    }
+};
+
+template <class C>
+__device__ __forceinline__ void producer(const KvAttnLaunch& p, Walk<C::NC>& w, uint8_t* ring, uint64_t* full,
+                                         uint64_t* empty, unsigned long long* masks, const Ctl& ctl) {
+    constexpr int S = C::kStages;
+    const int lane = threadIdx.x & 31;
+    const int pl = p.sh.page_log2;
+    const int pieces = pl >= 6 ? 1 : kTile >> pl;          // pages of a tile
+    const int tokens = pl >= 6 ? kTile : 1 << pl;          // tokens of a piece
+    const int piece = lane / 6, which = lane - 6 * piece;  // this lane's copy
+    const bool active = piece < pieces;
+    const uint32_t bytes = which < 2 ? (uint32_t)tokens * (C::D / 2) : (uint32_t)tokens * (C::NG * C::E);
+    const uint32_t row_bytes = which < 2 ? C::D / 2 : C::NG * C::E;
+    const uint8_t* src0 = static_cast<const uint8_t*>(
+        which == 0   ? static_cast<const void*>(p.k.packed)
+        : which == 1 ? static_cast<const void*>(p.v.packed)
+        : which == 2 ? p.k.scales
+        : which == 3 ? p.k.biases
+        : which == 4 ? p.v.scales
+                     : p.v.biases);
+    const uint32_t dst0 = (which < 2 ? which * C::kCodes : 2 * C::kCodes + (which - 2) * C::kSb) + piece * bytes;
+    const uint32_t ring_s = smem_u32(ring);
+    int seq = 0;
+    bool ok = true;
+    while (w.more() && ok) {
+        int a, b;
+        w.clip(a, b);
+        const int h = w.head();
+        const int* row = p.table + (long long)w.r * p.max_blocks;
+        const int nblk = (w.q.kv + (1 << pl) - 1) >> pl;
+        // the table's entries, 32 held by the lanes and the next 32 on their way
+        int cb = a < b ? ((((w.q.tile0 + a) * kTile) >> pl) & ~31) : 0;
+        int ids = cb + lane < nblk ? row[cb + lane] : -1;
+        int next = cb + 32 + lane < nblk ? row[cb + 32 + lane] : -1;
+        for (int t = a; t < b; ++t, ++seq) {
+            const int tok0 = (w.q.tile0 + t) * kTile;
+            const int blk = (tok0 >> pl) + piece;
+            if ((tok0 >> pl) >= cb + 32) {
+                cb += 32;
+                ids = next;
+                next = cb + 32 + lane < nblk ? row[cb + 32 + lane] : -1;
+            }
+            const int page = __shfl_sync(0xffffffffu, ids, (blk - cb) & 31);
+            const bool there = active && page >= 0 && page < p.sh.num_blocks;
+            const uint32_t votes = __ballot_sync(0xffffffffu, there && which == 0);
+            const int slot = seq % S;
+            if (!warp_wait(&empty[slot], ((seq / S) & 1) ^ 1, ctl)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                unsigned long long m = 0;
+                for (int i = 0; i < pieces; ++i)
+                    if ((votes >> (6 * i)) & 1u) m |= (tokens == 64 ? ~0ull : ((1ull << tokens) - 1)) << (i * tokens);
+                const int left = w.q.kv - tok0;
+                if (left < 64) m &= left <= 0 ? 0ull : (1ull << left) - 1;
+                masks[slot] = m;
+                mbar_arrive_expect_tx(&full[slot],
+                                      (uint32_t)__popc(votes) * (uint32_t)tokens * (C::D + 4 * C::NG * C::E));
+            }
+            __syncwarp();
+            if (there) {
+                const long long line = (((long long)page * p.sh.hkv + h) << pl) + (tok0 & ((1 << pl) - 1));
+                bulk_load(ring_s + (uint32_t)slot * C::kStage + dst0, src0 + line * row_bytes, bytes, &full[slot]);
+            }
+        }
+        w.advance();
+    }
+    // no copy may land after the CTA has gone
+    for (int i = seq > S ? seq - S : 0; i < seq; ++i) mbar_wait_drain(&full[i % S], (i / S) & 1, ctl.limit, ctl.status);
+}
+
+// per-warp running state of a unit
+template <class C>
+struct Acc {
+    float o[C::D / 16][C::NT][4];   // O^T: [value channel block][rows][...], in units of R 2^-14 2^-24 (2^-20)
+    float ab[C::NG][C::NT][2];      // sum p b
+    float m[C::NT][2], l[C::NT][2];
+    int re;                         // exponent field of R
+};
+
+template <class C>
+__device__ __forceinline__ void clear(Acc<C>& a) {
+#pragma unroll
+    for (int i = 0; i < C::D / 16; ++i)
+#pragma unroll
+        for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a.o[i][n][e] = 0.f;
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            a.m[n][e] = -INFINITY;
+            a.l[n][e] = 0.f;
+#pragma unroll
+            for (int g = 0; g < C::NG; ++g) a.ab[g][n][e] = 0.f;
+        }
+    a.re = 27;
+}
+
+// query operand of one unit
+template <class C>
+struct Query {
+    uint32_t b[C::kSplit ? 2 : 1][C::D / 16][C::NT][2];
+    float f[C::NT][2];            // score factor of columns 2t, 2t + 1: log2(e) scale, powers of two undone
+    float sq[C::NG][C::NT][2];    // log2(e) scale * sum of the group's elements
+};
+
+template <typename T>
+__device__ __forceinline__ void load_q8(const typename T::storage* s, bool vec, float (&x)[8]) {
+    if (!vec) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = T::to_f32(s[i]);
+    } else if constexpr (T::kBytes == 4) {
+        const float4 a = reinterpret_cast<const float4*>(s)[0], b = reinterpret_cast<const float4*>(s)[1];
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+        const uint4 a = *reinterpret_cast<const uint4*>(s);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = T::to_f32((uint16_t)w[i]);
+            x[2 * i + 1] = T::to_f32((uint16_t)(w[i] >> 16));
+        }
+    }
+}
+
+template <class C>
+__device__ __forceinline__ void load_query(const KvAttnLaunch& p, const Req& rq, int h, int rb, bool vec, Query<C>& Q) {
+    using T = typename C::T;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const float sl = p.scale * 1.4426950408889634f;
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n) {
+        const long long rr = (long long)rb * C::NC + n * 8 + g;
+        const bool valid = rr < (long long)rq.qn * p.group;
+        const int i = valid ? (int)(rr / p.group) : 0;
+        const int head = h * p.group + (valid ? (int)(rr - (long long)i * p.group) : 0);
+        const typename T::storage* src =
+            static_cast<const typename T::storage*>(p.q) + (rq.q0 + i) * p.q_stride + (long long)head * C::D;
+        float x[C::D / 32][8];
+        float amax = 0.f, sum[C::NG];
+#pragma unroll
+        for (int k = 0; k < C::NG; ++k) {
+            sum[k] = 0.f;
+#pragma unroll
+            for (int j = 0; j < C::GS / 32; ++j) {
+                const int wi = k * (C::GS / 32) + j;
+                float(&y)[8] = x[wi];
+                if (valid) {
+                    load_q8<T>(src + 8 * (k * (C::GS / 8) + t * (C::GS / 32) + j), vec, y);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    amax = fmaxf(amax, fabsf(y[e]));
+                    sum[k] += y[e];
+                }
+            }
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // largest element to [2^13, 2^14); exponents kept where both powers are normal
+        const int e = min(max((int)(__float_as_uint(amax) >> 23), 20), 254);
+        const float up = __uint_as_float((uint32_t)(267 - e) << 23), down = __uint_as_float((uint32_t)(e - 13) << 23);
+#pragma unroll
+        for (int k = 0; k < C::NG; ++k) {
+            sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
+            sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int from = (2 * t + c) * 4;
+            // 2^24 in two steps: down may be as large as 2^114
+            Q.f[n][c] = __shfl_sync(0xffffffffu, down * sl, from) * 16777216.f;
+#pragma unroll
+            for (int k = 0; k < C::NG; ++k) Q.sq[k][n][c] = __shfl_sync(0xffffffffu, sum[k], from) * sl;
+        }
+#pragma unroll
+        for (int wi = 0; wi < C::D / 32; ++wi) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                // elements (2 half, 2 half + 4) meet bits 0..3, the next ones bits 4..7
+                float y[4] = {x[wi][2 * half] * up, x[wi][2 * half + 4] * up, x[wi][2 * half + 1] * up * 0.0625f,
+                              x[wi][2 * half + 5] * up * 0.0625f};
+#pragma unroll
+                for (int part = 0; part < (C::kSplit ? 2 : 1); ++part) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t w = pack_f16(y[2 * k], y[2 * k + 1]);
+                        Q.b[part][2 * wi + half][n][k] = w;
+                        if constexpr (C::kSplit) {
+                            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&w));
+                            y[2 * k] -= back.x;
+                            y[2 * k + 1] -= back.y;
+                        }
+                    }
+                }
+            }
+        }
+    }
+}
+
+// what columns 2t and 2t + 1 of each 8-column block may see: keys [lo, hi)
+template <int NT>
+struct Limits {
+    int lo[NT][2], hi[NT][2];
+    int lo_max, hi_min;   // keys in [lo_max, hi_min) are seen by every row of the unit
+};
+
+template <class C>
+__device__ __forceinline__ Limits<C::NT> limits(const KvAttnLaunch& p, const Req& rq, int rb) {
+    Limits<C::NT> L;
+    const int t = threadIdx.x & 3;
+    const long long rows = (long long)rq.qn * p.group;
+    const long long pos0 = (long long)rq.kv - rq.qn;
+    auto low = [&](int i) { return p.window > 0 ? (int)max(pos0 + i - p.window + 1, 0ll) : 0; };
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const long long rr = (long long)rb * C::NC + n * 8 + 2 * t + c;
+            const int i = (int)(rr / p.group);
+            const bool valid = rr < rows;
+            L.hi[n][c] = valid ? (int)max(pos0 + i + 1, 0ll) : 0;
+            L.lo[n][c] = valid ? low(i) : 0;
+        }
+    const long long last = min((long long)rb * C::NC + C::NC, rows) - 1;
+    L.hi_min = (int)max(pos0 + (long long)rb * C::NC / p.group + 1, 0ll);
+    L.lo_max = low((int)(last / p.group));
+    return L;
+}
+
+template <class C>
+__device__ __forceinline__ void tile(const uint8_t* st, unsigned long long mask, int tok0, const Query<C>& Q,
+                                     const Limits<C::NT>& L, Acc<C>& A) {
+    using T = typename C::T;
+    constexpr int NT = C::NT, NG = C::NG, D = C::D, GS = C::GS;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint8_t* ksc = st + 2 * C::kCodes;
+    const uint8_t* kbi = ksc + C::kSb;
+    const uint8_t* vsc = kbi + C::kSb;
+    const uint8_t* vbi = vsc + C::kSb;
+    const int tg = row_token(g);
+
+    // ---- scores, in units of log2: x[16-token block][8-column block][row g | g + 8, column 2t | 2t + 1]
+    float x[4][NT][4];
+#pragma unroll
+    for (int mb = 0; mb < 4; ++mb) {
+        float s0[NG], s1[NG], b0[NG], b1[NG];
+        const int ra = 16 * mb + tg, rb = ra + 8;
+        load_groups<T, NG>(ksc + ra * NG * C::E, s0);
+        load_groups<T, NG>(ksc + rb * NG * C::E, s1);
+        load_groups<T, NG>(kbi + ra * NG * C::E, b0);
+        load_groups<T, NG>(kbi + rb * NG * C::E, b1);
+        float u[NT][4], v[NT][4];
+#pragma unroll
+        for (int k = 0; k < NG; ++k) {
+            constexpr int W = GS / 32;   // words per lane, row and group
+            uint32_t wa[W], wb[W];
+            const uint32_t* pa = reinterpret_cast<const uint32_t*>(st + ra * (D / 2) + k * (GS / 2)) + t * W;
+            const uint32_t* pb = reinterpret_cast<const uint32_t*>(st + rb * (D / 2) + k * (GS / 2)) + t * W;
+            if constexpr (W == 1) {
+                wa[0] = *pa;
+                wb[0] = *pb;
+            } else if constexpr (W == 2) {
+                const uint2 a = *reinterpret_cast<const uint2*>(pa), b = *reinterpret_cast<const uint2*>(pb);
+                wa[0] = a.x; wa[1] = a.y;
+                wb[0] = b.x; wb[1] = b.y;
+            } else {
+                const uint4 a = *reinterpret_cast<const uint4*>(pa), b = *reinterpret_cast<const uint4*>(pb);
+                wa[0] = a.x; wa[1] = a.y; wa[2] = a.z; wa[3] = a.w;
+                wb[0] = b.x; wb[1] = b.y; wb[2] = b.z; wb[3] = b.w;
+            }
+            float acc[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t a = half ? wa[j] >> 8 : wa[j], b = half ? wb[j] >> 8 : wb[j];
+                    const uint32_t a0 = a & 0x000F000Fu, a2 = a & 0x00F000F0u;
+                    const uint32_t a1 = b & 0x000F000Fu, a3 = b & 0x00F000F0u;
+                    const int ks = 2 * (k * W + j) + half;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma16816(acc[n], a0, a1, a2, a3, Q.b[0][ks][n][0], Q.b[0][ks][n][1]);
+                        if constexpr (C::kSplit)
+                            mma16816(acc[n], a0, a1, a2, a3, Q.b[1][ks][n][0], Q.b[1][ks][n][1]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float s = e < 2 ? s0[k] : s1[k], b = e < 2 ? b0[k] : b1[k];
+                    u[n][e] = k == 0 ? acc[n][e] * s : fmaf(acc[n][e], s, u[n][e]);
+                    v[n][e] = k == 0 ? b * Q.sq[k][n][e & 1] : fmaf(b, Q.sq[k][n][e & 1], v[n][e]);
+                }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[mb][n][e] = fmaf(u[n][e], Q.f[n][e & 1], v[n][e]);
+    }
+    // ---- masks: only on tiles that some row does not see in full
+    if (mask != ~0ull || tok0 + kTile > L.hi_min || tok0 < L.lo_max) {
+#pragma unroll
+        for (int mb = 0; mb < 4; ++mb)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int o = 16 * mb + tg + (e < 2 ? 0 : 8), j = tok0 + o;
+                    if (!((mask >> o) & 1) || j >= L.hi[n][e & 1] || j < L.lo[n][e & 1]) x[mb][n][e] = -INFINITY;
+                }
+    }
+    // ---- running maximum of every column
+    float mx[NT][2];
+    bool grew = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float m = fmaxf(x[0][n][c], x[0][n][c + 2]);
+#pragma unroll
+            for (int mb = 1; mb < 4; ++mb) m = fmaxf(m, fmaxf(x[mb][n][c], x[mb][n][c + 2]));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+            mx[n][c] = m;
+            grew |= m > A.m[n][c];
+        }
+    // value scales of this lane's tokens, and whether R has to grow
+    float vs[4][2][NG];
+    float smax = 0.f;
+#pragma unroll
+    for (int mb = 0; mb < 4; ++mb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            load_groups<T, NG>(vsc + (16 * mb + tg + 8 * e) * NG * C::E, vs[mb][e]);
+#pragma unroll
+            for (int k = 0; k < NG; ++k) smax = fmaxf(smax, fabsf(vs[mb][e][k]));
+        }
+    const bool wider = smax > __uint_as_float((uint32_t)A.re << 23);
+    if (__any_sync(0xffffffffu, grew || wider)) {
+        const uint32_t sb = __reduce_max_sync(0xffffffffu, __float_as_uint(smax));   // non-negative: ordered as integers
+        const int ne = max(A.re, min((int)(sb >> 23) + ((sb & 0x7fffffu) != 0), 254));
+        const float down = A.re == ne ? 1.f : ex2((float)(A.re - ne));
+        A.re = ne;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float m = fmaxf(A.m[n][c], mx[n][c]);
+                const float f = A.m[n][c] == -INFINITY ? 0.f : ex2(A.m[n][c] - m);
+                A.m[n][c] = m;
+                A.l[n][c] *= f;
+#pragma unroll
+                for (int k = 0; k < NG; ++k) A.ab[k][n][c] *= f;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    A.o[i][n][c] *= f * down;
+                    A.o[i][n][c + 2] *= f * down;
+                }
+            }
+    }
+    // ---- probabilities
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const float m = A.m[n][c] == -INFINITY ? 0.f : A.m[n][c];
+            float l = 0.f;
+#pragma unroll
+            for (int mb = 0; mb < 4; ++mb) {
+                x[mb][n][c] = ex2(x[mb][n][c] - m);
+                x[mb][n][c + 2] = ex2(x[mb][n][c + 2] - m);
+                l += x[mb][n][c] + x[mb][n][c + 2];
+            }
+            A.l[n][c] += l;
+        }
+    // ---- values
+    const float inv = __uint_as_float((uint32_t)(min(268 - A.re, 254)) << 23);   // 2^14 / R
+#pragma unroll
+    for (int mb = 0; mb < 4; ++mb) {
+        float b0[NG], b1[NG];
+        load_groups<T, NG>(vbi + (16 * mb + tg) * NG * C::E, b0);
+        load_groups<T, NG>(vbi + (16 * mb + tg + 8) * NG * C::E, b1);
+        uint32_t P[C::kSplit ? 2 : 1][NG][NT][2];
+#pragma unroll
+        for (int k = 0; k < NG; ++k) {
+            const float s[2] = {vs[mb][0][k] * inv, vs[mb][1][k] * inv};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    A.ab[k][n][c] = fmaf(x[mb][n][c + 2], b1[k], fmaf(x[mb][n][c], b0[k], A.ab[k][n][c]));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float y0 = x[mb][n][2 * e] * s[e], y1 = x[mb][n][2 * e + 1] * s[e];
+                    const uint32_t w = pack_f16(y0, y1);
+                    P[0][k][n][e] = transpose8(w);
+                    if constexpr (C::kSplit) {
+                        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&w));
+                        P[1][k][n][e] = transpose8(pack_f16(y0 - back.x, y1 - back.y));
+                    }
+                }
+            }
+        }
+        // rows g / g + 8 of a value block: codes 2i / 2i + 1 of this lane's word
+        const uint8_t* vc = st + C::kCodes + (16 * mb + t) * (D / 2);   // tokens t, t + 4, t + 8, t + 12
+        constexpr int kChunks = GS == 32 ? NG : D / 64;
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) {
+            const int word = GS == 32 ? 4 * j + (g >> 1) : 8 * j + g;
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(vc + i * (4 * D / 2) + word * 4);
+            constexpr int kHalves = GS == 32 ? 1 : 2;
+#pragma unroll
+            for (int hh = 0; hh < kHalves; ++hh) {
+                const uint32_t sel = GS == 32 ? ((g & 1) ? 0x7632u : 0x5410u) : (hh ? 0x7632u : 0x5410u);
+                const uint32_t a = __byte_perm(w[0], w[1], sel), b = __byte_perm(w[2], w[3], sel);
+                const int k = GS == 32 ? j : (j * 64) / GS;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const uint32_t aa = q ? a >> 8 : a, bb = q ? b >> 8 : b;
+                    const uint32_t a0 = aa & 0x000F000Fu, a1 = aa & 0x00F000F0u;
+                    const uint32_t a2 = bb & 0x000F000Fu, a3 = bb & 0x00F000F0u;
+                    const int blk = GS == 32 ? 2 * j + q : 4 * j + 2 * hh + q;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma16816(A.o[blk][n], a0, a1, a2, a3, P[0][k][n][0], P[0][k][n][1]);
+                        if constexpr (C::kSplit) mma16816(A.o[blk][n], a0, a1, a2, a3, P[1][k][n][0], P[1][k][n][1]);
+                    }
+                }
+            }
+        }
+    }
+}
+
+// joins the warps' results of a segment; thread i then owns four channels of
+// some columns and calls write(column, channel, float4 O, m, l) with O not yet divided by l
+template <class C, typename F>
+__device__ __forceinline__ void join(Acc<C>& A, uint8_t* buf, F&& write) {
+    constexpr int NT = C::NT, NC = C::NC, D = C::D, DP = C::DP;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float* o = reinterpret_cast<float*>(buf);
+    float* sm = o + kWarps * NC * DP;
+    float* sl = sm + kWarps * NC;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) {
+                A.l[n][c] += __shfl_xor_sync(0xffffffffu, A.l[n][c], s);
+#pragma unroll
+                for (int k = 0; k < C::NG; ++k) A.ab[k][n][c] += __shfl_xor_sync(0xffffffffu, A.ab[k][n][c], s);
+            }
+        }
+    consumer_sync();   // the previous unit's readers are done
+    const float R = __uint_as_float((uint32_t)A.re << 23);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int col = n * 8 + 2 * t + c;
+            if (g == 0) {
+                sm[warp * NC + col] = A.m[n][c];
+                sl[warp * NC + col] = A.l[n][c];
+            }
+            float* dst = o + (warp * NC + col) * DP;
+            if constexpr (C::GS == 32) {
+#pragma unroll
+                for (int k = 0; k < C::NG; ++k) {   // channels 32 k + 8 (g >> 1) + 4 (g & 1) + 0..3
+                    float4 f;
+                    f.x = fmaf(A.o[2 * k][n][c] * 1024.f, R, A.ab[k][n][c]);
+                    f.y = fmaf(A.o[2 * k][n][c + 2] * 64.f, R, A.ab[k][n][c]);
+                    f.z = fmaf(A.o[2 * k + 1][n][c] * 1024.f, R, A.ab[k][n][c]);
+                    f.w = fmaf(A.o[2 * k + 1][n][c + 2] * 64.f, R, A.ab[k][n][c]);
+                    *reinterpret_cast<float4*>(dst + 32 * k + 4 * g) = f;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {   // channels 64 j + 8 g + 4 hh + 0..3
+                        const int k = (j * 64) / C::GS, b = 4 * j + 2 * hh;
+                        float4 f;
+                        f.x = fmaf(A.o[b][n][c] * 1024.f, R, A.ab[k][n][c]);
+                        f.y = fmaf(A.o[b][n][c + 2] * 64.f, R, A.ab[k][n][c]);
+                        f.z = fmaf(A.o[b + 1][n][c] * 1024.f, R, A.ab[k][n][c]);
+                        f.w = fmaf(A.o[b + 1][n][c + 2] * 64.f, R, A.ab[k][n][c]);
+                        *reinterpret_cast<float4*>(dst + 64 * j + 8 * g + 4 * hh) = f;
+                    }
+            }
+        }
+    consumer_sync();
+    for (int i = threadIdx.x; i < NC * D / 4; i += 32 * kWarps) {
+        const int col = i / (D / 4), d = (i % (D / 4)) * 4;
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm[w * NC + col]);
+        float l = 0.f;
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float mw = sm[w * NC + col];
+            if (mw != -INFINITY) {   // (a warp that saw nothing adds nothing)
+                const float e = ex2(mw - m);
+                const float4 v = *reinterpret_cast<const float4*>(o + (w * NC + col) * DP + d);
+                l = fmaf(sl[w * NC + col], e, l);
+                f.x = fmaf(v.x, e, f.x);
+                f.y = fmaf(v.y, e, f.y);
+                f.z = fmaf(v.z, e, f.z);
+                f.w = fmaf(v.w, e, f.w);
+            }
+        }
+        write(col, d, f, m, l);
+    }
+}
+
+// one query row's four channels, divided by the softmax sum and rounded once
+template <typename T>
+__device__ __forceinline__ void store_out(const KvAttnLaunch& p, bool vec, long long row, int head, int D, int d, float4 f,
+                                          float m, float l) {
+    using St = typename T::storage;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (l == 0.f) f = make_float4(0.f, 0.f, 0.f, 0.f);
+    St* o = static_cast<St*>(p.out) + row * p.out_stride + (long long)head * D + d;
+    const St v[4] = {T::from_f32(f.x * inv), T::from_f32(f.y * inv), T::from_f32(f.z * inv), T::from_f32(f.w * inv)};
+    if (vec) {
+        if constexpr (T::kBytes == 4)
+            *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+        else
+            *reinterpret_cast<uint2*>(o) =
+                make_uint2((uint32_t)v[0] | ((uint32_t)v[1] << 16), (uint32_t)v[2] | ((uint32_t)v[3] << 16));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = v[i];
+    }
+    if (p.lse && d == 0)
+        p.lse[row * ((long long)p.sh.hkv * p.group) + head] =
+            l == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(l));
+}
+
+template <class C>
+__global__ void __launch_bounds__(kThreads, C::kCtas)
+    kv_attention_kernel(const __grid_constant__ KvAttnLaunch p, const int vec_q, const int vec_out) {
+    using T = typename C::T;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ long long warp_cost[kWarps + 1];
+    __shared__ long long start_off;
+    __shared__ int start_r, abort_flag;
+    constexpr int S = C::kStages;
+    uint8_t* ring = smem;
+    uint8_t* buf = ring + S * C::kStage;
+    uint64_t* full = reinterpret_cast<uint64_t*>(buf + C::kJoin);
+    uint64_t* empty = full + S;
+    unsigned long long* masks = reinterpret_cast<unsigned long long*>(empty + S);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_launch_dependents();
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    pdl_wait();
+
+    // the line of tiles: its length, and where this CTA's part begins. Each
+    // thread sums a strip of requests.
+    const int per_thread = (p.batch + kThreads - 1) / kThreads;
+    const int r0 = min(tid * per_thread, p.batch), r1 = min(r0 + per_thread, p.batch);
+    auto cost = [&](int r) {
+        const Req q = request(p, r);
+        return (long long)row_blocks(q, p.group, C::NC) * p.sh.hkv * q.ntile;
+    };
+    long long mine = 0;
+    for (int r = r0; r < r1; ++r) mine += cost(r);
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) warp_cost[warp] = inc;
+    __syncthreads();
+    long long total = 0, before = inc - mine;
+#pragma unroll
+    for (int i = 0; i <= kWarps; ++i) {
+        if (i < warp) before += warp_cost[i];
+        total += warp_cost[i];
+    }
+    const long long per = max((total + gridDim.x - 1) / gridDim.x, 1ll);
+    const long long c0 = min((long long)blockIdx.x * per, total), c1 = min(c0 + per, total);
+    if (c0 < c1 && before <= c0 && c0 < before + mine) {
+        int r = r0;
+        long long at = before;
+        for (long long n; at + (n = cost(r)) <= c0; ++r) at += n;
+        start_r = r;
+        start_off = c0 - at;
+    }
+    // rows that belong to no request
+    {
+        const int hq = p.sh.hkv * p.group;
+        const long long first = max(min((long long)p.cu_q[p.batch], (long long)p.num_tokens), 0ll);
+        for (long long row = first + blockIdx.x; row < p.num_tokens; row += gridDim.x) {
+            auto* o = static_cast<typename T::storage*>(p.out) + row * p.out_stride;
+            for (int i = tid; i < hq * C::D; i += kThreads) o[i] = T::from_f32(0.f);
+            if (p.lse)
+                for (int i = tid; i < hq; i += kThreads) p.lse[row * hq + i] = -INFINITY;
+        }
+    }
+    uint8_t* ws = static_cast<uint8_t*>(p.workspace);
+    int4* meta = reinterpret_cast<int4*>(ws) + blockIdx.x;
+    float* recs = reinterpret_cast<float*>(ws + meta_bytes(gridDim.x)) + blockIdx.x * 2 * rec_floats(C::NC, C::D);
+    __syncthreads();
+    if (c0 >= c1) {
+        if (tid == 0) *meta = make_int4(-1, 0, 0, 0);
+        return;
+    }
+
+    Walk<C::NC> w(p, lane, start_r, start_off, c0, c1);
+    const Ctl ctl{p.status, p.spin_limit, &abort_flag};
+    if (warp == kWarps) {
+        producer<C>(p, w, ring, full, empty, masks, ctl);
+        return;
+    }
+    // ---- consumers
+    int seq = 0;
+    bool cut = false;    // this CTA holds the beginning of a unit that goes on
+    while (w.more()) {
+        int a, b;
+        w.clip(a, b);
+        const int h = w.head(), rb = w.block();
+        Query<C> Q;
+        load_query<C>(p, w.q, h, rb, vec_q != 0, Q);
+        const Limits<C::NT> L = limits<C>(p, w.q, rb);
+        Acc<C> A;
+        clear<C>(A);
+        for (int t = a; t < b; ++t, ++seq) {
+            if (seq % kWarps != warp) continue;
+            const int slot = seq % S;
+            // after a time-out the outputs are undefined, but every role still ends
+            (void)warp_wait(&full[slot], (seq / S) & 1, ctl);
+            uint8_t* st = ring + (size_t)slot * C::kStage;
+            const unsigned long long mask = masks[slot];
+            if (mask != ~0ull) {
+                // scales and biases of slots without a token may hold anything
+                for (int o = lane; o < kTile; o += 32)
+                    if (!((mask >> o) & 1))
+                        for (int k = 0; k < 4; ++k)
+                            for (int i = 0; i < C::NG * C::E / 2; ++i)
+                                reinterpret_cast<uint16_t*>(st + 2 * C::kCodes + k * C::kSb)[o * (C::NG * C::E / 2) + i] = 0;
+                __syncwarp();
+            }
+            tile<C>(st, mask, (w.q.tile0 + t) * kTile, Q, L, A);
+            if (mask != ~0ull) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[slot]);
+        }
+        const bool begins = w.tile == 0, ends = w.tile + w.here() == w.q.ntile;
+        const long long rows = (long long)w.q.qn * p.group;
+        float* rec = recs + (begins ? rec_floats(C::NC, C::D) : 0);
+        join<C>(A, buf, [&](int col, int d, float4 f, float m, float l) {
+            if (begins && ends) {
+                const long long rr = (long long)rb * C::NC + col;
+                if (rr >= rows) return;
+                const int i = (int)(rr / p.group);
+                store_out<T>(p, vec_out != 0, w.q.q0 + i, h * p.group + (int)(rr - (long long)i * p.group), C::D, d, f, m, l);
+            } else {
+                *reinterpret_cast<float4*>(rec + col * C::D + d) = f;
+                if (d == 0) {
+                    rec[C::NC * C::D + col] = m;
+                    rec[C::NC * C::D + C::NC + col] = l;
+                }
+            }
+        });
+        if (begins && !ends) {
+            cut = true;
+            if (tid == 0) {
+                const long long end = w.c + w.q.ntile;   // of the unit, on the line
+                *meta = make_int4(w.r, w.unit, (int)((end - 1) / per), 0);
+            }
+        }
+        w.advance();
+    }
+    if (!cut && tid == 0) *meta = make_int4(-1, 0, 0, 0);
+}
+
+// joins the records of a cut unit, in the order of the CTAs: block (i, c) the
+// column c of the unit that begins in CTA i and goes on
+template <class C>
+__global__ void __launch_bounds__(128) kv_combine_kernel(const __grid_constant__ KvAttnLaunch p, const int ctas,
+                                                         const int vec_out) {
+    constexpr int D = C::D, NC = C::NC, G = 128 / (D / 4);   // groups of threads that share the records
+    __shared__ float sm[G], sl[G];
+    __shared__ float4 so[128];
+    pdl_launch_dependents();
+    pdl_wait();
+    const uint8_t* ws = static_cast<const uint8_t*>(p.workspace);
+    const int4 meta = reinterpret_cast<const int4*>(ws)[blockIdx.x];
+    if (meta.x < 0) return;
+    const int col = blockIdx.y;
+    const Req rq = request(p, meta.x);
+    const int nrb = row_blocks(rq, p.group, NC);
+    const int h = meta.y / nrb, rb = meta.y % nrb;
+    const long long rr = (long long)rb * NC + col;
+    if (rr >= (long long)rq.qn * p.group) return;
+    const float* recs = reinterpret_cast<const float*>(ws + meta_bytes(ctas));
+    const int gi = threadIdx.x / (D / 4), d = (threadIdx.x % (D / 4)) * 4;
+    const int n = meta.z - (int)blockIdx.x + 1;
+    float m = -INFINITY, l = 0.f;
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = gi; i < n; i += G) {
+        const float* rec = recs + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * rec_floats(NC, D);
+        const float mi = rec[NC * D + col], li = rec[NC * D + NC + col];
+        const float4 v = *reinterpret_cast<const float4*>(rec + col * D + d);
+        if (mi == -INFINITY) continue;
+        const float mn = fmaxf(m, mi);
+        const float c = m == -INFINITY ? 0.f : ex2(m - mn), e = ex2(mi - mn);
+        m = mn;
+        l = l * c + li * e;
+        f.x = f.x * c + v.x * e;
+        f.y = f.y * c + v.y * e;
+        f.z = f.z * c + v.z * e;
+        f.w = f.w * c + v.w * e;
+    }
+    so[threadIdx.x] = f;
+    if (d == 0) {
+        sm[gi] = m;
+        sl[gi] = l;
+    }
+    __syncthreads();
+    if (gi != 0) return;
+    float M = sm[0];
+#pragma unroll
+    for (int i = 1; i < G; ++i) M = fmaxf(M, sm[i]);
+    float Ls = 0.f;
+    float4 F = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+        if (sm[i] == -INFINITY) continue;
+        const float e = ex2(sm[i] - M);
+        const float4 v = so[i * (D / 4) + threadIdx.x];
+        Ls = fmaf(sl[i], e, Ls);
+        F.x = fmaf(v.x, e, F.x);
+        F.y = fmaf(v.y, e, F.y);
+        F.z = fmaf(v.z, e, F.z);
+        F.w = fmaf(v.w, e, F.w);
+    }
+    const int i = (int)(rr / p.group);
+    store_out<typename C::T>(p, vec_out != 0, rq.q0 + i, h * p.group + (int)(rr - (long long)i * p.group), D, d, F, M, Ls);
+}
+
+template <class C>
+cudaError_t launch(const KvAttnLaunch& L, cudaStream_t s) {
+    const int e = C::E;
+    const int vec_q = ((uintptr_t)L.q & 15) == 0 && L.q_stride * e % 16 == 0;
+    const int vec_out = ((uintptr_t)L.out & 15) == 0 && L.out_stride * e % 16 == 0;
+    const int ctas = num_sms() * C::kCtas;
+    cudaError_t err = cudaFuncSetAttribute(kv_attention_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (err != cudaSuccess) return err;
+    err = launch_pdl(kv_attention_kernel<C>, dim3(ctas), dim3(kThreads), C::kSmem, s, L, vec_q, vec_out);
+    if (err != cudaSuccess) return err;
+    return launch_pdl(kv_combine_kernel<C>, dim3(ctas, C::NC), dim3(128), 0, s, L, ctas, vec_out);
+}
+
+// 8 columns when the rows of a request and head fit them, else 16 (fewer
+// passes over the keys)
+template <typename T>
+cudaError_t launch_type(const KvAttnLaunch& L, cudaStream_t s) {
+    const bool one = L.max_q_len * L.group <= 8;
+    if (L.sh.d == 64) {
+        if (L.sh.gs == 32) return one ? launch<Cfg<T, 64, 32, 1>>(L, s) : launch<Cfg<T, 64, 32, 2>>(L, s);
+        return one ? launch<Cfg<T, 64, 64, 1>>(L, s) : launch<Cfg<T, 64, 64, 2>>(L, s);
+    }
+    if (L.sh.gs == 32) return one ? launch<Cfg<T, 128, 32, 1>>(L, s) : launch<Cfg<T, 128, 32, 2>>(L, s);
+    if (L.sh.gs == 64) return one ? launch<Cfg<T, 128, 64, 1>>(L, s) : launch<Cfg<T, 128, 64, 2>>(L, s);
+    return one ? launch<Cfg<T, 128, 128, 1>>(L, s) : launch<Cfg<T, 128, 128, 2>>(L, s);
+}
+
+}  // namespace kvs
+}  // namespace gai4
