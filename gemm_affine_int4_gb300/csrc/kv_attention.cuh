@@ -49,6 +49,7 @@ namespace kvs {
 using namespace pipe;
 
 constexpr int kTile = 64;
+constexpr int kStart = 4;                       // what the start and join of a unit cost, in tiles (see Walk)
 constexpr int kWarps = 7;                       // consumer warps: with the producer 8, so that the registers divide well
 constexpr int kThreads = 32 * (kWarps + 1);     // and one producer warp
 
@@ -158,22 +159,24 @@ __device__ __forceinline__ int row_blocks(const Req& q, int group, int nc) {
 }
 
 // A warp's walk along the line of tiles: the requests' sizes are held by the
-// lanes, 32 at a time.
+// lanes, 32 at a time. Each unit begins with kStart places without work, which
+// stand for its query load and join, so that CTAs with many short units get
+// fewer tiles; a unit belongs to the CTA that has its first tile's place.
 template <int NC>
 struct Walk {
     const KvAttnLaunch& p;
     int base, lane;
     Req mine;
     long long c, c1;
-    int r, unit, tile;    // current request, unit within it, tile within the unit
+    int r, unit, place;   // current request, unit within it, place within the unit (tile + kStart)
     Req q;
     int nrb, units;
 
     __device__ Walk(const KvAttnLaunch& p_, int lane_, int r0, long long off, long long c0, long long c1_)
         : p(p_), base(-1), lane(lane_), c(c0), c1(c1_), r(r0) {
         load();
-        unit = (int)(off / q.ntile);
-        tile = (int)(off - (long long)unit * q.ntile);
+        unit = (int)(off / (q.ntile + kStart));
+        place = (int)(off - (long long)unit * (q.ntile + kStart));
     }
     __device__ void load() {
         if (base < 0 || r - base >= 32) {
@@ -191,7 +194,10 @@ struct Walk {
         units = nrb * p.sh.hkv;
     }
     __device__ bool more() const { return c < c1; }
-    __device__ int here() const { return (int)min((long long)(q.ntile - tile), c1 - c); }   // tiles of this segment
+    __device__ int here() const { return (int)min((long long)(q.ntile + kStart - place), c1 - c); }   // places of this segment
+    __device__ bool idle() const { return place + here() <= kStart; }    // no tile among them
+    __device__ bool begins() const { return place <= kStart; }
+    __device__ bool ends() const { return place + here() == q.ntile + kStart; }
     __device__ int head() const { return unit / nrb; }
     __device__ int block() const { return unit % nrb; }
     // tiles [a, b) of the segment that some row of the unit can see
@@ -201,15 +207,15 @@ struct Walk {
         const int i1 = min((int)(((long long)rb * NC + NC - 1) / p.group), q.qn - 1);
         const long long end = (long long)q.kv - q.qn + i1 + 1;      // keys below it
         const long long lo = p.window > 0 ? max((long long)q.kv - q.qn + i0 - p.window + 1, 0ll) : 0;
-        a = max(tile, (int)(lo / kTile) - q.tile0);
-        b = min(tile + here(), (int)((max(end, 0ll) + kTile - 1) / kTile) - q.tile0);
+        a = max(max(place - kStart, 0), (int)(lo / kTile) - q.tile0);
+        b = min(place - kStart + here(), (int)((max(end, 0ll) + kTile - 1) / kTile) - q.tile0);
     }
     __device__ void advance() {
         const int n = here();
         c += n;
-        tile += n;
-        if (tile == q.ntile) {
-            tile = 0;
+        place += n;
+        if (place == q.ntile + kStart) {
+            place = 0;
             if (++unit == units) {
                 unit = 0;
                 if (c < c1) {
@@ -247,6 +253,10 @@ __device__ __forceinline__ void producer(const KvAttnLaunch& p, Walk<C::NC>& w, 
     int seq = 0;
     bool ok = true;
     while (w.more() && ok) {
+        if (w.idle()) {
+            w.advance();
+            continue;
+        }
         int a, b;
         w.clip(a, b);
         const int h = w.head();
@@ -430,38 +440,33 @@ __device__ __forceinline__ void load_query(const KvAttnLaunch& p, const Req& rq,
 }
 
 // what columns 2t and 2t + 1 of each 8-column block may see: keys [lo, hi)
-template <int NT>
 struct Limits {
-    int lo[NT][2], hi[NT][2];
+    int rows;             // rows of the unit, at most NC
+    int first;            // index of row 0 among the request's tokens x heads, modulo the heads
+    int i0;               // token of row 0
     int lo_max, hi_min;   // keys in [lo_max, hi_min) are seen by every row of the unit
 };
 
+__device__ __forceinline__ int lowest_key(const KvAttnLaunch& p, long long pos) {
+    return p.window > 0 ? (int)max(pos - p.window + 1, 0ll) : 0;
+}
+
 template <class C>
-__device__ __forceinline__ Limits<C::NT> limits(const KvAttnLaunch& p, const Req& rq, int rb) {
-    Limits<C::NT> L;
-    const int t = threadIdx.x & 3;
-    const long long rows = (long long)rq.qn * p.group;
-    const long long pos0 = (long long)rq.kv - rq.qn;
-    auto low = [&](int i) { return p.window > 0 ? (int)max(pos0 + i - p.window + 1, 0ll) : 0; };
-#pragma unroll
-    for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const long long rr = (long long)rb * C::NC + n * 8 + 2 * t + c;
-            const int i = (int)(rr / p.group);
-            const bool valid = rr < rows;
-            L.hi[n][c] = valid ? (int)max(pos0 + i + 1, 0ll) : 0;
-            L.lo[n][c] = valid ? low(i) : 0;
-        }
-    const long long last = min((long long)rb * C::NC + C::NC, rows) - 1;
-    L.hi_min = (int)max(pos0 + (long long)rb * C::NC / p.group + 1, 0ll);
-    L.lo_max = low((int)(last / p.group));
+__device__ __forceinline__ Limits limits(const KvAttnLaunch& p, const Req& rq, int rb) {
+    Limits L;
+    const long long rr0 = (long long)rb * C::NC;
+    L.rows = (int)min((long long)C::NC, (long long)rq.qn * p.group - rr0);
+    L.i0 = (int)(rr0 / p.group);
+    L.first = (int)(rr0 - (long long)L.i0 * p.group);
+    const long long pos0 = (long long)rq.kv - rq.qn + L.i0;
+    L.hi_min = (int)max(pos0 + 1, 0ll);
+    L.lo_max = lowest_key(p, pos0 + (L.first + L.rows - 1) / p.group);
     return L;
 }
 
 template <class C>
 __device__ __forceinline__ void tile(const uint8_t* st, unsigned long long mask, int tok0, const Query<C>& Q,
-                                     const Limits<C::NT>& L, Acc<C>& A) {
+                                     const KvAttnLaunch& p, const Req& rq, const Limits& L, Acc<C>& A) {
     using T = typename C::T;
     constexpr int NT = C::NT, NG = C::NG, D = C::D, GS = C::GS;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -538,14 +543,20 @@ __device__ __forceinline__ void tile(const uint8_t* st, unsigned long long mask,
     // ---- masks: only on tiles that some row does not see in full
     if (mask != ~0ull || tok0 + kTile > L.hi_min || tok0 < L.lo_max) {
 #pragma unroll
-        for (int mb = 0; mb < 4; ++mb)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int c = 0; c < 2; ++c) {
+                const int col = n * 8 + 2 * t + c;
+                const long long pos = (long long)rq.kv - rq.qn + L.i0 + (L.first + col) / p.group;
+                const int hi = col < L.rows ? (int)max(pos + 1, 0ll) : 0, lo = lowest_key(p, pos);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int o = 16 * mb + tg + (e < 2 ? 0 : 8), j = tok0 + o;
-                    if (!((mask >> o) & 1) || j >= L.hi[n][e & 1] || j < L.lo[n][e & 1]) x[mb][n][e] = -INFINITY;
-                }
+                for (int mb = 0; mb < 4; ++mb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int o = 16 * mb + tg + 8 * e, j = tok0 + o;
+                        if (!((mask >> o) & 1) || j >= hi || j < lo) x[mb][n][2 * e + c] = -INFINITY;
+                    }
+            }
     }
     // ---- running maximum of every column
     float mx[NT][2];
@@ -563,17 +574,15 @@ __device__ __forceinline__ void tile(const uint8_t* st, unsigned long long mask,
             mx[n][c] = m;
             grew |= m > A.m[n][c];
         }
-    // value scales of this lane's tokens, and whether R has to grow
-    float vs[4][2][NG];
+    // whether R has to grow: the largest value scale of the tile
     float smax = 0.f;
+    constexpr int kPer = kTile * NG / 32;   // neighbouring scales of a lane
 #pragma unroll
-    for (int mb = 0; mb < 4; ++mb)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            load_groups<T, NG>(vsc + (16 * mb + tg + 8 * e) * NG * C::E, vs[mb][e]);
-#pragma unroll
-            for (int k = 0; k < NG; ++k) smax = fmaxf(smax, fabsf(vs[mb][e][k]));
-        }
+    for (int i = 0; i < kPer; i += 2) {
+        float two[2];
+        load_groups<T, 2>(vsc + (lane * kPer + i) * C::E, two);
+        smax = fmaxf(smax, fmaxf(fabsf(two[0]), fabsf(two[1])));
+    }
     const bool wider = smax > __uint_as_float((uint32_t)A.re << 23);
     if (__any_sync(0xffffffffu, grew || wider)) {
         const uint32_t sb = __reduce_max_sync(0xffffffffu, __float_as_uint(smax));   // non-negative: ordered as integers
@@ -616,13 +625,15 @@ __device__ __forceinline__ void tile(const uint8_t* st, unsigned long long mask,
     const float inv = __uint_as_float((uint32_t)(min(268 - A.re, 254)) << 23);   // 2^14 / R
 #pragma unroll
     for (int mb = 0; mb < 4; ++mb) {
-        float b0[NG], b1[NG];
+        float b0[NG], b1[NG], v0[NG], v1[NG];
+        load_groups<T, NG>(vsc + (16 * mb + tg) * NG * C::E, v0);
+        load_groups<T, NG>(vsc + (16 * mb + tg + 8) * NG * C::E, v1);
         load_groups<T, NG>(vbi + (16 * mb + tg) * NG * C::E, b0);
         load_groups<T, NG>(vbi + (16 * mb + tg + 8) * NG * C::E, b1);
         uint32_t P[C::kSplit ? 2 : 1][NG][NT][2];
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
-            const float s[2] = {vs[mb][0][k] * inv, vs[mb][1][k] * inv};
+            const float s[2] = {v0[k] * inv, v1[k] * inv};
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -811,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     const int r0 = min(tid * per_thread, p.batch), r1 = min(r0 + per_thread, p.batch);
     auto cost = [&](int r) {
         const Req q = request(p, r);
-        return (long long)row_blocks(q, p.group, C::NC) * p.sh.hkv * q.ntile;
+        return (long long)row_blocks(q, p.group, C::NC) * p.sh.hkv * (q.ntile + kStart);
     };
     long long mine = 0;
     for (int r = r0; r < r1; ++r) mine += cost(r);
@@ -868,12 +879,16 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     int seq = 0;
     bool cut = false;    // this CTA holds the beginning of a unit that goes on
     while (w.more()) {
+        if (w.idle()) {
+            w.advance();
+            continue;
+        }
         int a, b;
         w.clip(a, b);
         const int h = w.head(), rb = w.block();
         Query<C> Q;
         load_query<C>(p, w.q, h, rb, vec_q != 0, Q);
-        const Limits<C::NT> L = limits<C>(p, w.q, rb);
+        const Limits L = limits<C>(p, w.q, rb);
         Acc<C> A;
         clear<C>(A);
         for (int t = a; t < b; ++t, ++seq) {
@@ -892,12 +907,12 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
                                 reinterpret_cast<uint16_t*>(st + 2 * C::kCodes + k * C::kSb)[o * (C::NG * C::E / 2) + i] = 0;
                 __syncwarp();
             }
-            tile<C>(st, mask, (w.q.tile0 + t) * kTile, Q, L, A);
+            tile<C>(st, mask, (w.q.tile0 + t) * kTile, Q, p, w.q, L, A);
             if (mask != ~0ull) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[slot]);
         }
-        const bool begins = w.tile == 0, ends = w.tile + w.here() == w.q.ntile;
+        const bool begins = w.begins(), ends = w.ends();
         const long long rows = (long long)w.q.qn * p.group;
         float* rec = recs + (begins ? rec_floats(C::NC, C::D) : 0);
         join<C>(A, buf, [&](int col, int d, float4 f, float m, float l) {
@@ -917,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         if (begins && !ends) {
             cut = true;
             if (tid == 0) {
-                const long long end = w.c + w.q.ntile;   // of the unit, on the line
+                const long long end = w.c - w.place + w.q.ntile + kStart;   // of the unit, on the line
                 *meta = make_int4(w.r, w.unit, (int)((end - 1) / per), 0);
             }
         }
