@@ -27,7 +27,7 @@
 // that mma.sync reaches at the memory's speed; tcgen05 would need the codes
 // expanded through shared memory first.
 //
-// Work split. Tokens are cut into 64-token tiles; a unit is (request,
+// Work split. Tokens are cut into 32-token tiles; a unit is (request,
 // key/value head, block of 8 NT query rows), and all units' tiles form one
 // line that is cut evenly over the CTAs: ragged lengths and few long requests
 // alike fill the GPU. In a CTA a producer warp streams tiles through a ring of
@@ -48,8 +48,10 @@ namespace kvs {
 
 using namespace pipe;
 
-constexpr int kTile = 64;
-constexpr int kStart = 4;                       // what the start and join of a unit cost, in tiles (see Walk)
+constexpr int kTile = 32;                       // tokens: half of the ring's stages are then on their way while every
+                                                // consumer warp works on one (64: one stage on its way, 141 us for 73)
+constexpr int kBlocks = kTile / 16;             // 16-token blocks of a tile
+constexpr int kStart = 8;                       // what the start and join of a unit cost, in tiles (see Walk)
 constexpr int kWarps = 7;                       // consumer warps: with the producer 8, so that the registers divide well
 constexpr int kThreads = 32 * (kWarps + 1);     // and one producer warp
 
@@ -67,9 +69,9 @@ struct Cfg {
     static constexpr uint32_t kJoin = kWarps * NC * DP * 4 + 2 * kWarps * NC * 4;
     static constexpr int kCtas = NT == 1 && !kSplit ? 2 : 1;   // resident CTAs per SM
     static constexpr uint32_t kBudget = (kCtas == 2 ? 112 : 225) * 1024 - kJoin - 1024;
-    static constexpr int kStages = kBudget / (kStage + 24) < 24 ? kBudget / (kStage + 24) : 24;
+    static constexpr int kStages = kBudget / (kStage + 24) < 32 ? kBudget / (kStage + 24) : 32;
     static constexpr uint32_t kSmem = kStages * kStage + kJoin + kStages * 24 + 256;
-    static_assert(kStages >= 4, "ring too short");
+    static_assert(kStages >= 6, "ring too short");
 };
 
 // records of cut units in the workspace: per CTA two of (O [NC][D], m [NC],
@@ -229,18 +231,25 @@ struct Walk {
     }
 };
 
+// The producer: six copies (codes, scales, biases of keys and values) of five
+// tiles, or of two tiles of two 16-token pages, at a time, one per lane. (One
+// tile at a time its chain of waits and votes, about 1200 cycles, set the
+// pace of the whole kernel.)
 template <class C>
 __device__ __forceinline__ void producer(const KvAttnLaunch& p, Walk<C::NC>& w, uint8_t* ring, uint64_t* full,
-                                         uint64_t* empty, unsigned long long* masks, const Ctl& ctl) {
+                                         uint64_t* empty, uint32_t* masks, const Ctl& ctl) {
     constexpr int S = C::kStages;
     const int lane = threadIdx.x & 31;
     const int pl = p.sh.page_log2;
-    const int pieces = pl >= 6 ? 1 : kTile >> pl;          // pages of a tile
-    const int tokens = pl >= 6 ? kTile : 1 << pl;          // tokens of a piece
-    const int piece = lane / 6, which = lane - 6 * piece;  // this lane's copy
-    const bool active = piece < pieces;
-    const uint32_t bytes = which < 2 ? (uint32_t)tokens * (C::D / 2) : (uint32_t)tokens * (C::NG * C::E);
+    const int two = pl < 5;                                 // pages per tile - 1
+    const int tokens = two ? 16 : kTile;                    // tokens of a piece
+    const int batch = two ? 2 : 5;                          // tiles at a time
+    const int item = lane / 6, which = lane - 6 * item;     // this lane's piece and array
+    const int tl = item >> two, piece = item & two;
+    const bool active = tl < batch;
+    const bool leader = which == 0 && piece == 0;
     const uint32_t row_bytes = which < 2 ? C::D / 2 : C::NG * C::E;
+    const uint32_t bytes = (uint32_t)tokens * row_bytes;
     const uint8_t* src0 = static_cast<const uint8_t*>(
         which == 0   ? static_cast<const void*>(p.k.packed)
         : which == 1 ? static_cast<const void*>(p.v.packed)
@@ -248,9 +257,10 @@ __device__ __forceinline__ void producer(const KvAttnLaunch& p, Walk<C::NC>& w, 
         : which == 3 ? p.k.biases
         : which == 4 ? p.v.scales
                      : p.v.biases);
-    const uint32_t dst0 = (which < 2 ? which * C::kCodes : 2 * C::kCodes + (which - 2) * C::kSb) + piece * bytes;
-    const uint32_t ring_s = smem_u32(ring);
-    int seq = 0;
+    const uint32_t dst0 = smem_u32(ring) + (which < 2 ? which * C::kCodes : 2 * C::kCodes + (which - 2) * C::kSb) + piece * bytes;
+    const int in_page = (1 << pl) - 1;
+    int seq = 0;                  // tiles issued
+    int slot = tl, phase = 1;     // of this lane's tile; parity of its "empty" wait
     bool ok = true;
     while (w.more() && ok) {
         if (w.idle()) {
@@ -261,41 +271,42 @@ __device__ __forceinline__ void producer(const KvAttnLaunch& p, Walk<C::NC>& w, 
         w.clip(a, b);
         const int h = w.head();
         const int* row = p.table + (long long)w.r * p.max_blocks;
-        const int nblk = (w.q.kv + (1 << pl) - 1) >> pl;
-        // the table's entries, 32 held by the lanes and the next 32 on their way
-        int cb = a < b ? ((((w.q.tile0 + a) * kTile) >> pl) & ~31) : 0;
-        int ids = cb + lane < nblk ? row[cb + lane] : -1;
-        int next = cb + 32 + lane < nblk ? row[cb + 32 + lane] : -1;
-        for (int t = a; t < b; ++t, ++seq) {
-            const int tok0 = (w.q.tile0 + t) * kTile;
-            const int blk = (tok0 >> pl) + piece;
-            if ((tok0 >> pl) >= cb + 32) {
-                cb += 32;
-                ids = next;
-                next = cb + 32 + lane < nblk ? row[cb + 32 + lane] : -1;
-            }
-            const int page = __shfl_sync(0xffffffffu, ids, (blk - cb) & 31);
-            const bool there = active && page >= 0 && page < p.sh.num_blocks;
-            const uint32_t votes = __ballot_sync(0xffffffffu, there && which == 0);
-            const int slot = seq % S;
-            if (!warp_wait(&empty[slot], ((seq / S) & 1) ^ 1, ctl)) {
+        const int nblk = (w.q.kv + in_page) >> pl;
+        int tok = (w.q.tile0 + a + tl) * kTile + piece * 16;     // first token of this lane's piece
+        int page = active && (tok >> pl) < nblk ? row[tok >> pl] : -1;
+        for (int t = a; t < b; t += batch) {
+            const int n = min(batch, b - t);
+            const bool live = active && tl < n;
+            const bool there = live && page >= 0 && page < p.sh.num_blocks;
+            const int now = page, tok_next = tok + batch * kTile;
+            page = active && (tok_next >> pl) < nblk ? row[tok_next >> pl] : -1;    // for the next turn
+            bool mine = true;
+            if (live) mine = mbar_wait(&empty[slot], (uint32_t)phase, ctl);
+            const uint32_t votes = __ballot_sync(0xffffffffu, there);
+            if (!__all_sync(0xffffffffu, mine)) {
                 ok = false;
                 break;
             }
-            if (lane == 0) {
-                unsigned long long m = 0;
-                for (int i = 0; i < pieces; ++i)
-                    if ((votes >> (6 * i)) & 1u) m |= (tokens == 64 ? ~0ull : ((1ull << tokens) - 1)) << (i * tokens);
-                const int left = w.q.kv - tok0;
-                if (left < 64) m &= left <= 0 ? 0ull : (1ull << left) - 1;
+            if (live && leader) {
+                uint32_t m = there ? (two ? 0xffffu : ~0u) : 0u;
+                const uint32_t second = two ? (votes >> (lane + 6)) & 1u : 0u;
+                if (second) m |= 0xffff0000u;
+                const int left = w.q.kv - tok;
+                if (left < 32) m &= left <= 0 ? 0u : (1u << left) - 1u;
                 masks[slot] = m;
-                mbar_arrive_expect_tx(&full[slot],
-                                      (uint32_t)__popc(votes) * (uint32_t)tokens * (C::D + 4 * C::NG * C::E));
+                mbar_arrive_expect_tx(&full[slot], ((there ? 1u : 0u) + second) * (uint32_t)tokens * (C::D + 4 * C::NG * C::E));
             }
             __syncwarp();
             if (there) {
-                const long long line = (((long long)page * p.sh.hkv + h) << pl) + (tok0 & ((1 << pl) - 1));
-                bulk_load(ring_s + (uint32_t)slot * C::kStage + dst0, src0 + line * row_bytes, bytes, &full[slot]);
+                const long long line = (((long long)now * p.sh.hkv + h) << pl) + (tok & in_page);
+                bulk_load(dst0 + (uint32_t)slot * C::kStage, src0 + line * row_bytes, bytes, &full[slot]);
+            }
+            seq += n;
+            tok = tok_next;
+            slot += n;
+            if (slot >= S) {
+                slot -= S;
+                phase ^= 1;
             }
         }
         w.advance();
@@ -465,7 +476,7 @@ __device__ __forceinline__ Limits limits(const KvAttnLaunch& p, const Req& rq, i
 }
 
 template <class C>
-__device__ __forceinline__ void tile(const uint8_t* st, unsigned long long mask, int tok0, const Query<C>& Q,
+__device__ __forceinline__ void tile(const uint8_t* st, uint32_t mask, int tok0, const Query<C>& Q,
                                      const KvAttnLaunch& p, const Req& rq, const Limits& L, Acc<C>& A) {
     using T = typename C::T;
     constexpr int NT = C::NT, NG = C::NG, D = C::D, GS = C::GS;
@@ -477,9 +488,9 @@ __device__ __forceinline__ void tile(const uint8_t* st, unsigned long long mask,
     const int tg = row_token(g);
 
     // ---- scores, in units of log2: x[16-token block][8-column block][row g | g + 8, column 2t | 2t + 1]
-    float x[4][NT][4];
+    float x[kBlocks][NT][4];
 #pragma unroll
-    for (int mb = 0; mb < 4; ++mb) {
+    for (int mb = 0; mb < kBlocks; ++mb) {
         float s0[NG], s1[NG], b0[NG], b1[NG];
         const int ra = 16 * mb + tg, rb = ra + 8;
         load_groups<T, NG>(ksc + ra * NG * C::E, s0);
@@ -541,7 +552,7 @@ __device__ __forceinline__ void tile(const uint8_t* st, unsigned long long mask,
             for (int e = 0; e < 4; ++e) x[mb][n][e] = fmaf(u[n][e], Q.f[n][e & 1], v[n][e]);
     }
     // ---- masks: only on tiles that some row does not see in full
-    if (mask != ~0ull || tok0 + kTile > L.hi_min || tok0 < L.lo_max) {
+    if (mask != ~0u || tok0 + kTile > L.hi_min || tok0 < L.lo_max) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -550,7 +561,7 @@ __device__ __forceinline__ void tile(const uint8_t* st, unsigned long long mask,
                 const long long pos = (long long)rq.kv - rq.qn + L.i0 + (L.first + col) / p.group;
                 const int hi = col < L.rows ? (int)max(pos + 1, 0ll) : 0, lo = lowest_key(p, pos);
 #pragma unroll
-                for (int mb = 0; mb < 4; ++mb)
+                for (int mb = 0; mb < kBlocks; ++mb)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int o = 16 * mb + tg + 8 * e, j = tok0 + o;
@@ -567,7 +578,7 @@ __device__ __forceinline__ void tile(const uint8_t* st, unsigned long long mask,
         for (int c = 0; c < 2; ++c) {
             float m = fmaxf(x[0][n][c], x[0][n][c + 2]);
 #pragma unroll
-            for (int mb = 1; mb < 4; ++mb) m = fmaxf(m, fmaxf(x[mb][n][c], x[mb][n][c + 2]));
+            for (int mb = 1; mb < kBlocks; ++mb) m = fmaxf(m, fmaxf(x[mb][n][c], x[mb][n][c + 2]));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -576,12 +587,12 @@ __device__ __forceinline__ void tile(const uint8_t* st, unsigned long long mask,
         }
     // whether R has to grow: the largest value scale of the tile
     float smax = 0.f;
-    constexpr int kPer = kTile * NG / 32;   // neighbouring scales of a lane
+    static_assert(kTile == 32, "a lane per token");
+    {
+        float s[NG];
+        load_groups<T, NG>(vsc + lane * NG * C::E, s);
 #pragma unroll
-    for (int i = 0; i < kPer; i += 2) {
-        float two[2];
-        load_groups<T, 2>(vsc + (lane * kPer + i) * C::E, two);
-        smax = fmaxf(smax, fmaxf(fabsf(two[0]), fabsf(two[1])));
+        for (int k = 0; k < NG; ++k) smax = fmaxf(smax, fabsf(s[k]));
     }
     const bool wider = smax > __uint_as_float((uint32_t)A.re << 23);
     if (__any_sync(0xffffffffu, grew || wider)) {
@@ -614,7 +625,7 @@ __device__ __forceinline__ void tile(const uint8_t* st, unsigned long long mask,
             const float m = A.m[n][c] == -INFINITY ? 0.f : A.m[n][c];
             float l = 0.f;
 #pragma unroll
-            for (int mb = 0; mb < 4; ++mb) {
+            for (int mb = 0; mb < kBlocks; ++mb) {
                 x[mb][n][c] = ex2(x[mb][n][c] - m);
                 x[mb][n][c + 2] = ex2(x[mb][n][c + 2] - m);
                 l += x[mb][n][c] + x[mb][n][c + 2];
@@ -624,7 +635,7 @@ __device__ __forceinline__ void tile(const uint8_t* st, unsigned long long mask,
     // ---- values
     const float inv = __uint_as_float((uint32_t)(min(268 - A.re, 254)) << 23);   // 2^14 / R
 #pragma unroll
-    for (int mb = 0; mb < 4; ++mb) {
+    for (int mb = 0; mb < kBlocks; ++mb) {
         float b0[NG], b1[NG], v0[NG], v1[NG];
         load_groups<T, NG>(vsc + (16 * mb + tg) * NG * C::E, v0);
         load_groups<T, NG>(vsc + (16 * mb + tg + 8) * NG * C::E, v1);
@@ -802,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     uint8_t* buf = ring + S * C::kStage;
     uint64_t* full = reinterpret_cast<uint64_t*>(buf + C::kJoin);
     uint64_t* empty = full + S;
-    unsigned long long* masks = reinterpret_cast<unsigned long long*>(empty + S);
+    uint32_t* masks = reinterpret_cast<uint32_t*>(empty + S);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
     if (tid == 0) {
@@ -897,18 +908,17 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
             // after a time-out the outputs are undefined, but every role still ends
             (void)warp_wait(&full[slot], (seq / S) & 1, ctl);
             uint8_t* st = ring + (size_t)slot * C::kStage;
-            const unsigned long long mask = masks[slot];
-            if (mask != ~0ull) {
+            const uint32_t mask = masks[slot];
+            if (mask != ~0u) {
                 // scales and biases of slots without a token may hold anything
-                for (int o = lane; o < kTile; o += 32)
-                    if (!((mask >> o) & 1))
-                        for (int k = 0; k < 4; ++k)
-                            for (int i = 0; i < C::NG * C::E / 2; ++i)
-                                reinterpret_cast<uint16_t*>(st + 2 * C::kCodes + k * C::kSb)[o * (C::NG * C::E / 2) + i] = 0;
+                if (!((mask >> lane) & 1))
+                    for (int k = 0; k < 4; ++k)
+                        for (int i = 0; i < C::NG * C::E / 2; ++i)
+                            reinterpret_cast<uint16_t*>(st + 2 * C::kCodes + k * C::kSb)[lane * (C::NG * C::E / 2) + i] = 0;
                 __syncwarp();
             }
             tile<C>(st, mask, (w.q.tile0 + t) * kTile, Q, p, w.q, L, A);
-            if (mask != ~0ull) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (mask != ~0u) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[slot]);
         }
