@@ -69,9 +69,13 @@ struct Cfg {
     static constexpr uint32_t kJoin = kWarps * NC * DP * 4 + 2 * kWarps * NC * 4;
     static constexpr int kCtas = NT == 1 && !kSplit ? 2 : 1;   // resident CTAs per SM
     static constexpr uint32_t kBudget = (kCtas == 2 ? 112 : 225) * 1024 - kJoin - 1024;
-    static constexpr int kStages = kBudget / (kStage + 24) < 32 ? kBudget / (kStage + 24) : 32;
+    // A multiple of kWarps, so that a slot is always waited on by the same warp,
+    // fill after fill: try_wait.parity takes a fill two behind for done, and with
+    // other depths a warp could wait for a slot's next fill while the one before,
+    // another warp's, is still on its way.
+    static constexpr int kStages = (kBudget / (kStage + 24) < 4 * kWarps ? kBudget / (kStage + 24) : 4 * kWarps) / kWarps * kWarps;
     static constexpr uint32_t kSmem = kStages * kStage + kJoin + kStages * 24 + 256;
-    static_assert(kStages >= 6, "ring too short");
+    static_assert(kStages >= 2 * kWarps && kStages % kWarps == 0, "ring too short");
 };
 
 // records of cut units in the workspace: per CTA two of (O [NC][D], m [NC],
@@ -887,7 +891,8 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         return;
     }
     // ---- consumers
-    int seq = 0;
+    int seq = 0;                              // first tile of the current segment
+    int my = warp, slot = warp, phase = 0;    // this warp's next tile: every kWarps-th
     bool cut = false;    // this CTA holds the beginning of a unit that goes on
     while (w.more()) {
         if (w.idle()) {
@@ -902,11 +907,11 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         const Limits L = limits<C>(p, w.q, rb);
         Acc<C> A;
         clear<C>(A);
-        for (int t = a; t < b; ++t, ++seq) {
-            if (seq % kWarps != warp) continue;
-            const int slot = seq % S;
+        const int tiles = max(b - a, 0);
+        for (; my < seq + tiles; my += kWarps) {
+            const int t = a + (my - seq);
             // after a time-out the outputs are undefined, but every role still ends
-            (void)warp_wait(&full[slot], (seq / S) & 1, ctl);
+            (void)warp_wait(&full[slot], (uint32_t)phase, ctl);
             uint8_t* st = ring + (size_t)slot * C::kStage;
             const uint32_t mask = masks[slot];
             if (mask != ~0u) {
@@ -921,7 +926,13 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
             if (mask != ~0u) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[slot]);
+            slot += kWarps;
+            if (slot >= S) {
+                slot -= S;
+                phase ^= 1;
+            }
         }
+        seq += tiles;
         const bool begins = w.begins(), ends = w.ends();
         const long long rows = (long long)w.q.qn * p.group;
         float* rec = recs + (begins ? rec_floats(C::NC, C::D) : 0);
