@@ -37,6 +37,9 @@ gai4_status check_cache(const KvCache& c) {
     return GAI4_OK;
 }
 
+// query rows per key/value head up to which a request is the split kernel's
+constexpr int kManyRows = 32;
+
 // two records of 16 query rows (32-bit O, m, l) for each of two CTAs per SM,
 // and a line of 16 bytes per CTA
 size_t attention_workspace(int d) {
@@ -161,11 +164,18 @@ gai4_status gai4_kv_attention(const void* q, int64_t q_token_stride, const uint3
     L.status = status_ptr();
     L.spin_limit = 2000000000LL;   // ~1 s of SM clock per wait
     if (!L.status) return GAI4_ERR_CUDA;
-    switch (dtype) {
-    case GAI4_F32: return done(launch_kv_attention_f32(L, (cudaStream_t)stream));
-    case GAI4_F16: return done(launch_kv_attention_f16(L, (cudaStream_t)stream));
-    default: return done(launch_kv_attention_bf16(L, (cudaStream_t)stream));
+    cudaStream_t cs = (cudaStream_t)stream;
+    L.max_rows = INT64_MAX;
+    if (dtype == GAI4_F32) return done(launch_kv_attention_f32(L, cs));
+    const bool tc = max_q_len * L.group > kManyRows;
+    int min_rows = 1;
+    if (!tc || num_tokens != batch * max_q_len) {   // (else, as far as the host knows, every request has max_q_len rows)
+        if (tc) L.max_rows = kManyRows;
+        min_rows = kManyRows + 1;
+        const cudaError_t e = dtype == GAI4_F16 ? launch_kv_attention_f16(L, cs) : launch_kv_attention_bf16(L, cs);
+        if (e != cudaSuccess || !tc) return done(e);
     }
+    return done(launch_kv_attention_tc(L, min_rows, cs));
 }
 
 }  // extern "C"

@@ -160,8 +160,10 @@ __device__ __forceinline__ Req request(const KvAttnLaunch& p, int r) {
     q.ntile = max((q.kv + kTile - 1) / kTile - q.tile0, 1);
     return q;
 }
-__device__ __forceinline__ int row_blocks(const Req& q, int group, int nc) {
-    return (int)(((long long)q.qn * group + nc - 1) / nc);
+// blocks of nc query rows; none for requests that the tensor-core kernel takes
+__device__ __forceinline__ int row_blocks(const KvAttnLaunch& p, const Req& q, int nc) {
+    const long long rows = (long long)q.qn * p.group;
+    return rows > p.max_rows ? 0 : (int)((rows + nc - 1) / nc);
 }
 
 // A warp's walk along the line of tiles: the requests' sizes are held by the
@@ -196,7 +198,7 @@ struct Walk {
         q.kv = __shfl_sync(0xffffffffu, mine.kv, s);
         q.tile0 = __shfl_sync(0xffffffffu, mine.tile0, s);
         q.ntile = __shfl_sync(0xffffffffu, mine.ntile, s);
-        nrb = row_blocks(q, p.group, NC);
+        nrb = row_blocks(p, q, NC);
         units = nrb * p.sh.hkv;
     }
     __device__ bool more() const { return c < c1; }
@@ -837,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     const int r0 = min(tid * per_thread, p.batch), r1 = min(r0 + per_thread, p.batch);
     auto cost = [&](int r) {
         const Req q = request(p, r);
-        return (long long)row_blocks(q, p.group, C::NC) * p.sh.hkv * (q.ntile + kStart);
+        return (long long)row_blocks(p, q, C::NC) * p.sh.hkv * (q.ntile + kStart);
     };
     long long mine = 0;
     for (int r = r0; r < r1; ++r) mine += cost(r);
@@ -977,7 +979,7 @@ __global__ void __launch_bounds__(128) kv_combine_kernel(const __grid_constant__
     if (meta.x < 0) return;
     const int col = blockIdx.y;
     const Req rq = request(p, meta.x);
-    const int nrb = row_blocks(rq, p.group, NC);
+    const int nrb = row_blocks(p, rq, NC);
     const int h = meta.y / nrb, rb = meta.y % nrb;
     const long long rr = (long long)rb * NC + col;
     if (rr >= (long long)rq.qn * p.group) return;
