@@ -13,7 +13,6 @@ with T = torch.bfloat16, torch.float16 or torch.float32.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 from typing import NamedTuple
 
@@ -365,32 +364,60 @@ def _need(cond: bool, what: str):
         raise ValueError("gai4: " + what)
 
 
+# The step's calls are short on the GPU, so these marshal without helper
+# objects: addresses as integers, and the current stream's handle directly.
+def _addr(*tensors):
+    """Device addresses of contiguous CUDA tensors."""
+    for t in tensors:
+        if not t.is_cuda:
+            raise ValueError("gai4: tensors must live on a CUDA device")
+        if not t.is_contiguous():
+            raise ValueError("gai4: tensors must be contiguous")
+    return [t.data_ptr() for t in tensors]
+
+
+def _addr32(*tensors):
+    """The same for int32 tensors."""
+    for t in tensors:
+        if t.dtype is not torch.int32:
+            raise ValueError("gai4: lengths, tables, offsets and free lists must be int32")
+    return _addr(*tensors)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_handle(stream, t: torch.Tensor) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
 def _kv_shape(cache, group_size: int):
-    """(num_blocks, kv_heads, page_size, head_dim, dtype number) of a cache."""
+    """(num_blocks, kv_heads, page_size, head_dim) of a cache."""
     packed, scales, biases = cache
     _need(packed.dim() == 4 and packed.element_size() == 4, "a cache's packed tensor is 32-bit [blocks, heads, page, D/8]")
     nb, h, page, words = packed.shape
     _need(scales.shape == (nb, h, page, words * 8 // group_size) and biases.shape == scales.shape and
           biases.dtype == scales.dtype, "scales and biases are [blocks, heads, page, D/group_size] of one type")
-    return nb, h, page, words * 8, _dtype(scales)
+    return nb, h, page, words * 8
 
 
-def _i32(t: torch.Tensor, what: str):
-    _need(t.dtype == torch.int32, f"{what} must be int32")
-    return _ptr(t)
+def _same_caches(k_cache, v_cache):
+    for a, b in zip(k_cache, v_cache):
+        _need(a.shape == b.shape and a.dtype == b.dtype, "key and value caches differ in shape or type")
 
 
-def _slots(t: torch.Tensor, n: int):
-    _need(t.dtype == torch.int64 and t.dim() == 1 and t.shape[0] == n, "slots must be int64, one per row")
-    return _ptr(t)
-
-
-def _rows(t: torch.Tensor, heads: int, d: int, dtype, what: str):
-    """(address, token stride) of [tokens, heads, d] rows with contiguous heads."""
-    _need(t.dim() == 3 and t.shape[1] == heads and t.shape[2] == d and t.dtype == dtype,
-          f"{what} must be [tokens, {heads}, {d}] of the cache's type")
-    _need(t.stride(2) == 1 and (heads == 1 or t.stride(1) == d), f"{what}: heads must be contiguous within a token")
-    return _ptr_strided(t), (t.stride(0) if t.shape[0] > 1 else heads * d)
+def _token_stride(t: torch.Tensor, heads: int, d: int, dtype, what: str) -> int:
+    """Token stride of [tokens, heads, d] rows with contiguous heads."""
+    n, h, e = t.shape
+    s0, s1, s2 = t.stride()
+    _need(h == heads and e == d and t.dtype == dtype, f"{what} must be [tokens, {heads}, {d}] of the cache's type")
+    _need(s2 == 1 and (s1 == d or heads == 1), f"{what}: heads must be contiguous within a token")
+    _need(t.is_cuda, "tensors must live on a CUDA device")
+    return s0 if n > 1 else heads * d
 
 
 def gai4_kv_plan(kv_lens, q_lens, block_table, free_blocks, free_count, page_size: int, num_tokens: int,
@@ -400,24 +427,28 @@ def gai4_kv_plan(kv_lens, q_lens, block_table, free_blocks, free_count, page_siz
     free_blocks [capacity] and free_count [1] are int32 and contiguous;
     block_table and free_blocks are updated in place. A negative q_lens frees
     the request's pages. `out` gives tensors to write into."""
-    B = kv_lens.shape[0]
-    _need(q_lens.shape == (B,) and block_table.dim() == 2 and block_table.shape[0] == B and free_count.numel() == 1,
+    B, width = block_table.shape
+    _need(kv_lens.shape == (B,) and q_lens.shape == (B,) and free_count.numel() == 1,
           "kv_lens, q_lens [B], block_table [B, max_blocks], free_count [1]")
+    kv, q, table, free, count = _addr32(kv_lens, q_lens, block_table, free_blocks, free_count)
     if out is None:
-        dev = kv_lens.device
-        # one allocation for the 32-bit outputs
-        a = torch.empty(num_tokens + 2 * B + 6, dtype=torch.int32, device=dev)
-        positions, cu_q, lens, count, info = a.split([num_tokens, B + 1, B, 1, 4])
-        out = KvPlan(torch.empty(num_tokens, dtype=torch.int64, device=dev), positions, cu_q, lens, count, info)
+        # one allocation: slots first (8 bytes each), then the 32-bit outputs
+        a = torch.empty(3 * num_tokens + 2 * B + 6, dtype=torch.int32, device=kv_lens.device)
+        slots, positions, cu_q, lens, left, info = a.split((2 * num_tokens, num_tokens, B + 1, B, 1, 4))
+        out = KvPlan(slots.view(torch.int64), positions, cu_q, lens, left, info)
+        n2 = a.data_ptr()
+        n3 = n2 + 8 * num_tokens
+        n4 = n3 + 4 * num_tokens
+        o_slots, o_pos, o_cu, o_lens, o_left, o_info = n2, n3, n4, n4 + 4 * B + 4, n4 + 8 * B + 4, n4 + 8 * B + 8
     else:
-        _need(out.positions.shape == (num_tokens,) and out.cu_q.shape == (B + 1,) and out.kv_lens.shape == (B,) and
-              out.free_count.numel() == 1 and out.info.numel() == 4, "out: wrong shapes")
+        _need(out.slots.shape == (num_tokens,) and out.positions.shape == (num_tokens,) and
+              out.cu_q.shape == (B + 1,) and out.kv_lens.shape == (B,) and out.free_count.numel() == 1 and
+              out.info.numel() == 4 and out.slots.dtype == torch.int64, "out: wrong shapes")
+        o_slots, = _addr(out.slots)
+        o_pos, o_cu, o_lens, o_left, o_info = _addr32(out.positions, out.cu_q, out.kv_lens, out.free_count, out.info)
     _check("gai4_kv_plan", lib().gai4_kv_plan(
-        _i32(kv_lens, "kv_lens"), _i32(q_lens, "q_lens"), _i32(block_table, "block_table"), block_table.shape[1],
-        _i32(free_blocks, "free_blocks"), free_blocks.numel(), _i32(free_count, "free_count"),
-        _slots(out.slots, num_tokens), _i32(out.positions, "positions"), num_tokens, _i32(out.cu_q, "cu_q"),
-        _i32(out.kv_lens, "kv_lens"), _i32(out.free_count, "free_count"), _i32(out.info, "info"), B, page_size,
-        _stream(stream)))
+        kv, q, table, width, free, free_blocks.numel(), count, o_slots, o_pos, num_tokens, o_cu, o_lens, o_left,
+        o_info, B, page_size, _stream_handle(stream, kv_lens)))
     return out
 
 
@@ -425,28 +456,32 @@ def gai4_kv_append(k, v, slots, k_cache, v_cache, group_size: int = 64, stream=N
     """Quantize key and value rows k, v [tokens, kv_heads, head_dim] (any token
     stride) into the caches' slots; rows with a slot outside the pool (such as
     -1) are skipped."""
-    nb, h, page, d, dt = _kv_shape(k_cache, group_size)
-    _need(_kv_shape(v_cache, group_size) == (nb, h, page, d, dt), "key and value caches differ in shape or type")
-    n = k.shape[0]
-    _need(v.shape[0] == n, "k and v differ in length")
-    kp, ks = _rows(k, h, d, k_cache[1].dtype, "k")
-    vp, vs = _rows(v, h, d, k_cache[1].dtype, "v")
-    _check("gai4_kv_append", lib().gai4_kv_append(kp, ks, vp, vs, _slots(slots, n), *map(_ptr, k_cache),
-                                                  *map(_ptr, v_cache), dt, group_size, n, h, d, nb, page,
-                                                  _stream(stream)))
+    nb, h, page, d = _kv_shape(k_cache, group_size)
+    _same_caches(k_cache, v_cache)
+    n, T = k.shape[0], k_cache[1].dtype
+    _need(v.shape[0] == n and slots.shape == (n,) and slots.dtype == torch.int64,
+          "k, v and slots (int64) have one entry per token")
+    ks, vs = _token_stride(k, h, d, T, "k"), _token_stride(v, h, d, T, "v")
+    _check("gai4_kv_append", lib().gai4_kv_append(
+        k.data_ptr(), ks, v.data_ptr(), vs, *_addr(slots, *k_cache, *v_cache), _dtype(k), group_size, n, h, d, nb,
+        page, _stream_handle(stream, k)))
 
 
 def gai4_kv_read(cache, slots, group_size: int = 64, out=None, stream=None) -> torch.Tensor:
     """Values of cached rows, float32 [tokens, kv_heads, head_dim]; zeros where
     the slot is outside the pool."""
-    nb, h, page, d, dt = _kv_shape(cache, group_size)
-    n = slots.shape[0]
+    nb, h, page, d = _kv_shape(cache, group_size)
+    n, = slots.shape
+    _need(slots.dtype == torch.int64, "slots must be int64")
     if out is None:
         out = torch.empty((n, h, d), dtype=torch.float32, device=slots.device)
     _need(out.shape == (n, h, d) and out.dtype == torch.float32, "out must be float32 [tokens, kv_heads, head_dim]")
-    _check("gai4_kv_read", lib().gai4_kv_read(*map(_ptr, cache), _slots(slots, n), _ptr(out), dt, group_size, n, h, d,
-                                              nb, page, _stream(stream)))
+    _check("gai4_kv_read", lib().gai4_kv_read(*_addr(*cache, slots, out), _dtype(cache[1]), group_size, n, h, d, nb,
+                                              page, _stream_handle(stream, slots)))
     return out
+
+
+_kv_workspace = {}   # (device, q_heads, kv_heads, head_dim, dtype) -> bytes
 
 
 def gai4_kv_attention_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int, dtype) -> int:
@@ -462,28 +497,39 @@ def gai4_kv_attention(q, k_cache, v_cache, block_table, kv_lens, cu_q, group_siz
     request, guides the choice of kernel. lse, when given, float32 [tokens,
     q_heads], takes the logarithms of the softmax sums. A workspace is
     allocated here when none is given."""
-    nb, h, page, d, dt = _kv_shape(k_cache, group_size)
-    _need(_kv_shape(v_cache, group_size) == (nb, h, page, d, dt), "key and value caches differ in shape or type")
-    n, hq = q.shape[0], q.shape[1]
-    B = kv_lens.shape[0]
+    nb, h, page, d = _kv_shape(k_cache, group_size)
+    _same_caches(k_cache, v_cache)
+    n, hq, _ = q.shape
+    B, width = block_table.shape
     T = k_cache[1].dtype
-    qp, qs = _rows(q, hq, d, T, "q")
-    _need(block_table.dim() == 2 and block_table.shape[0] == B and cu_q.shape == (B + 1,),
-          "block_table [B, max_blocks], cu_q [B + 1]")
+    qs = _token_stride(q, hq, d, T, "q")
+    _need(kv_lens.shape == (B,) and cu_q.shape == (B + 1,), "block_table [B, max_blocks], kv_lens [B], cu_q [B + 1]")
     if out is None:
         out = torch.empty((n, hq, d), dtype=T, device=q.device)
-    _need(out.shape[0] == n, "out must have a row for each row of q")
-    op, os_ = _rows(out, hq, d, T, "out")
+        os_ = hq * d
+    else:
+        _need(out.shape[0] == n, "out must have a row for each row of q")
+        os_ = _token_stride(out, hq, d, T, "out")
+    lse_ptr = None
     if lse is not None:
         _need(lse.shape == (n, hq) and lse.dtype == torch.float32, "lse must be float32 [tokens, q_heads]")
+        lse_ptr, = _addr(lse)
     if workspace is None:
-        nbytes = gai4_kv_attention_workspace_bytes(hq, h, d, T)
-        workspace = torch.empty(nbytes // 4, dtype=torch.float32, device=q.device) if nbytes else None
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        key = (q.get_device(), hq, h, d, T)
+        nbytes = _kv_workspace.get(key)
+        if nbytes is None:
+            nbytes = _kv_workspace[key] = gai4_kv_attention_workspace_bytes(hq, h, d, T)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        ws = workspace.data_ptr()
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+        ws, = _addr(workspace)
+    kp, ksc, kb, vp, vsc, vb = _addr(*k_cache, *v_cache)
+    table, lens, cu = _addr32(block_table, kv_lens, cu_q)
     _check("gai4_kv_attention", lib().gai4_kv_attention(
-        qp, qs, *map(_ptr, k_cache), *map(_ptr, v_cache), _i32(block_table, "block_table"), block_table.shape[1],
-        _i32(kv_lens, "kv_lens"), _i32(cu_q, "cu_q"), op, os_, _ptr(lse), dt, group_size, B, n, max_q_len, hq, h, d,
-        nb, page, 1.0 / math.sqrt(d) if scale is None else scale, window, _ptr(workspace), ws_bytes, _stream(stream)))
+        q.data_ptr(), qs, kp, ksc, kb, vp, vsc, vb, table, width, lens, cu, out.data_ptr(), os_, lse_ptr, _dtype(q),
+        group_size, B, n, max_q_len, hq, h, d, nb, page, d ** -0.5 if scale is None else scale, window, ws, nbytes,
+        _stream_handle(stream, q)))
     return out
 
 

@@ -43,6 +43,20 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// Allows a kernel `bytes` of dynamic shared memory, once per kernel and device
+// (the attribute call costs a microsecond of every launch otherwise). `done`
+// is a static array of the caller, one entry per device.
+template <typename Kernel>
+inline cudaError_t allow_smem_once(Kernel kernel, size_t bytes, bool (&done)[64]) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+    return e;
+}
+
 // ---------------------------------------------------------------------------
 // dtype traits: storage type, conversion to/from binary32
 // ---------------------------------------------------------------------------

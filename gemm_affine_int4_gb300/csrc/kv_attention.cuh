@@ -1035,7 +1035,8 @@ cudaError_t launch(const KvAttnLaunch& L, cudaStream_t s) {
     const int vec_q = ((uintptr_t)L.q & 15) == 0 && L.q_stride * e % 16 == 0;
     const int vec_out = ((uintptr_t)L.out & 15) == 0 && L.out_stride * e % 16 == 0;
     const int ctas = num_sms() * C::kCtas;
-    cudaError_t err = cudaFuncSetAttribute(kv_attention_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static bool allowed[64];
+    cudaError_t err = allow_smem_once(kv_attention_kernel<C>, C::kSmem, allowed);
     if (err != cudaSuccess) return err;
     err = launch_pdl(kv_attention_kernel<C>, dim3(ctas), dim3(kThreads), C::kSmem, s, L, vec_q, vec_out);
     if (err != cudaSuccess) return err;

@@ -638,8 +638,8 @@ cudaError_t launch(const KvAttnLaunch& L, int min_rows, cudaStream_t s) {
     const int vec_q = ((uintptr_t)L.q & 15) == 0 && L.q_stride % 8 == 0;
     const int vec_out = ((uintptr_t)L.out & 15) == 0 && L.out_stride % 8 == 0;
     const size_t smem = Smem<D>::total + 1024;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kv_attention_tc_kernel<BF, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static bool allowed[64];
+    const cudaError_t e = allow_smem_once(kv_attention_tc_kernel<BF, D>, smem, allowed);
     if (e != cudaSuccess) return e;
     // at most: every request leaves a partly filled block
     const int64_t rows = L.num_tokens * L.group;

@@ -307,8 +307,8 @@ cudaError_t by_sizes(int d, int gs, F&& f) {
 cudaError_t launch_kv_plan(const KvPlanLaunch& L, cudaStream_t s) {
     const size_t smem = 3 * sizeof(int) * (size_t)(L.batch + 1);
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   3 * sizeof(int) * (kKvPlanMaxBatch + 1));
+        static bool allowed[64];
+        const cudaError_t e = allow_smem_once(kv_plan_kernel, 3 * sizeof(int) * (kKvPlanMaxBatch + 1), allowed);
         if (e != cudaSuccess) return e;
     }
     int64_t blocks = (L.num_tokens + 2 * kPlanThreads - 1) / (2 * kPlanThreads);
