@@ -174,7 +174,6 @@ struct KvAttnLaunch {
     int group;          // query heads per key/value head
     float scale;
     int64_t window;
-    int64_t max_rows;   // requests with more query rows per key/value head are another kernel's
     void* workspace;
     int* status;
     long long spin_limit;
@@ -182,8 +181,9 @@ struct KvAttnLaunch {
 cudaError_t launch_kv_attention_bf16(const KvAttnLaunch& L, cudaStream_t s);
 cudaError_t launch_kv_attention_f16(const KvAttnLaunch& L, cudaStream_t s);
 cudaError_t launch_kv_attention_f32(const KvAttnLaunch& L, cudaStream_t s);
-// bf16 / f16, requests with at least min_rows query rows per key/value head (kv_attention_tc.cu)
-cudaError_t launch_kv_attention_tc(const KvAttnLaunch& L, int min_rows, cudaStream_t s);
+// bf16 / f16 with many query rows per key/value head (kv_attention_tc.cu)
+cudaError_t launch_kv_attention_tc(const KvAttnLaunch& L, cudaStream_t s);
+size_t kv_attention_tc_workspace(int d);
 
 int* status_ptr();  // device status word of the current device
 int num_sms();  // SM count of the current device (cached)

@@ -2,6 +2,8 @@
 // include/gai4.h): argument validation and launch. No allocation.
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -37,14 +39,18 @@ gai4_status check_cache(const KvCache& c) {
     return GAI4_OK;
 }
 
-// query rows per key/value head up to which a request is the split kernel's
+// Query rows per key/value head up to which the split kernel (16 rows a pass
+// over the keys, memory-bound) is taken; above, the tensor-core kernel (256
+// rows a pass).
 constexpr int kManyRows = 32;
 
-// two records of 16 query rows (32-bit O, m, l) for each of two CTAs per SM,
-// and a line of 16 bytes per CTA
-size_t attention_workspace(int d) {
+// the split kernel: two records of 16 query rows (32-bit O, m, l) for each of
+// two CTAs per SM, and a line of 16 bytes per CTA; the tensor-core kernel's
+// records are longer
+size_t attention_workspace(int d, int dtype) {
     const size_t ctas = 2 * (size_t)num_sms();
-    return (ctas * 16 + 255) / 256 * 256 + ctas * 2 * 16 * (size_t)(d + 2) * 4;
+    const size_t split = (ctas * 16 + 255) / 256 * 256 + ctas * 2 * 16 * (size_t)(d + 2) * 4;
+    return dtype == GAI4_F32 ? split : std::max(split, kv_attention_tc_workspace(d));
 }
 
 gai4_status done(cudaError_t e) { return e == cudaSuccess ? GAI4_OK : GAI4_ERR_CUDA; }
@@ -115,7 +121,7 @@ size_t gai4_kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int 
     KvShape sh;
     if (check_shape(dtype, 32, kv_heads, head_dim, 1, 16, &sh) != GAI4_OK) return 0;
     if (q_heads < 1 || q_heads % kv_heads != 0 || q_heads / kv_heads > 65535) return 0;
-    return attention_workspace(head_dim);
+    return attention_workspace(head_dim, dtype);
 }
 
 gai4_status gai4_kv_attention(const void* q, int64_t q_token_stride, const uint32_t* k_packed, const void* k_scales,
@@ -144,7 +150,7 @@ gai4_status gai4_kv_attention(const void* q, int64_t q_token_stride, const uint3
         !aligned_to(cu_q, 4) || !aligned_to(lse, 4))
         return GAI4_ERR_MISALIGNED;
     L.group = (int)(q_heads / kv_heads);
-    if (!workspace || workspace_bytes < attention_workspace(head_dim)) return GAI4_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < attention_workspace(head_dim, dtype)) return GAI4_ERR_WORKSPACE;
     if (!aligned_to(workspace, 16)) return GAI4_ERR_MISALIGNED;
     L.q = q;
     L.q_stride = q_token_stride;
@@ -165,17 +171,9 @@ gai4_status gai4_kv_attention(const void* q, int64_t q_token_stride, const uint3
     L.spin_limit = 2000000000LL;   // ~1 s of SM clock per wait
     if (!L.status) return GAI4_ERR_CUDA;
     cudaStream_t cs = (cudaStream_t)stream;
-    L.max_rows = INT64_MAX;
     if (dtype == GAI4_F32) return done(launch_kv_attention_f32(L, cs));
-    const bool tc = max_q_len * L.group > kManyRows;
-    int min_rows = 1;
-    if (!tc || num_tokens != batch * max_q_len) {   // (else, as far as the host knows, every request has max_q_len rows)
-        if (tc) L.max_rows = kManyRows;
-        min_rows = kManyRows + 1;
-        const cudaError_t e = dtype == GAI4_F16 ? launch_kv_attention_f16(L, cs) : launch_kv_attention_bf16(L, cs);
-        if (e != cudaSuccess || !tc) return done(e);
-    }
-    return done(launch_kv_attention_tc(L, min_rows, cs));
+    if (max_q_len * L.group > kManyRows) return done(launch_kv_attention_tc(L, cs));
+    return done(dtype == GAI4_F16 ? launch_kv_attention_f16(L, cs) : launch_kv_attention_bf16(L, cs));
 }
 
 }  // extern "C"

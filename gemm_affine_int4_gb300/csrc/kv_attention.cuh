@@ -160,10 +160,8 @@ __device__ __forceinline__ Req request(const KvAttnLaunch& p, int r) {
     q.ntile = max((q.kv + kTile - 1) / kTile - q.tile0, 1);
     return q;
 }
-// blocks of nc query rows; none for requests that the tensor-core kernel takes
 __device__ __forceinline__ int row_blocks(const KvAttnLaunch& p, const Req& q, int nc) {
-    const long long rows = (long long)q.qn * p.group;
-    return rows > p.max_rows ? 0 : (int)((rows + nc - 1) / nc);
+    return (int)(((long long)q.qn * p.group + nc - 1) / nc);
 }
 
 // A warp's walk along the line of tiles: the requests' sizes are held by the
