@@ -51,7 +51,13 @@ using namespace pipe;
 
 constexpr int kKeys = 128;            // tokens of a key tile
 constexpr int kRows = 256;            // query rows of a CTA
-constexpr int kThreads = 32 * 14;     // 8 softmax warps, 4 expanding, 1 product issuer, 1 producer
+// 8 softmax warps, 4 expanding, 1 product issuer, 1 producer, 2 idle (warpgroups
+// share a register count)
+constexpr int kThreads = 32 * 16;
+// registers of a thread: launched with 128 (512 x 128 = 65536); softmax, which
+// holds a row's 128 scores, then takes what the others leave:
+// 256 x 184 + 128 x 96 + 128 x 40 = 64512
+constexpr int kSoftmaxRegs = 184, kExpandRegs = 96, kIssueRegs = 40;
 constexpr int kRing = 3;              // packed stages (keys and values in turn)
 constexpr int kStart = 8;             // what the start and end of a unit cost, in key tiles
 constexpr int kPart = 16;             // places of a key tile
@@ -109,16 +115,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&v)[32]) {
         : "r"(a)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&v)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(a),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&v)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -127,6 +123,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&v)[16]) {
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(a)
+        : "memory");
+}
+// bits 0..n - 1
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -361,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::bars);
     uint64_t *ring_full = bars, *ring_empty = bars + kRing, *k_full = bars + 2 * kRing, *k_empty = k_full + 2,
              *v_full = k_full + 4, *v_empty = k_full + 6, *s_full = k_full + 8, *p_full = k_full + 10,
-             *q_full = k_full + 12, *o_full = k_full + 13, *fin = k_full + 14;
+             *q_full = k_full + 14, *o_full = k_full + 15, *fin = k_full + 16;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
     if (tid == 0) {
@@ -375,7 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&v_full[i], 4);
             mbar_init(&v_empty[i], 1);
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
+            mbar_init(&p_full[2 * i], 4);       // probabilities of the first 64 keys
+            mbar_init(&p_full[2 * i + 1], 4);   // and of the others
         }
         mbar_init(q_full, 8);
         mbar_init(o_full, 1);
@@ -455,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const Ctl ctl{p.status, p.spin_limit, &abort_flag};
 
+    if (warp >= 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == 13) {
         // ---------------- producer: packed keys and values of each tile in turn ----------------
         const int pl = p.sh.page_log2;
@@ -532,11 +541,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             commit(&s_full[i]);
         };
-        auto pv = [&](int i, int j, bool add) {
+        auto pv = [&](int i, int j, int half, bool add) {
 #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
+            for (int k = 0; k < kKeys / 32; ++k) {
+                const int kk = k + (kKeys / 32) * half;
                 mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * kk, desc_n(vb + (j & 1) * M::kTile + kk * 2048), id_o,
-                       add || kk > 0);
+                       add || k > 0);
+            }
         };
         bool ok = true;
         int units = 0, jj = 0;          // segments and tiles so far
@@ -552,11 +563,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; ok && j < n; ++j, ++jj) {
                 ok = warp_wait(&v_full[jj & 1], (jj >> 1) & 1, ctl);
                 for (int i = 0; ok && i < nm; ++i) {
-                    ok = warp_wait(&p_full[i], (np >> i) & 1u, ctl);
+                    for (int half = 0; ok && half < 2; ++half) {
+                        ok = warp_wait(&p_full[2 * i + half], (np >> i) & 1u, ctl);
+                        if (!ok) break;
+                        fence_after();
+                        pv(i, jj, half, j > 0 || half > 0);
+                    }
                     if (!ok) break;
                     np ^= 1u << i;
-                    fence_after();
-                    pv(i, jj, j > 0);
                     if (i == nm - 1) commit(&v_empty[jj & 1]);
                     if (j + 1 < n) {
                         if (i == 0) ok = warp_wait(&k_full[(jj + 1) & 1], ((jj + 1) >> 1) & 1, ctl);
@@ -574,7 +588,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit(fin);
         if (lane == 0) mbar_wait_drain(fin, 0, ctl.limit, ctl.status);
         __syncwarp();
+    } else if (warp >= 14) {
     } else if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kExpandRegs));
         // ---------------- expanding keys and values: one token per thread ----------------
         const int r = (warp - 8) * 32 + lane;
         const int ng = D >> gs_log2;
@@ -621,6 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ---------------- softmax: M tile i, one row per thread ----------------
         const int i = warp >> 2, r = (warp & 3) * 32 + lane;
         int units = 0, ns = 0;         // segments and score tiles so far
@@ -689,29 +706,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const uint32_t holes = __ballot_sync(0xffffffffu, gone);
                 const bool masked = holes != 0 || key0 + kKeys > hi_min || key0 < lo_max;
-                const int hi = hi_key - key0, lo_ = lo_key - key0;
-                auto hide = [&](int c, float s) {
-                    return c >= hi || c < lo_ || ((holes >> (c >> 4)) & 1u) ? -INFINITY : s;
-                };
                 (void)warp_wait(&s_full[i], ns & 1, ctl);
                 ++ns;
                 fence_after();
-                // (the chunk loops stay rolled: unrolled, with the other roles'
-                // code, they miss the instruction cache)
-                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32];
-                    tmem_ld32(s_tm + 32 * c, v);
-                    tmem_ld_wait();
-                    if (masked) {
+                uint32_t v[4][32];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(hide(32 * c + e, __uint_as_float(v[e])));
+                for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, v[c]);
+                tmem_ld_wait();
+                if (masked) {
+                    const int hi = hi_key - key0, lo_ = lo_key - key0;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        // bits of the keys that the row sees
+                        uint32_t see = below(hi - 32 * c) & ~below(lo_ - 32 * c);
+                        if ((holes >> (2 * c)) & 1u) see &= 0xffff0000u;
+                        if ((holes >> (2 * c + 1)) & 1u) see &= 0x0000ffffu;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(see & (1u << e))) v[c][e] = 0xff800000u;   // -inf
                     }
+                }
+                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int e = 0; e < 32; e += 2)
-                        mx4[(e >> 1) & 3] = max3(mx4[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-                }
+                        mx4[(e >> 1) & 3] = max3(mx4[(e >> 1) & 3], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
                 float mx = max3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3]));
                 mx *= f;
                 if (__any_sync(0xffffffffu, mx > m + 8.f || (m == -INFINITY && mx > m))) {
@@ -719,13 +739,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float a = m == -INFINITY ? 0.f : ex2(m - mn);
                     if (j > t_a) {
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t v[32];
-                            tmem_ld32(o_tm + 32 * c, v);
+                        for (int c = 0; c < D / 16; ++c) {   // (16 columns: the scores stay in registers)
+                            uint32_t y[16];
+                            tmem_ld16(o_tm + 16 * c, y);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * a);
-                            tmem_st32(o_tm + 32 * c, v);
+                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * a);
+                            tmem_st16(o_tm + 16 * c, y);
                         }
                     }
                     l *= a;
@@ -734,30 +754,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float shift = m == -INFINITY ? 0.f : -m;
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 const float2 f2 = make_float2(f, f), shift2 = make_float2(shift, shift);
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32], o[16];
-                    tmem_ld32(s_tm + 32 * c, v);
-                    tmem_ld_wait();
-                    if (masked) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(hide(32 * c + e, __uint_as_float(v[e])));
-                    }
+                for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float2 x = fma2f(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), f2, shift2);
-                        x.x = ex2(x.x);
-                        x.y = ex2(x.y);
-                        sum[(e >> 1) & 1] = add2f(sum[(e >> 1) & 1], x);
-                        o[e / 2] = pack2<BF>(x.x, x.y);
+                    for (int c = 2 * half; c < 2 * half + 2; ++c) {
+                        uint32_t o[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float2 x = fma2f(make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), f2, shift2);
+                            x.x = ex2(x.x);
+                            x.y = ex2(x.y);
+                            sum[(e >> 1) & 1] = add2f(sum[(e >> 1) & 1], x);
+                            o[e / 2] = pack2<BF>(x.x, x.y);
+                        }
+                        tmem_st16(s_tm + 16 * c, o);
                     }
-                    tmem_st16(s_tm + 16 * c, o);
+                    tmem_st_wait();
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[2 * i + half]);
                 }
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                tmem_st_wait();
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[i]);
             }
             // ---- output, or a record of it
             (void)warp_wait(o_full, units & 1, ctl);
