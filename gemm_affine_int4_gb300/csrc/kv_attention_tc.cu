@@ -49,17 +49,19 @@ namespace kvt {
 
 using namespace pipe;
 
-constexpr int kKeys = 128;            // tokens of a key tile
+constexpr int kKeys = 128;            // tokens of a key tile and of a packed stage
 constexpr int kRows = 256;            // query rows of a CTA
-// 8 softmax warps, 4 expanding, 1 product issuer, 1 producer, 2 idle (warpgroups
-// share a register count)
+// warp 0 issues the products, 1 loads, 2-3 are idle (the four warps of a
+// warpgroup share a register count), 4-11 softmax, 12-15 expand.
 constexpr int kThreads = 32 * 16;
+constexpr int kLoader = 1, kSoftmax = 4, kExpand = 12;
 // registers of a thread: launched with 128 (512 x 128 = 65536); softmax, which
 // holds a row's 128 scores, then takes what the others leave:
-// 256 x 184 + 128 x 96 + 128 x 40 = 64512
-constexpr int kSoftmaxRegs = 184, kExpandRegs = 96, kIssueRegs = 40;
-constexpr int kRing = 3;              // packed stages (keys and values in turn)
-constexpr int kStart = 8;             // what the start and end of a unit cost, in key tiles
+// 256 x 184 + 128 x 88 + 128 x 48 = 64512
+constexpr int kSoftmaxRegs = 184, kExpandRegs = 88, kIssueRegs = 48;
+constexpr int kRing = 3;              // packed stages, keys and values in turn
+constexpr int kBufs = 2;              // expanded key tiles, and value tiles
+constexpr int kStart = 6;             // what the start and end of a unit cost, in key tiles
 constexpr int kPart = 16;             // places of a key tile
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -80,23 +82,43 @@ constexpr uint32_t idesc(bool bf, int n, bool b_n_major) {
            ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// issued by a converged warp: one elected lane
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p, e;\n .reg .b32 r;\n .reg .b64 x, y;\n elect.sync r|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-        " mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}" ::"r"(d),
-        "r"(a_lo), "r"(b_lo), "r"(id), "r"(acc), "r"(kDescHi)
-        : "memory");
+// Products of one tile, issued by a converged warp: one lane is elected for
+// all of them, as the issuing warp's instructions are on the critical path.
+// Operands step through shared memory by offsets (in 16 bytes) of their
+// descriptors, P through tensor memory 8 columns (16 elements) at a time.
+#define KVT_OPEN                                                                                                  \
+    "{\n .reg .pred e, z, o;\n .reg .b32 r, t, u;\n .reg .b64 x, y;\n elect.sync r|e, 0xffffffff;\n"              \
+    " setp.ne.b32 z, %5, 0;\n setp.eq.b32 o, 0, 0;\n"
+#define KVT_SS(k, acc)                                                                                            \
+    " add.u32 u, %1, " #k ";\n mov.b64 x, {u, %4};\n add.u32 t, %2, " #k ";\n mov.b64 y, {t, %4};\n"             \
+    " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, " #acc ";\n"
+#define KVT_TS(a, b, acc)                                                                                         \
+    " add.u32 u, %1, " #a ";\n add.u32 t, %2, " #b ";\n mov.b64 y, {t, %4};\n"                                   \
+    " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %3, " #acc ";\n"
+#define KVT_COMMIT " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n"
+// S = Q K^T: both K-major, 64 or 128 channels (4 or 8 steps); then the commit
+template <int D>
+__device__ __forceinline__ void products_qk(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t id, uint64_t* bar) {
+    if constexpr (D == 64)
+        asm volatile(KVT_OPEN KVT_SS(0, z) KVT_SS(2, o) KVT_SS(4, o) KVT_SS(6, o) KVT_COMMIT "}" ::"r"(d), "r"(a_lo),
+                     "r"(b_lo), "r"(id), "r"(kDescHi), "r"(0), "r"(smem_u32(bar))
+                     : "memory");
+    else
+        asm volatile(KVT_OPEN KVT_SS(0, z) KVT_SS(2, o) KVT_SS(4, o) KVT_SS(6, o) KVT_SS(1024, o) KVT_SS(1026, o)
+                         KVT_SS(1028, o) KVT_SS(1030, o) KVT_COMMIT "}" ::"r"(d),
+                     "r"(a_lo), "r"(b_lo), "r"(id), "r"(kDescHi), "r"(0), "r"(smem_u32(bar))
+                     : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t id, uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p, e;\n .reg .b32 r;\n .reg .b64 y;\n elect.sync r|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-        " mov.b64 y, {%2, %5};\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}" ::"r"(d),
-        "r"(a), "r"(b_lo), "r"(id), "r"(acc), "r"(kDescHi)
-        : "memory");
+// O += P V over 64 keys (4 steps); V is N-major
+__device__ __forceinline__ void products_pv(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t id, uint32_t acc) {
+    asm volatile(KVT_OPEN KVT_TS(0, 0, z) KVT_TS(8, 128, o) KVT_TS(16, 256, o) KVT_TS(24, 384, o) "}" ::"r"(d), "r"(a),
+                 "r"(b_lo), "r"(id), "r"(kDescHi), "r"(acc)
+                 : "memory");
 }
+#undef KVT_OPEN
+#undef KVT_SS
+#undef KVT_TS
+#undef KVT_COMMIT
 __device__ __forceinline__ void commit(uint64_t* bar) {
     asm volatile(
         "{\n .reg .pred e;\n .reg .b32 r;\n elect.sync r|e, 0xffffffff;\n"
@@ -123,14 +145,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&v)[16]) {
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-        "[%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(a)
-        : "memory");
+__device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 // bits 0..n - 1
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
@@ -231,13 +255,16 @@ __device__ __forceinline__ uint4 expand(uint32_t w, const Group<BF>& g) {
     return o;
 }
 
+// columns of tensor memory (128 for each M tile)
+constexpr uint32_t kS = 0, kO = 256;
+
 template <int D>
 struct Smem {
     static constexpr uint32_t kAtom = 128 * 128;                        // 128 rows x 64 channels
-    static constexpr uint32_t kTile = (D / 64) * kAtom;                 // one Q, K or V tile
+    static constexpr uint32_t kTile = (D / 64) * kAtom;                 // one tile of queries, keys or values
     static constexpr uint32_t kMaxNG = D / 32;
     static constexpr uint32_t kStage = kKeys * (D / 2 + 4 * kMaxNG);    // codes, scales, biases
-    static constexpr uint32_t q = 0, k = 2 * kTile, v = k + 2 * kTile, ring = v + 2 * kTile,
+    static constexpr uint32_t q = 0, k = 2 * kTile, v = k + kBufs * kTile, ring = v + kBufs * kTile,
                               masks = ring + kRing * kStage, bars = masks + kRing * 16, total = bars + 256;
 };
 
@@ -312,12 +339,13 @@ struct Walk {
     // tiles of this segment
     __device__ int first() const { return (int)(place * n / places); }
     __device__ int last() const { return (int)((place + here()) * n / places); }
-    __device__ void advance(const KvAttnLaunch& p) {
+    __device__ void advance(const KvAttnLaunch& p) { advance_to(p, *this); }
+    __device__ void advance_to(const KvAttnLaunch& p, Walk& to) const {
         __syncwarp();   // every lane has read what it needs
         Walk w = *this;
         w.step(p);
         __syncwarp();
-        *this = w;
+        to = w;
         __syncwarp();
     }
     __device__ void step(const KvAttnLaunch& p) {
@@ -340,18 +368,35 @@ struct Walk {
     __device__ int tiles_m() const { return rows - row0 > 128 ? 2 : 1; }
 };
 
-// eight channels of an output row, in the order 0 4 1 5 2 6 3 7, rounded once
+// 16-token pieces of keys [a, b) (a multiple of 128) that have no page: bit n
+// of the result for piece n, n modulo 32; called by a whole warp
+__device__ __forceinline__ uint32_t holes(const KvAttnLaunch& p, const Walk& w, int a, int b, int lane) {
+    const int pl = p.sh.page_log2;
+    const int* table = p.table + (long long)w.r * p.max_blocks;
+    const int end = min(b, w.q.kv);
+    bool gone = false;
+    for (int key = a + 16 * lane; key < end; key += 512) {
+        const int page = table[key >> pl];
+        gone |= page < 0 || page >= p.sh.num_blocks;
+    }
+    return __ballot_sync(0xffffffffu, gone);
+}
+
+// eight channels of an output row, given in the order 0 4 1 5 2 6 3 7, rounded once
 template <typename T>
-__device__ __forceinline__ void store8(uint16_t* d, const float (&y)[8], int vec) {
-    uint16_t z[8];
+__device__ __forceinline__ uint4 round8(const float (&y)[8]) {
+    uint32_t z[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) z[(e >> 1) + 4 * (e & 1)] = T::from_f32(y[e]);
+    return make_uint4(z[0] | (z[1] << 16), z[2] | (z[3] << 16), z[4] | (z[5] << 16), z[6] | (z[7] << 16));
+}
+__device__ __forceinline__ void put8(uint16_t* d, uint4 y, int vec) {
     if (vec) {
-        *reinterpret_cast<uint4*>(d) = make_uint4(z[0] | ((uint32_t)z[1] << 16), z[2] | ((uint32_t)z[3] << 16),
-                                                  z[4] | ((uint32_t)z[5] << 16), z[6] | ((uint32_t)z[7] << 16));
+        *reinterpret_cast<uint4*>(d) = y;
     } else {
+        const uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] = z[e];
+        for (int e = 0; e < 8; ++e) d[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
     }
 }
 
@@ -366,9 +411,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t tmem_slot;
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::bars);
-    uint64_t *ring_full = bars, *ring_empty = bars + kRing, *k_full = bars + 2 * kRing, *k_empty = k_full + 2,
-             *v_full = k_full + 4, *v_empty = k_full + 6, *s_full = k_full + 8, *p_full = k_full + 10,
-             *q_full = k_full + 14, *o_full = k_full + 15, *fin = k_full + 16;
+    // (two of most: keys / values, M tiles, buffers)
+    // (done[t % kBufs]: the products QK of tile t have finished, and with them PV of tile t - 1)
+    uint64_t *ring_full = bars, *ring_empty = bars + kRing, *k_full = bars + 2 * kRing, *v_full = k_full + kBufs,
+             *done = v_full + kBufs, *s_full = done + kBufs, *p_full = s_full + 2, *q_full = s_full + 6, *o_full = s_full + 7,
+             *fin = s_full + 8;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
     if (tid == 0) {
@@ -376,11 +423,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ring_full[i], 1);
             mbar_init(&ring_empty[i], 4);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kBufs; ++i) {
             mbar_init(&k_full[i], 4);
-            mbar_init(&k_empty[i], 1);
             mbar_init(&v_full[i], 4);
-            mbar_init(&v_empty[i], 1);
+            mbar_init(&done[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[2 * i], 4);       // probabilities of the first 64 keys
             mbar_init(&p_full[2 * i + 1], 4);   // and of the others
@@ -443,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* recs = reinterpret_cast<float*>(ws + meta_bytes(gridDim.x)) + blockIdx.x * 2 * rec_floats(D);
     if (tid < 2 && c0 >= c1) meta[tid] = make_int4(-1, 0, 0, 0);
     if (c0 >= c1) return;
-    if (warp == 12) {
+    if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -453,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_after();
     const uint32_t tmem = tmem_slot;
 
-    __shared__ Walk walks[kThreads / 32];
+    __shared__ Walk walks[kThreads / 32 + 8];   // (two for each softmax warp)
     Walk& w = walks[warp];
     {
         Walk first;
@@ -463,136 +511,150 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const Ctl ctl{p.status, p.spin_limit, &abort_flag};
 
-    if (warp >= 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-    if (warp == 13) {
-        // ---------------- producer: packed keys and values of each tile in turn ----------------
+    if (warp < kSoftmax) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (warp == kLoader) {
+        // ---------------- loader: packed keys and values of each tile in turn ----------------
+        // lane: page of the tile, and one of three arrays
         const int pl = p.sh.page_log2;
         const int pieces = pl >= 7 ? 1 : kKeys >> pl, tokens = pl >= 7 ? kKeys : 1 << pl;
-        const int piece = lane / 3, which = lane - 3 * piece;
+        const int piece = lane / 3, array = lane - 3 * piece;    // codes, scales, biases
         const bool active = piece < pieces;
         const int ng = D >> gs_log2;
-        const uint32_t row_bytes = which == 0 ? D / 2 : 2 * ng;
+        const uint32_t row_bytes = array == 0 ? D / 2 : 2 * ng;
         const uint32_t bytes = tokens * row_bytes;
         const uint32_t dst0 = smem_u32(smem + M::ring) +
-                              (which == 0 ? 0u : kKeys * (D / 2) + (which - 1) * kKeys * 2 * ng) + piece * bytes;
-        const uint8_t* src[2];
-        src[0] = static_cast<const uint8_t*>(which == 0   ? static_cast<const void*>(p.k.packed)
-                                             : which == 1 ? p.k.scales
-                                                          : p.k.biases);
-        src[1] = static_cast<const uint8_t*>(which == 0   ? static_cast<const void*>(p.v.packed)
-                                             : which == 1 ? p.v.scales
-                                                          : p.v.biases);
+                              (array == 0 ? 0u : kKeys * (D / 2) + (array - 1) * kKeys * 2 * ng) + piece * bytes;
+        auto source = [&](const KvCache& c) {
+            return static_cast<const uint8_t*>(array == 0 ? static_cast<const void*>(c.packed) : array == 1 ? c.scales : c.biases);
+        };
+        const uint8_t* const src_k = source(p.k);
+        const uint8_t* const src_v = source(p.v);
         uint32_t* masks = reinterpret_cast<uint32_t*>(smem + M::masks);
-        int issued = 0;
+        int issued = 0, s = 0;
+        uint32_t parity = 1;
         bool ok = true;
         for (; w.more() && ok; w.advance(p)) {
-        const int t_a = w.first(), t_b = w.last(), h = w.h;
-        const int* table = p.table + (long long)w.r * p.max_blocks;
-        const int npages = (w.q.kv + (1 << pl) - 1) >> pl;
-        int tok = (w.t_first + t_a) * kKeys + piece * tokens;
-        int page = t_a < t_b && active && (tok >> pl) < npages ? table[tok >> pl] : -1;
-        for (int t = t_a; t < t_b && ok; ++t) {
-            const bool there = active && page >= 0 && page < p.sh.num_blocks;
-            const uint32_t votes = __ballot_sync(0xffffffffu, there && which == 0);
-            const long long line = there ? (((long long)page * p.sh.hkv + h) << pl) + (tok & ((1 << pl) - 1)) : 0;
-            const int left = w.q.kv - (w.t_first + t) * kKeys;
-            tok += kKeys;
-            page = active && (tok >> pl) < npages ? table[tok >> pl] : -1;   // of the next tile
-            // token bits of this tile, 32 per lane for lanes 0..3
-            uint32_t m = 0;
-            for (int b = 0; b < 32; b += 16) {
-                const int o = (lane & 3) * 32 + b;
-                const int pc = o / tokens;
-                if ((votes >> (3 * pc)) & 1u) m |= 0xffffu << b;
-            }
-            const int l = left - (lane & 3) * 32;
-            if (l < 32) m &= l <= 0 ? 0u : (1u << l) - 1u;
-            for (int kv = 0; kv < 2; ++kv, ++issued) {
-                const int s = issued % kRing;
-                if (!warp_wait(&ring_empty[s], ((issued / kRing) & 1) ^ 1, ctl)) {
-                    ok = false;
-                    break;
+            const int h = w.h, kv_len = w.q.kv;
+            const int* table = p.table + (long long)w.r * p.max_blocks;
+            const int npages = (kv_len + (1 << pl) - 1) >> pl;
+            int key = (w.t_first + w.first()) * kKeys;           // first token of the tile
+            const int end = (w.t_first + w.last()) * kKeys;
+            int at = (key + piece * tokens) >> pl;
+            int page = key < end && active && at < npages ? table[at] : -1;
+            for (; key < end && ok; key += kKeys) {
+                const bool there = active && page >= 0 && page < p.sh.num_blocks;
+                const uint32_t votes = __ballot_sync(0xffffffffu, there && array == 0);
+                const long long line =
+                    there ? (((long long)page * p.sh.hkv + h) << pl) + ((key + piece * tokens) & ((1 << pl) - 1)) : 0;
+                at = (key + kKeys + piece * tokens) >> pl;
+                page = active && at < npages ? table[at] : -1;   // of the next tile
+                // bits of the tokens that are there, 32 for each of lanes 0 to 3
+                uint32_t m = 0;
+#pragma unroll
+                for (int b = 0; b < 32; b += 16)
+                    if ((votes >> (3 * (((lane & 3) * 32 + b) / tokens))) & 1u) m |= 0xffffu << b;
+                m &= below(kv_len - key - (lane & 3) * 32);
+#pragma unroll
+                for (int side = 0; side < 2; ++side) {
+                    ok = warp_wait(&ring_empty[s], parity, ctl);
+                    if (!ok) break;
+                    if (lane < 4) masks[s * 4 + lane] = m;
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&ring_full[s], (uint32_t)__popc(votes) * tokens * (D / 2 + 4 * ng));
+                    __syncwarp();
+                    if (there)
+                        asm volatile(
+                            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                dst0 + s * M::kStage),
+                            "l"((side ? src_v : src_k) + line * row_bytes), "r"(bytes), "r"(smem_u32(&ring_full[s]))
+                            : "memory");
+                    ++issued;
+                    if (++s == kRing) {
+                        s = 0;
+                        parity ^= 1u;
+                    }
                 }
-                if (lane < 4) masks[s * 4 + lane] = m;
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&ring_full[s], (uint32_t)__popc(votes) * tokens * (D / 2 + 4 * ng));
-                __syncwarp();
-                if (there)
-                    asm volatile(
-                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                            dst0 + s * M::kStage),
-                        "l"(src[kv] + line * row_bytes), "r"(bytes), "r"(smem_u32(&ring_full[s]))
-                        : "memory");
             }
-        }
         }
         for (int i = issued > kRing ? issued - kRing : 0; i < issued; ++i)
             mbar_wait_drain(&ring_full[i % kRing], (i / kRing) & 1, ctl.limit, ctl.status);
-    } else if (warp == 12) {
+    } else if (warp == 0) {
         // ---------------- products ----------------
         constexpr uint32_t id_s = idesc(BF, kKeys, false), id_o = idesc(BF, D, true);
-        const uint32_t qb = smem_u32(smem + M::q), kb = smem_u32(smem + M::k), vb = smem_u32(smem + M::v);
-        auto qk = [&](int i, int j) {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t o = (kk >> 2) * M::kAtom + (kk & 3) * 32;
-                mma_ss(tmem + 128 * i, desc_k(qb + i * M::kTile + o), desc_k(kb + (j & 1) * M::kTile + o), id_s, kk > 0);
-            }
-            commit(&s_full[i]);
+        // (addresses below 2^18: offsets do not carry out of their field)
+        const uint32_t q0 = desc_k(smem_u32(smem + M::q)), k0 = desc_k(smem_u32(smem + M::k)),
+                       v0 = desc_n(smem_u32(smem + M::v));
+        // key tile j and value tile j are in buffer j % kBufs
+        auto qk = [&](int i, int buf) {
+            products_qk<D>(tmem + kS + 128 * i, q0 + i * (M::kTile >> 4), k0 + buf * (M::kTile >> 4), id_s, &s_full[i]);
         };
-        auto pv = [&](int i, int j, int half, bool add) {
-#pragma unroll
-            for (int k = 0; k < kKeys / 32; ++k) {
-                const int kk = k + (kKeys / 32) * half;
-                mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * kk, desc_n(vb + (j & 1) * M::kTile + kk * 2048), id_o,
-                       add || k > 0);
-            }
+        auto pv = [&](int i, int buf, int half, bool add) {
+            products_pv(tmem + kO + 128 * i, tmem + kS + 128 * i + 32 * half, v0 + buf * (M::kTile >> 4) + 512 * half, id_o, add);
         };
+        // a wait without the vote of warp_wait: the lanes leave the loop
+        // together as a rule, and meet again before the next product
         bool ok = true;
-        int units = 0, jj = 0;          // segments and tiles so far
-        uint32_t np = 0;                // parity of the probabilities of each M tile, one bit each
-        for (; w.more() && ok; w.advance(p)) {
-            const int n = w.last() - w.first(), nm = w.tiles_m();
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            if (!mbar_try_wait(bar, parity) && !mbar_wait(bar, parity, ctl)) ok = false;
+            __syncwarp();
+        };
+        int units = 0, buf = 0;         // segments so far, buffer of the tile in work
+        uint32_t parity = 0;            // of that buffer's barriers
+        uint32_t np0 = 0, np1 = 0;      // of the probabilities of each M tile
+        for (; w.more(); w.advance(p)) {
+            const int n = w.last() - w.first();
+            const bool both = w.tiles_m() == 2;
             if (n == 0) continue;
-            ok = warp_wait(q_full, units & 1, ctl) && warp_wait(&k_full[jj & 1], (jj >> 1) & 1, ctl);
-            if (!ok) break;
+            wait(q_full, units & 1);
+            wait(&k_full[buf], parity);
             fence_after();
-            for (int i = 0; i < nm; ++i) qk(i, jj);
-            commit(&k_empty[jj & 1]);
-            for (int j = 0; ok && j < n; ++j, ++jj) {
-                ok = warp_wait(&v_full[jj & 1], (jj >> 1) & 1, ctl);
-                for (int i = 0; ok && i < nm; ++i) {
-                    for (int half = 0; ok && half < 2; ++half) {
-                        ok = warp_wait(&p_full[2 * i + half], (np >> i) & 1u, ctl);
-                        if (!ok) break;
-                        fence_after();
-                        pv(i, jj, half, j > 0 || half > 0);
-                    }
-                    if (!ok) break;
-                    np ^= 1u << i;
-                    if (i == nm - 1) commit(&v_empty[jj & 1]);
-                    if (j + 1 < n) {
-                        if (i == 0) ok = warp_wait(&k_full[(jj + 1) & 1], ((jj + 1) >> 1) & 1, ctl);
-                        if (!ok) break;
-                        fence_after();
-                        qk(i, jj + 1);
-                        if (i == nm - 1) commit(&k_empty[(jj + 1) & 1]);
-                    }
+            qk(0, buf);
+            if (both) qk(1, buf);
+            commit(&done[buf]);
+            for (int j = 0; j < n; ++j) {
+                const bool more = j + 1 < n;
+                const int next = buf + 1 == kBufs ? 0 : buf + 1;
+                const uint32_t next_parity = next == 0 ? parity ^ 1u : parity;
+                // (keys and values are there before the probabilities as a rule)
+                wait(&v_full[buf], parity);
+                if (more) wait(&k_full[next], next_parity);
+                wait(&p_full[0], np0);
+                if (__any_sync(0xffffffffu, !ok)) break;   // a wait timed out
+                fence_after();
+                pv(0, buf, 0, j > 0);
+                wait(&p_full[1], np0);
+                np0 ^= 1u;
+                fence_after();
+                pv(0, buf, 1, true);
+                if (more) qk(0, next);
+                if (both) {
+                    wait(&p_full[2], np1);
+                    fence_after();
+                    pv(1, buf, 0, j > 0);
+                    wait(&p_full[3], np1);
+                    np1 ^= 1u;
+                    fence_after();
+                    pv(1, buf, 1, true);
+                    if (more) qk(1, next);
                 }
+                if (more) commit(&done[next]);
+                buf = next;
+                parity = next_parity;
             }
             commit(o_full);
+            if (__any_sync(0xffffffffu, !ok)) break;
             ++units;
         }
         // no product may outlive the tensor memory
         commit(fin);
         if (lane == 0) mbar_wait_drain(fin, 0, ctl.limit, ctl.status);
         __syncwarp();
-    } else if (warp >= 14) {
-    } else if (warp >= 8) {
+    } else if (warp < kSoftmax) {
+    } else if (warp >= kExpand) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kExpandRegs));
         // ---------------- expanding keys and values: one token per thread ----------------
-        const int r = (warp - 8) * 32 + lane;
+        const int r = (warp - kExpand) * 32 + lane;
         const int ng = D >> gs_log2;
         // 32 channels at a time; neighbouring rows take them in another order
         // (banks). Offsets of the packed words, of the row's scales and of the
@@ -607,80 +669,133 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) chunk[k] = (k ^ (r & 3)) << 4;
-        const uint32_t* masks = reinterpret_cast<const uint32_t*>(smem + M::masks);
-        int i = 0;                     // keys and values of all tiles in turn
+        const uint32_t* masks = reinterpret_cast<const uint32_t*>(smem + M::masks) + (r >> 5);
+        int j = 0, s = 0;              // tiles so far, packed stage
+        uint32_t parity = 0;           // of that stage
         for (; w.more(); w.advance(p)) {
-        for (const int end = i + 2 * (w.last() - w.first()); i < end; ++i) {
-            const int s = i % kRing, j = i >> 1;
-            uint64_t *full = i & 1 ? &v_full[j & 1] : &k_full[j & 1], *empty = i & 1 ? &v_empty[j & 1] : &k_empty[j & 1];
-            uint8_t* dst = smem + (i & 1 ? M::v : M::k) + (j & 1) * M::kTile;
-            (void)warp_wait(&ring_full[s], (i / kRing) & 1, ctl);
-            (void)warp_wait(empty, ((j >> 1) & 1) ^ 1, ctl);
-            const uint8_t* st = smem + M::ring + s * M::kStage;
-            const bool valid = (masks[s * 4 + (r >> 5)] >> (r & 31)) & 1u;   // else zeros: the slot may hold anything
+            for (const int end = j + (w.last() - w.first()); j < end; ++j) {
+                const int buf = j & 1;
+#pragma unroll 1
+                for (int side = 0; side < 2; ++side) {      // keys, values
+                    uint8_t* dst = smem + (side ? M::v : M::k) + buf * M::kTile;
+                    (void)warp_wait(&ring_full[s], parity, ctl);
+                    // the buffer's last tile was j - kBufs
+                    const int t = j - kBufs + side;
+                    if (t >= 0) (void)warp_wait(&done[t & 1], (t >> 1) & 1, ctl);
+                    const uint8_t* st = smem + M::ring + s * M::kStage;
+                    const bool valid = (masks[4 * s] >> (r & 31)) & 1u;   // else zeros: the slot may hold anything
 #pragma unroll
-            for (int x = 0; x < D / 32; ++x) {
-                const uint4 w = *reinterpret_cast<const uint4*>(st + from[x]);
-                const uint8_t* sc = st + group[x];
-                const Group<BF> gr(valid ? *reinterpret_cast<const uint16_t*>(sc) : 0u,
-                                   valid ? *reinterpret_cast<const uint16_t*>(sc + kKeys * 2 * ng) : 0u);
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                    for (int x = 0; x < D / 32; ++x) {
+                        const uint4 y = *reinterpret_cast<const uint4*>(st + from[x]);
+                        const uint8_t* sc = st + group[x];
+                        const Group<BF> gr(valid ? *reinterpret_cast<const uint16_t*>(sc) : 0u,
+                                           valid ? *reinterpret_cast<const uint16_t*>(sc + kKeys * 2 * ng) : 0u);
+                        const uint32_t ww[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(dst + to[x] + chunk[k]) = expand<BF>(ww[k], gr);
+                        for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(dst + to[x] + chunk[e]) = expand<BF>(ww[e], gr);
+                    }
+                    fence_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(side ? &v_full[buf] : &k_full[buf]);
+                        mbar_arrive(&ring_empty[s]);
+                    }
+                    if (++s == kRing) {
+                        s = 0;
+                        parity ^= 1u;
+                    }
+                }
             }
-            fence_async();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(full);
-                mbar_arrive(&ring_empty[s]);
-            }
-        }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
         // ---------------- softmax: M tile i, one row per thread ----------------
-        const int i = warp >> 2, r = (warp & 3) * 32 + lane;
-        int units = 0, ns = 0;         // segments and score tiles so far
-        bool has0 = false, has1 = false;
-        for (; w.more(); w.advance(p)) {
-        const int t_a = w.first(), t_b = w.last();
-        if (t_a == t_b) continue;
-        const int rq_q0 = w.q.q0, rq_kv = w.q.kv, pos0 = rq_kv - w.q.qn, h = w.h, nm = w.tiles_m();
-        const int row = w.row0 + i * 128 + r;
-        const bool live = row < w.rows;
-        const int tok = live ? row / p.group : 0;
-        const int head = h * p.group + (live ? row - tok * p.group : 0);
-        // query row into shared memory; a negative scale turns its sign
-        {
-            const uint16_t* src = static_cast<const uint16_t*>(p.q) + (long long)(rq_q0 + tok) * p.q_stride + (long long)head * D;
-            const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
-            uint8_t* dst = smem + M::q + i * M::kTile + r * 128;
-#pragma unroll 4
-            for (int ch = 0; ch < D / 8; ++ch) {
-                uint32_t w[4] = {0u, 0u, 0u, 0u};
-                if (live) {
-                    if (vec_q) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(src + 8 * ch);
-                        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-                    } else {
+        const int i = (warp - kSoftmax) >> 2, r = (warp & 3) * 32 + lane;
+        // Queries come and outputs go a warp at a time, D / 8 lanes to a row
+        // (row by thread would touch 32 lines an instruction), the outputs by
+        // way of the query tile, which is free by then.
+        constexpr int L = D / 8, R = 32 / L;        // lanes of a row, rows at a time
+        const int lr = lane / L, lc = lane % L;     // this lane's row and 16-byte chunk
+        uint8_t* const qtile = smem + M::q + i * M::kTile;
+        auto chunk_at = [&](int row, int ch) { return qtile + (ch >> 3) * M::kAtom + row * 128 + (((ch & 7) ^ (row & 7)) << 4); };
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_tm = tmem + kS + 128 * i + lanes, o_tm = tmem + kO + 128 * i + lanes;
+        const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;   // a negative scale turns the queries' sign
+        // f(k, address or null) for this lane's chunk of its row number k, of
+        // `rows` [.., heads, D] with a token stride
+        auto each_row = [&](const Walk& w, auto* base, long long stride, auto&& f) {
+            const int first = w.row0 + i * 128 + (warp & 3) * 32 + lr;
+            const int tok = first / p.group;
+            int hd = first - tok * p.group, left = w.rows - first;
+            auto* at = base + (w.q.q0 + tok) * stride + (w.h * p.group + hd) * D + lc * 8;
+            const long long wrap = stride - p.group * D;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            w[k] = (uint32_t)src[8 * ch + 2 * k] | ((uint32_t)src[8 * ch + 2 * k + 1] << 16);
+            for (int k = 0; k < 32 / R; ++k) {
+                f(k, left > k * R ? at : nullptr);
+                at += R * D;
+                hd += R;
+#pragma unroll
+                for (int e = 0; e < R; ++e)
+                    if (hd >= p.group) {
+                        hd -= p.group;
+                        at += wrap;
+                    }
+            }
+        };
+        // this lane's chunk of its row number k in the query tile
+        uint8_t* const my_chunk = qtile + (lc >> 3) * M::kAtom + ((warp & 3) * 32 + lr) * 128;
+        const uint32_t my_swizzle = ((lc & 7) ^ lr) << 4;
+        auto tile_at = [&](int k) {
+            return reinterpret_cast<uint4*>(my_chunk + k * R * 128 + (my_swizzle ^ (((k * R) & 7) << 4)));
+        };
+        auto prefetch_q = [&](const Walk& w) {
+            each_row(w, static_cast<const uint16_t*>(p.q), p.q_stride, [&](int, const uint16_t* src) {
+                if (src) asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+            });
+        };
+        auto load_q = [&](const Walk& w) {
+            uint4 y[32 / R];
+            each_row(w, static_cast<const uint16_t*>(p.q), p.q_stride, [&](int k, const uint16_t* src) {
+                y[k] = make_uint4(0u, 0u, 0u, 0u);
+                if (src) {
+                    if (vec_q) {
+                        y[k] = *reinterpret_cast<const uint4*>(src);
+                    } else {
+                        uint32_t x[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[e] = (uint32_t)src[2 * e] | ((uint32_t)src[2 * e + 1] << 16);
+                        y[k] = make_uint4(x[0], x[1], x[2], x[3]);
                     }
                 }
+            });
+#pragma unroll
+            for (int k = 0; k < 32 / R; ++k) {
                 uint4 o;
-                o.x = __byte_perm(w[0], w[2], 0x5410) ^ flip;
-                o.y = __byte_perm(w[0], w[2], 0x7632) ^ flip;
-                o.z = __byte_perm(w[1], w[3], 0x5410) ^ flip;
-                o.w = __byte_perm(w[1], w[3], 0x7632) ^ flip;
-                *reinterpret_cast<uint4*>(dst + (ch >> 3) * M::kAtom + (((ch & 7) ^ (r & 7)) << 4)) = o;
+                o.x = __byte_perm(y[k].x, y[k].z, 0x5410) ^ flip;
+                o.y = __byte_perm(y[k].x, y[k].z, 0x7632) ^ flip;
+                o.z = __byte_perm(y[k].y, y[k].w, 0x5410) ^ flip;
+                o.w = __byte_perm(y[k].y, y[k].w, 0x7632) ^ flip;
+                *tile_at(k) = o;
             }
             fence_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
-        }
-        if (i < nm) {
-            const long long pos = (long long)pos0 + tok;
+        };
+        // the segment in work and the next one that has a tile: what is not
+        // needed in the loop over the keys stays in shared memory
+        Walk* cur = &w;
+        Walk* next = &walks[kThreads / 32 + warp - kSoftmax];
+        uint32_t s_parity = 0, o_parity = 0;   // of the score tiles and segments so far
+        if (tid == 32 * kSoftmax) meta[0] = meta[1] = make_int4(-1, 0, 0, 0);
+        while (cur->more() && cur->first() == cur->last()) cur->advance(p);
+        bool more = cur->more();
+        if (more) load_q(*cur);
+        while (more) {
+        float m = -INFINITY, l = 0.f;
+        if (i < cur->tiles_m()) {
+            const int row = cur->row0 + i * 128 + r;
+            const bool live = row < cur->rows;
+            const long long pos = (long long)cur->q.kv - cur->q.qn + (live ? row / p.group : 0);
             // keys [lo_key, hi_key) of this row
             const int hi_key = live ? (int)max(pos + 1, 0ll) : 0;
             const int lo_key = p.window > 0 && live ? (int)max(pos - p.window + 1, 0ll) : 0;
@@ -689,38 +804,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             lo_max = __reduce_max_sync(0xffffffffu, lo_max);
             // scores to powers of two; a tiny factor in the place of 0 keeps masked scores at -inf
             const float f = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-30f) * kUndo<BF>;
-            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-            const uint32_t s_tm = tmem + 128 * i + lanes, o_tm = tmem + 256 + 128 * i + lanes;
-            const int pl = p.sh.page_log2;
-            const int* table = p.table + (long long)w.r * p.max_blocks;
-            const int npages = (rq_kv + (1 << pl) - 1) >> pl;
-            const int t_first = w.t_first;
-            float m = -INFINITY, l = 0.f;
-            for (int j = t_a; j < t_b; ++j) {
-                const int key0 = (t_first + j) * kKeys;
-                // 16-token pieces without a page
-                bool gone = false;
-                if (lane < 8 && ((key0 + 16 * lane) >> pl) < npages) {
-                    const int page = table[(key0 + 16 * lane) >> pl];
-                    gone = page < 0 || page >= p.sh.num_blocks;
-                }
-                const uint32_t holes = __ballot_sync(0xffffffffu, gone);
-                const bool masked = holes != 0 || key0 + kKeys > hi_min || key0 < lo_max;
-                (void)warp_wait(&s_full[i], ns & 1, ctl);
-                ++ns;
+            const int first_key = (cur->t_first + cur->first()) * kKeys, end_key = (cur->t_first + cur->last()) * kKeys;
+            const bool holes_here = holes(p, *cur, first_key, end_key, lane) != 0;
+            for (int key0 = first_key; key0 < end_key; key0 += kKeys) {
+                const bool masked = holes_here || key0 + kKeys > hi_min || key0 < lo_max;
+                (void)warp_wait(&s_full[i], s_parity, ctl);
+                s_parity ^= 1u;
                 fence_after();
-                uint32_t v[4][32];
+                uint32_t v[kKeys / 32][32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + 32 * c, v[c]);
+                for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(s_tm + 32 * c, v[c]);
                 tmem_ld_wait();
                 if (masked) {
                     const int hi = hi_key - key0, lo_ = lo_key - key0;
+                    const uint32_t gone = holes_here ? holes(p, *cur, key0, key0 + kKeys, lane) : 0u;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < kKeys / 32; ++c) {
                         // bits of the keys that the row sees
                         uint32_t see = below(hi - 32 * c) & ~below(lo_ - 32 * c);
-                        if ((holes >> (2 * c)) & 1u) see &= 0xffff0000u;
-                        if ((holes >> (2 * c + 1)) & 1u) see &= 0x0000ffffu;
+                        if ((gone >> (2 * c)) & 1u) see &= 0xffff0000u;
+                        if ((gone >> (2 * c + 1)) & 1u) see &= 0x0000ffffu;
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (!(see & (1u << e))) v[c][e] = 0xff800000u;   // -inf
@@ -728,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < kKeys / 32; ++c)
 #pragma unroll
                     for (int e = 0; e < 32; e += 2)
                         mx4[(e >> 1) & 3] = max3(mx4[(e >> 1) & 3], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
@@ -737,15 +840,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (__any_sync(0xffffffffu, mx > m + 8.f || (m == -INFINITY && mx > m))) {
                     const float mn = fmaxf(m, mx);
                     const float a = m == -INFINITY ? 0.f : ex2(m - mn);
-                    if (j > t_a) {
+                    if (key0 > first_key) {
 #pragma unroll 1
-                        for (int c = 0; c < D / 16; ++c) {   // (16 columns: the scores stay in registers)
-                            uint32_t y[16];
-                            tmem_ld16(o_tm + 16 * c, y);
+                        for (int c = 0; c < D / 8; ++c) {   // (8 columns: the scores stay in registers)
+                            uint32_t y[8];
+                            tmem_ld8(o_tm + 8 * c, y);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * a);
-                            tmem_st16(o_tm + 16 * c, y);
+                            for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * a);
+                            tmem_st8(o_tm + 8 * c, y);
                         }
                     }
                     l *= a;
@@ -776,62 +879,75 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
-            // ---- output, or a record of it
-            (void)warp_wait(o_full, units & 1, ctl);
-            fence_after();
-            const bool begins = t_a == 0, whole = begins && t_b == w.n;
+        }
+        cur->advance_to(p, *next);
+        while (next->more() && next->first() == next->last()) next->advance(p);
+        more = next->more();
+        if (more) prefetch_q(*next);   // (held in registers during the output they spill)
+        // ---- output, or a record of it
+        (void)warp_wait(o_full, o_parity, ctl);
+        o_parity ^= 1u;
+        fence_after();
+        const bool begins = cur->first() == 0, whole = begins && cur->last() == cur->n, mine = i < cur->tiles_m();
+        const int row0 = cur->row0, rows = cur->rows, rq_q0 = cur->q.q0, h = cur->h;
+        if (mine && whole) {
             const float inv = l > 0.f ? kUndo<BF> / l : 0.f;
-            uint16_t* dst = static_cast<uint16_t*>(p.out) + (long long)(rq_q0 + tok) * p.out_stride + (long long)head * D;
-            float* rec = recs + (begins ? rec_floats(D) : 0);
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t v[32];
                 tmem_ld32(o_tm + 32 * c, v);
                 tmem_ld_wait();
-                if (whole) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float y[8];
+                for (int k = 0; k < 4; ++k) {
+                    float y[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = l == 0.f ? 0.f : __uint_as_float(v[8 * k + e]) * inv;
-                        if (live) store8<T>(dst + 32 * c + 8 * k, y, vec_out);
-                    }
-                } else {
+                    for (int e = 0; e < 8; ++e) y[e] = l == 0.f ? 0.f : __uint_as_float(v[8 * k + e]) * inv;
+                    *reinterpret_cast<uint4*>(chunk_at(r, 4 * c + k)) = round8<T>(y);
+                }
+            }
+            __syncwarp();
+            each_row(*cur, static_cast<uint16_t*>(p.out), p.out_stride, [&](int k, uint16_t* dst) {
+                if (dst) put8(dst, *tile_at(k), vec_out);
+            });
+            __syncwarp();
+            const int row = row0 + i * 128 + r;
+            if (p.lse && row < rows) {
+                const int tok = row / p.group;
+                p.lse[(long long)(rq_q0 + tok) * (p.sh.hkv * p.group) + h * p.group + (row - tok * p.group)] =
+                    l == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(l));
+            }
+        } else if (!whole) {
+            float* rec = recs + (begins ? rec_floats(D) : 0);
+            if (mine) {
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32(o_tm + 32 * c, v);
+                    tmem_ld_wait();
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         reinterpret_cast<uint4*>(rec)[(8 * c + k) * kRows + i * 128 + r] =
                             make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
                 }
-            }
-            if (whole) {
-                if (live && p.lse)
-                    p.lse[(long long)(rq_q0 + tok) * (p.sh.hkv * p.group) + head] =
-                        l == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(l));
-            } else {
                 rec[kRows * D + i * 128 + r] = m;
                 rec[kRows * (D + 1) + i * 128 + r] = l;
-                if (tid == 0) {
-                    const int unit = w.blk * p.sh.hkv + h;
-                    // record 1 begins a unit that goes on: its last CTA holds the unit's last place
-                    meta[begins ? 0 : 1] = make_int4(w.r, unit, (int)((w.c - w.place + w.places - 1) / per), 0);
-                }
-                (begins ? has1 : has0) = true;
             }
-            fence_before();
-        } else {
-            (void)warp_wait(o_full, units & 1, ctl);
+            // record 1 begins a unit that goes on
+            if (tid == 32 * kSoftmax)
+                meta[begins ? 0 : 1] = make_int4(cur->r, cur->blk * p.sh.hkv + h,
+                                                 (int)((cur->c - cur->place + cur->places - 1) / per), 0);
         }
-        ++units;
-        }
-        if (tid == 0) {
-            if (!has1) meta[0] = make_int4(-1, 0, 0, 0);
-            if (!has0) meta[1] = make_int4(-1, 0, 0, 0);
+        fence_before();
+        if (more) load_q(*next);
+        Walk* const done = cur;
+        cur = next;
+        next = done;
         }
     }
     fence_before();
     __syncthreads();
     fence_after();
-    if (warp == 12)
+    if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
@@ -886,7 +1002,7 @@ __global__ void __launch_bounds__(kRows)
         float z[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) z[e] = l == 0.f ? 0.f : y[8 * k + e] * inv;
-        store8<T>(dst + 8 * k, z, vec_out);
+        put8(dst + 8 * k, round8<T>(z), vec_out);
     }
     if (p.lse && c == 0)
         p.lse[(long long)(rq.q0 + tok) * (p.sh.hkv * p.group) + head] =
