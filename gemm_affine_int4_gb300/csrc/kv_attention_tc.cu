@@ -336,9 +336,13 @@ struct Walk {
     }
     __device__ bool more() const { return c < c1; }
     __device__ long long here() const { return min(places - place, c1 - c); }
-    // tiles of this segment
-    __device__ int first() const { return (int)(place * n / places); }
-    __device__ int last() const { return (int)((place + here()) * n / places); }
+    // tiles of this segment: kStart tiles' places come before the first
+    // tile's (places are only an estimate: the last place ends the last tile)
+    __device__ int tile_at(long long x) const {
+        return x >= places ? n : min(max((int)(x / kPart) - kStart, 0), n);
+    }
+    __device__ int first() const { return tile_at(place); }
+    __device__ int last() const { return tile_at(place + here()); }
     __device__ void advance(const KvAttnLaunch& p) { advance_to(p, *this); }
     __device__ void advance_to(const KvAttnLaunch& p, Walk& to) const {
         __syncwarp();   // every lane has read what it needs
@@ -475,6 +479,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         start_r = r;
         start_off = c0 - at;
     }
+    if (warp == 0 && c0 < c1) {
+        __syncwarp();
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
     // rows that belong to no request
     {
         const int hq = p.sh.hkv * p.group;
@@ -491,11 +501,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* recs = reinterpret_cast<float*>(ws + meta_bytes(gridDim.x)) + blockIdx.x * 2 * rec_floats(D);
     if (tid < 2 && c0 >= c1) meta[tid] = make_int4(-1, 0, 0, 0);
     if (c0 >= c1) return;
-    if (warp == 0) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
     fence_before();
     __syncthreads();
     fence_after();
@@ -924,10 +929,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t v[32];
                     tmem_ld32(o_tm + 32 * c, v);
                     tmem_ld_wait();
+                    if (row0 + i * 128 + r < rows) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        reinterpret_cast<uint4*>(rec)[(8 * c + k) * kRows + i * 128 + r] =
-                            make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                        for (int k = 0; k < 8; ++k)
+                            reinterpret_cast<uint4*>(rec)[(8 * c + k) * kRows + i * 128 + r] =
+                                make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    }
                 }
                 rec[kRows * D + i * 128 + r] = m;
                 rec[kRows * (D + 1) + i * 128 + r] = l;
