@@ -27,7 +27,7 @@
 // that mma.sync reaches at the memory's speed; tcgen05 would need the codes
 // expanded through shared memory first.
 //
-// Work split. Tokens are cut into 32-token tiles; a unit is (request,
+// Work split. Tokens are cut into 64-token tiles; a unit is (request,
 // key/value head, block of 8 NT query rows), and all units' tiles form one
 // line that is cut evenly over the CTAs: ragged lengths and few long requests
 // alike fill the GPU. In a CTA a producer warp streams tiles through a ring of
@@ -48,12 +48,10 @@ namespace kvs {
 
 using namespace pipe;
 
-constexpr int kTile = 32;                       // tokens: half of the ring's stages are then on their way while every
-                                                // consumer warp works on one (64: one stage on its way, 141 us for 73)
-constexpr int kBlocks = kTile / 16;             // 16-token blocks of a tile
-constexpr int kStart = 8;                       // what the start and join of a unit cost, in tiles (see Walk)
-constexpr int kWarps = 7;                       // consumer warps: with the producer 8, so that the registers divide well
-constexpr int kThreads = 32 * (kWarps + 1);     // and one producer warp
+constexpr int kTile = 64;                       // tokens of a stage of the ring, loaded at once
+constexpr int kSub = 32;                        // tokens that a consumer warp works on: half a stage
+constexpr int kBlocks = kSub / 16;              // 16-token blocks of a sub-tile
+constexpr int kStart = 4;                       // what the start and join of a unit cost, in tiles (see Walk)
 
 template <typename T_, int D_, int GS_, int NT_>
 struct Cfg {
@@ -66,16 +64,20 @@ struct Cfg {
     static constexpr uint32_t kCodes = kTile * D / 2, kSb = kTile * NG * E;
     static constexpr uint32_t kStage = 2 * kCodes + 4 * kSb;
     static constexpr int DP = D + 4;                        // padded row of the join buffer
-    static constexpr uint32_t kJoin = kWarps * NC * DP * 4 + 2 * kWarps * NC * 4;
+    // Consumer warps, and one producer: 8 warps divide the registers well (two
+    // CTAs of 128 registers a thread, or one of 255); 12 where 168 are enough.
     static constexpr int kCtas = NT == 1 && !kSplit ? 2 : 1;   // resident CTAs per SM
+    static constexpr int kWarps = kSplit && NT == 1 && D == 64 ? 11 : 7;
+    static constexpr int kThreads = 32 * (kWarps + 1);
+    static constexpr uint32_t kJoin = kWarps * NC * DP * 4 + 2 * kWarps * NC * 4;
     static constexpr uint32_t kBudget = (kCtas == 2 ? 112 : 225) * 1024 - kJoin - 1024;
-    // A multiple of kWarps, so that a slot is always waited on by the same warp,
-    // fill after fill: try_wait.parity takes a fill two behind for done, and with
-    // other depths a warp could wait for a slot's next fill while the one before,
-    // another warp's, is still on its way.
-    static constexpr int kStages = (kBudget / (kStage + 24) < 4 * kWarps ? kBudget / (kStage + 24) : 4 * kWarps) / kWarps * kWarps;
+    // A multiple of kWarps (odd), so that half a slot is always waited on by the
+    // same warp, fill after fill: try_wait.parity takes a fill two behind for
+    // done, and with other depths a warp could wait for a slot's next fill while
+    // the one before, another warp's, is still on its way.
+    static constexpr int kStages = (kBudget / (kStage + 24) < 2 * kWarps ? kBudget / (kStage + 24) : 2 * kWarps) / kWarps * kWarps;
     static constexpr uint32_t kSmem = kStages * kStage + kJoin + kStages * 24 + 256;
-    static_assert(kStages >= 2 * kWarps && kStages % kWarps == 0, "ring too short");
+    static_assert(kStages >= kWarps && kStages % kWarps == 0 && kWarps % 2 == 1, "ring too short");
 };
 
 // records of cut units in the workspace: per CTA two of (O [NC][D], m [NC],
@@ -101,8 +103,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -111,7 +112,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
 }
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+template <int WARPS>
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory"); }
 
 // token of row r (0..7) of a product's 8-row block: the P operand's rows 2t
 // and 2t + 1 are tokens t and t + 4, so that neighbouring lanes of the value
@@ -235,21 +237,23 @@ struct Walk {
     }
 };
 
-// The producer: six copies (codes, scales, biases of keys and values) of five
-// tiles, or of two tiles of two 16-token pages, at a time, one per lane. (One
-// tile at a time its chain of waits and votes, about 1200 cycles, set the
-// pace of the whole kernel.)
+// The producer: six copies (codes, scales, biases of keys and values) for each
+// page of a stage, one per lane, two stages at a time with pages of 32 tokens
+// or more. (One 32-token tile at a time its chain of waits and votes, about
+// 1200 cycles, set the pace of the whole kernel; and the copies of scales and
+// biases, 256 bytes each here, cost as much as their number: with 128-byte
+// ones 4 x 131072 tokens took 127 us, without them 101.)
 template <class C>
 __device__ __forceinline__ void producer(const KvAttnLaunch& p, Walk<C::NC>& w, uint8_t* ring, uint64_t* full,
                                          uint64_t* empty, uint32_t* masks, const Ctl& ctl) {
     constexpr int S = C::kStages;
     const int lane = threadIdx.x & 31;
     const int pl = p.sh.page_log2;
-    const int two = pl < 5;                                 // pages per tile - 1
-    const int tokens = two ? 16 : kTile;                    // tokens of a piece
-    const int batch = two ? 2 : 5;                          // tiles at a time
+    const int pp = pl >= 6 ? 0 : 6 - pl;                    // log2 of the pages of a stage
+    const int tokens = kTile >> pp;                         // tokens of a piece
+    const int batch = pp == 2 ? 1 : 2;                      // stages at a time
     const int item = lane / 6, which = lane - 6 * item;     // this lane's piece and array
-    const int tl = item >> two, piece = item & two;
+    const int tl = item >> pp, piece = item & ((1 << pp) - 1);
     const bool active = tl < batch;
     const bool leader = which == 0 && piece == 0;
     const uint32_t row_bytes = which < 2 ? C::D / 2 : C::NG * C::E;
@@ -263,8 +267,8 @@ __device__ __forceinline__ void producer(const KvAttnLaunch& p, Walk<C::NC>& w, 
                      : p.v.biases);
     const uint32_t dst0 = smem_u32(ring) + (which < 2 ? which * C::kCodes : 2 * C::kCodes + (which - 2) * C::kSb) + piece * bytes;
     const int in_page = (1 << pl) - 1;
-    int seq = 0;                  // tiles issued
-    int slot = tl, phase = 1;     // of this lane's tile; parity of its "empty" wait
+    int seq = 0;                  // stages issued
+    int slot = tl, phase = 1;     // of this lane's stage; parity of its "empty" wait
     bool ok = true;
     while (w.more() && ok) {
         if (w.idle()) {
@@ -276,7 +280,7 @@ __device__ __forceinline__ void producer(const KvAttnLaunch& p, Walk<C::NC>& w, 
         const int h = w.head();
         const int* row = p.table + (long long)w.r * p.max_blocks;
         const int nblk = (w.q.kv + in_page) >> pl;
-        int tok = (w.q.tile0 + a + tl) * kTile + piece * 16;     // first token of this lane's piece
+        int tok = (w.q.tile0 + a + tl) * kTile + piece * tokens;     // first token of this lane's piece
         int page = active && (tok >> pl) < nblk ? row[tok >> pl] : -1;
         for (int t = a; t < b; t += batch) {
             const int n = min(batch, b - t);
@@ -292,13 +296,18 @@ __device__ __forceinline__ void producer(const KvAttnLaunch& p, Walk<C::NC>& w, 
                 break;
             }
             if (live && leader) {
-                uint32_t m = there ? (two ? 0xffffu : ~0u) : 0u;
-                const uint32_t second = two ? (votes >> (lane + 6)) & 1u : 0u;
-                if (second) m |= 0xffff0000u;
+                unsigned long long m = 0;
+                uint32_t pages = 0;
+                for (int i = 0; i < 1 << pp; ++i)
+                    if ((votes >> (lane + 6 * i)) & 1u) {
+                        m |= (pp == 0 ? ~0ull : (1ull << tokens) - 1) << (i * tokens);
+                        ++pages;
+                    }
                 const int left = w.q.kv - tok;
-                if (left < 32) m &= left <= 0 ? 0u : (1u << left) - 1u;
-                masks[slot] = m;
-                mbar_arrive_expect_tx(&full[slot], ((there ? 1u : 0u) + second) * (uint32_t)tokens * (C::D + 4 * C::NG * C::E));
+                if (left < 64) m &= left <= 0 ? 0ull : (1ull << left) - 1;
+                masks[2 * slot] = (uint32_t)m;
+                masks[2 * slot + 1] = (uint32_t)(m >> 32);
+                mbar_arrive_expect_tx(&full[slot], pages * (uint32_t)tokens * (C::D + 4 * C::NG * C::E));
             }
             __syncwarp();
             if (there) {
@@ -480,83 +489,104 @@ __device__ __forceinline__ Limits limits(const KvAttnLaunch& p, const Req& rq, i
 }
 
 template <class C>
-__device__ __forceinline__ void tile(const uint8_t* st, uint32_t mask, int tok0, const Query<C>& Q,
+__device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mask, int tok0, const Query<C>& Q,
                                      const KvAttnLaunch& p, const Req& rq, const Limits& L, Acc<C>& A) {
     using T = typename C::T;
     constexpr int NT = C::NT, NG = C::NG, D = C::D, GS = C::GS;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint8_t* ksc = st + 2 * C::kCodes;
+    const uint8_t* st = stage + sub * (kSub * D / 2);                       // this half's key codes; value codes kCodes on
+    const uint8_t* ksc = stage + 2 * C::kCodes + sub * (kSub * NG * C::E);
     const uint8_t* kbi = ksc + C::kSb;
     const uint8_t* vsc = kbi + C::kSb;
     const uint8_t* vbi = vsc + C::kSb;
     const int tg = row_token(g);
 
-    // ---- scores, in units of log2: x[16-token block][8-column block][row g | g + 8, column 2t | 2t + 1]
+    // ---- scores, in units of log2: x[16-token block][8-column block][row g | g + 8, column 2t | 2t + 1].
+    // The products of both blocks and of a pair of groups are interleaved:
+    // each depends on its own last one only.
     float x[kBlocks][NT][4];
+    {
+        constexpr int W = GS / 32;            // words per lane, row and group
+        constexpr int KP = NG == 1 ? 1 : 2;   // groups at a time
+        float u[kBlocks][NT][4], v[kBlocks][NT][4];
 #pragma unroll
-    for (int mb = 0; mb < kBlocks; ++mb) {
-        float s0[NG], s1[NG], b0[NG], b1[NG];
-        const int ra = 16 * mb + tg, rb = ra + 8;
-        load_groups<T, NG>(ksc + ra * NG * C::E, s0);
-        load_groups<T, NG>(ksc + rb * NG * C::E, s1);
-        load_groups<T, NG>(kbi + ra * NG * C::E, b0);
-        load_groups<T, NG>(kbi + rb * NG * C::E, b1);
-        float u[NT][4], v[NT][4];
+        for (int k0 = 0; k0 < NG; k0 += KP) {
+            uint32_t wd[kBlocks][2][KP][W];   // [block][row g | g + 8][group][word]
+            float acc[kBlocks][KP][NT][4];
 #pragma unroll
-        for (int k = 0; k < NG; ++k) {
-            constexpr int W = GS / 32;   // words per lane, row and group
-            uint32_t wa[W], wb[W];
-            const uint32_t* pa = reinterpret_cast<const uint32_t*>(st + ra * (D / 2) + k * (GS / 2)) + t * W;
-            const uint32_t* pb = reinterpret_cast<const uint32_t*>(st + rb * (D / 2) + k * (GS / 2)) + t * W;
-            if constexpr (W == 1) {
-                wa[0] = *pa;
-                wb[0] = *pb;
-            } else if constexpr (W == 2) {
-                const uint2 a = *reinterpret_cast<const uint2*>(pa), b = *reinterpret_cast<const uint2*>(pb);
-                wa[0] = a.x; wa[1] = a.y;
-                wb[0] = b.x; wb[1] = b.y;
-            } else {
-                const uint4 a = *reinterpret_cast<const uint4*>(pa), b = *reinterpret_cast<const uint4*>(pb);
-                wa[0] = a.x; wa[1] = a.y; wa[2] = a.z; wa[3] = a.w;
-                wb[0] = b.x; wb[1] = b.y; wb[2] = b.z; wb[3] = b.w;
-            }
-            float acc[NT][4];
+            for (int mb = 0; mb < kBlocks; ++mb)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int k = 0; k < KP; ++k) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t a = half ? wa[j] >> 8 : wa[j], b = half ? wb[j] >> 8 : wb[j];
-                    const uint32_t a0 = a & 0x000F000Fu, a2 = a & 0x00F000F0u;
-                    const uint32_t a1 = b & 0x000F000Fu, a3 = b & 0x00F000F0u;
-                    const int ks = 2 * (k * W + j) + half;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        mma16816(acc[n], a0, a1, a2, a3, Q.b[0][ks][n][0], Q.b[0][ks][n][1]);
-                        if constexpr (C::kSplit)
-                            mma16816(acc[n], a0, a1, a2, a3, Q.b[1][ks][n][0], Q.b[1][ks][n][1]);
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t* w = reinterpret_cast<const uint32_t*>(st + (16 * mb + 8 * e + tg) * (D / 2) +
+                                                                              (k0 + k) * (GS / 2)) + t * W;
+                        if constexpr (W == 1) {
+                            wd[mb][e][k][0] = *w;
+                        } else if constexpr (W == 2) {
+                            const uint2 y = *reinterpret_cast<const uint2*>(w);
+                            wd[mb][e][k][0] = y.x;
+                            wd[mb][e][k][1] = y.y;
+                        } else {
+                            const uint4 y = *reinterpret_cast<const uint4*>(w);
+                            wd[mb][e][k][0] = y.x;
+                            wd[mb][e][k][1] = y.y;
+                            wd[mb][e][k][2] = y.z;
+                            wd[mb][e][k][3] = y.w;
+                        }
                     }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[mb][k][n][e] = 0.f;
                 }
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int part = 0; part < (C::kSplit ? 2 : 1); ++part)
+#pragma unroll
+                        for (int k = 0; k < KP; ++k)
+#pragma unroll
+                            for (int mb = 0; mb < kBlocks; ++mb) {
+                                const uint32_t a = half ? wd[mb][0][k][j] >> 8 : wd[mb][0][k][j];
+                                const uint32_t b = half ? wd[mb][1][k][j] >> 8 : wd[mb][1][k][j];
+                                const int ks = 2 * ((k0 + k) * W + j) + half;
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+                                    mma16816(acc[mb][k][n], a & 0x000F000Fu, b & 0x000F000Fu, a & 0x00F000F0u,
+                                             b & 0x00F000F0u, Q.b[part][ks][n][0], Q.b[part][ks][n][1]);
+                            }
+#pragma unroll
+            for (int mb = 0; mb < kBlocks; ++mb) {
+                float sc[2][NG], bi[2][NG];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    load_groups<T, NG>(ksc + (16 * mb + 8 * e + tg) * NG * C::E, sc[e]);
+                    load_groups<T, NG>(kbi + (16 * mb + 8 * e + tg) * NG * C::E, bi[e]);
+                }
+#pragma unroll
+                for (int k = 0; k < KP; ++k)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float s = sc[e >> 1][k0 + k], b = bi[e >> 1][k0 + k], q = Q.sq[k0 + k][n][e & 1];
+                            u[mb][n][e] = k0 + k == 0 ? acc[mb][k][n][e] * s : fmaf(acc[mb][k][n][e], s, u[mb][n][e]);
+                            v[mb][n][e] = k0 + k == 0 ? b * q : fmaf(b, q, v[mb][n][e]);
+                        }
             }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float s = e < 2 ? s0[k] : s1[k], b = e < 2 ? b0[k] : b1[k];
-                    u[n][e] = k == 0 ? acc[n][e] * s : fmaf(acc[n][e], s, u[n][e]);
-                    v[n][e] = k == 0 ? b * Q.sq[k][n][e & 1] : fmaf(b, Q.sq[k][n][e & 1], v[n][e]);
-                }
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int mb = 0; mb < kBlocks; ++mb)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[mb][n][e] = fmaf(u[n][e], Q.f[n][e & 1], v[n][e]);
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[mb][n][e] = fmaf(u[mb][n][e], Q.f[n][e & 1], v[mb][n][e]);
     }
     // ---- masks: only on tiles that some row does not see in full
-    if (mask != ~0u || tok0 + kTile > L.hi_min || tok0 < L.lo_max) {
+    if (mask != ~0u || tok0 + kSub > L.hi_min || tok0 < L.lo_max) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -591,7 +621,7 @@ __device__ __forceinline__ void tile(const uint8_t* st, uint32_t mask, int tok0,
         }
     // whether R has to grow: the largest value scale of the tile
     float smax = 0.f;
-    static_assert(kTile == 32, "a lane per token");
+    static_assert(kSub == 32, "a lane per token");
     {
         float s[NG];
         load_groups<T, NG>(vsc + lane * NG * C::E, s);
@@ -705,8 +735,8 @@ __device__ __forceinline__ void join(Acc<C>& A, uint8_t* buf, F&& write) {
     constexpr int NT = C::NT, NC = C::NC, D = C::D, DP = C::DP;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float* o = reinterpret_cast<float*>(buf);
-    float* sm = o + kWarps * NC * DP;
-    float* sl = sm + kWarps * NC;
+    float* sm = o + C::kWarps * NC * DP;
+    float* sl = sm + C::kWarps * NC;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -718,7 +748,7 @@ __device__ __forceinline__ void join(Acc<C>& A, uint8_t* buf, F&& write) {
                 for (int k = 0; k < C::NG; ++k) A.ab[k][n][c] += __shfl_xor_sync(0xffffffffu, A.ab[k][n][c], s);
             }
         }
-    consumer_sync();   // the previous unit's readers are done
+    consumer_sync<C::kWarps>();   // the previous unit's readers are done
     const float R = __uint_as_float((uint32_t)A.re << 23);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -755,16 +785,16 @@ __device__ __forceinline__ void join(Acc<C>& A, uint8_t* buf, F&& write) {
                     }
             }
         }
-    consumer_sync();
-    for (int i = threadIdx.x; i < NC * D / 4; i += 32 * kWarps) {
+    consumer_sync<C::kWarps>();
+    for (int i = threadIdx.x; i < NC * D / 4; i += 32 * C::kWarps) {
         const int col = i / (D / 4), d = (i % (D / 4)) * 4;
         float m = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sm[w * NC + col]);
+        for (int w = 0; w < C::kWarps; ++w) m = fmaxf(m, sm[w * NC + col]);
         float l = 0.f;
         float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < C::kWarps; ++w) {
             const float mw = sm[w * NC + col];
             if (mw != -INFINITY) {   // (a warp that saw nothing adds nothing)
                 const float e = ex2(mw - m);
@@ -805,11 +835,11 @@ __device__ __forceinline__ void store_out(const KvAttnLaunch& p, bool vec, long 
 }
 
 template <class C>
-__global__ void __launch_bounds__(kThreads, C::kCtas)
+__global__ void __launch_bounds__(C::kThreads, C::kCtas)
     kv_attention_kernel(const __grid_constant__ KvAttnLaunch p, const int vec_q, const int vec_out) {
     using T = typename C::T;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long warp_cost[kWarps + 1];
+    __shared__ long long warp_cost[C::kWarps + 1];
     __shared__ long long start_off;
     __shared__ int start_r, abort_flag;
     constexpr int S = C::kStages;
@@ -823,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], 2);   // one warp for each half
         }
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -833,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
 
     // the line of tiles: its length, and where this CTA's part begins. Each
     // thread sums a strip of requests.
-    const int per_thread = (p.batch + kThreads - 1) / kThreads;
+    const int per_thread = (p.batch + C::kThreads - 1) / C::kThreads;
     const int r0 = min(tid * per_thread, p.batch), r1 = min(r0 + per_thread, p.batch);
     auto cost = [&](int r) {
         const Req q = request(p, r);
@@ -851,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
     __syncthreads();
     long long total = 0, before = inc - mine;
 #pragma unroll
-    for (int i = 0; i <= kWarps; ++i) {
+    for (int i = 0; i <= C::kWarps; ++i) {
         if (i < warp) before += warp_cost[i];
         total += warp_cost[i];
     }
@@ -870,9 +900,9 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         const long long first = max(min((long long)p.cu_q[p.batch], (long long)p.num_tokens), 0ll);
         for (long long row = first + blockIdx.x; row < p.num_tokens; row += gridDim.x) {
             auto* o = static_cast<typename T::storage*>(p.out) + row * p.out_stride;
-            for (int i = tid; i < hq * C::D; i += kThreads) o[i] = T::from_f32(0.f);
+            for (int i = tid; i < hq * C::D; i += C::kThreads) o[i] = T::from_f32(0.f);
             if (p.lse)
-                for (int i = tid; i < hq; i += kThreads) p.lse[row * hq + i] = -INFINITY;
+                for (int i = tid; i < hq; i += C::kThreads) p.lse[row * hq + i] = -INFINITY;
         }
     }
     uint8_t* ws = static_cast<uint8_t*>(p.workspace);
@@ -886,13 +916,13 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
 
     Walk<C::NC> w(p, lane, start_r, start_off, c0, c1);
     const Ctl ctl{p.status, p.spin_limit, &abort_flag};
-    if (warp == kWarps) {
+    if (warp == C::kWarps) {
         producer<C>(p, w, ring, full, empty, masks, ctl);
         return;
     }
     // ---- consumers
-    int seq = 0;                              // first tile of the current segment
-    int my = warp, slot = warp, phase = 0;    // this warp's next tile: every kWarps-th
+    int seq = 0;                                   // first sub-tile of the current segment (two to a stage)
+    int my = warp, slot = warp >> 1, phase = 0;    // this warp's next sub-tile: every kWarps-th, and its stage's slot
     bool cut = false;    // this CTA holds the beginning of a unit that goes on
     while (w.more()) {
         if (w.idle()) {
@@ -907,32 +937,35 @@ __global__ void __launch_bounds__(kThreads, C::kCtas)
         const Limits L = limits<C>(p, w.q, rb);
         Acc<C> A;
         clear<C>(A);
-        const int tiles = max(b - a, 0);
-        for (; my < seq + tiles; my += kWarps) {
-            const int t = a + (my - seq);
+        const int subs = 2 * max(b - a, 0);
+        for (; my < seq + subs; my += C::kWarps) {
+            const int sub = my & 1, tok0 = (w.q.tile0 + a) * kTile + (my - seq) * kSub;
             // after a time-out the outputs are undefined, but every role still ends
             (void)warp_wait(&full[slot], (uint32_t)phase, ctl);
             uint8_t* st = ring + (size_t)slot * C::kStage;
-            const uint32_t mask = masks[slot];
-            if (mask != ~0u) {
-                // scales and biases of slots without a token may hold anything
-                if (!((mask >> lane) & 1))
-                    for (int k = 0; k < 4; ++k)
-                        for (int i = 0; i < C::NG * C::E / 2; ++i)
-                            reinterpret_cast<uint16_t*>(st + 2 * C::kCodes + k * C::kSb)[lane * (C::NG * C::E / 2) + i] = 0;
-                __syncwarp();
+            const uint32_t mask = masks[2 * slot + sub];
+            if (mask != 0) {
+                if (mask != ~0u) {
+                    // scales and biases of slots without a token may hold anything
+                    if (!((mask >> lane) & 1))
+                        for (int k = 0; k < 4; ++k)
+                            for (int i = 0; i < C::NG * C::E / 2; ++i)
+                                reinterpret_cast<uint16_t*>(st + 2 * C::kCodes + k * C::kSb)[(sub * kSub + lane) * (C::NG * C::E / 2) + i] = 0;
+                    __syncwarp();
+                }
+                tile<C>(st, sub, mask, tok0, Q, p, w.q, L, A);
+                if (mask != ~0u) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
-            tile<C>(st, mask, (w.q.tile0 + t) * kTile, Q, p, w.q, L, A);
-            if (mask != ~0u) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[slot]);
-            slot += kWarps;
+            const int next = (my + C::kWarps) >> 1;
+            slot += next - (my >> 1);
             if (slot >= S) {
                 slot -= S;
                 phase ^= 1;
             }
         }
-        seq += tiles;
+        seq += subs;
         const bool begins = w.begins(), ends = w.ends();
         const long long rows = (long long)w.q.qn * p.group;
         float* rec = recs + (begins ? rec_floats(C::NC, C::D) : 0);
@@ -1036,7 +1069,7 @@ cudaError_t launch(const KvAttnLaunch& L, cudaStream_t s) {
     static bool allowed[64];
     cudaError_t err = allow_smem_once(kv_attention_kernel<C>, C::kSmem, allowed);
     if (err != cudaSuccess) return err;
-    err = launch_pdl(kv_attention_kernel<C>, dim3(ctas), dim3(kThreads), C::kSmem, s, L, vec_q, vec_out);
+    err = launch_pdl(kv_attention_kernel<C>, dim3(ctas), dim3(C::kThreads), C::kSmem, s, L, vec_q, vec_out);
     if (err != cudaSuccess) return err;
     return launch_pdl(kv_combine_kernel<C>, dim3(ctas, C::NC), dim3(128), 0, s, L, ctas, vec_out);
 }
