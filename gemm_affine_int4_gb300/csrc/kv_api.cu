@@ -142,6 +142,7 @@ gai4_status gai4_kv_attention(const void* q, int64_t q_token_stride, const uint3
     L.k = KvCache{k_packed, k_scales, k_biases};
     L.v = KvCache{v_packed, v_scales, v_biases};
     if ((st = check_cache(L.k)) != GAI4_OK || (st = check_cache(L.v)) != GAI4_OK) return st;
+    if (num_tokens * (q_heads / kv_heads) > 0x7fffffff) return GAI4_ERR_UNSUPPORTED;   // 32-bit row numbers
     if (num_tokens == 0) return GAI4_OK;
     if (!q || !out || !block_table || !kv_lens || !cu_q) return GAI4_ERR_INVALID_ARG;
     if (q_token_stride < q_heads * head_dim || out_token_stride < q_heads * head_dim) return GAI4_ERR_INVALID_ARG;

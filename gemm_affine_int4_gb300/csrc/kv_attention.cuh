@@ -112,9 +112,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
 }
-template <int WARPS>
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory"); }
-
 // token of row r (0..7) of a product's 8-row block: the P operand's rows 2t
 // and 2t + 1 are tokens t and t + 4, so that neighbouring lanes of the value
 // loads read neighbouring tokens
@@ -163,169 +160,189 @@ __device__ __forceinline__ Req request(const KvAttnLaunch& p, int r) {
     return q;
 }
 __device__ __forceinline__ int row_blocks(const KvAttnLaunch& p, const Req& q, int nc) {
-    return (int)(((long long)q.qn * p.group + nc - 1) / nc);
+    return (q.qn * p.group + nc - 1) / nc;   // (num_tokens * group is below 2^31)
 }
 
-// A warp's walk along the line of tiles: the requests' sizes are held by the
-// lanes, 32 at a time. Each unit begins with kStart places without work, which
-// stand for its query load and join, so that CTAs with many short units get
-// fewer tiles; a unit belongs to the CTA that has its first tile's place.
+// what the rows of a unit may see
+struct Limits {
+    int rows;             // rows of the unit, at most NC
+    int first;            // index of row 0 among the request's tokens x heads, modulo the heads
+    int i0;               // token of row 0
+    int lo_max, hi_min;   // keys in [lo_max, hi_min) are seen by every row of the unit
+};
+
+__device__ __forceinline__ int lowest_key(const KvAttnLaunch& p, long long pos) {
+    return p.window > 0 ? (int)max(pos - p.window + 1, 0ll) : 0;
+}
+
+// A warp's walk along the line of tiles. Each unit begins with kStart places
+// without work, which stand for its query load and join, so that CTAs with
+// many short units get fewer tiles; a unit belongs to the CTA that has its
+// first tile's place. Kept in shared memory (every lane writes the same): it
+// is needed between segments, and the consumers have no registers to spare.
 template <int NC>
 struct Walk {
-    const KvAttnLaunch& p;
-    int base, lane;
-    Req mine;
     long long c, c1;
-    int r, unit, place;   // current request, unit within it, place within the unit (tile + kStart)
+    int r, h, rb, nrb, place;   // request, head, row block (of nrb), place within the unit (tile + kStart)
     Req q;
-    int nrb, units;
+    int a, b;                   // tiles of the segment that some row of the unit can see
+    Limits L;
 
-    __device__ Walk(const KvAttnLaunch& p_, int lane_, int r0, long long off, long long c0, long long c1_)
-        : p(p_), base(-1), lane(lane_), c(c0), c1(c1_), r(r0) {
-        load();
-        unit = (int)(off / (q.ntile + kStart));
-        place = (int)(off - (long long)unit * (q.ntile + kStart));
-    }
-    __device__ void load() {
-        if (base < 0 || r - base >= 32) {
-            base = r;
-            mine = Req{0, 0, 0, 0, 1};
-            if (r + lane < p.batch) mine = request(p, r + lane);
-        }
-        const int s = r - base;
-        q.q0 = __shfl_sync(0xffffffffu, mine.q0, s);
-        q.qn = __shfl_sync(0xffffffffu, mine.qn, s);
-        q.kv = __shfl_sync(0xffffffffu, mine.kv, s);
-        q.tile0 = __shfl_sync(0xffffffffu, mine.tile0, s);
-        q.ntile = __shfl_sync(0xffffffffu, mine.ntile, s);
+    __device__ void init(const KvAttnLaunch& p, int r0, long long off, long long c0, long long c1_) {
+        c = c0;
+        c1 = c1_;
+        r = r0;
+        q = request(p, r);
         nrb = row_blocks(p, q, NC);
-        units = nrb * p.sh.hkv;
+        const int unit = (int)(off / (q.ntile + kStart));
+        place = (int)(off - (long long)unit * (q.ntile + kStart));
+        h = unit / nrb;
+        rb = unit - h * nrb;
+        settle(p);
     }
     __device__ bool more() const { return c < c1; }
     __device__ int here() const { return (int)min((long long)(q.ntile + kStart - place), c1 - c); }   // places of this segment
-    __device__ bool idle() const { return place + here() <= kStart; }    // no tile among them
     __device__ bool begins() const { return place <= kStart; }
     __device__ bool ends() const { return place + here() == q.ntile + kStart; }
-    __device__ int head() const { return unit / nrb; }
-    __device__ int block() const { return unit % nrb; }
-    // tiles [a, b) of the segment that some row of the unit can see
-    __device__ void clip(int& a, int& b) const {
-        const int rb = block();
-        const int i0 = (int)((long long)rb * NC / p.group);
-        const int i1 = min((int)(((long long)rb * NC + NC - 1) / p.group), q.qn - 1);
-        const long long end = (long long)q.kv - q.qn + i1 + 1;      // keys below it
-        const long long lo = p.window > 0 ? max((long long)q.kv - q.qn + i0 - p.window + 1, 0ll) : 0;
-        a = max(max(place - kStart, 0), (int)(lo / kTile) - q.tile0);
-        b = min(place - kStart + here(), (int)((max(end, 0ll) + kTile - 1) / kTile) - q.tile0);
-    }
-    __device__ void advance() {
+    __device__ void step(const KvAttnLaunch& p) {
         const int n = here();
         c += n;
         place += n;
-        if (place == q.ntile + kStart) {
-            place = 0;
-            if (++unit == units) {
-                unit = 0;
-                if (c < c1) {
-                    do {
-                        ++r;
-                        load();
-                    } while (units == 0 && r + 1 < p.batch);
-                }
-            }
-        }
+        if (place < q.ntile + kStart) return;
+        place = 0;
+        if (++rb < nrb) return;
+        rb = 0;
+        if (++h < p.sh.hkv || c >= c1) return;
+        h = 0;
+        do {
+            q = request(p, ++r);
+            nrb = row_blocks(p, q, NC);
+        } while (nrb == 0);   // (c < c1: there is another unit)
+    }
+    // on to a segment with a tile's place (or the end), and its limits
+    __device__ void settle(const KvAttnLaunch& p) {
+        while (more() && place + here() <= kStart) step(p);
+        if (!more()) return;
+        const int rr0 = rb * NC;
+        L.rows = min(NC, q.qn * p.group - rr0);
+        L.i0 = rr0 / p.group;
+        L.first = rr0 - L.i0 * p.group;
+        const long long pos0 = (long long)q.kv - q.qn + L.i0, pos1 = pos0 + (L.first + L.rows - 1) / p.group;
+        L.hi_min = (int)max(pos0 + 1, 0ll);
+        L.lo_max = lowest_key(p, pos1);
+        a = max(max(place - kStart, 0), lowest_key(p, pos0) / kTile - q.tile0);
+        b = max(a, min(place - kStart + here(), (int)((max(pos1 + 1, 0ll) + kTile - 1) / kTile) - q.tile0));
+    }
+    __device__ void advance(const KvAttnLaunch& p) {
+        __syncwarp();   // every lane has read what it needs
+        Walk w = *this;
+        w.step(p);
+        w.settle(p);
+        __syncwarp();
+        *this = w;
+        __syncwarp();
     }
 };
 
-// The producer: six copies (codes, scales, biases of keys and values) for each
-// page of a stage, one per lane, two stages at a time with pages of 32 tokens
-// or more. (One 32-token tile at a time its chain of waits and votes, about
-// 1200 cycles, set the pace of the whole kernel; and the copies of scales and
-// biases, 256 bytes each here, cost as much as their number: with 128-byte
-// ones 4 x 131072 tokens took 127 us, without them 101.)
+// The producer, two stages at a time (its chain of waits and votes costs about
+// a thousand cycles beside busy consumers: with one stage at a time it set the
+// pace). Of each stage the codes come by bulk copies, one for each page and
+// side, issued by one lane each; scales and biases, a ninth of the bytes, by
+// 16-byte asynchronous copies of the whole warp: bulk copies take a lane's
+// issue each, and with small pages there would be up to 24 of them.
 template <class C>
 __device__ __forceinline__ void producer(const KvAttnLaunch& p, Walk<C::NC>& w, uint8_t* ring, uint64_t* full,
                                          uint64_t* empty, uint32_t* masks, const Ctl& ctl) {
     constexpr int S = C::kStages;
+    constexpr int kRow = C::NG * C::E;                      // bytes of a token's scales (or biases)
+    constexpr int kPer = C::kSb / 16;                       // 16-byte chunks of each of the four arrays
+    constexpr int kCopies = 4 * kPer / 32;                  // of them for each lane
     const int lane = threadIdx.x & 31;
-    const int pl = p.sh.page_log2;
+    const int pl = p.sh.page_log2, in_page = (1 << pl) - 1;
     const int pp = pl >= 6 ? 0 : 6 - pl;                    // log2 of the pages of a stage
-    const int tokens = kTile >> pp;                         // tokens of a piece
-    const int batch = pp == 2 ? 1 : 2;                      // stages at a time
-    const int item = lane / 6, which = lane - 6 * item;     // this lane's piece and array
-    const int tl = item >> pp, piece = item & ((1 << pp) - 1);
-    const bool active = tl < batch;
-    const bool leader = which == 0 && piece == 0;
-    const uint32_t row_bytes = which < 2 ? C::D / 2 : C::NG * C::E;
-    const uint32_t bytes = (uint32_t)tokens * row_bytes;
-    const uint8_t* src0 = static_cast<const uint8_t*>(
-        which == 0   ? static_cast<const void*>(p.k.packed)
-        : which == 1 ? static_cast<const void*>(p.v.packed)
-        : which == 2 ? p.k.scales
-        : which == 3 ? p.k.biases
-        : which == 4 ? p.v.scales
-                     : p.v.biases);
-    const uint32_t dst0 = smem_u32(ring) + (which < 2 ? which * C::kCodes : 2 * C::kCodes + (which - 2) * C::kSb) + piece * bytes;
-    const int in_page = (1 << pl) - 1;
-    int seq = 0;                  // stages issued
-    int slot = tl, phase = 1;     // of this lane's stage; parity of its "empty" wait
+    const int tokens = kTile >> pp;                         // tokens of a page in it
+    const int pieces = 1 << pp;
+    // bulk copies: lane = page + pieces * (side + 2 * stage of the two)
+    const int piece = lane & (pieces - 1), side = (lane >> pp) & 1, j = lane >> (pp + 1);
+    const bool leader = (lane & (2 * pieces - 1)) == 0;
+    const uint32_t code_bytes = (uint32_t)tokens * (C::D / 2);
+    const uint8_t* codes = reinterpret_cast<const uint8_t*>(side == 0 ? p.k.packed : p.v.packed);
+    const uint32_t ring_s = smem_u32(ring);
+    const uint32_t code_dst = ring_s + side * C::kCodes + piece * code_bytes;
+    // 16-byte copies: chunk lane + 32 i of the arrays laid end to end
+    const uint8_t* sb_src[kCopies];
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+        const int idx = lane + 32 * i, array = idx / kPer, chunk = idx % kPer, pc = chunk * 16 / kRow / tokens;
+        const void* base = array == 0 ? p.k.scales : array == 1 ? p.k.biases : array == 2 ? p.v.scales : p.v.biases;
+        sb_src[i] = static_cast<const uint8_t*>(base) + (chunk * 16 - pc * tokens * kRow);
+    }
+    const uint32_t sb_dst = ring_s + 2 * C::kCodes + lane * 16;
+    int slot = 0, issued = 0;       // next stage's slot, stages issued
+    uint32_t phase = 1;             // parity of the slot's "empty" wait
     bool ok = true;
-    while (w.more() && ok) {
-        if (w.idle()) {
-            w.advance();
-            continue;
-        }
-        int a, b;
-        w.clip(a, b);
-        const int h = w.head();
+    for (; w.more() && ok; w.advance(p)) {
+        const int a = w.a, b = w.b, h = w.h, kv_len = w.q.kv;
         const int* row = p.table + (long long)w.r * p.max_blocks;
-        const int nblk = (w.q.kv + in_page) >> pl;
-        int tok = (w.q.tile0 + a + tl) * kTile + piece * tokens;     // first token of this lane's piece
-        int page = active && (tok >> pl) < nblk ? row[tok >> pl] : -1;
-        for (int t = a; t < b; t += batch) {
-            const int n = min(batch, b - t);
-            const bool live = active && tl < n;
+        const int nblk = (kv_len + in_page) >> pl;
+        int tok0 = (w.q.tile0 + a + j) * kTile;             // first token of this lane's stage
+        int at = (tok0 + piece * tokens) >> pl;
+        int page = j < 2 && a + j < b && at < nblk ? row[at] : -1;
+        for (int t = a; t < b; t += 2, tok0 += 2 * kTile) {
+            const int n = min(2, b - t);
+            const bool live = j < n;
             const bool there = live && page >= 0 && page < p.sh.num_blocks;
-            const int now = page, tok_next = tok + batch * kTile;
-            page = active && (tok_next >> pl) < nblk ? row[tok_next >> pl] : -1;    // for the next turn
-            bool mine = true;
-            if (live) mine = mbar_wait(&empty[slot], (uint32_t)phase, ctl);
             const uint32_t votes = __ballot_sync(0xffffffffu, there);
+            const int off = (tok0 + piece * tokens) & in_page;
+            const long long line = there ? (((long long)page * p.sh.hkv + h) << pl) + off : 0;   // first row
+            at = (tok0 + 2 * kTile + piece * tokens) >> pl;
+            page = j < 2 && t + 2 + j < b && at < nblk ? row[at] : -1;   // for the next turn
+            int my_slot = slot + j;
+            const bool wrapped = my_slot >= S;
+            if (wrapped) my_slot -= S;
+            bool mine = true;
+            if (live) mine = mbar_wait(&empty[my_slot], wrapped ? phase ^ 1u : phase, ctl);
             if (!__all_sync(0xffffffffu, mine)) {
                 ok = false;
                 break;
             }
             if (live && leader) {
+                const uint32_t got = (votes >> lane) & ((1u << pieces) - 1u);
                 unsigned long long m = 0;
-                uint32_t pages = 0;
-                for (int i = 0; i < 1 << pp; ++i)
-                    if ((votes >> (lane + 6 * i)) & 1u) {
-                        m |= (pp == 0 ? ~0ull : (1ull << tokens) - 1) << (i * tokens);
-                        ++pages;
-                    }
-                const int left = w.q.kv - tok;
+                for (int i = 0; i < pieces; ++i)
+                    if ((got >> i) & 1u) m |= (pp == 0 ? ~0ull : (1ull << tokens) - 1) << (i * tokens);
+                const int left = kv_len - tok0;
                 if (left < 64) m &= left <= 0 ? 0ull : (1ull << left) - 1;
-                masks[2 * slot] = (uint32_t)m;
-                masks[2 * slot + 1] = (uint32_t)(m >> 32);
-                mbar_arrive_expect_tx(&full[slot], pages * (uint32_t)tokens * (C::D + 4 * C::NG * C::E));
+                masks[2 * my_slot] = (uint32_t)m;
+                masks[2 * my_slot + 1] = (uint32_t)(m >> 32);
+                mbar_arrive_expect_tx(&full[my_slot], __popc(got) * 2u * code_bytes);
             }
             __syncwarp();
-            if (there) {
-                const long long line = (((long long)now * p.sh.hkv + h) << pl) + (tok & in_page);
-                bulk_load(dst0 + (uint32_t)slot * C::kStage, src0 + line * row_bytes, bytes, &full[slot]);
+            if (there) bulk_load(code_dst + (uint32_t)my_slot * C::kStage, codes + line * (C::D / 2), code_bytes, &full[my_slot]);
+            __syncwarp();
+            for (int k = 0; k < n; ++k) {
+                const uint32_t dst = sb_dst + (uint32_t)slot * C::kStage;
+                const int first = k * 2 * pieces;           // lane of the stage's first page
+#pragma unroll
+                for (int i = 0; i < kCopies; ++i) {
+                    const int pc = (lane + 32 * i) % kPer * 16 / kRow / tokens;
+                    const long long ln = __shfl_sync(0xffffffffu, line, first + pc);
+                    if ((votes >> (first + pc)) & 1u)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 512 * i), "l"(sb_src[i] + ln * kRow)
+                                     : "memory");
+                }
+                // this lane's copies count as its arrival once they have landed
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full[slot])) : "memory");
+                if (++slot == S) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
             }
-            seq += n;
-            tok = tok_next;
-            slot += n;
-            if (slot >= S) {
-                slot -= S;
-                phase ^= 1;
-            }
+            issued += n;
         }
-        w.advance();
     }
     // no copy may land after the CTA has gone
-    for (int i = seq > S ? seq - S : 0; i < seq; ++i) mbar_wait_drain(&full[i % S], (i / S) & 1, ctl.limit, ctl.status);
+    for (int i = issued > S ? issued - S : 0; i < issued; ++i) mbar_wait_drain(&full[i % S], (i / S) & 1, ctl.limit, ctl.status);
 }
 
 // per-warp running state of a unit
@@ -365,39 +382,55 @@ struct Query {
     float sq[C::NG][C::NT][2];    // log2(e) scale * sum of the group's elements
 };
 
-template <typename T>
-__device__ __forceinline__ void load_q8(const typename T::storage* s, bool vec, float (&x)[8]) {
-    if (!vec) {
+// A unit's query elements as they come: word k (GS / 32) + j of the lane holds
+// channels 8 (k (GS / 8) + t (GS / 32) + j) on
+template <class C>
+struct RawQuery {
+    uint4 w[C::NT][C::D / 32][C::E / 2];
+};
+
+template <class C>
+__device__ __forceinline__ void fetch_query(const KvAttnLaunch& p, const Req& rq, int h, int rb, bool vec, RawQuery<C>& R) {
+    using St = typename C::T::storage;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = T::to_f32(s[i]);
-    } else if constexpr (T::kBytes == 4) {
-        const float4 a = reinterpret_cast<const float4*>(s)[0], b = reinterpret_cast<const float4*>(s)[1];
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    } else {
-        const uint4 a = *reinterpret_cast<const uint4*>(s);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    for (int n = 0; n < C::NT; ++n) {
+        const int rr = rb * C::NC + n * 8 + g;
+        const bool valid = rr < rq.qn * p.group;
+        const int i = valid ? rr / p.group : 0;
+        const int head = h * p.group + (valid ? rr - i * p.group : 0);
+        const St* src = static_cast<const St*>(p.q) + (rq.q0 + i) * p.q_stride + (long long)head * C::D;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = T::to_f32((uint16_t)w[i]);
-            x[2 * i + 1] = T::to_f32((uint16_t)(w[i] >> 16));
-        }
+        for (int k = 0; k < C::NG; ++k)
+#pragma unroll
+            for (int j = 0; j < C::GS / 32; ++j) {
+                uint4(&y)[C::E / 2] = R.w[n][k * (C::GS / 32) + j];
+                const St* s = src + 8 * (k * (C::GS / 8) + t * (C::GS / 32) + j);
+#pragma unroll
+                for (int e = 0; e < C::E / 2; ++e) {
+                    y[e] = make_uint4(0u, 0u, 0u, 0u);
+                    if (valid && vec) {
+                        y[e] = reinterpret_cast<const uint4*>(s)[e];
+                    } else if (valid) {
+                        uint32_t z[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if constexpr (C::E == 4) z[x] = __float_as_uint(s[4 * e + x]);
+                            else z[x] = (uint32_t)s[2 * x] | ((uint32_t)s[2 * x + 1] << 16);
+                        y[e] = make_uint4(z[0], z[1], z[2], z[3]);
+                    }
+                }
+            }
     }
 }
 
 template <class C>
-__device__ __forceinline__ void load_query(const KvAttnLaunch& p, const Req& rq, int h, int rb, bool vec, Query<C>& Q) {
+__device__ __forceinline__ void make_query(const KvAttnLaunch& p, const RawQuery<C>& R, Query<C>& Q) {
     using T = typename C::T;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int lane = threadIdx.x & 31, t = lane & 3;
     const float sl = p.scale * 1.4426950408889634f;
 #pragma unroll
     for (int n = 0; n < C::NT; ++n) {
-        const long long rr = (long long)rb * C::NC + n * 8 + g;
-        const bool valid = rr < (long long)rq.qn * p.group;
-        const int i = valid ? (int)(rr / p.group) : 0;
-        const int head = h * p.group + (valid ? (int)(rr - (long long)i * p.group) : 0);
-        const typename T::storage* src =
-            static_cast<const typename T::storage*>(p.q) + (rq.q0 + i) * p.q_stride + (long long)head * C::D;
         float x[C::D / 32][8];
         float amax = 0.f, sum[C::NG];
 #pragma unroll
@@ -407,11 +440,18 @@ __device__ __forceinline__ void load_query(const KvAttnLaunch& p, const Req& rq,
             for (int j = 0; j < C::GS / 32; ++j) {
                 const int wi = k * (C::GS / 32) + j;
                 float(&y)[8] = x[wi];
-                if (valid) {
-                    load_q8<T>(src + 8 * (k * (C::GS / 8) + t * (C::GS / 32) + j), vec, y);
-                } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = 0.f;
+                for (int e = 0; e < C::E / 2; ++e) {
+                    const uint4 r = R.w[n][wi][e];
+                    const uint32_t z[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if constexpr (C::E == 4) {
+                            y[4 * e + i] = __uint_as_float(z[i]);
+                        } else {
+                            y[2 * i] = T::to_f32((uint16_t)z[i]);
+                            y[2 * i + 1] = T::to_f32((uint16_t)(z[i] >> 16));
+                        }
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -464,33 +504,9 @@ __device__ __forceinline__ void load_query(const KvAttnLaunch& p, const Req& rq,
 }
 
 // what columns 2t and 2t + 1 of each 8-column block may see: keys [lo, hi)
-struct Limits {
-    int rows;             // rows of the unit, at most NC
-    int first;            // index of row 0 among the request's tokens x heads, modulo the heads
-    int i0;               // token of row 0
-    int lo_max, hi_min;   // keys in [lo_max, hi_min) are seen by every row of the unit
-};
-
-__device__ __forceinline__ int lowest_key(const KvAttnLaunch& p, long long pos) {
-    return p.window > 0 ? (int)max(pos - p.window + 1, 0ll) : 0;
-}
-
-template <class C>
-__device__ __forceinline__ Limits limits(const KvAttnLaunch& p, const Req& rq, int rb) {
-    Limits L;
-    const long long rr0 = (long long)rb * C::NC;
-    L.rows = (int)min((long long)C::NC, (long long)rq.qn * p.group - rr0);
-    L.i0 = (int)(rr0 / p.group);
-    L.first = (int)(rr0 - (long long)L.i0 * p.group);
-    const long long pos0 = (long long)rq.kv - rq.qn + L.i0;
-    L.hi_min = (int)max(pos0 + 1, 0ll);
-    L.lo_max = lowest_key(p, pos0 + (L.first + L.rows - 1) / p.group);
-    return L;
-}
-
 template <class C>
 __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mask, int tok0, const Query<C>& Q,
-                                     const KvAttnLaunch& p, const Req& rq, const Limits& L, Acc<C>& A) {
+                                     const KvAttnLaunch& p, const Walk<C::NC>& w, int lo_max, int hi_min, Acc<C>& A) {
     using T = typename C::T;
     constexpr int NT = C::NT, NG = C::NG, D = C::D, GS = C::GS;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -586,14 +602,14 @@ __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mas
                 for (int e = 0; e < 4; ++e) x[mb][n][e] = fmaf(u[mb][n][e], Q.f[n][e & 1], v[mb][n][e]);
     }
     // ---- masks: only on tiles that some row does not see in full
-    if (mask != ~0u || tok0 + kSub > L.hi_min || tok0 < L.lo_max) {
+    if (mask != ~0u || tok0 + kSub > hi_min || tok0 < lo_max) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int col = n * 8 + 2 * t + c;
-                const long long pos = (long long)rq.kv - rq.qn + L.i0 + (L.first + col) / p.group;
-                const int hi = col < L.rows ? (int)max(pos + 1, 0ll) : 0, lo = lowest_key(p, pos);
+                const long long pos = (long long)w.q.kv - w.q.qn + w.L.i0 + (w.L.first + col) / p.group;
+                const int hi = col < w.L.rows ? (int)max(pos + 1, 0ll) : 0, lo = lowest_key(p, pos);
 #pragma unroll
                 for (int mb = 0; mb < kBlocks; ++mb)
 #pragma unroll
@@ -728,10 +744,9 @@ __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mas
     }
 }
 
-// joins the warps' results of a segment; thread i then owns four channels of
-// some columns and calls write(column, channel, float4 O, m, l) with O not yet divided by l
-template <class C, typename F>
-__device__ __forceinline__ void join(Acc<C>& A, uint8_t* buf, F&& write) {
+// a warp's results of a segment into its place of the join buffer
+template <class C>
+__device__ __forceinline__ void deposit(Acc<C>& A, uint8_t* buf) {
     constexpr int NT = C::NT, NC = C::NC, D = C::D, DP = C::DP;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float* o = reinterpret_cast<float*>(buf);
@@ -748,7 +763,6 @@ __device__ __forceinline__ void join(Acc<C>& A, uint8_t* buf, F&& write) {
                 for (int k = 0; k < C::NG; ++k) A.ab[k][n][c] += __shfl_xor_sync(0xffffffffu, A.ab[k][n][c], s);
             }
         }
-    consumer_sync<C::kWarps>();   // the previous unit's readers are done
     const float R = __uint_as_float((uint32_t)A.re << 23);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -785,8 +799,24 @@ __device__ __forceinline__ void join(Acc<C>& A, uint8_t* buf, F&& write) {
                     }
             }
         }
-    consumer_sync<C::kWarps>();
-    for (int i = threadIdx.x; i < NC * D / 4; i += 32 * C::kWarps) {
+}
+// one that had no sub-tile of the segment
+template <class C>
+__device__ __forceinline__ void deposit_nothing(uint8_t* buf) {
+    float* sm = reinterpret_cast<float*>(buf) + C::kWarps * C::NC * C::DP;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane < C::NC) sm[warp * C::NC + lane] = -INFINITY;
+}
+
+// joins what the warps have deposited, by one warp: each lane four channels of
+// a column, write(column, channel, float4 O, m, l) with O not yet divided by l
+template <class C, typename F>
+__device__ __forceinline__ void join(const uint8_t* buf, int columns, F&& write) {
+    constexpr int NC = C::NC, D = C::D, DP = C::DP;
+    const float* o = reinterpret_cast<const float*>(buf);
+    const float* sm = o + C::kWarps * NC * DP;
+    const float* sl = sm + C::kWarps * NC;
+    for (int i = threadIdx.x & 31; i < columns * (D / 4); i += 32) {
         const int col = i / (D / 4), d = (i % (D / 4)) * 4;
         float m = -INFINITY;
 #pragma unroll
@@ -848,11 +878,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     uint64_t* full = reinterpret_cast<uint64_t*>(buf + C::kJoin);
     uint64_t* empty = full + S;
     uint32_t* masks = reinterpret_cast<uint32_t*>(empty + S);
+    uint64_t *deposited = reinterpret_cast<uint64_t*>(masks + 2 * S), *joined = deposited + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
     if (tid == 0) {
+        mbar_init(deposited, C::kWarps);
+        mbar_init(joined, 1);
         for (int i = 0; i < S; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], 33);   // the codes' copies, and each lane's of scales and biases
             mbar_init(&empty[i], 2);   // one warp for each half
         }
         abort_flag = 0;
@@ -914,85 +947,104 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         return;
     }
 
-    Walk<C::NC> w(p, lane, start_r, start_off, c0, c1);
+    __shared__ Walk<C::NC> walks[C::kWarps + 1];
+    Walk<C::NC>& w = walks[warp];
+    {
+        Walk<C::NC> first;
+        first.init(p, start_r, start_off, c0, c1);
+        w = first;
+        __syncwarp();
+    }
     const Ctl ctl{p.status, p.spin_limit, &abort_flag};
     if (warp == C::kWarps) {
         producer<C>(p, w, ring, full, empty, masks, ctl);
         return;
     }
-    // ---- consumers
+    // ---- consumers. Each warp deposits its part of a segment and goes on; the
+    // warps take turns at joining. (With a barrier of all warps instead, every
+    // segment cost the time that the slowest warp was behind.)
     int seq = 0;                                   // first sub-tile of the current segment (two to a stage)
     int my = warp, slot = warp >> 1, phase = 0;    // this warp's next sub-tile: every kWarps-th, and its stage's slot
-    bool cut = false;    // this CTA holds the beginning of a unit that goes on
-    while (w.more()) {
-        if (w.idle()) {
-            w.advance();
-            continue;
-        }
-        int a, b;
-        w.clip(a, b);
-        const int h = w.head(), rb = w.block();
-        Query<C> Q;
-        load_query<C>(p, w.q, h, rb, vec_q != 0, Q);
-        const Limits L = limits<C>(p, w.q, rb);
-        Acc<C> A;
-        clear<C>(A);
-        const int subs = 2 * max(b - a, 0);
-        for (; my < seq + subs; my += C::kWarps) {
-            const int sub = my & 1, tok0 = (w.q.tile0 + a) * kTile + (my - seq) * kSub;
-            // after a time-out the outputs are undefined, but every role still ends
-            (void)warp_wait(&full[slot], (uint32_t)phase, ctl);
-            uint8_t* st = ring + (size_t)slot * C::kStage;
-            const uint32_t mask = masks[2 * slot + sub];
-            if (mask != 0) {
-                if (mask != ~0u) {
-                    // scales and biases of slots without a token may hold anything
-                    if (!((mask >> lane) & 1))
-                        for (int k = 0; k < 4; ++k)
-                            for (int i = 0; i < C::NG * C::E / 2; ++i)
-                                reinterpret_cast<uint16_t*>(st + 2 * C::kCodes + k * C::kSb)[(sub * kSub + lane) * (C::NG * C::E / 2) + i] = 0;
-                    __syncwarp();
+    int turn = 0;                                  // the warp that joins the current segment
+    uint32_t parity = 0;                           // of the segments' number
+    if (tid == 0) *meta = make_int4(-1, 0, 0, 0);  // until this CTA holds the beginning of a unit that goes on
+    RawQuery<C> raw;                               // (fetched by every warp, with a part in the segment or not: by
+    bool more = w.more();                          // some, it would live in registers all along)
+    if (more) fetch_query<C>(p, w.q, w.h, w.rb, vec_q != 0, raw);
+    while (more) {
+        const int end = seq + 2 * (w.b - w.a);     // sub-tiles up to this segment's last
+        const bool part = my < end;
+        if (part) {
+            Query<C> Q;
+            make_query<C>(p, raw, Q);
+            Acc<C> A;
+            clear<C>(A);
+            const int lo_max = w.L.lo_max, hi_min = w.L.hi_min, key0 = (w.q.tile0 + w.a) * kTile - seq * kSub;
+            for (; my < end; my += C::kWarps) {
+                const int sub = my & 1, tok0 = key0 + my * kSub;
+                // after a time-out the outputs are undefined, but every role still ends
+                (void)warp_wait(&full[slot], (uint32_t)phase, ctl);
+                uint8_t* st = ring + (size_t)slot * C::kStage;
+                const uint32_t mask = masks[2 * slot + sub];
+                if (mask != 0) {
+                    if (mask != ~0u) {
+                        // scales and biases of slots without a token may hold anything
+                        if (!((mask >> lane) & 1))
+                            for (int k = 0; k < 4; ++k)
+                                for (int i = 0; i < C::NG * C::E / 2; ++i)
+                                    reinterpret_cast<uint16_t*>(st + 2 * C::kCodes +
+                                                                k * C::kSb)[(sub * kSub + lane) * (C::NG * C::E / 2) + i] = 0;
+                        __syncwarp();
+                    }
+                    tile<C>(st, sub, mask, tok0, Q, p, w, lo_max, hi_min, A);
                 }
-                tile<C>(st, sub, mask, tok0, Q, p, w.q, L, A);
-                if (mask != ~0u) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[slot]);
+                slot += ((my + C::kWarps) >> 1) - (my >> 1);
+                if (slot >= S) {
+                    slot -= S;
+                    phase ^= 1;
+                }
             }
+            (void)warp_wait(joined, parity ^ 1u, ctl);   // the buffer is free
+            deposit<C>(A, buf);
+        } else {
+            (void)warp_wait(joined, parity ^ 1u, ctl);
+            deposit_nothing<C>(buf);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(deposited);
+        seq = end;
+        const bool begins = w.begins(), whole = begins && w.ends();
+        const int q0 = w.q.q0 + w.L.i0, h = w.h, first = w.L.first, rows = w.L.rows;
+        if (begins && !whole && tid == 0) {
+            const long long end_of_unit = w.c - w.place + w.q.ntile + kStart;   // on the line
+            *meta = make_int4(w.r, w.h * w.nrb + w.rb, (int)((end_of_unit - 1) / per), 0);
+        }
+        w.advance(p);
+        more = w.more();
+        if (more) fetch_query<C>(p, w.q, w.h, w.rb, vec_q != 0, raw);
+        if (turn == warp) {
+            (void)warp_wait(deposited, parity, ctl);
+            float* rec = recs + (begins ? rec_floats(C::NC, C::D) : 0);
+            join<C>(buf, rows, [&](int col, int d, float4 f, float m, float l) {
+                if (whole) {
+                    const int i = (first + col) / p.group;
+                    store_out<T>(p, vec_out != 0, q0 + i, h * p.group + (first + col - i * p.group), C::D, d, f, m, l);
+                } else {
+                    *reinterpret_cast<float4*>(rec + col * C::D + d) = f;
+                    if (d == 0) {
+                        rec[C::NC * C::D + col] = m;
+                        rec[C::NC * C::D + C::NC + col] = l;
+                    }
+                }
+            });
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[slot]);
-            const int next = (my + C::kWarps) >> 1;
-            slot += next - (my >> 1);
-            if (slot >= S) {
-                slot -= S;
-                phase ^= 1;
-            }
+            if (lane == 0) mbar_arrive(joined);
         }
-        seq += subs;
-        const bool begins = w.begins(), ends = w.ends();
-        const long long rows = (long long)w.q.qn * p.group;
-        float* rec = recs + (begins ? rec_floats(C::NC, C::D) : 0);
-        join<C>(A, buf, [&](int col, int d, float4 f, float m, float l) {
-            if (begins && ends) {
-                const long long rr = (long long)rb * C::NC + col;
-                if (rr >= rows) return;
-                const int i = (int)(rr / p.group);
-                store_out<T>(p, vec_out != 0, w.q.q0 + i, h * p.group + (int)(rr - (long long)i * p.group), C::D, d, f, m, l);
-            } else {
-                *reinterpret_cast<float4*>(rec + col * C::D + d) = f;
-                if (d == 0) {
-                    rec[C::NC * C::D + col] = m;
-                    rec[C::NC * C::D + C::NC + col] = l;
-                }
-            }
-        });
-        if (begins && !ends) {
-            cut = true;
-            if (tid == 0) {
-                const long long end = w.c - w.place + w.q.ntile + kStart;   // of the unit, on the line
-                *meta = make_int4(w.r, w.unit, (int)((end - 1) / per), 0);
-            }
-        }
-        w.advance();
+        parity ^= 1u;
+        if (++turn == C::kWarps) turn = 0;
     }
-    if (!cut && tid == 0) *meta = make_int4(-1, 0, 0, 0);
 }
 
 // joins the records of a cut unit, in the order of the CTAs: block (i, c) the
@@ -1012,8 +1064,8 @@ __global__ void __launch_bounds__(128) kv_combine_kernel(const __grid_constant__
     const Req rq = request(p, meta.x);
     const int nrb = row_blocks(p, rq, NC);
     const int h = meta.y / nrb, rb = meta.y % nrb;
-    const long long rr = (long long)rb * NC + col;
-    if (rr >= (long long)rq.qn * p.group) return;
+    const int rr = rb * NC + col;
+    if (rr >= rq.qn * p.group) return;
     const float* recs = reinterpret_cast<const float*>(ws + meta_bytes(ctas));
     const int gi = threadIdx.x / (D / 4), d = (threadIdx.x % (D / 4)) * 4;
     const int n = meta.z - (int)blockIdx.x + 1;
@@ -1056,8 +1108,8 @@ __global__ void __launch_bounds__(128) kv_combine_kernel(const __grid_constant__
         F.z = fmaf(v.z, e, F.z);
         F.w = fmaf(v.w, e, F.w);
     }
-    const int i = (int)(rr / p.group);
-    store_out<typename C::T>(p, vec_out != 0, rq.q0 + i, h * p.group + (int)(rr - (long long)i * p.group), D, d, F, M, Ls);
+    const int i = rr / p.group;
+    store_out<typename C::T>(p, vec_out != 0, rq.q0 + i, h * p.group + (rr - i * p.group), D, d, F, M, Ls);
 }
 
 template <class C>
