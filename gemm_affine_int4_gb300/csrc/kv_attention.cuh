@@ -51,7 +51,7 @@ using namespace pipe;
 constexpr int kTile = 64;                       // tokens of a stage of the ring, loaded at once
 constexpr int kSub = 32;                        // tokens that a consumer warp works on: half a stage
 constexpr int kBlocks = kSub / 16;              // 16-token blocks of a sub-tile
-constexpr int kStart = 4;                       // what the start and join of a unit cost, in tiles (see Walk)
+constexpr int kStart = 6;                       // what the start and join of a unit cost, in tiles (see Walk)
 
 template <typename T_, int D_, int GS_, int NT_>
 struct Cfg {

@@ -202,57 +202,122 @@ __device__ __forceinline__ void load8(const void* p, long long at, float (&x)[8]
     }
 }
 
-// One group is GS / 8 neighbouring lanes; its extremes come from a butterfly
-// over them. Scale, bias and codes are those of gai4_quantize: the same
-// binary32 steps, each rounded once.
-template <typename T, int D, int GS, bool VEC>
-__global__ void __launch_bounds__(256) kv_append_kernel(const void* k, long long ks, const void* v, long long vs,
-                                                        const int64_t* __restrict__ slots, KvCache kc, KvCache vc,
-                                                        KvShape sh, int rows) {
-    constexpr int LPR = D / 8, LPG = GS / 8;   // lanes per row and per group
-    pdl_launch_dependents();
-    pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int sub = lane / LPR, li = lane % LPR;
-    const int row = (blockIdx.x * 8 + (threadIdx.x >> 5)) * (32 / LPR) + sub;   // (token, k or v, head)
-    const bool live = row < rows;
-    const int per_token = 2 * sh.hkv;
-    const int token = live ? row / per_token : 0;
-    int h = live ? row - token * per_token : 0;
-    const bool is_v = h >= sh.hkv;
-    if (is_v) h -= sh.hkv;
-    const long long dst = live ? cache_row(slots[token], h, sh) : -1;
-    float x[8];
-    load8<T, VEC>(is_v ? v : k, token * (is_v ? vs : ks) + (long long)h * D + li * 8, x);
-    float mn = x[0], mx = x[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        mn = fminf(mn, x[i]);
-        mx = fmaxf(mx, x[i]);
-    }
-#pragma unroll
-    for (int o = 1; o < LPG; o <<= 1) {
-        mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    }
-    const typename T::storage s_h = T::from_f32(__fdiv_rn(__fsub_rn(mx, mn), 15.0f)), b_h = T::from_f32(mn);
-    const float s = T::to_f32(s_h), b = T::to_f32(b_h);
+// two binary32 operations at once
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n"
+        " mov.b64 {%0, %1}, d;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+        " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float mul_sat(float a, float b) {
+    float d;
+    asm("mul.rn.sat.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Codes of eight elements: clamp(rint((x - b) / s), 0, 15), the quotient an
+// IEEE division. A fifteenth of the reciprocal, clamped to [0, 1] and taken
+// fifteenfold, is within 1e-5 of the quotient clamped to [0, 15], so its
+// rounding is the code unless it lies next to a half; only then (and where the
+// reciprocal is not finite) the divisions are done. Adding 3 * 2^22 rounds to
+// an integer, in the sum's low bits.
+__device__ __forceinline__ uint32_t codes8(const float (&x)[8], float s, float b) {
+    if (s == 0.0f) return 0u;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    const float k = inv * (1.0f / 15.0f), magic = 12582912.0f;
+    const float2 nb = make_float2(-b, -b), up = make_float2(magic, magic), down = make_float2(-magic, -magic);
+    const float2 c15 = make_float2(15.0f, 15.0f), m15 = make_float2(-15.0f, -15.0f);
     uint32_t word = 0;
-    if (s != 0.0f) {
+    float far = 0.0f;   // largest distance from an integer
 #pragma unroll
+    for (int i = 6; i >= 0; i -= 2) {
+        float2 u = add2(make_float2(x[i], x[i + 1]), nb);
+        u.x = mul_sat(u.x, k);
+        u.y = mul_sat(u.y, k);
+        const float2 y = fma2(u, c15, up);
+        const float2 d = fma2(u, m15, add2(y, down));
+        far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
+        word = word * 16u + (__float_as_uint(y.y) & 15u);
+        word = word * 16u + (__float_as_uint(y.x) & 15u);
+    }
+    if (far >= 0.4999f || !(inv < 1e38f)) {
+        word = 0;
         for (int i = 0; i < 8; ++i) {
             const float r = rintf(__fdiv_rn(__fsub_rn(x[i], b), s));
             const uint32_t q = r <= 0.0f ? 0u : (r >= 15.0f ? 15u : (uint32_t)r);
             word |= q << (4 * i);
         }
     }
-    if (dst < 0) return;
-    const KvCache& c = is_v ? vc : kc;
-    const_cast<uint32_t*>(c.packed)[dst * LPR + li] = word;
-    if (li % LPG == 0) {
-        const long long g = dst * (D / GS) + li / LPG;
-        static_cast<typename T::storage*>(const_cast<void*>(c.scales))[g] = s_h;
-        static_cast<typename T::storage*>(const_cast<void*>(c.biases))[g] = b_h;
+    return word;
+}
+
+// One group is GS / 8 neighbouring lanes; its extremes come from a butterfly
+// over them. Scale, bias and codes are those of gai4_quantize: the same
+// binary32 steps, each rounded once. A warp has SETS sets of rows in flight:
+// four where they still give every SM work, else one (64 tokens of 2 x 8 rows:
+// 6.0 us a call with one, 8.9 with four; 20011 tokens: 46 us with four, 82
+// with one, before the divisions went).
+template <typename T, int D, int GS, bool VEC, int SETS>
+__global__ void __launch_bounds__(256) kv_append_kernel(const void* k, long long ks, const void* v, long long vs,
+                                                        const int64_t* __restrict__ slots, KvCache kc, KvCache vc,
+                                                        KvShape sh, int rows) {
+    constexpr int LPR = D / 8, LPG = GS / 8;   // lanes per row and per group
+    constexpr int RPW = 32 / LPR;              // rows of a warp's set
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int sub = lane / LPR, li = lane % LPR;
+    const int row0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * RPW * SETS + sub;   // (token, k or v, head)
+    const int per_token = 2 * sh.hkv;
+    float x[SETS][8];
+    long long dst[SETS];
+    bool is_v[SETS];
+#pragma unroll
+    for (int u = 0; u < SETS; ++u) {
+        const int row = row0 + u * RPW;
+        const bool live = row < rows;
+        const int token = live ? row / per_token : 0;
+        int h = live ? row - token * per_token : 0;
+        is_v[u] = h >= sh.hkv;
+        if (is_v[u]) h -= sh.hkv;
+        load8<T, VEC>(is_v[u] ? v : k, token * (is_v[u] ? vs : ks) + (long long)h * D + li * 8, x[u]);
+        dst[u] = live ? cache_row(slots[token], h, sh) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < SETS; ++u) {
+        float mn = x[u][0], mx = x[u][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+            mn = fminf(mn, x[u][i]);
+            mx = fmaxf(mx, x[u][i]);
+        }
+#pragma unroll
+        for (int o = 1; o < LPG; o <<= 1) {
+            mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        }
+        const typename T::storage s_h = T::from_f32(__fdiv_rn(__fsub_rn(mx, mn), 15.0f)), b_h = T::from_f32(mn);
+        const uint32_t word = codes8(x[u], T::to_f32(s_h), T::to_f32(b_h));
+        if (dst[u] >= 0) {
+            const KvCache& c = is_v[u] ? vc : kc;
+            const_cast<uint32_t*>(c.packed)[dst[u] * LPR + li] = word;
+            if (li % LPG == 0) {
+                const long long g = dst[u] * (D / GS) + li / LPG;
+                static_cast<typename T::storage*>(const_cast<void*>(c.scales))[g] = s_h;
+                static_cast<typename T::storage*>(const_cast<void*>(c.biases))[g] = b_h;
+            }
+        }
     }
 }
 
@@ -330,15 +395,15 @@ cudaError_t launch_kv_append(const void* k, int64_t ks, const void* v, int64_t v
             const int64_t chunk = (1ll << 30) / (2 * sh.hkv);
             for (int64_t t0 = 0; t0 < num_tokens; t0 += chunk) {
                 const int64_t n = num_tokens - t0 < chunk ? num_tokens - t0 : chunk;
-                const int rows = (int)(n * 2 * sh.hkv), per_block = 8 * (32 / (Z::D / 8));
+                const int rows = (int)(n * 2 * sh.hkv), per_set = 8 * (32 / (Z::D / 8));
+                const int sets = rows >= 4 * 8 * per_set * num_sms() ? 4 : 1, per_block = per_set * sets;
                 const dim3 grid((unsigned)((rows + per_block - 1) / per_block));
                 const void* kp = static_cast<const char*>(k) + t0 * ks * T::kBytes;
                 const void* vp = static_cast<const char*>(v) + t0 * vs * T::kBytes;
-                const cudaError_t e =
-                    vec ? launch_pdl(kv_append_kernel<T, Z::D, Z::GS, true>, grid, dim3(256), 0, s, kp, (long long)ks,
-                                     vp, (long long)vs, slots + t0, kc, vc, sh, rows)
-                        : launch_pdl(kv_append_kernel<T, Z::D, Z::GS, false>, grid, dim3(256), 0, s, kp, (long long)ks,
-                                     vp, (long long)vs, slots + t0, kc, vc, sh, rows);
+                const auto kernel = vec ? (sets == 4 ? kv_append_kernel<T, Z::D, Z::GS, true, 4> : kv_append_kernel<T, Z::D, Z::GS, true, 1>)
+                                        : (sets == 4 ? kv_append_kernel<T, Z::D, Z::GS, false, 4> : kv_append_kernel<T, Z::D, Z::GS, false, 1>);
+                const cudaError_t e = launch_pdl(kernel, grid, dim3(256), 0, s, kp, (long long)ks, vp, (long long)vs,
+                                                 slots + t0, kc, vc, sh, rows);
                 if (e != cudaSuccess) return e;
             }
             return cudaSuccess;
