@@ -265,33 +265,36 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8], float s, float b
 // One group is GS / 8 neighbouring lanes; its extremes come from a butterfly
 // over them. Scale, bias and codes are those of gai4_quantize: the same
 // binary32 steps, each rounded once. A warp has SETS sets of rows in flight:
-// four where they still give every SM work, else one (64 tokens of 2 x 8 rows:
-// 6.0 us a call with one, 8.9 with four; 20011 tokens: 46 us with four, 82
-// with one, before the divisions went).
+// four where they still give every SM work, else one (64 tokens of 2 x 8 rows
+// and two reads: 5.5 us with one, 8.9 with four). Bound by instructions: 20011
+// tokens of 2 x 8 rows of 128 f16 values in groups of 32 (113 MB), 36 us; with
+// a division for every code it took 82.
 template <typename T, int D, int GS, bool VEC, int SETS>
 __global__ void __launch_bounds__(256) kv_append_kernel(const void* k, long long ks, const void* v, long long vs,
                                                         const int64_t* __restrict__ slots, KvCache kc, KvCache vc,
-                                                        KvShape sh, int rows) {
+                                                        KvShape sh, int tokens) {
     constexpr int LPR = D / 8, LPG = GS / 8;   // lanes per row and per group
     constexpr int RPW = 32 / LPR;              // rows of a warp's set
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const int sub = lane / LPR, li = lane % LPR;
-    const int row0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * RPW * SETS + sub;   // (token, k or v, head)
-    const int per_token = 2 * sh.hkv;
+    // a block's rows: consecutive tokens of one head of k or v (whose slots
+    // are neighbours as a rule)
+    const int tb = blockIdx.x / (2 * sh.hkv), unit = blockIdx.x - tb * (2 * sh.hkv);
+    const bool is_v = unit >= sh.hkv;
+    const int h = is_v ? unit - sh.hkv : unit;
+    const void* in = is_v ? v : k;
+    const long long stride = is_v ? vs : ks;
+    const KvCache c = is_v ? vc : kc;
+    const int token0 = (tb * 8 + (threadIdx.x >> 5)) * RPW * SETS + sub;
     float x[SETS][8];
     long long dst[SETS];
-    bool is_v[SETS];
 #pragma unroll
     for (int u = 0; u < SETS; ++u) {
-        const int row = row0 + u * RPW;
-        const bool live = row < rows;
-        const int token = live ? row / per_token : 0;
-        int h = live ? row - token * per_token : 0;
-        is_v[u] = h >= sh.hkv;
-        if (is_v[u]) h -= sh.hkv;
-        load8<T, VEC>(is_v[u] ? v : k, token * (is_v[u] ? vs : ks) + (long long)h * D + li * 8, x[u]);
+        const int token = token0 + u * RPW;
+        const bool live = token < tokens;
+        load8<T, VEC>(in, (live ? token : 0) * stride + (long long)h * D + li * 8, x[u]);
         dst[u] = live ? cache_row(slots[token], h, sh) : -1;
     }
 #pragma unroll
@@ -310,7 +313,6 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const void* k, long long
         const typename T::storage s_h = T::from_f32(__fdiv_rn(__fsub_rn(mx, mn), 15.0f)), b_h = T::from_f32(mn);
         const uint32_t word = codes8(x[u], T::to_f32(s_h), T::to_f32(b_h));
         if (dst[u] >= 0) {
-            const KvCache& c = is_v[u] ? vc : kc;
             const_cast<uint32_t*>(c.packed)[dst[u] * LPR + li] = word;
             if (li % LPG == 0) {
                 const long long g = dst[u] * (D / GS) + li / LPG;
@@ -321,30 +323,34 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const void* k, long long
     }
 }
 
+// A thread expands one word (eight values, two stores); neighbouring threads
+// write on. Bound by the writes: 20011 tokens of 8 rows of 128 values (82 MB
+// out, 15 in), 22 us, where a fill of 82 MB takes 15; with four values a thread
+// it took 24, with the tokens of one head a block 25.
 template <typename T, int D, int GS>
 __global__ void __launch_bounds__(256) kv_read_kernel(KvCache c, const int64_t* __restrict__ slots, float* out,
-                                                      KvShape sh, long long words) {
-    constexpr int LPR = D / 8;
+                                                      KvShape sh, long long rows) {
+    constexpr int LPR = D / 8, RPB = 256 / LPR;   // threads of a row, rows of a block
     pdl_launch_dependents();
     pdl_wait();
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;   // word (token, head, li)
-    if (i >= words) return;
-    const long long row = i / LPR;
-    const int li = (int)(i % LPR);
+    const int li = threadIdx.x % LPR;
+    const long long row = (long long)blockIdx.x * RPB + threadIdx.x / LPR;   // (token, head)
+    if (row >= rows) return;
     const long long token = row / sh.hkv;
     const long long src = cache_row(slots[token], (int)(row - token * sh.hkv), sh);
-    float4 o[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    uint32_t w = 0u;
+    float s = 0.0f, b = 0.0f;
     if (src >= 0) {
-        const uint32_t w = c.packed[src * LPR + li];
+        w = c.packed[src * LPR + li];
         const long long g = src * (D / GS) + li / (GS / 8);
-        const float s = T::to_f32(static_cast<const typename T::storage*>(c.scales)[g]);
-        const float b = T::to_f32(static_cast<const typename T::storage*>(c.biases)[g]);
-        float* f = reinterpret_cast<float*>(o);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = fmaf(s, (float)((w >> (4 * j)) & 15u), b);
+        s = T::to_f32(static_cast<const typename T::storage*>(c.scales)[g]);
+        b = T::to_f32(static_cast<const typename T::storage*>(c.biases)[g]);
     }
-    reinterpret_cast<float4*>(out)[2 * i] = o[0];
-    reinterpret_cast<float4*>(out)[2 * i + 1] = o[1];
+    float4* o = reinterpret_cast<float4*>(out) + (row * LPR + li) * 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        o[i] = make_float4(fmaf(s, (float)((w >> (16 * i)) & 15u), b), fmaf(s, (float)((w >> (16 * i + 4)) & 15u), b),
+                           fmaf(s, (float)((w >> (16 * i + 8)) & 15u), b), fmaf(s, (float)((w >> (16 * i + 12)) & 15u), b));
 }
 
 // calls f<T, D, GS>() for the runtime type, head size and group size
@@ -391,19 +397,19 @@ cudaError_t launch_kv_append(const void* k, int64_t ks, const void* v, int64_t v
             using Z = decltype(z);
             const bool vec = ((uintptr_t)k & 15) == 0 && ((uintptr_t)v & 15) == 0 && ks * T::kBytes % 16 == 0 &&
                              vs * T::kBytes % 16 == 0;
-            // row numbers of one launch stay below 2^31
-            const int64_t chunk = (1ll << 30) / (2 * sh.hkv);
+            // block numbers of one launch stay below 2^31
+            constexpr int per_set = 8 * (32 / (Z::D / 8));   // tokens of a block with one set of rows a warp
+            const int64_t chunk = ((1ll << 30) / (2 * sh.hkv)) * per_set;
             for (int64_t t0 = 0; t0 < num_tokens; t0 += chunk) {
                 const int64_t n = num_tokens - t0 < chunk ? num_tokens - t0 : chunk;
-                const int rows = (int)(n * 2 * sh.hkv), per_set = 8 * (32 / (Z::D / 8));
-                const int sets = rows >= 4 * 8 * per_set * num_sms() ? 4 : 1, per_block = per_set * sets;
-                const dim3 grid((unsigned)((rows + per_block - 1) / per_block));
+                const int sets = n * 2 * sh.hkv >= 4ll * 8 * per_set * num_sms() ? 4 : 1, per_block = per_set * sets;
+                const dim3 grid((unsigned)((n + per_block - 1) / per_block * (2 * sh.hkv)));
                 const void* kp = static_cast<const char*>(k) + t0 * ks * T::kBytes;
                 const void* vp = static_cast<const char*>(v) + t0 * vs * T::kBytes;
                 const auto kernel = vec ? (sets == 4 ? kv_append_kernel<T, Z::D, Z::GS, true, 4> : kv_append_kernel<T, Z::D, Z::GS, true, 1>)
                                         : (sets == 4 ? kv_append_kernel<T, Z::D, Z::GS, false, 4> : kv_append_kernel<T, Z::D, Z::GS, false, 1>);
                 const cudaError_t e = launch_pdl(kernel, grid, dim3(256), 0, s, kp, (long long)ks, vp, (long long)vs,
-                                                 slots + t0, kc, vc, sh, rows);
+                                                 slots + t0, kc, vc, sh, (int)n);
                 if (e != cudaSuccess) return e;
             }
             return cudaSuccess;
@@ -417,11 +423,10 @@ cudaError_t launch_kv_read(KvCache c, const int64_t* slots, float* out, const Kv
         using T = decltype(t);
         return by_sizes(sh.d, sh.gs, [&](auto z) {
             using Z = decltype(z);
-            const long long words = num_tokens * sh.hkv * (Z::D / 8);
-            const long long blocks = (words + 255) / 256;
+            constexpr int per_block = 256 / (Z::D / 8);
+            const long long rows = num_tokens * sh.hkv, blocks = (rows + per_block - 1) / per_block;
             if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-            return launch_pdl(kv_read_kernel<T, Z::D, Z::GS>, dim3((unsigned)blocks), dim3(256), 0, s, c, slots, out,
-                              sh, words);
+            return launch_pdl(kv_read_kernel<T, Z::D, Z::GS>, dim3((unsigned)blocks), dim3(256), 0, s, c, slots, out, sh, rows);
         });
     });
 }
