@@ -348,8 +348,8 @@ __device__ __forceinline__ void producer(const KvAttnLaunch& p, Walk<C::NC>& w, 
 // per-warp running state of a unit
 template <class C>
 struct Acc {
-    float o[C::D / 16][C::NT][4];   // O^T: [value channel block][rows][...], in units of R 2^-14 2^-24 (2^-20)
-    float ab[C::NG][C::NT][2];      // sum p b
+    float o[C::D / 16][C::NT][4];   // O^T less sum p (b + 8 s): [value channel block][rows][..], in units of R 2^-14 and of 2^-24, 2^-20 (f32: 1)
+    float ab[C::NG][C::NT][2];      // sum p (b + 8 s)
     float m[C::NT][2], l[C::NT][2];
     int re;                         // exponent field of R
 };
@@ -504,6 +504,20 @@ __device__ __forceinline__ void make_query(const KvAttnLaunch& p, const RawQuery
 }
 
 // what columns 2t and 2t + 1 of each 8-column block may see: keys [lo, hi)
+// two codes as binary16: c 2^-24 (bits 0..3 of the halves) or c 2^-20 (bits
+// 4..7) as they stand, or c - 8 (exact)
+template <bool CENTRED, int HIGH>
+__device__ __forceinline__ uint32_t value_codes(uint32_t w) {
+    const uint32_t c = w & (HIGH ? 0x00F000F0u : 0x000F000Fu);
+    if constexpr (!CENTRED) return c;
+    uint32_t d;
+    if constexpr (HIGH)   // (1024 + 16 c) / 16 - 72
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(c | 0x64006400u), "r"(0x2C002C00u), "r"(0xD480D480u));
+    else                  // (1024 + c) - 1032
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(c | 0x64006400u), "r"(0x64086408u));
+    return d;
+}
+
 template <class C>
 __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mask, int tok0, const Query<C>& Q,
                                      const KvAttnLaunch& p, const Walk<C::NC>& w, int lo_max, int hi_min, Acc<C>& A) {
@@ -682,63 +696,104 @@ __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mas
             }
             A.l[n][c] += l;
         }
-    // ---- values
+    // ---- values. What the matrix unit sums are p s (c - 8), the mean of the
+    // codes taken off, and only over this sub-tile; sum p (b + 8 s) and the sums
+    // over the sub-tiles are binary32 additions. (The unit truncates its sums:
+    // over a whole unit, with uncentred codes, 30 f32 requests were 2e-5 off.)
+    // bf16 / f16: the sums of the codes as they are start at -8 sum p s, which
+    // leaves a few 2^-24 of it. f32: the codes themselves are centred.
     const float inv = __uint_as_float((uint32_t)(min(268 - A.re, 254)) << 23);   // 2^14 / R
+    constexpr int kParts = C::kSplit ? 2 : 1;
+    uint32_t P[kBlocks][kParts][NG][NT][2];
 #pragma unroll
     for (int mb = 0; mb < kBlocks; ++mb) {
-        float b0[NG], b1[NG], v0[NG], v1[NG];
-        load_groups<T, NG>(vsc + (16 * mb + tg) * NG * C::E, v0);
-        load_groups<T, NG>(vsc + (16 * mb + tg + 8) * NG * C::E, v1);
-        load_groups<T, NG>(vbi + (16 * mb + tg) * NG * C::E, b0);
-        load_groups<T, NG>(vbi + (16 * mb + tg + 8) * NG * C::E, b1);
-        uint32_t P[C::kSplit ? 2 : 1][NG][NT][2];
+        float sc[2][NG], bi[2][NG];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            load_groups<T, NG>(vsc + (16 * mb + tg + 8 * e) * NG * C::E, sc[e]);
+            load_groups<T, NG>(vbi + (16 * mb + tg + 8 * e) * NG * C::E, bi[e]);
+        }
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
-            const float s[2] = {v0[k] * inv, v1[k] * inv};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
+            for (int e = 0; e < 2; ++e) {
+                const float mid = fmaf(8.f, sc[e][k], bi[e][k]), f = sc[e][k] * inv;
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    A.ab[k][n][c] = fmaf(x[mb][n][c + 2], b1[k], fmaf(x[mb][n][c], b0[k], A.ab[k][n][c]));
+                for (int n = 0; n < NT; ++n) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float y0 = x[mb][n][2 * e] * s[e], y1 = x[mb][n][2 * e + 1] * s[e];
+                    for (int c = 0; c < 2; ++c) A.ab[k][n][c] = fmaf(x[mb][n][2 * e + c], mid, A.ab[k][n][c]);
+                    const float y0 = x[mb][n][2 * e] * f, y1 = x[mb][n][2 * e + 1] * f;
                     const uint32_t w = pack_f16(y0, y1);
-                    P[0][k][n][e] = transpose8(w);
+                    P[mb][0][k][n][e] = transpose8(w);
                     if constexpr (C::kSplit) {
                         const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&w));
-                        P[1][k][n][e] = transpose8(pack_f16(y0 - back.x, y1 - back.y));
+                        P[mb][1][k][n][e] = transpose8(pack_f16(y0 - back.x, y1 - back.y));
                     }
                 }
             }
         }
-        // rows g / g + 8 of a value block: codes 2i / 2i + 1 of this lane's word
-        const uint8_t* vc = st + C::kCodes + (16 * mb + t) * (D / 2);   // tokens t, t + 4, t + 8, t + 12
-        constexpr int kChunks = GS == 32 ? NG : D / 64;
+    }
+    // -8 sum p s, in the units of rows g (2^-24) and g + 8 (2^-20): where the sums start (f32: at 0)
+    float start[NG][NT][4];
 #pragma unroll
-        for (int j = 0; j < kChunks; ++j) {
-            const int word = GS == 32 ? 4 * j + (g >> 1) : 8 * j + g;
-            uint32_t w[4];
+    for (int k = 0; k < NG; ++k)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(vc + i * (4 * D / 2) + word * 4);
-            constexpr int kHalves = GS == 32 ? 1 : 2;
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int hh = 0; hh < kHalves; ++hh) {
-                const uint32_t sel = GS == 32 ? ((g & 1) ? 0x7632u : 0x5410u) : (hh ? 0x7632u : 0x5410u);
-                const uint32_t a = __byte_perm(w[0], w[1], sel), b = __byte_perm(w[2], w[3], sel);
-                const int k = GS == 32 ? j : (j * 64) / GS;
+            for (int e = 0; e < 4; ++e) start[k][n][e] = 0.f;
+            if constexpr (!C::kSplit) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const uint32_t aa = q ? a >> 8 : a, bb = q ? b >> 8 : b;
-                    const uint32_t a0 = aa & 0x000F000Fu, a1 = aa & 0x00F000F0u;
-                    const uint32_t a2 = bb & 0x000F000Fu, a3 = bb & 0x00F000F0u;
-                    const int blk = GS == 32 ? 2 * j + q : 4 * j + 2 * hh + q;
+                for (int mb = 0; mb < kBlocks; ++mb)
+                    mma16816(start[k][n], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, P[mb][0][k][n][0],
+                             P[mb][0][k][n][1]);
+            }
+        }
+    // rows g / g + 8 of a value block: codes 2i / 2i + 1 of this lane's word
+    const uint8_t* vc = st + C::kCodes + t * (D / 2);   // tokens t, t + 4, t + 8, t + 12 of each 16-token block
+    constexpr int kChunks = GS == 32 ? NG : D / 64;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        mma16816(A.o[blk][n], a0, a1, a2, a3, P[0][k][n][0], P[0][k][n][1]);
-                        if constexpr (C::kSplit) mma16816(A.o[blk][n], a0, a1, a2, a3, P[1][k][n][0], P[1][k][n][1]);
-                    }
+    for (int j = 0; j < kChunks; ++j) {
+        const int word = GS == 32 ? 4 * j + (g >> 1) : 8 * j + g;
+        uint32_t w[kBlocks][4];
+#pragma unroll
+        for (int mb = 0; mb < kBlocks; ++mb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[mb][i] = *reinterpret_cast<const uint32_t*>(vc + (16 * mb + 4 * i) * (D / 2) + word * 4);
+        constexpr int kHalves = GS == 32 ? 1 : 2;
+#pragma unroll
+        for (int hh = 0; hh < kHalves; ++hh) {
+            const uint32_t sel = GS == 32 ? ((g & 1) ? 0x7632u : 0x5410u) : (hh ? 0x7632u : 0x5410u);
+            const int k = GS == 32 ? j : (j * 64) / GS;
+            uint32_t a[kBlocks], b[kBlocks];
+#pragma unroll
+            for (int mb = 0; mb < kBlocks; ++mb) {
+                a[mb] = __byte_perm(w[mb][0], w[mb][1], sel);
+                b[mb] = __byte_perm(w[mb][2], w[mb][3], sel);
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int blk = GS == 32 ? 2 * j + q : 4 * j + 2 * hh + q;
+                float acc[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[n][e] = start[k][n][e];
+#pragma unroll
+                for (int mb = 0; mb < kBlocks; ++mb) {
+                    const uint32_t aa = q ? a[mb] >> 8 : a[mb], bb = q ? b[mb] >> 8 : b[mb];
+                    const uint32_t a0 = value_codes<C::kSplit, 0>(aa), a1 = value_codes<C::kSplit, 1>(aa);
+                    const uint32_t a2 = value_codes<C::kSplit, 0>(bb), a3 = value_codes<C::kSplit, 1>(bb);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int part = 0; part < kParts; ++part)
+                            mma16816(acc[n], a0, a1, a2, a3, P[mb][part][k][n][0], P[mb][part][k][n][1]);
                 }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) A.o[blk][n][e] += acc[n][e];
             }
         }
     }
@@ -764,6 +819,7 @@ __device__ __forceinline__ void deposit(Acc<C>& A, uint8_t* buf) {
             }
         }
     const float R = __uint_as_float((uint32_t)A.re << 23);
+    constexpr float kLow = C::kSplit ? 1.f / 16384.f : 1024.f, kHigh = C::kSplit ? 1.f / 16384.f : 64.f;   // 2^-14 / the codes' unit
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -778,10 +834,10 @@ __device__ __forceinline__ void deposit(Acc<C>& A, uint8_t* buf) {
 #pragma unroll
                 for (int k = 0; k < C::NG; ++k) {   // channels 32 k + 8 (g >> 1) + 4 (g & 1) + 0..3
                     float4 f;
-                    f.x = fmaf(A.o[2 * k][n][c] * 1024.f, R, A.ab[k][n][c]);
-                    f.y = fmaf(A.o[2 * k][n][c + 2] * 64.f, R, A.ab[k][n][c]);
-                    f.z = fmaf(A.o[2 * k + 1][n][c] * 1024.f, R, A.ab[k][n][c]);
-                    f.w = fmaf(A.o[2 * k + 1][n][c + 2] * 64.f, R, A.ab[k][n][c]);
+                    f.x = fmaf(A.o[2 * k][n][c] * kLow, R, A.ab[k][n][c]);
+                    f.y = fmaf(A.o[2 * k][n][c + 2] * kHigh, R, A.ab[k][n][c]);
+                    f.z = fmaf(A.o[2 * k + 1][n][c] * kLow, R, A.ab[k][n][c]);
+                    f.w = fmaf(A.o[2 * k + 1][n][c + 2] * kHigh, R, A.ab[k][n][c]);
                     *reinterpret_cast<float4*>(dst + 32 * k + 4 * g) = f;
                 }
             } else {
@@ -791,10 +847,10 @@ __device__ __forceinline__ void deposit(Acc<C>& A, uint8_t* buf) {
                     for (int hh = 0; hh < 2; ++hh) {   // channels 64 j + 8 g + 4 hh + 0..3
                         const int k = (j * 64) / C::GS, b = 4 * j + 2 * hh;
                         float4 f;
-                        f.x = fmaf(A.o[b][n][c] * 1024.f, R, A.ab[k][n][c]);
-                        f.y = fmaf(A.o[b][n][c + 2] * 64.f, R, A.ab[k][n][c]);
-                        f.z = fmaf(A.o[b + 1][n][c] * 1024.f, R, A.ab[k][n][c]);
-                        f.w = fmaf(A.o[b + 1][n][c + 2] * 64.f, R, A.ab[k][n][c]);
+                        f.x = fmaf(A.o[b][n][c] * kLow, R, A.ab[k][n][c]);
+                        f.y = fmaf(A.o[b][n][c + 2] * kHigh, R, A.ab[k][n][c]);
+                        f.z = fmaf(A.o[b + 1][n][c] * kLow, R, A.ab[k][n][c]);
+                        f.w = fmaf(A.o[b + 1][n][c + 2] * kHigh, R, A.ab[k][n][c]);
                         *reinterpret_cast<float4*>(dst + 64 * j + 8 * g + 4 * hh) = f;
                     }
             }
