@@ -432,14 +432,14 @@ def gai4_kv_plan(kv_lens, q_lens, block_table, free_blocks, free_count, page_siz
           "kv_lens, q_lens [B], block_table [B, max_blocks], free_count [1]")
     kv, q, table, free, count = _addr32(kv_lens, q_lens, block_table, free_blocks, free_count)
     if out is None:
-        # one allocation: slots first (8 bytes each), then the 32-bit outputs
-        a = torch.empty(3 * num_tokens + 2 * B + 6, dtype=torch.int32, device=kv_lens.device)
-        slots, positions, cu_q, lens, left, info = a.split((2 * num_tokens, num_tokens, B + 1, B, 1, 4))
-        out = KvPlan(slots.view(torch.int64), positions, cu_q, lens, left, info)
-        n2 = a.data_ptr()
-        n3 = n2 + 8 * num_tokens
-        n4 = n3 + 4 * num_tokens
-        o_slots, o_pos, o_cu, o_lens, o_left, o_info = n2, n3, n4, n4 + 4 * B + 4, n4 + 8 * B + 4, n4 + 8 * B + 8
+        # one allocation for the 32-bit outputs
+        slots = torch.empty(num_tokens, dtype=torch.int64, device=kv_lens.device)
+        a = torch.empty(num_tokens + 2 * B + 6, dtype=torch.int32, device=kv_lens.device)
+        n1, n2 = num_tokens + B + 1, num_tokens + 2 * B + 1
+        out = KvPlan(slots, a.as_strided((num_tokens,), (1,), 0), a.as_strided((B + 1,), (1,), num_tokens),
+                     a.as_strided((B,), (1,), n1), a.as_strided((1,), (1,), n2), a.as_strided((4,), (1,), n2 + 1))
+        o_slots, o_pos = slots.data_ptr(), a.data_ptr()
+        o_cu, o_lens, o_left, o_info = o_pos + 4 * num_tokens, o_pos + 4 * n1, o_pos + 4 * n2, o_pos + 4 * n2 + 4
     else:
         _need(out.slots.shape == (num_tokens,) and out.positions.shape == (num_tokens,) and
               out.cu_q.shape == (B + 1,) and out.kv_lens.shape == (B,) and out.free_count.numel() == 1 and

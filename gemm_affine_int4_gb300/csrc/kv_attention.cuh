@@ -101,11 +101,24 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// d = A B + c
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, const float* c) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+// two binary32 operations at once, on neighbouring registers
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+    asm("{\n .reg .b64 u, v;\n mov.b64 u, {%0, %1};\n mov.b64 v, {%2, %3};\n add.rn.f32x2 u, u, v;\n mov.b64 {%0, %1}, u;\n}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float c, float d) {   // x = x a + c, y = y b + d
+    asm("{\n .reg .b64 u, v, w;\n mov.b64 u, {%0, %1};\n mov.b64 v, {%2, %3};\n mov.b64 w, {%4, %5};\n"
+        " fma.rn.f32x2 u, u, v, w;\n mov.b64 {%0, %1}, u;\n}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -565,11 +578,8 @@ __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mas
                             wd[mb][e][k][3] = y.w;
                         }
                     }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[mb][k][n][e] = 0.f;
                 }
+            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < W; ++j)
 #pragma unroll
@@ -586,7 +596,8 @@ __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mas
 #pragma unroll
                                 for (int n = 0; n < NT; ++n)
                                     mma16816(acc[mb][k][n], a & 0x000F000Fu, b & 0x000F000Fu, a & 0x00F000F0u,
-                                             b & 0x00F000F0u, Q.b[part][ks][n][0], Q.b[part][ks][n][1]);
+                                             b & 0x00F000F0u, Q.b[part][ks][n][0], Q.b[part][ks][n][1],
+                                             j + half + part == 0 ? zero : acc[mb][k][n]);
                             }
 #pragma unroll
             for (int mb = 0; mb < kBlocks; ++mb) {
@@ -613,7 +624,11 @@ __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mas
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[mb][n][e] = fmaf(u[mb][n][e], Q.f[n][e & 1], v[mb][n][e]);
+                for (int e = 0; e < 4; e += 2) {
+                    x[mb][n][e] = u[mb][n][e];
+                    x[mb][n][e + 1] = u[mb][n][e + 1];
+                    fma2(x[mb][n][e], x[mb][n][e + 1], Q.f[n][0], Q.f[n][1], v[mb][n][e], v[mb][n][e + 1]);
+                }
     }
     // ---- masks: only on tiles that some row does not see in full
     if (mask != ~0u || tok0 + kSub > hi_min || tok0 < lo_max) {
@@ -683,19 +698,18 @@ __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mas
     }
     // ---- probabilities
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+        const float m0 = A.m[n][0] == -INFINITY ? 0.f : -A.m[n][0], m1 = A.m[n][1] == -INFINITY ? 0.f : -A.m[n][1];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const float m = A.m[n][c] == -INFINITY ? 0.f : A.m[n][c];
-            float l = 0.f;
+        for (int mb = 0; mb < kBlocks; ++mb)
 #pragma unroll
-            for (int mb = 0; mb < kBlocks; ++mb) {
-                x[mb][n][c] = ex2(x[mb][n][c] - m);
-                x[mb][n][c + 2] = ex2(x[mb][n][c + 2] - m);
-                l += x[mb][n][c] + x[mb][n][c + 2];
+            for (int e = 0; e < 4; e += 2) {
+                add2(x[mb][n][e], x[mb][n][e + 1], m0, m1);
+                x[mb][n][e] = ex2(x[mb][n][e]);
+                x[mb][n][e + 1] = ex2(x[mb][n][e + 1]);
+                add2(A.l[n][0], A.l[n][1], x[mb][n][e], x[mb][n][e + 1]);
             }
-            A.l[n][c] += l;
-        }
+    }
     // ---- values. What the matrix unit sums are p s (c - 8), the mean of the
     // codes taken off, and only over this sub-tile; sum p (b + 8 s) and the sums
     // over the sub-tiles are binary32 additions. (The unit truncates its sums:
@@ -742,10 +756,11 @@ __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mas
 #pragma unroll
             for (int e = 0; e < 4; ++e) start[k][n][e] = 0.f;
             if constexpr (!C::kSplit) {
+                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int mb = 0; mb < kBlocks; ++mb)
                     mma16816(start[k][n], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, P[mb][0][k][n][0],
-                             P[mb][0][k][n][1]);
+                             P[mb][0][k][n][1], mb == 0 ? zero : start[k][n]);
             }
         }
     // rows g / g + 8 of a value block: codes 2i / 2i + 1 of this lane's word
@@ -776,10 +791,6 @@ __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mas
                 const int blk = GS == 32 ? 2 * j + q : 4 * j + 2 * hh + q;
                 float acc[NT][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[n][e] = start[k][n][e];
-#pragma unroll
                 for (int mb = 0; mb < kBlocks; ++mb) {
                     const uint32_t aa = q ? a[mb] >> 8 : a[mb], bb = q ? b[mb] >> 8 : b[mb];
                     const uint32_t a0 = value_codes<C::kSplit, 0>(aa), a1 = value_codes<C::kSplit, 1>(aa);
@@ -788,12 +799,13 @@ __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mas
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int part = 0; part < kParts; ++part)
-                            mma16816(acc[n], a0, a1, a2, a3, P[mb][part][k][n][0], P[mb][part][k][n][1]);
+                            mma16816(acc[n], a0, a1, a2, a3, P[mb][part][k][n][0], P[mb][part][k][n][1],
+                                     mb + part == 0 ? start[k][n] : acc[n]);
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) A.o[blk][n][e] += acc[n][e];
+                    for (int e = 0; e < 4; e += 2) add2(A.o[blk][n][e], A.o[blk][n][e + 1], acc[n][e], acc[n][e + 1]);
             }
         }
     }
