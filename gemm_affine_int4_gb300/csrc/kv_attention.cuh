@@ -82,7 +82,8 @@ struct Cfg {
 
 // records of cut units in the workspace: per CTA two of (O [NC][D], m [NC],
 // l [NC]), number 0 for the end (or a middle) of a unit, 1 for its beginning,
-// and one int4 {request or -1, unit of the request, last CTA of the unit, 0}
+// and one int4 about the latter: {last CTA of the unit or -1, query row of its
+// row 0, head and place of row 0 among the head's query heads, rows}
 __host__ __device__ constexpr size_t rec_floats(int nc, int d) { return (size_t)nc * (d + 2); }
 __host__ __device__ constexpr size_t meta_bytes(int ctas) { return ((size_t)ctas * 16 + 255) / 256 * 256; }
 
@@ -1087,7 +1088,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         const int q0 = w.q.q0 + w.L.i0, h = w.h, first = w.L.first, rows = w.L.rows;
         if (begins && !whole && tid == 0) {
             const long long end_of_unit = w.c - w.place + w.q.ntile + kStart;   // on the line
-            *meta = make_int4(w.r, w.h * w.nrb + w.rb, (int)((end_of_unit - 1) / per), 0);
+            *meta = make_int4((int)((end_of_unit - 1) / per), q0, h << 16 | first, rows);
         }
         w.advance(p);
         more = w.more();
@@ -1127,18 +1128,14 @@ __global__ void __launch_bounds__(128) kv_combine_kernel(const __grid_constant__
     pdl_wait();
     const uint8_t* ws = static_cast<const uint8_t*>(p.workspace);
     const int4 meta = reinterpret_cast<const int4*>(ws)[blockIdx.x];
-    if (meta.x < 0) return;
     const int col = blockIdx.y;
-    const Req rq = request(p, meta.x);
-    const int nrb = row_blocks(p, rq, NC);
-    const int h = meta.y / nrb, rb = meta.y % nrb;
-    const int rr = rb * NC + col;
-    if (rr >= rq.qn * p.group) return;
+    if (meta.x < 0 || col >= meta.w) return;
     const float* recs = reinterpret_cast<const float*>(ws + meta_bytes(ctas));
     const int gi = threadIdx.x / (D / 4), d = (threadIdx.x % (D / 4)) * 4;
-    const int n = meta.z - (int)blockIdx.x + 1;
+    const int n = meta.x - (int)blockIdx.x + 1;
     float m = -INFINITY, l = 0.f;
     float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int i = gi; i < n; i += G) {
         const float* rec = recs + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * rec_floats(NC, D);
         const float mi = rec[NC * D + col], li = rec[NC * D + NC + col];
@@ -1176,8 +1173,8 @@ __global__ void __launch_bounds__(128) kv_combine_kernel(const __grid_constant__
         F.z = fmaf(v.z, e, F.z);
         F.w = fmaf(v.w, e, F.w);
     }
-    const int i = rr / p.group;
-    store_out<typename C::T>(p, vec_out != 0, rq.q0 + i, h * p.group + (rr - i * p.group), D, d, F, M, Ls);
+    const int h = (uint32_t)meta.z >> 16, rr = (meta.z & 0xffff) + col, i = rr / p.group;
+    store_out<typename C::T>(p, vec_out != 0, meta.y + i, h * p.group + (rr - i * p.group), D, d, F, M, Ls);
 }
 
 template <class C>
