@@ -456,3 +456,73 @@ def test_step_on_another_stream_and_in_a_graph():
         assert bool(((out.double() - ref).abs() <= bound).all())
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+def test_plan_writes_only_its_outputs():
+    rng = random.Random(3)
+    kv, q, table, free, count = make_step(rng, 37, 16, 9, 50, 4)
+    T = sum(max(n, 0) for n in q) + 5
+    want = plan_reference(kv, q, table, free, count, 16, T)
+    pads, parts = [], []
+    for n, dt in ((T, torch.int64), (T, torch.int32), (38, torch.int32), (37, torch.int32), (1, torch.int32), (4, torch.int32)):
+        raw = torch.full((n + 64,), 0x5A5A5A5A, dtype=dt, device="cuda")
+        pads.append((raw, n))
+        parts.append(raw[32:32 + n])
+    tb, fr = i32(table), i32(free)
+    p = g4.gai4_kv_plan(i32(kv), i32(q), tb, fr, i32([count]), 16, T, out=g4.KvPlan(*parts))
+    assert p.slots.tolist() == want["slots"] and p.positions.tolist() == want["positions"]
+    assert p.cu_q.tolist() == want["cu_q"] and p.kv_lens.tolist() == want["kv_lens"] and int(p.free_count) == want["count"]
+    assert tb.tolist() == want["table"] and fr.tolist() == want["free"]
+    for raw, n in pads:
+        assert bool((raw[:32] == 0x5A5A5A5A).all()) and bool((raw[32 + n:] == 0x5A5A5A5A).all())
+
+
+def test_append_infinite_and_nan_rows_stay_their_own():
+    H, D, gs, page = 2, 64, 32, 16
+    x = torch.randn(6, H, D, generator=torch.Generator().manual_seed(2)).bfloat16()
+    bad = x.clone()
+    bad[1, 0, 3], bad[2, 1, 40], bad[4, 0, 0] = float("nan"), float("inf"), -float("inf")
+    slots = torch.arange(6, device="cuda")
+    caches = []
+    for y in (x, bad):
+        kc, vc = (g4.gai4_kv_cache(1, H, page, D, gs) for _ in range(2))
+        g4.gai4_kv_append(y.cuda(), y.cuda(), slots, kc, vc, group_size=gs)
+        caches.append(g4.gai4_kv_read(kc, slots, group_size=gs))
+    touched = torch.zeros(6, H, D // gs, dtype=torch.bool)
+    touched[1, 0, 0] = touched[2, 1, 1] = touched[4, 0, 0] = True
+    same = (caches[0] == caches[1]).view(6, H, D // gs, gs).all(-1).cpu()
+    assert bool((same | touched).all())
+
+
+@pytest.mark.parametrize("dt,most", [("f32", 1e-5), ("f16", 4e-4)])
+@pytest.mark.parametrize("d,gs", [(64, 32), (128, 64), (128, 128)])
+def test_long_contexts_keep_their_precision(dt, most, d, gs):
+    """The norm of the error over that of the output, where thousands of values nearly cancel: f16 by the rounding of
+    the output (2^-12 on average over sqrt 3, 2.1e-4 at most) and of the probabilities times centred codes (as much
+    again by one and a half); f32 by binary32 sums of a few 2^-24 of the centred codes."""
+    q, kc, vc, table, kv, cu = problem([30000, 9000], [1, 1], 2, 4, d, gs, 64, dt, 83)
+    out = g4.gai4_kv_attention(q, kc, vc, table, i32(kv), i32(cu), group_size=gs)
+    ref, _, _, _ = attention64(q, kc, vc, table, kv, cu, gs, d ** -0.5, 0, dt)
+    assert float((out.double() - ref).norm() / ref.norm()) < most
+
+
+def test_many_steps_in_sequence():
+    """Thirty decoding steps without a synchronisation between them: every step's attention sees its own append."""
+    hkv, g, d, gs, page, B = 2, 4, 64, 32, 16, 3
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    kc, vc = (g4.gai4_kv_cache(12, hkv, page, d, gs) for _ in range(2))
+    lens, free, count = i32([0] * B), i32(list(range(12))), i32([12])
+    table = i32([[-1] * 4] * B)
+    q_lens, xs, outs = i32([1] * B), [], []
+    for _ in range(30):
+        x = torch.randn(B, (g + 2) * hkv, d, generator=gen, device="cuda").bfloat16()
+        q, k, v = x.split([g * hkv, hkv, hkv], 1)
+        p = g4.gai4_kv_plan(lens, q_lens, table, free, count, page, B)
+        g4.gai4_kv_append(k, v, p.slots, kc, vc, group_size=gs)
+        outs.append(g4.gai4_kv_attention(q, kc, vc, table, p.kv_lens, p.cu_q, group_size=gs))
+        lens, count = p.kv_lens, p.free_count
+        xs.append(x)
+    for n in (1, 2, 7, 16, 17, 30):
+        q = xs[n - 1][:, :g * hkv]
+        ref, bound, _, _ = attention64(q, kc, vc, table, [n] * B, [0, 1, 2, 3], gs, d ** -0.5, 0, "bf16")
+        assert bool(((outs[n - 1].double() - ref).abs() <= bound).all()), n
