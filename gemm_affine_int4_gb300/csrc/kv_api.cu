@@ -164,7 +164,7 @@ gai4_status gai4_kv_attention(const void* q, int64_t q_token_stride, const uint3
     L.lse = lse;
     L.batch = (int)batch;
     L.num_tokens = num_tokens;
-    L.max_q_len = max_q_len;
+    L.max_q_len = std::min(max_q_len, num_tokens);   // (times the group: below 2^31)
     L.scale = scale;
     L.window = window;
     L.workspace = workspace;
@@ -173,7 +173,7 @@ gai4_status gai4_kv_attention(const void* q, int64_t q_token_stride, const uint3
     if (!L.status) return GAI4_ERR_CUDA;
     cudaStream_t cs = (cudaStream_t)stream;
     if (dtype == GAI4_F32) return done(launch_kv_attention_f32(L, cs));
-    if (max_q_len * L.group > kManyRows) return done(launch_kv_attention_tc(L, cs));
+    if (L.max_q_len * L.group > kManyRows) return done(launch_kv_attention_tc(L, cs));
     return done(dtype == GAI4_F16 ? launch_kv_attention_f16(L, cs) : launch_kv_attention_bf16(L, cs));
 }
 

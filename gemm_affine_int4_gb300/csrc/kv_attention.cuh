@@ -39,6 +39,8 @@
 
 #include <math.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 #include "pipeline.cuh"
@@ -51,6 +53,13 @@ using namespace pipe;
 constexpr int kTile = 64;                       // tokens of a stage of the ring, loaded at once
 constexpr int kSub = 32;                        // tokens that a consumer warp works on: half a stage
 constexpr int kBlocks = kSub / 16;              // 16-token blocks of a sub-tile
+// Units of up to so many tokens, by the width of the block table or the window:
+// they are not cut, and the joining kernel is not launched. Measured not cut / cut, in us, at 8 key/value heads
+// of 128 and 4 query heads each: one request of 60 tokens 6.4/9.0, of 300
+// 8.3/8.9, of 500 9.7/9.3, of 1000 12.6/10.4; 16 requests of 500 11.6/13.1, of
+// 1000 15.6/14.5; 64 of 500 20.8/24.1, of 1000 30.2/32.1, of 2000 46.9/42.5.
+// The host's part of a call falls by 2.5 us as well.
+constexpr int kWholeTokens = 512;
 constexpr int kStart = 6;                       // what the start and join of a unit cost, in tiles (see Walk)
 
 template <typename T_, int D_, int GS_, int NT_>
@@ -192,9 +201,10 @@ __device__ __forceinline__ int lowest_key(const KvAttnLaunch& p, long long pos) 
 // A warp's walk along the line of tiles. Each unit begins with kStart places
 // without work, which stand for its query load and join, so that CTAs with
 // many short units get fewer tiles; a unit belongs to the CTA that has its
-// first tile's place. Kept in shared memory (every lane writes the same): it
+// first tile's place. Without CUT that CTA has all of it, and no other kernel
+// has to join anything. Kept in shared memory (every lane writes the same): it
 // is needed between segments, and the consumers have no registers to spare.
-template <int NC>
+template <int NC, bool CUT>
 struct Walk {
     long long c, c1;
     int r, h, rb, nrb, place;   // request, head, row block (of nrb), place within the unit (tile + kStart)
@@ -215,7 +225,13 @@ struct Walk {
         settle(p);
     }
     __device__ bool more() const { return c < c1; }
-    __device__ int here() const { return (int)min((long long)(q.ntile + kStart - place), c1 - c); }   // places of this segment
+    // places of this segment
+    __device__ int here() const {
+        const int rest = q.ntile + kStart - place;
+        return CUT ? (int)min((long long)rest, c1 - c) : rest;
+    }
+    // it has no tile (without CUT: none of this CTA's)
+    __device__ bool idle() const { return CUT ? place + here() <= kStart : place > kStart || c + (kStart - place) >= c1; }
     __device__ bool begins() const { return place <= kStart; }
     __device__ bool ends() const { return place + here() == q.ntile + kStart; }
     __device__ void step(const KvAttnLaunch& p) {
@@ -235,7 +251,7 @@ struct Walk {
     }
     // on to a segment with a tile's place (or the end), and its limits
     __device__ void settle(const KvAttnLaunch& p) {
-        while (more() && place + here() <= kStart) step(p);
+        while (more() && idle()) step(p);
         if (!more()) return;
         const int rr0 = rb * NC;
         L.rows = min(NC, q.qn * p.group - rr0);
@@ -264,8 +280,8 @@ struct Walk {
 // side, issued by one lane each; scales and biases, a ninth of the bytes, by
 // 16-byte asynchronous copies of the whole warp: bulk copies take a lane's
 // issue each, and with small pages there would be up to 24 of them.
-template <class C>
-__device__ __forceinline__ void producer(const KvAttnLaunch& p, Walk<C::NC>& w, uint8_t* ring, uint64_t* full,
+template <class C, bool CUT>
+__device__ __forceinline__ void producer(const KvAttnLaunch& p, Walk<C::NC, CUT>& w, uint8_t* ring, uint64_t* full,
                                          uint64_t* empty, uint32_t* masks, const Ctl& ctl) {
     constexpr int S = C::kStages;
     constexpr int kRow = C::NG * C::E;                      // bytes of a token's scales (or biases)
@@ -532,9 +548,9 @@ __device__ __forceinline__ uint32_t value_codes(uint32_t w) {
     return d;
 }
 
-template <class C>
+template <class C, bool CUT>
 __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mask, int tok0, const Query<C>& Q,
-                                     const KvAttnLaunch& p, const Walk<C::NC>& w, int lo_max, int hi_min, Acc<C>& A) {
+                                     const KvAttnLaunch& p, const Walk<C::NC, CUT>& w, int lo_max, int hi_min, Acc<C>& A) {
     using T = typename C::T;
     constexpr int NT = C::NT, NG = C::NG, D = C::D, GS = C::GS;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -933,7 +949,7 @@ __device__ __forceinline__ void store_out(const KvAttnLaunch& p, bool vec, long 
             l == 0.f ? -INFINITY : fmaf(m, 0.6931471805599453f, logf(l));
 }
 
-template <class C>
+template <class C, bool CUT>
 __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     kv_attention_kernel(const __grid_constant__ KvAttnLaunch p, const int vec_q, const int vec_out) {
     using T = typename C::T;
@@ -1012,21 +1028,21 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     float* recs = reinterpret_cast<float*>(ws + meta_bytes(gridDim.x)) + blockIdx.x * 2 * rec_floats(C::NC, C::D);
     __syncthreads();
     if (c0 >= c1) {
-        if (tid == 0) *meta = make_int4(-1, 0, 0, 0);
+        if (CUT && tid == 0) *meta = make_int4(-1, 0, 0, 0);
         return;
     }
 
-    __shared__ Walk<C::NC> walks[C::kWarps + 1];
-    Walk<C::NC>& w = walks[warp];
+    __shared__ Walk<C::NC, CUT> walks[C::kWarps + 1];
+    Walk<C::NC, CUT>& w = walks[warp];
     {
-        Walk<C::NC> first;
+        Walk<C::NC, CUT> first;
         first.init(p, start_r, start_off, c0, c1);
         w = first;
         __syncwarp();
     }
     const Ctl ctl{p.status, p.spin_limit, &abort_flag};
     if (warp == C::kWarps) {
-        producer<C>(p, w, ring, full, empty, masks, ctl);
+        producer<C, CUT>(p, w, ring, full, empty, masks, ctl);
         return;
     }
     // ---- consumers. Each warp deposits its part of a segment and goes on; the
@@ -1036,7 +1052,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     int my = warp, slot = warp >> 1, phase = 0;    // this warp's next sub-tile: every kWarps-th, and its stage's slot
     int turn = 0;                                  // the warp that joins the current segment
     uint32_t parity = 0;                           // of the segments' number
-    if (tid == 0) *meta = make_int4(-1, 0, 0, 0);  // until this CTA holds the beginning of a unit that goes on
+    if (CUT && tid == 0) *meta = make_int4(-1, 0, 0, 0);  // until this CTA holds the beginning of a unit that goes on
     RawQuery<C> raw;                               // (fetched by every warp, with a part in the segment or not: by
     bool more = w.more();                          // some, it would live in registers all along)
     if (more) fetch_query<C>(p, w.q, w.h, w.rb, vec_q != 0, raw);
@@ -1065,7 +1081,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
                                                                 k * C::kSb)[(sub * kSub + lane) * (C::NG * C::E / 2) + i] = 0;
                         __syncwarp();
                     }
-                    tile<C>(st, sub, mask, tok0, Q, p, w, lo_max, hi_min, A);
+                    tile<C, CUT>(st, sub, mask, tok0, Q, p, w, lo_max, hi_min, A);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[slot]);
@@ -1086,7 +1102,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         seq = end;
         const bool begins = w.begins(), whole = begins && w.ends();
         const int q0 = w.q.q0 + w.L.i0, h = w.h, first = w.L.first, rows = w.L.rows;
-        if (begins && !whole && tid == 0) {
+        if (CUT && begins && !whole && tid == 0) {
             const long long end_of_unit = w.c - w.place + w.q.ntile + kStart;   // on the line
             *meta = make_int4((int)((end_of_unit - 1) / per), q0, h << 16 | first, rows);
         }
@@ -1097,7 +1113,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
             (void)warp_wait(deposited, parity, ctl);
             float* rec = recs + (begins ? rec_floats(C::NC, C::D) : 0);
             join<C>(buf, rows, [&](int col, int d, float4 f, float m, float l) {
-                if (whole) {
+                if (!CUT || whole) {
                     const int i = (first + col) / p.group;
                     store_out<T>(p, vec_out != 0, q0 + i, h * p.group + (first + col - i * p.group), C::D, d, f, m, l);
                 } else {
@@ -1183,10 +1199,17 @@ cudaError_t launch(const KvAttnLaunch& L, cudaStream_t s) {
     const int vec_q = ((uintptr_t)L.q & 15) == 0 && L.q_stride * e % 16 == 0;
     const int vec_out = ((uintptr_t)L.out & 15) == 0 && L.out_stride * e % 16 == 0;
     const int ctas = num_sms() * C::kCtas;
-    static bool allowed[64];
-    cudaError_t err = allow_smem_once(kv_attention_kernel<C>, C::kSmem, allowed);
+    static bool allowed[2][64];
+    long long tokens = L.max_blocks << L.sh.page_log2;   // of the longest unit
+    if (L.window > 0 && L.window <= kWholeTokens) tokens = std::min(tokens, (long long)(L.window + L.max_q_len));
+    if (tokens <= kWholeTokens) {
+        const cudaError_t err = allow_smem_once(kv_attention_kernel<C, false>, C::kSmem, allowed[0]);
+        if (err != cudaSuccess) return err;
+        return launch_pdl(kv_attention_kernel<C, false>, dim3(ctas), dim3(C::kThreads), C::kSmem, s, L, vec_q, vec_out);
+    }
+    cudaError_t err = allow_smem_once(kv_attention_kernel<C, true>, C::kSmem, allowed[1]);
     if (err != cudaSuccess) return err;
-    err = launch_pdl(kv_attention_kernel<C>, dim3(ctas), dim3(C::kThreads), C::kSmem, s, L, vec_q, vec_out);
+    err = launch_pdl(kv_attention_kernel<C, true>, dim3(ctas), dim3(C::kThreads), C::kSmem, s, L, vec_q, vec_out);
     if (err != cudaSuccess) return err;
     return launch_pdl(kv_combine_kernel<C>, dim3(ctas, C::NC), dim3(128), 0, s, L, ctas, vec_out);
 }

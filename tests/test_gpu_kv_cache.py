@@ -283,6 +283,23 @@ def test_window(dt, window, q_len):
     check(*problem(kv, [q_len] * len(kv), 2, 4, 128, 64, 32, dt, 31), 64, dt, window=window)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("width_extra,window", [(0, 0), (1, 0), (60, 300), (60, 510), (60, 511)])
+@pytest.mark.parametrize("q_len", [1, 2])
+def test_units_up_to_and_above_512_tokens(dt, width_extra, window, q_len):
+    """Block tables of 512 tokens and of one page more; windows that with the queries end at or above 512."""
+    kv = [512, 511, 449, 448, 65, 64, 1, 0, 130, 512, 20]
+    q = [min(q_len, k) for k in kv]
+    check(*problem(kv, q, 2, 4, 128, 64, 16, dt, 47, width_extra=width_extra), 64, dt, window=window)
+
+
+def test_largest_query_length_is_only_a_hint():
+    """max_q_len picks the kernel: any value gives the rows their answer, within the wider bound."""
+    a = problem([70, 300, 5], [1, 40, 3], 2, 4, 64, 32, 32, "bf16", 49)
+    for max_q in (0, 1, 2, 3, 8, 9, 40, 1000, 2**62):
+        check(*a, 32, "bf16", max_q=max_q, many=True)
+
+
 def test_window_pages_may_be_gone():
     """Pages that the window has passed: invalid table entries in their place."""
     q, kc, vc, table, kv, cu = problem([700], [2], 2, 4, 128, 64, 32, "f16", 37)
