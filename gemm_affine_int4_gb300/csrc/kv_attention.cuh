@@ -533,7 +533,6 @@ __device__ __forceinline__ void make_query(const KvAttnLaunch& p, const RawQuery
     }
 }
 
-// what columns 2t and 2t + 1 of each 8-column block may see: keys [lo, hi)
 // two codes as binary16: c 2^-24 (bits 0..3 of the halves) or c 2^-20 (bits
 // 4..7) as they stand, or c - 8 (exact)
 template <bool CENTRED, int HIGH>
@@ -546,6 +545,44 @@ __device__ __forceinline__ uint32_t value_codes(uint32_t w) {
     else                  // (1024 + c) - 1032
         asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(c | 0x64006400u), "r"(0x64086408u));
     return d;
+}
+
+// Tokens (bits of `bad`) with groups of values that are not finite: the rows
+// that see such a token get NaN in the group's channels, and the group is
+// zeroed in the stage, so that 0 x NaN does not reach the rows that do not see
+// it, nor an infinite scale the others' R.
+template <class C, bool CUT>
+__device__ __forceinline__ void set_apart(const uint8_t* stage, int sub, uint32_t bad, int tok0, const Walk<C::NC, CUT>& w,
+                                          const KvAttnLaunch& p, Acc<C>& A) {
+    using St = typename C::T::storage;
+    const int lane = threadIdx.x & 31, t = lane & 3;
+    St* vsc = reinterpret_cast<St*>(const_cast<uint8_t*>(stage) + 2 * C::kCodes + 2 * C::kSb) + (sub * kSub + lane) * C::NG;
+    St* vbi = vsc + kTile * C::NG;
+    uint32_t groups = 0;
+#pragma unroll
+    for (int k = 0; k < C::NG; ++k) {
+        const float s = C::T::to_f32(vsc[k]), b = C::T::to_f32(vbi[k]);
+        if (fabsf(s) < INFINITY && fabsf(b) < INFINITY) continue;
+        groups |= 1u << k;
+        vsc[k] = vbi[k] = St(0);
+    }
+    for (; bad != 0; bad &= bad - 1) {
+        const int o = __ffs(bad) - 1, j = tok0 + o;
+        const uint32_t of = __shfl_sync(0xffffffffu, groups, o);
+#pragma unroll
+        for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int col = n * 8 + 2 * t + c;
+                const long long pos = (long long)w.q.kv - w.q.qn + w.L.i0 + (w.L.first + col) / p.group;
+                if (col >= w.L.rows || j > pos || j < lowest_key(p, pos)) continue;
+#pragma unroll
+                for (int k = 0; k < C::NG; ++k)
+                    if ((of >> k) & 1u) A.ab[k][n][c] = __uint_as_float(0x7fffffffu);
+            }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the next fill
+    __syncwarp();
 }
 
 template <class C, bool CUT>
@@ -681,18 +718,31 @@ __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mas
             mx[n][c] = m;
             grew |= m > A.m[n][c];
         }
-    // whether R has to grow: the largest value scale of the tile
-    float smax = 0.f;
+    // whether R has to grow: the largest value scale of the tile (non-negative
+    // numbers, infinity and NaN are ordered as integers)
+    uint32_t smax = 0, bmax = 0;
     static_assert(kSub == 32, "a lane per token");
     {
-        float s[NG];
+        float s[NG], b[NG];
         load_groups<T, NG>(vsc + lane * NG * C::E, s);
+        load_groups<T, NG>(vbi + lane * NG * C::E, b);
 #pragma unroll
-        for (int k = 0; k < NG; ++k) smax = fmaxf(smax, fabsf(s[k]));
+        for (int k = 0; k < NG; ++k) {
+            smax = max(smax, __float_as_uint(s[k]) & 0x7fffffffu);
+            bmax = max(bmax, __float_as_uint(b[k]) & 0x7fffffffu);
+        }
     }
-    const bool wider = smax > __uint_as_float((uint32_t)A.re << 23);
-    if (__any_sync(0xffffffffu, grew || wider)) {
-        const uint32_t sb = __reduce_max_sync(0xffffffffu, __float_as_uint(smax));   // non-negative: ordered as integers
+    if (__any_sync(0xffffffffu, grew || smax > (uint32_t)A.re << 23 || bmax >= 0x7f800000u)) {
+        const uint32_t bad = __ballot_sync(0xffffffffu, max(smax, bmax) >= 0x7f800000u);
+        if (bad != 0) {
+            set_apart<C, CUT>(stage, sub, bad, tok0, w, p, A);
+            float s[NG];
+            load_groups<T, NG>(vsc + lane * NG * C::E, s);
+            smax = 0;
+#pragma unroll
+            for (int k = 0; k < NG; ++k) smax = max(smax, __float_as_uint(s[k]) & 0x7fffffffu);
+        }
+        const uint32_t sb = __reduce_max_sync(0xffffffffu, smax);
         const int ne = max(A.re, min((int)(sb >> 23) + ((sb & 0x7fffffu) != 0), 254));
         const float down = A.re == ne ? 1.f : ex2((float)(A.re - ne));
         A.re = ne;
@@ -1079,6 +1129,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
                                 for (int i = 0; i < C::NG * C::E / 2; ++i)
                                     reinterpret_cast<uint16_t*>(st + 2 * C::kCodes +
                                                                 k * C::kSb)[(sub * kSub + lane) * (C::NG * C::E / 2) + i] = 0;
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the next fill
                         __syncwarp();
                     }
                     tile<C, CUT>(st, sub, mask, tok0, Q, p, w, lo_max, hi_min, A);

@@ -255,6 +255,14 @@ __device__ __forceinline__ uint4 expand(uint32_t w, const Group<BF>& g) {
     return o;
 }
 
+// Values of a group that cannot be expanded: scale or bias is not finite (bf16:
+// or the scale is 2^35 or more). A sign bit of one of the result's halves says
+// so, the scale's in the lower one.
+template <bool BF>
+__device__ __forceinline__ uint32_t too_wide(uint32_t s, uint32_t b) {
+    return ((s | b << 16) & 0x7fff7fffu) + (BF ? 0x00802F00u : 0x04000400u);
+}
+
 // columns of tensor memory (128 for each M tile)
 constexpr uint32_t kS = 0, kO = 256;
 
@@ -412,6 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t raw[];
     __shared__ long long warp_cost[kThreads / 32], start_off;
     __shared__ int start_r, abort_flag;
+    __shared__ volatile int wide_values;   // some value tile had groups that were set apart (see below)
     __shared__ uint32_t tmem_slot;
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::bars);
@@ -441,6 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(o_full, 1);
         mbar_init(fin, 1);
         abort_flag = 0;
+        wide_values = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
     }
@@ -684,27 +694,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int side = 0; side < 2; ++side) {      // keys, values
                     uint8_t* dst = smem + (side ? M::v : M::k) + buf * M::kTile;
                     (void)warp_wait(&ring_full[s], parity, ctl);
+                    const uint8_t* st = smem + M::ring + s * M::kStage;
+                    const bool valid = (masks[4 * s] >> (r & 31)) & 1u;   // else zeros: the slot may hold anything
+                    uint4 y[D / 32];
+                    uint32_t scale[D / 32], bias[D / 32];
+#pragma unroll
+                    for (int x = 0; x < D / 32; ++x) {   // (all loads before the first store: they may not pass one)
+                        y[x] = *reinterpret_cast<const uint4*>(st + from[x]);
+                        const uint8_t* sc = st + group[x];
+                        scale[x] = valid ? *reinterpret_cast<const uint16_t*>(sc) : 0u;
+                        bias[x] = valid ? *reinterpret_cast<const uint16_t*>(sc + kKeys * 2 * ng) : 0u;
+                    }
+                    // Values that are not finite would reach the rows that do not see their token, as 0 x NaN: zeros
+                    // in their place, and the softmax warps put NaN into the outputs that need it.
+                    uint32_t wide = 0;
+#pragma unroll
+                    for (int x = 0; x < D / 32; ++x) wide |= too_wide<BF>(scale[x], bias[x]);
+                    if (side && (wide & 0x80008000u)) {
+#pragma unroll
+                        for (int x = 0; x < D / 32; ++x)
+                            if (too_wide<BF>(scale[x], bias[x]) & 0x80008000u) scale[x] = bias[x] = 0;
+                        wide_values = 1;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ring_empty[s]);
                     // the buffer's last tile was j - kBufs
                     const int t = j - kBufs + side;
                     if (t >= 0) (void)warp_wait(&done[t & 1], (t >> 1) & 1, ctl);
-                    const uint8_t* st = smem + M::ring + s * M::kStage;
-                    const bool valid = (masks[4 * s] >> (r & 31)) & 1u;   // else zeros: the slot may hold anything
 #pragma unroll
                     for (int x = 0; x < D / 32; ++x) {
-                        const uint4 y = *reinterpret_cast<const uint4*>(st + from[x]);
-                        const uint8_t* sc = st + group[x];
-                        const Group<BF> gr(valid ? *reinterpret_cast<const uint16_t*>(sc) : 0u,
-                                           valid ? *reinterpret_cast<const uint16_t*>(sc + kKeys * 2 * ng) : 0u);
-                        const uint32_t ww[4] = {y.x, y.y, y.z, y.w};
+                        const Group<BF> gr(scale[x], bias[x]);
+                        const uint32_t ww[4] = {y[x].x, y[x].y, y[x].z, y[x].w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(dst + to[x] + chunk[e]) = expand<BF>(ww[e], gr);
                     }
                     fence_async();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(side ? &v_full[buf] : &k_full[buf]);
-                        mbar_arrive(&ring_empty[s]);
-                    }
+                    if (lane == 0) mbar_arrive(side ? &v_full[buf] : &k_full[buf]);
                     if (++s == kRing) {
                         s = 0;
                         parity ^= 1u;
@@ -895,6 +921,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_after();
         const bool begins = cur->first() == 0, whole = begins && cur->last() == cur->n, mine = i < cur->tiles_m();
         const int row0 = cur->row0, rows = cur->rows, rq_q0 = cur->q.q0, h = cur->h;
+        // groups whose channels are NaN in this row: values that were set apart (a flag of the CTA, which stays)
+        uint32_t nan_groups = 0;
+        if (mine && wide_values) {
+            const int row = row0 + i * 128 + r, pl = p.sh.page_log2, ng = D >> gs_log2;
+            const long long pos = (long long)cur->q.kv - cur->q.qn + row / p.group;
+            const long long lo = p.window > 0 ? pos - p.window + 1 : 0;
+            const int end = min((cur->t_first + cur->last()) * kKeys, cur->q.kv);
+            const int* table = p.table + (long long)cur->r * p.max_blocks;
+#pragma unroll 1
+            for (int key0 = (cur->t_first + cur->first()) * kKeys; key0 < end; key0 += 32) {
+                const int key = key0 + lane, page = key < end ? table[key >> pl] : -1;
+                uint32_t groups = 0;
+                if (page >= 0 && page < p.sh.num_blocks) {
+                    const long long at = ((((long long)page * p.sh.hkv + h) << pl) + (key & ((1 << pl) - 1))) * ng;
+#pragma unroll 1
+                    for (int g = 0; g < ng; ++g)
+                        if (too_wide<BF>(static_cast<const uint16_t*>(p.v.scales)[at + g],
+                                         static_cast<const uint16_t*>(p.v.biases)[at + g]) & 0x80008000u)
+                            groups |= 1u << g;
+                }
+#pragma unroll 1
+                for (uint32_t some = __ballot_sync(0xffffffffu, groups != 0); some != 0; some &= some - 1) {
+                    const int o = __ffs(some) - 1;
+                    const uint32_t of = __shfl_sync(0xffffffffu, groups, o);
+                    if (key0 + o >= lo && key0 + o <= pos) nan_groups |= of;
+                }
+            }
+        }
+        auto is_nan = [&](int c) { return ((nan_groups >> ((32 * c) >> gs_log2)) & 1u) != 0; };   // channels 32 c on
         if (mine && whole) {
             const float inv = l > 0.f ? kUndo<BF> / l : 0.f;
 #pragma unroll 1
@@ -902,6 +957,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t v[32];
                 tmem_ld32(o_tm + 32 * c, v);
                 tmem_ld_wait();
+                if (is_nan(c)) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0x7fffffffu;
+                }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float y[8];
@@ -929,6 +988,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t v[32];
                     tmem_ld32(o_tm + 32 * c, v);
                     tmem_ld_wait();
+                    if (is_nan(c)) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = 0x7fffffffu;
+                    }
                     if (row0 + i * 128 + r < rows) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)

@@ -350,6 +350,40 @@ def test_sharp_and_wide_values(dt, many):
     check(qq, kc, vc, table, kv, cu, 64, dt, many=many, scale=-0.7)
 
 
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("dt,kv,q,window,many", [
+    ("bf16", 300, 1, 50, False), ("f16", 300, 3, 0, False), ("f16", 1000, 5, 70, False), ("f32", 300, 4, 0, False),
+    ("f32", 500, 40, 100, False), ("bf16", 300, 100, 0, True), ("f16", 1100, 300, 130, True),
+    ("bf16", 9000, 20, 5000, True)])
+def test_rows_do_not_meet_tokens_they_do_not_see(dt, kv, q, window, many, what, value):
+    """Scales or biases of one group that are not finite, at tokens that some rows see and others do not (and one that
+    none sees): keys touch the rows that see them (an infinite score may be minus infinity), values the group's channels
+    of these rows, and nothing else."""
+    hkv, g, d, gs, page = 2, 4, 64, 32, 32
+    qs, kc, vc, table, kvs, cu = problem([kv], [q], hkv, g, d, gs, page, dt, 53)
+    clean, bound, _, _ = attention64(qs, kc, vc, table, kvs, cu, gs, d ** -0.5, window, dt, many)
+    tokens = {kv - 1: 1, kv - 1 - q // 2: 2}                 # token: scale (1) or bias (2)
+    if window:
+        tokens.update({kv - q - window: 1, kv - q + 1 - window + q // 2: 2})
+    cache = tuple(x.clone() for x in (kc if what == "k" else vc))
+    for t, field in tokens.items():
+        cache[field][int(table[0, t // page]), 1, t % page, 1] = value
+    args = (qs, cache, vc) if what == "k" else (qs, kc, cache)
+    out = g4.gai4_kv_attention(*args, table, i32(kvs), i32(cu), group_size=gs, scale=d ** -0.5, window=window, max_q_len=q)
+    pos = torch.arange(kv - q, kv, device="cuda")
+    hit = torch.zeros(q, dtype=torch.bool, device="cuda")
+    for t in tokens:
+        hit |= (t <= pos) & ((t > pos - window) if window else True)
+    assert bool(hit.any()) and (q == 1 or not bool(hit.all()) or window)
+    gone = torch.zeros(q, hkv * g, d, dtype=torch.bool, device="cuda")
+    gone[hit, g:, 0 if what == "k" else gs:] = True
+    if what == "v" or value != value:
+        assert not bool(out[gone].isfinite().any())
+    err = torch.where(gone, 0.0, (out.double() - clean).abs())
+    assert bool((err <= bound).all()), f"{int((~(err <= bound)).sum())} outside"
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_extreme_queries(dt):
     """Query magnitudes from 2^-60 to 2^60 (scores stay finite through the scale), zero and tiny rows."""
