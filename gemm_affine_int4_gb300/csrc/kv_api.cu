@@ -39,9 +39,13 @@ gai4_status check_cache(const KvCache& c) {
     return GAI4_OK;
 }
 
-// Query rows per key/value head up to which the split kernel (16 rows a pass
-// over the keys, memory-bound) is taken; above, the tensor-core kernel (256
-// rows a pass).
+// Query rows per key/value head up to which the split kernel (8 or 16 rows a
+// pass over the keys) is taken; above, the tensor-core kernel (256 rows a
+// pass). Split / tensor-core kernel in us, bf16, 8 key/value heads of 128, at
+// 16, 24, 32 and 40 rows: 16 requests of 4000 tokens 45/67, 70/67, 76/68,
+// 102/68; 20 of 16000 138/215, -, 257/217, 369/217; 64 of 1000 78/110, -,
+// 133/112, -; one of 4000 17/-, 18/-, 18/-, 21/37. The two meet between 24 and
+// 32 rows, and up to there the split kernel also rounds less.
 constexpr int kManyRows = 32;
 
 // the split kernel: two records of 16 query rows (32-bit O, m, l) for each of

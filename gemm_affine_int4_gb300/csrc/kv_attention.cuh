@@ -6,8 +6,9 @@
 // sum_g s_g (q_g . c_g) + b_g (sum of q_g): the 4-bit codes go into the matrix
 // unit as they are (exact in binary16) and scale and bias are applied to the
 // products in binary32. For values, p_j s_j is rounded to binary16 and
-// multiplied with the codes, and sum_j p_j b_j is kept in binary32. So no key
-// or value is ever rounded; softmax maximum and sum run over the keys once.
+// multiplied with the codes less 8, and sum_j p_j (b_j + 8 s_j) is kept in
+// binary32. So no key or value is ever rounded; softmax maximum and sum run
+// over the keys once.
 //
 //  * A code masked out of its word is a binary16 subnormal, c * 2^-24 (bits
 //    0..3 of a half) or c * 2^-20 (bits 4..7): no conversion at all. The query
@@ -16,25 +17,36 @@
 //    that meet bits 4..7); the powers of two leave in the score's factor.
 //  * The value side's p s is scaled by a power of two R that follows the
 //    largest |s| seen (accumulators are rescaled when it grows), so any range
-//    of scales works and binary16 has 38 bits of room.
+//    of scales works and binary16 has 38 bits of room. Rounding p s to 11 bits
+//    is the path's one rounding below 32 bits: its errors are independent from
+//    key to key, and bf16 / f16 outputs are rounded to 8 / 11 bits after it
+//    (4 requests of 131072 f16 tokens: 3.1e-4 of the outputs' size, against
+//    2.1e-4 for the output's rounding alone).
 //  * f32 queries and f32 p s are split in two binary16 parts (22 bits).
 //
 // Shape of the products (mma m16n8k16, tokens or value channels along M, query
 // rows along N): S^T = K Q^T and O^T = V^T P^T. One N tile is 8 query rows
 // (tokens x query heads of one key/value head), so the usual 4 to 8 query
-// heads per key head waste little. The matrix rate is no limit here: at 8
-// rows a cached row of 144 bytes takes 4096 multiply-adds, a fifth of the rate
-// that mma.sync reaches at the memory's speed; tcgen05 would need the codes
-// expanded through shared memory first.
+// heads per key head waste little. The matrix unit is no limit here (24 % busy);
+// tcgen05 would need the codes expanded through shared memory first, which
+// costs more than all the rest of this kernel.
 //
 // Work split. Tokens are cut into 64-token tiles; a unit is (request,
 // key/value head, block of 8 NT query rows), and all units' tiles form one
 // line that is cut evenly over the CTAs: ragged lengths and few long requests
 // alike fill the GPU. In a CTA a producer warp streams tiles through a ring of
-// shared-memory stages (one bulk copy per page and array), consumer warps take
-// tiles in turn with accumulators of their own and join them at the end of
-// the unit. A unit that is cut leaves (m, l, O) records in the workspace,
-// which a second kernel joins in order; its launch overlaps the first.
+// shared-memory stages (one bulk copy per page and side for the codes, 16-byte
+// asynchronous copies for scales and biases), consumer warps take half a tile
+// in turn with accumulators of their own, and take turns at joining them at
+// the end of a unit, while the others go on. A unit that is cut leaves (m, l,
+// O) records in the workspace, which a second kernel joins in order; its
+// launch overlaps the first. No sum depends on timing: results repeat.
+//
+// What bounds it: instruction issue (58 % of the cycles; the rest are waits
+// within the two consumer warps that an SMSP has). 4 requests of 90001 to
+// 131072 tokens, 8 key/value heads of 128 f16 values, 8 query heads each (494
+// MB): 114 us, 4.3 TB/s; with the loads alone 83 us, with the products alone
+// 111. 48 requests of up to 4500 tokens (126 MB): 43 us.
 #pragma once
 
 #include <math.h>
@@ -53,14 +65,17 @@ using namespace pipe;
 constexpr int kTile = 64;                       // tokens of a stage of the ring, loaded at once
 constexpr int kSub = 32;                        // tokens that a consumer warp works on: half a stage
 constexpr int kBlocks = kSub / 16;              // 16-token blocks of a sub-tile
-// Units of up to so many tokens, by the width of the block table or the window:
-// they are not cut, and the joining kernel is not launched. Measured not cut / cut, in us, at 8 key/value heads
-// of 128 and 4 query heads each: one request of 60 tokens 6.4/9.0, of 300
+// Units of up to so many tokens, by the width of the block table or the
+// window: they are not cut, and the joining kernel is not launched. Measured
+// not cut / cut, in us, at 8 key/value heads of 128 and 4 query heads each: one request of 60 tokens 6.4/9.0, of 300
 // 8.3/8.9, of 500 9.7/9.3, of 1000 12.6/10.4; 16 requests of 500 11.6/13.1, of
 // 1000 15.6/14.5; 64 of 500 20.8/24.1, of 1000 30.2/32.1, of 2000 46.9/42.5.
 // The host's part of a call falls by 2.5 us as well.
 constexpr int kWholeTokens = 512;
-constexpr int kStart = 6;                       // what the start and join of a unit cost, in tiles (see Walk)
+// What the start and join of a unit cost, in tiles (see Walk). Measured with 2,
+// 4, 6 and 9: 48 ragged requests of up to 4500 tokens 52.7, 45.8, 42.2, 42.3
+// us; 96 of up to 2000 in a step 65, 57, 54, 54; 30 in f32 36.6, 34.0, 35.2, 36.1.
+constexpr int kStart = 6;
 
 template <typename T_, int D_, int GS_, int NT_>
 struct Cfg {
@@ -1266,7 +1281,10 @@ cudaError_t launch(const KvAttnLaunch& L, cudaStream_t s) {
 }
 
 // 8 columns when the rows of a request and head fit them, else 16 (fewer
-// passes over the keys)
+// passes over the keys, but half the warps per SM). With 16 rows, 8 / 16
+// columns, bf16, 8 key/value heads of 128: 20 requests of 16000 tokens 167/138
+// us, 16 of 4000 48.4/45.3, 64 of 1000 66/78, one of 4000 14.8/17.1; with 8
+// rows: 92/128, 30.9/39.1, -, -. Long contexts decide, where a call takes long.
 template <typename T>
 cudaError_t launch_type(const KvAttnLaunch& L, cudaStream_t s) {
     const bool one = L.max_q_len * L.group <= 8;

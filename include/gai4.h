@@ -443,13 +443,20 @@ gai4_status gai4_kv_read(const uint32_t* packed, const void* scales, const void*
  *        never read from, and their tokens are left out.
  *   max_q_len: the largest number of query rows of a request as far as the
  *        host knows; it only guides the choice of kernel.
+ * A row does not depend on tokens that it does not see, whatever their codes,
+ * scales and biases hold. A scale or bias that is infinite or NaN makes the
+ * rows that see it NaN: all of a row for keys (unless the score is -inf), the
+ * group's channels for values.
  * bf16 / f16: with few rows per key/value head the codes enter the matrix unit
  * as they are and scales and biases are applied in binary32; with many rows
- * (max_q_len * q_heads / kv_heads above 32) keys and values are rounded once
- * to T and multiplied on the tensor cores as in gai4_qmm_t. Softmax and sums
- * are binary32; scores, probabilities and lse in the f32 form are as exact as
- * binary32 sums are. Results do not depend on the contents of the workspace,
- * and repeat bit for bit.
+ * (max_q_len * q_heads / kv_heads above 32) keys, values and probabilities are
+ * rounded once to T and multiplied on the tensor cores as in gai4_qmm_t; keys
+ * and values are then at most 2^37 (bf16: values whose scale is 2^35 or more
+ * count as infinite) or 65504 (f16) in magnitude. Softmax and sums are
+ * binary32. f32: queries and probabilities enter as two binary16 parts, 22
+ * bits. Results do not depend on the contents of the workspace, and repeat bit
+ * for bit. num_tokens * (q_heads / kv_heads) above 2^31 - 1 is UNSUPPORTED;
+ * 1 <= batch < 2^27, page_size * max_blocks < 2^31.
  * workspace: 16-byte aligned, >= gai4_kv_attention_workspace_bytes(...).
  */
 gai4_status gai4_kv_attention(const void* q, int64_t q_token_stride, const uint32_t* k_packed, const void* k_scales,
