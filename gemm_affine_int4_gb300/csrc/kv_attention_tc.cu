@@ -44,14 +44,19 @@
 // Every barrier is waited on by the same role phase after phase.
 //
 // What bounds it: the chain scores - softmax - products of each M tile, of
-// which two hide each other only in part. A prompt of 8192 bf16 tokens, 8
+// which two hide each other only in part (of 3770 cycles a key tile, the
+// products take at least 2050, a row's softmax 2500 beside its neighbours), and
+// shared memory: Q K^T alone reads its full 128 bytes a cycle. A prompt of 8192 bf16 tokens, 8
 // key/value heads of 128, 4 query heads each (550 GFLOP below the diagonal):
-// 459 us, 1.2 PFLOP/s; without the exponentials 446, without the expansion 439,
+// 460 us, 1.2 PFLOP/s; without the exponentials 446, without the expansion 439,
 // without both 405. Six prompts' chunks of 333 to 1500 rows behind up to 7000
 // tokens: 336 us. Tensor pipe 53 % of the cycles.
 // Slower, and not kept: two warps that issue products (641 us at the time, with
 // one 456), eight warps that expand (532), 64-key tiles with the queries in
-// tensor memory (536), any further unrolling (the instruction cache).
+// tensor memory (536), any further unrolling (the instruction cache), two
+// threads a row (579; the expanding warps then wait for issue slots), the first
+// probabilities under the last tile's maximum beside the search for the new one
+// (468).
 #include <math.h>
 
 #include "common.cuh"
@@ -441,10 +446,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + M::bars);
     // (two of most: keys / values, M tiles, buffers)
-    // (done[t % kBufs]: the products QK of tile t have finished, and with them PV of tile t - 1)
+    // (done[t % kBufs]: the products QK of tile t have finished, and with them PV of tile t - 1; v_free[t % kBufs]: PV of
+    // tile t, which comes before QK of the second M tile's next scores)
     uint64_t *ring_full = bars, *ring_empty = bars + kRing, *k_full = bars + 2 * kRing, *v_full = k_full + kBufs,
              *done = v_full + kBufs, *s_full = done + kBufs, *p_full = s_full + 2, *q_full = s_full + 6, *o_full = s_full + 7,
-             *fin = s_full + 8;
+             *fin = s_full + 8, *v_free = s_full + 9;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
     if (tid == 0) {
@@ -456,6 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&k_full[i], 4);
             mbar_init(&v_full[i], 4);
             mbar_init(&done[i], 1);
+            mbar_init(&v_free[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
@@ -658,6 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 np0 ^= 1u;
                 fence_after();
                 pv(0, buf, 1, true);
+                if (!both) commit(&v_free[buf]);
                 if (more) qk(0, next);
                 if (both) {
                     wait(&p_full[2], np1);
@@ -667,6 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     np1 ^= 1u;
                     fence_after();
                     pv(1, buf, 1, true);
+                    commit(&v_free[buf]);
                     if (more) qk(1, next);
                 }
                 if (more) commit(&done[next]);
@@ -734,9 +743,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ring_empty[s]);
-                    // the buffer's last tile was j - kBufs
-                    const int t = j - kBufs + side;
-                    if (t >= 0) (void)warp_wait(&done[t & 1], (t >> 1) & 1, ctl);
+                    // the buffer's last tile
+                    const int t = j - kBufs;
+                    if (t >= 0) (void)warp_wait(side ? &v_free[buf] : &done[buf], (t >> 1) & 1, ctl);
 #pragma unroll
                     for (int x = 0; x < D / 32; ++x) {
                         const Group<BF> gr(scale[x], bias[x]);
