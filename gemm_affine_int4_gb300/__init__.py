@@ -395,6 +395,15 @@ def _stream_handle(stream, t: torch.Tensor) -> int:
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """torch.empty of the stream that will use it: the allocator hands a freed
+    block out again in the order of its own stream only."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _kv_shape(cache, group_size: int):
     """(num_blocks, kv_heads, page_size, head_dim) of a cache."""
     packed, scales, biases = cache
@@ -433,8 +442,8 @@ def gai4_kv_plan(kv_lens, q_lens, block_table, free_blocks, free_count, page_siz
     kv, q, table, free, count = _addr32(kv_lens, q_lens, block_table, free_blocks, free_count)
     if out is None:
         # one allocation for the 32-bit outputs
-        slots = torch.empty(num_tokens, dtype=torch.int64, device=kv_lens.device)
-        a = torch.empty(num_tokens + 2 * B + 6, dtype=torch.int32, device=kv_lens.device)
+        slots = _empty(num_tokens, torch.int64, kv_lens.device, stream)
+        a = _empty(num_tokens + 2 * B + 6, torch.int32, kv_lens.device, stream)
         n1, n2 = num_tokens + B + 1, num_tokens + 2 * B + 1
         out = KvPlan(slots, a.as_strided((num_tokens,), (1,), 0), a.as_strided((B + 1,), (1,), num_tokens),
                      a.as_strided((B,), (1,), n1), a.as_strided((1,), (1,), n2), a.as_strided((4,), (1,), n2 + 1))
@@ -474,7 +483,7 @@ def gai4_kv_read(cache, slots, group_size: int = 64, out=None, stream=None) -> t
     n, = slots.shape
     _need(slots.dtype == torch.int64, "slots must be int64")
     if out is None:
-        out = torch.empty((n, h, d), dtype=torch.float32, device=slots.device)
+        out = _empty((n, h, d), torch.float32, slots.device, stream)
     _need(out.shape == (n, h, d) and out.dtype == torch.float32, "out must be float32 [tokens, kv_heads, head_dim]")
     _check("gai4_kv_read", lib().gai4_kv_read(*_addr(*cache, slots, out), _dtype(cache[1]), group_size, n, h, d, nb,
                                               page, _stream_handle(stream, slots)))
@@ -505,7 +514,7 @@ def gai4_kv_attention(q, k_cache, v_cache, block_table, kv_lens, cu_q, group_siz
     qs = _token_stride(q, hq, d, T, "q")
     _need(kv_lens.shape == (B,) and cu_q.shape == (B + 1,), "block_table [B, max_blocks], kv_lens [B], cu_q [B + 1]")
     if out is None:
-        out = torch.empty((n, hq, d), dtype=T, device=q.device)
+        out = _empty((n, hq, d), T, q.device, stream)
         os_ = hq * d
     else:
         _need(out.shape[0] == n, "out must have a row for each row of q")
@@ -519,7 +528,7 @@ def gai4_kv_attention(q, k_cache, v_cache, block_table, kv_lens, cu_q, group_siz
         nbytes = _kv_workspace.get(key)
         if nbytes is None:
             nbytes = _kv_workspace[key] = gai4_kv_attention_workspace_bytes(hq, h, d, T)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        workspace = _empty(nbytes, torch.uint8, q.device, stream)
         ws = workspace.data_ptr()
     else:
         nbytes = workspace.numel() * workspace.element_size()

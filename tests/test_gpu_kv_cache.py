@@ -509,6 +509,28 @@ def test_step_on_another_stream_and_in_a_graph():
         assert torch.equal(a, b)
 
 
+def test_what_a_call_allocates_belongs_to_its_stream(monkeypatch):
+    """A workspace of the current stream would be handed out again there while the call on `stream` still runs."""
+    q, kc, vc, table, kv, cu = problem([70, 1500], [1, 1], 2, 4, 64, 32, 32, "bf16", 81)
+    want = g4.gai4_kv_attention(q, kc, vc, table, i32(kv), i32(cu), group_size=32)
+    kvd, cud, slots = i32(kv), i32(cu), torch.arange(5, device="cuda")
+    plan = [i32([3, 0]), i32([1, 1]), i32([[0], [-1]]), i32([1, 2]), i32([2])]
+    torch.cuda.synchronize()
+    s, seen, empty = torch.cuda.Stream(), [], torch.empty
+
+    def watched(*a, **k):
+        seen.append(torch.cuda.current_stream().cuda_stream)
+        return empty(*a, **k)
+    monkeypatch.setattr(torch, "empty", watched)
+    out = g4.gai4_kv_attention(q, kc, vc, table, kvd, cud, group_size=32, stream=s)
+    g4.gai4_kv_read(kc, slots, group_size=32, stream=s)
+    g4.gai4_kv_plan(*plan, 32, 2, stream=s)
+    monkeypatch.undo()
+    s.synchronize()
+    assert torch.equal(out, want)
+    assert len(seen) == 5 and set(seen) == {s.cuda_stream}
+
+
 def test_plan_writes_only_its_outputs():
     rng = random.Random(3)
     kv, q, table, free, count = make_step(rng, 37, 16, 9, 50, 4)
