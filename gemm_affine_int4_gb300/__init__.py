@@ -445,8 +445,7 @@ def gai4_kv_plan(kv_lens, q_lens, block_table, free_blocks, free_count, page_siz
         slots = _empty(num_tokens, torch.int64, kv_lens.device, stream)
         a = _empty(num_tokens + 2 * B + 6, torch.int32, kv_lens.device, stream)
         n1, n2 = num_tokens + B + 1, num_tokens + 2 * B + 1
-        out = KvPlan(slots, a.as_strided((num_tokens,), (1,), 0), a.as_strided((B + 1,), (1,), num_tokens),
-                     a.as_strided((B,), (1,), n1), a.as_strided((1,), (1,), n2), a.as_strided((4,), (1,), n2 + 1))
+        out = KvPlan(slots, *a.split_with_sizes((num_tokens, B + 1, B, 1, 4)))
         o_slots, o_pos = slots.data_ptr(), a.data_ptr()
         o_cu, o_lens, o_left, o_info = o_pos + 4 * num_tokens, o_pos + 4 * n1, o_pos + 4 * n2, o_pos + 4 * n2 + 4
     else:
