@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <utility>
@@ -155,6 +156,11 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+
+// Whether a part of a softmax row (its maximum m and sum l) saw no key and adds
+// nothing. The maximum passes NaN scores over: where all that a part saw are
+// NaN, m is -inf like that of a part without keys, but l is NaN, and the row is.
+__device__ __forceinline__ bool saw_nothing(float m, float l) { return m == -INFINITY && l == 0.f; }
 
 // f16 bit pattern (low 16 bits) -> binary32, all classes
 __device__ __forceinline__ float f16_bits_to_f32(uint32_t h) {

@@ -954,8 +954,12 @@ __device__ __forceinline__ void deposit(Acc<C>& A, uint8_t* buf) {
 template <class C>
 __device__ __forceinline__ void deposit_nothing(uint8_t* buf) {
     float* sm = reinterpret_cast<float*>(buf) + C::kWarps * C::NC * C::DP;
+    float* sl = sm + C::kWarps * C::NC;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane < C::NC) sm[warp * C::NC + lane] = -INFINITY;
+    if (lane < C::NC) {
+        sm[warp * C::NC + lane] = -INFINITY;
+        sl[warp * C::NC + lane] = 0.f;
+    }
 }
 
 // joins what the warps have deposited, by one warp: each lane four channels of
@@ -975,11 +979,11 @@ __device__ __forceinline__ void join(const uint8_t* buf, int columns, F&& write)
         float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < C::kWarps; ++w) {
-            const float mw = sm[w * NC + col];
-            if (mw != -INFINITY) {   // (a warp that saw nothing adds nothing)
+            const float mw = sm[w * NC + col], lw = sl[w * NC + col];
+            if (!saw_nothing(mw, lw)) {
                 const float e = ex2(mw - m);
                 const float4 v = *reinterpret_cast<const float4*>(o + (w * NC + col) * DP + d);
-                l = fmaf(sl[w * NC + col], e, l);
+                l = fmaf(lw, e, l);
                 f.x = fmaf(v.x, e, f.x);
                 f.y = fmaf(v.y, e, f.y);
                 f.z = fmaf(v.z, e, f.z);
@@ -1222,7 +1226,7 @@ __global__ void __launch_bounds__(128) kv_combine_kernel(const __grid_constant__
         const float* rec = recs + ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * rec_floats(NC, D);
         const float mi = rec[NC * D + col], li = rec[NC * D + NC + col];
         const float4 v = *reinterpret_cast<const float4*>(rec + col * D + d);
-        if (mi == -INFINITY) continue;
+        if (saw_nothing(mi, li)) continue;
         const float mn = fmaxf(m, mi);
         const float c = m == -INFINITY ? 0.f : ex2(m - mn), e = ex2(mi - mn);
         m = mn;
@@ -1246,7 +1250,7 @@ __global__ void __launch_bounds__(128) kv_combine_kernel(const __grid_constant__
     float4 F = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-        if (sm[i] == -INFINITY) continue;
+        if (saw_nothing(sm[i], sl[i])) continue;
         const float e = ex2(sm[i] - M);
         const float4 v = so[i * (D / 4) + threadIdx.x];
         Ls = fmaf(sl[i], e, Ls);

@@ -1076,7 +1076,7 @@ __global__ void __launch_bounds__(kRows)
         float4 v[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = reinterpret_cast<const float4*>(rec)[(8 * c + k) * kRows + threadIdx.x];
-        if (mi == -INFINITY) continue;
+        if (saw_nothing(mi, li)) continue;
         const float mn = fmaxf(m, mi);
         const float a = m == -INFINITY ? 0.f : ex2(m - mn), b = ex2(mi - mn);
         m = mn;

@@ -1,0 +1,81 @@
+"""Edges of the paged 4-bit key/value cache on the GPU, within the bounds of kv_ref.py unless a test says otherwise."""
+import numpy as np
+import pytest
+import torch
+
+import gemm_affine_int4_gb300 as g4
+from kv_ref import attention64
+from test_gpu_kv_cache import i32, problem
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(q, kc, vc, table, kv, cu, gs, max_q, window=0, scale=None):
+    """(out, lse) over sentinels."""
+    n, hq, d = q.shape
+    lse = torch.full((n, hq), 5.0, device="cuda")
+    out = torch.full((n, hq, d), 7.0, dtype=q.dtype, device="cuda")
+    g4.gai4_kv_attention(q, kc, vc, table, i32(kv), i32(cu), group_size=gs, max_q_len=max_q, window=window, scale=scale,
+                         out=out, lse=lse)
+    assert g4.gai4_last_device_status() == 0
+    return out, lse
+
+
+def compare(out, lse, ref, gone):
+    """NaN in the (row, head) pairs of `gone`, the reference's values within its bounds in the others."""
+    want, bound, rl, lb = ref
+    assert bool(out[gone].isnan().all()) and bool(lse[gone].isnan().all()), "a row that should be NaN is not"
+    stay = ~gone
+    err = (out.double() - want).abs()[stay]
+    assert bool((err <= bound[stay]).all()), f"{int((~(err <= bound[stay])).sum())} outside"
+    empty = rl == -np.inf
+    assert torch.equal((lse == -np.inf)[stay], empty[stay])
+    le = torch.where(empty, 0.0, (lse.double() - rl).abs())[stay]
+    assert bool((le <= lb[stay]).all())
+
+
+# few rows: units of up to 512 tokens (not cut) and longer ones; many rows: one request (every unit cut) and many (most
+# units whole)
+FORMS = [("bf16", [60], 1, 0), ("f16", [60, 1, 33], 1, 0), ("f32", [60, 400], 1, 0), ("bf16", [5000], 1, 0),
+         ("f16", [9000, 40], 1, 0), ("f32", [5000, 2100], 1, 0), ("f16", [3000, 70], 4, 0), ("bf16", [700], 2, 100),
+         ("f32", [300, 900], 30, 0), ("bf16", [5000], 40, 0), ("f16", [300, 90], 60, 0), ("bf16", [70] * 170, 40, 0),
+         ("f16", [150] * 160, 33, 50)]
+
+
+@pytest.mark.parametrize("dt,kv,q_len,window", FORMS)
+def test_nan_queries_give_nan_rows(dt, kv, q_len, window):
+    q, kc, vc, table, kv, cu = problem(kv, [min(q_len, k) for k in kv], 2, 4, 64, 32, 32, dt, 91)
+    many = q_len * 4 > 32
+    gone = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    gone[0, 1] = gone[-1, 6] = gone[q.shape[0] // 2, 3] = True
+    q[gone, 5] = float("nan")
+    ref = attention64(torch.where(gone[:, :, None], 0.0, q), kc, vc, table, kv, cu, 32, 64 ** -0.5, window, dt, many)
+    compare(*attend(q, kc, vc, table, kv, cu, 32, q_len, window), ref, gone)
+
+
+def test_nan_queries_that_see_nothing_give_zeros():
+    for q_len in (1, 40):
+        q, kc, vc, table, kv, cu = problem([0, 5], [q_len] * 2, 2, 4, 64, 32, 32, "bf16", 92)
+        q[0] = float("nan")
+        out, lse = attend(q, kc, vc, table, kv, cu, 32, q_len)
+        assert bool((out[0] == 0).all()) and bool((lse[0] == -np.inf).all())
+
+
+@pytest.mark.parametrize("dt,kv,q_len,first,last", [
+    ("bf16", 1, 1, 0, 1), ("f16", 1, 1, 0, 1), ("f32", 1, 1, 0, 1),          # the only key
+    ("bf16", 33, 1, 32, 33), ("f16", 33, 2, 32, 33), ("f32", 65, 2, 64, 65),   # the newest, alone in its 32 tokens
+    ("bf16", 400, 1, 0, 400), ("f16", 5000, 1, 0, 5000), ("f32", 5000, 2, 0, 5000),   # all
+    ("bf16", 9000, 1, 3000, 6000), ("f32", 9000, 3, 4000, 7000),              # all that some blocks of a cut unit have
+    ("bf16", 129, 40, 128, 129), ("f16", 9000, 40, 3000, 6000), ("bf16", 3000, 64, 0, 3000)])
+def test_nan_keys_reach_every_row_that_sees_them(dt, kv, q_len, first, last):
+    hkv, g, d, gs, page = 2, 4, 64, 32, 32
+    q, kc, vc, table, kvs, cu = problem([kv], [q_len], hkv, g, d, gs, page, dt, 93)
+    many = q_len * g > 32
+    ref = attention64(q, kc, vc, table, kvs, cu, gs, d ** -0.5, 0, dt, many)
+    j = torch.arange(first, last, device="cuda")
+    scales = kc[1].clone()
+    scales[table[0, j // page].long(), 1, j % page, 0] = float("nan")       # one group, key/value head 1
+    pos = torch.arange(kv - q_len, kv, device="cuda")
+    gone = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    gone[pos >= first, g:] = True
+    compare(*attend(q, (kc[0], scales, kc[2]), vc, table, kvs, cu, gs, q_len), ref, gone)
