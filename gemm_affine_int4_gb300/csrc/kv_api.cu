@@ -170,7 +170,7 @@ gai4_status gai4_kv_attention(const void* q, int64_t q_token_stride, const uint3
     L.num_tokens = num_tokens;
     L.max_q_len = std::min(max_q_len, num_tokens);   // (times the group: below 2^31)
     L.scale = scale;
-    L.window = window;
+    L.window = std::min<int64_t>(window, 0x7fffffff);   // no position is beyond it, and position - window stays in 64 bits
     L.workspace = workspace;
     L.status = status_ptr();
     L.spin_limit = 2000000000LL;   // ~1 s of SM clock per wait

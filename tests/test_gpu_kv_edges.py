@@ -79,3 +79,14 @@ def test_nan_keys_reach_every_row_that_sees_them(dt, kv, q_len, first, last):
     gone = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
     gone[pos >= first, g:] = True
     compare(*attend(q, (kc[0], scales, kc[2]), vc, table, kvs, cu, gs, q_len), ref, gone)
+
+
+@pytest.mark.parametrize("window", [2**63 - 1, 2**63 - 100, 2**62, 2**31, 2**31 - 1])
+@pytest.mark.parametrize("dt,q_len", [("bf16", 3), ("f32", 150), ("f16", 150), ("bf16", 300)])
+def test_windows_of_any_length(dt, q_len, window):
+    """Windows beyond every position, with requests of more queries than tokens: as without one."""
+    kv = [100, 260, 0, 1]
+    q, kc, vc, table, kv, cu = problem(kv, [q_len] * 4, 2, 2, 64, 32, 16, dt, 99)
+    out, lse = attend(q, kc, vc, table, kv, cu, 32, q_len, window=window)
+    compare(out, lse, attention64(q, kc, vc, table, kv, cu, 32, 64 ** -0.5, 0, dt, q_len > 16),
+            torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda"))
