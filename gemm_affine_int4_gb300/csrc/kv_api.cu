@@ -140,8 +140,10 @@ gai4_status gai4_kv_attention(const void* q, int64_t q_token_stride, const uint3
     gai4_status st = check_shape(dtype, group_size, kv_heads, head_dim, num_blocks, page_size, &L.sh);
     if (st != GAI4_OK) return st;
     if (q_heads < 1 || q_heads % kv_heads != 0 || q_heads / kv_heads > 65535) return GAI4_ERR_INVALID_ARG;
+    // the kernels step through a request's tokens in 32 bits, up to 1200 past its last tile
+    constexpr int64_t most_tokens = 0x80000000ll - 4096;
     if (batch < 1 || batch > 0x7ffffff || num_tokens < 0 || num_tokens > 0x7fffffff || max_q_len < 0 || max_blocks < 1 ||
-        max_blocks > (0x7fffffff >> L.sh.page_log2) || window < 0)
+        max_blocks > (most_tokens >> L.sh.page_log2) || window < 0)
         return GAI4_ERR_INVALID_ARG;
     L.k = KvCache{k_packed, k_scales, k_biases};
     L.v = KvCache{v_packed, v_scales, v_biases};

@@ -456,7 +456,7 @@ gai4_status gai4_kv_read(const uint32_t* packed, const void* scales, const void*
  * binary32. f32: queries and probabilities enter as two binary16 parts, 22
  * bits. Results do not depend on the contents of the workspace, and repeat bit
  * for bit. num_tokens * (q_heads / kv_heads) above 2^31 - 1 is UNSUPPORTED;
- * 1 <= batch < 2^27, page_size * max_blocks < 2^31.
+ * 1 <= batch < 2^27, page_size * max_blocks <= 2^31 - 4096.
  * workspace: 16-byte aligned, >= gai4_kv_attention_workspace_bytes(...).
  */
 gai4_status gai4_kv_attention(const void* q, int64_t q_token_stride, const uint32_t* k_packed, const void* k_scales,
