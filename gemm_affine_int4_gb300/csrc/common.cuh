@@ -16,14 +16,14 @@ namespace gai4 {
 // ---------------------------------------------------------------------------
 // Programmatic dependent launch. The hot-path kernels are launched so that
 // the next kernel in the stream may start (its launch and set-up: barriers,
-// tensor-memory allocation) while this one finishes: every kernel lets its
-// dependents be scheduled at entry, and waits for the kernels before it to
-// complete -- with their memory visible -- before it reads activations or
-// writes any output or workspace. The streaming GEMV / GEMM kernels read the
-// packed weights (which no kernel of the library writes, and no kernel that
-// does not signal programmatic launch can still be writing) before that
-// wait. A kernel that reads another call's output is therefore ordered
-// exactly as with plain stream order.
+// tensor-memory allocation) while this one finishes: every kernel but those
+// that write packed weights lets its dependents be scheduled at entry, and waits
+// for the kernels before it to complete -- with their memory visible -- before
+// it reads activations or writes any output or workspace. The streaming GEMV /
+// GEMM kernels read the packed weights before that wait: a kernel that writes
+// some (gai4_quantize's, gai4_kv_append's) does not signal programmatic launch,
+// so none is still being written by then. A kernel that reads another call's
+// output is therefore ordered exactly as with plain stream order.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -272,13 +272,15 @@ __device__ __forceinline__ uint32_t codes8(const float (&x)[8], float s, float b
 // and two reads: 5.5 us with one, 8.9 with four). Bound by instructions: 20011
 // tokens of 2 x 8 rows of 128 f16 values in groups of 32 (113 MB), 36 us; with
 // a division for every code it took 82.
+// No signal of programmatic launch here: what is written is in the form of
+// packed weights, which gai4_qmv and gai4_qmm_t read before the kernels ahead of
+// them have ended.
 template <typename T, int D, int GS, bool VEC, int SETS>
 __global__ void __launch_bounds__(256) kv_append_kernel(const void* k, long long ks, const void* v, long long vs,
                                                         const int64_t* __restrict__ slots, KvCache kc, KvCache vc,
                                                         KvShape sh, int tokens) {
     constexpr int LPR = D / 8, LPG = GS / 8;   // lanes per row and per group
     constexpr int RPW = 32 / LPR;              // rows of a warp's set
-    pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const int sub = lane / LPR, li = lane % LPR;

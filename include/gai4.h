@@ -13,8 +13,9 @@
  *    gai4_qmm_t_noalloc, both static __device__ variables.
  *  - Kernels are launched with programmatic dependent launch: a call may
  *    start while the kernel before it in the stream finishes, if that kernel
- *    allows it (this library's kernels do; a kernel that does not signal it
- *    is waited for in full, as usual). The packed weights, scales, biases and
+ *    allows it (this library's kernels do, but for those of gai4_quantize and
+ *    gai4_kv_append, which write weights; a kernel that does not signal it is
+ *    waited for in full, as usual). The packed weights, scales, biases and
  *    quantized blocks may be read from the start of the call; activations are
  *    read, and outputs and workspaces written, only after the preceding
  *    kernels have completed. So a kernel that writes weights must not signal

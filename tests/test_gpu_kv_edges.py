@@ -90,3 +90,35 @@ def test_windows_of_any_length(dt, q_len, window):
     out, lse = attend(q, kc, vc, table, kv, cu, 32, q_len, window=window)
     compare(out, lse, attention64(q, kc, vc, table, kv, cu, 32, 64 ** -0.5, 0, dt, q_len > 16),
             torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda"))
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 8, 40])
+@pytest.mark.parametrize("between", [False, True])
+def test_products_with_cached_rows_right_after_an_append(M, between):
+    """The cache as a weight matrix of gai4_qmv and gai4_qmm_t (which read weights before the kernels ahead of them have
+    ended): codes, scales and biases of the append just before, with another call of the library between or not."""
+    hkv, d, gs, page, nb = 8, 128, 64, 64, 320
+    T = nb * page
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    rows = [torch.randn(T, hkv, d, generator=gen, device="cuda").bfloat16() for _ in range(2)]
+    slots = torch.randperm(T, generator=gen, device="cuda")
+    kc, vc = (g4.gai4_kv_cache(nb, hkv, page, d, gs) for _ in range(2))
+    x = torch.randn(M, d, generator=gen, device="cuda").bfloat16()
+
+    def product(c):
+        w = (c[0].view(-1, d // 8), c[1].view(-1, d // gs), c[2].view(-1, d // gs))
+        return g4.gai4_qmv(*w, x[0], group_size=gs) if M == 1 else g4.gai4_qmm_t(*w, x, group_size=gs)
+
+    want = []
+    for i in range(2):
+        g4.gai4_kv_append(rows[i], rows[1 - i], slots, kc, vc, group_size=gs)
+        torch.cuda.synchronize()
+        want.append((product(kc), product(vc)))
+        torch.cuda.synchronize()
+    for turn in range(20):
+        i = turn & 1
+        g4.gai4_kv_append(rows[i], rows[1 - i], slots, kc, vc, group_size=gs)
+        if between:
+            g4.gai4_kv_read(kc, slots[:3], group_size=gs)
+        got = product(kc), product(vc)
+        assert torch.equal(got[0], want[i][0]) and torch.equal(got[1], want[i][1]), turn
