@@ -30,8 +30,8 @@
 // and fma(c 2^-133, s 2^93, b 2^-40) is the value times 2^-40, rounded once;
 // the power leaves through f and through the last division. Keys and values
 // from 2^-86 to 2^37 keep all their bits.
-// f16: codes by the offset of 1024, then fma(c, s, b); keys and values up to
-// 65504.
+// f16: codes by the offset of 1024, then fma(c, s, b); keys up to 65504. Value
+// groups that may have larger values are multiplied apart, in binary32.
 //
 // Work split: a unit is (request, block of 256 rows, key/value head); all
 // units lie on one line, each with places in proportion to its key tiles (and
@@ -282,6 +282,14 @@ __device__ __forceinline__ uint4 expand(uint32_t w, const Group<BF>& g) {
 template <bool BF>
 __device__ __forceinline__ uint32_t too_wide(uint32_t s, uint32_t b) {
     return ((s | b << 16) & 0x7fff7fffu) + (BF ? 0x00802F00u : 0x04000400u);
+}
+// The same signs for values that the tensor cores do not multiply: those, and
+// f16 groups with |s| >= 2048 or |b| >= 32768. Below, |15 s + b| is less than
+// 65504, so no code expands to an infinity. (A test of the sum itself would be
+// exact, but not as short, and every tile of values goes through it.)
+template <bool BF>
+__device__ __forceinline__ uint32_t set_apart(uint32_t s, uint32_t b) {
+    return BF ? too_wide<BF>(s, b) : ((s | b << 16) & 0x7fff7fffu) + 0x08001800u;
 }
 
 // columns of tensor memory (128 for each M tile)
@@ -730,15 +738,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         scale[x] = valid ? *reinterpret_cast<const uint16_t*>(sc) : 0u;
                         bias[x] = valid ? *reinterpret_cast<const uint16_t*>(sc + kKeys * 2 * ng) : 0u;
                     }
-                    // Values that are not finite would reach the rows that do not see their token, as 0 x NaN: zeros
-                    // in their place, and the softmax warps put NaN into the outputs that need it.
+                    // Values that are not finite once expanded would reach the rows that do not see their token, as
+                    // 0 x NaN: zeros in their place, and the softmax warps add to the outputs that need it what was
+                    // left out.
                     uint32_t wide = 0;
 #pragma unroll
-                    for (int x = 0; x < D / 32; ++x) wide |= too_wide<BF>(scale[x], bias[x]);
+                    for (int x = 0; x < D / 32; ++x) wide |= set_apart<BF>(scale[x], bias[x]);
                     if (side && (wide & 0x80008000u)) {
 #pragma unroll
                         for (int x = 0; x < D / 32; ++x)
-                            if (too_wide<BF>(scale[x], bias[x]) & 0x80008000u) scale[x] = bias[x] = 0;
+                            if (set_apart<BF>(scale[x], bias[x]) & 0x80008000u) scale[x] = bias[x] = 0;
                         wide_values = 1;
                     }
                     __syncwarp();
@@ -946,31 +955,75 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_after();
         const bool begins = cur->first() == 0, whole = begins && cur->last() == cur->n, mine = i < cur->tiles_m();
         const int row0 = cur->row0, rows = cur->rows, rq_q0 = cur->q.q0, h = cur->h;
-        // groups whose channels are NaN in this row: values that were set apart (a flag of the CTA, which stays)
+        // Values that were set apart (a flag of the CTA, which stays), a token at a time: groups whose channels are NaN
+        // in this row, and f16 products that are added to O in binary32, with the score taken once more, as the
+        // probability is gone. Rare: only the result counts.
         uint32_t nan_groups = 0;
         if (mine && wide_values) {
             const int row = row0 + i * 128 + r, pl = p.sh.page_log2, ng = D >> gs_log2;
-            const long long pos = (long long)cur->q.kv - cur->q.qn + row / p.group;
+            const bool live = row < rows;
+            const int tok = live ? row / p.group : 0, head = h * p.group + (live ? row - tok * p.group : 0);
+            const long long pos = live ? (long long)cur->q.kv - cur->q.qn + tok : -1;
             const long long lo = p.window > 0 ? pos - p.window + 1 : 0;
             const int end = min((cur->t_first + cur->last()) * kKeys, cur->q.kv);
             const int* table = p.table + (long long)cur->r * p.max_blocks;
+            const uint16_t *vs = static_cast<const uint16_t*>(p.v.scales), *vb = static_cast<const uint16_t*>(p.v.biases);
 #pragma unroll 1
             for (int key0 = (cur->t_first + cur->first()) * kKeys; key0 < end; key0 += 32) {
                 const int key = key0 + lane, page = key < end ? table[key >> pl] : -1;
-                uint32_t groups = 0;
+                uint32_t groups = 0, large = 0;
+                long long line = 0;                 // cache row
                 if (page >= 0 && page < p.sh.num_blocks) {
-                    const long long at = ((((long long)page * p.sh.hkv + h) << pl) + (key & ((1 << pl) - 1))) * ng;
+                    line = (((long long)page * p.sh.hkv + h) << pl) + (key & ((1 << pl) - 1));
 #pragma unroll 1
-                    for (int g = 0; g < ng; ++g)
-                        if (too_wide<BF>(static_cast<const uint16_t*>(p.v.scales)[at + g],
-                                         static_cast<const uint16_t*>(p.v.biases)[at + g]) & 0x80008000u)
-                            groups |= 1u << g;
+                    for (int g = 0; g < ng; ++g) {
+                        const uint32_t s = vs[line * ng + g], b = vb[line * ng + g];
+                        if (too_wide<BF>(s, b) & 0x80008000u) groups |= 1u << g;
+                        else if (set_apart<BF>(s, b) & 0x80008000u) large |= 1u << g;
+                    }
                 }
 #pragma unroll 1
-                for (uint32_t some = __ballot_sync(0xffffffffu, groups != 0); some != 0; some &= some - 1) {
+                for (uint32_t some = __ballot_sync(0xffffffffu, (groups | large) != 0); some != 0; some &= some - 1) {
                     const int o = __ffs(some) - 1;
                     const uint32_t of = __shfl_sync(0xffffffffu, groups, o);
-                    if (key0 + o >= lo && key0 + o <= pos) nan_groups |= of;
+                    const bool sees = key0 + o >= lo && key0 + o <= pos;
+                    if (sees) nan_groups |= of;
+                    if constexpr (!BF) {
+                        const uint32_t add = __shfl_sync(0xffffffffu, large, o);
+                        if (add == 0) continue;
+                        const long long at = __shfl_sync(0xffffffffu, line, o);
+                        auto code = [&](const uint32_t* w, int d) { return (w[at * (D / 8) + (d >> 3)] >> (4 * (d & 7))) & 15u; };
+                        float prob = 0.f;
+                        if (sees) {
+                            const uint16_t* q = static_cast<const uint16_t*>(p.q) + (rq_q0 + tok) * p.q_stride + (long long)head * D;
+                            float dot = 0.f;
+#pragma unroll 1
+                            for (int d = 0; d < D; ++d) {
+                                const long long g = at * ng + (d >> gs_log2);
+                                const __half k = __hfma(__ushort2half_rn((unsigned short)code(p.k.packed, d)),
+                                                        __ushort_as_half(static_cast<const uint16_t*>(p.k.scales)[g]),
+                                                        __ushort_as_half(static_cast<const uint16_t*>(p.k.biases)[g]));
+                                dot = fmaf(F16::to_f32(q[d]), __half2float(k), dot);
+                            }
+                            prob = ex2(fmaf(dot, p.scale * 1.4426950408889634f, m == -INFINITY ? 0.f : -m));
+                        }
+#pragma unroll 1
+                        for (int c = 0; c < D / 8; ++c) {
+                            const int g = (8 * c) >> gs_log2;
+                            if (!((add >> g) & 1u)) continue;
+                            const float s = F16::to_f32(vs[at * ng + g]), b = F16::to_f32(vb[at * ng + g]);
+                            uint32_t y[8];
+                            tmem_ld8(o_tm + 8 * c, y);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {   // (channels in the order 0 4 1 5 2 6 3 7)
+                                const float v = fmaf(s, (float)code(p.v.packed, 8 * c + (e >> 1) + 4 * (e & 1)), b);
+                                if (sees) y[e] = __float_as_uint(fmaf(prob, v, __uint_as_float(y[e])));
+                            }
+                            tmem_st8(o_tm + 8 * c, y);
+                            tmem_st_wait();
+                        }
+                    }
                 }
             }
         }

@@ -452,8 +452,8 @@ gai4_status gai4_kv_read(const uint32_t* packed, const void* scales, const void*
  * as they are and scales and biases are applied in binary32; with many rows
  * (max_q_len * q_heads / kv_heads above 32) keys, values and probabilities are
  * rounded once to T and multiplied on the tensor cores as in gai4_qmm_t; keys
- * and values are then at most 2^37 (bf16: values whose scale is 2^35 or more
- * count as infinite) or 65504 (f16) in magnitude. Softmax and sums are
+ * are then at most 2^37 (f16: 65504) in magnitude, and bf16 values at most 2^37
+ * (a scale of 2^35 or more counts as infinite). Softmax and sums are
  * binary32. f32: queries and probabilities enter as two binary16 parts, 22
  * bits. Results do not depend on the contents of the workspace, and repeat bit
  * for bit. num_tokens * (q_heads / kv_heads) above 2^31 - 1 is UNSUPPORTED;

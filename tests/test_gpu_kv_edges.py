@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import gemm_affine_int4_gb300 as g4
-from kv_ref import attention64
+from kv_ref import U, attention64, rows64
 from test_gpu_kv_cache import i32, problem
 
 pytestmark = pytest.mark.gpu
@@ -122,3 +122,72 @@ def test_products_with_cached_rows_right_after_an_append(M, between):
             g4.gai4_kv_read(kc, slots[:3], group_size=gs)
         got = product(kc), product(vc)
         assert torch.equal(got[0], want[i][0]) and torch.equal(got[1], want[i][1]), turn
+
+
+def many_rows64(q, k, v, pos, window, scale, u):
+    """(out, bound) of query rows at positions pos over keys and values [kv, hkv, d] in float64, the bound as in
+    kv_ref.attention64 for many rows (the score's by |k|: its keys are what the kernel multiplies)."""
+    n, hq, d = q.shape
+    kv, hkv = k.shape[:2]
+    j = torch.arange(kv, device=q.device)
+    see = j <= pos[:, None]
+    if window:
+        see &= j > pos[:, None] - window
+    qh = q.double().unflatten(1, (hkv, hq // hkv))
+    s = torch.where(see[:, None, None], scale * torch.einsum("thgd,khd->thgk", qh, k), -np.inf)
+    S = abs(scale) * torch.where(see[:, None, None], torch.einsum("thgd,khd->thgk", qh.abs(), k.abs()), 0.0).amax(-1)
+    p = torch.softmax(s, -1).nan_to_num(0.0)
+    out, A = (torch.einsum("thgk,khd->thgd", p, x).flatten(1, 2) for x in (v, v.abs()))
+    delta = (140 * 2.0**-24 + u) * S + 2.0**-21 * (1 + S)
+    rel = (torch.exp(2 * delta) - 1 + 2 * u + kv * 2.0**-24).flatten(1, 2)
+    return out, rel[..., None] * A + out.abs() * 2 * u + 2.0**-24
+
+
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("s,b,code", [(10000.0, 0.0, 15), (-10000.0, 30000.0, 15), (4368.0, 0.0, 15), (65504.0, 65504.0, 9),
+                                      (8736.0, -65504.0, 15), (1.0, 65504.0, 15), (-65504.0, -65504.0, 12), (3000.0, 0.0, 11)])
+def test_f16_groups_of_large_values(what, s, b, code):
+    """Many rows: finite scales and biases whose combination is beyond binary16 (or nearly), at tokens that some rows do
+    not see. These keep their result; values are computed in the others as well (keys are at most 65504)."""
+    hkv, g, d, gs, page, kv, q_len, window, dt = 2, 4, 64, 32, 32, 500, 60, 200, "f16"
+    q, kc, vc, table, kvs, cu = problem([kv], [q_len], hkv, g, d, gs, page, dt, 95)
+    cache = [x.clone() for x in (kc if what == "k" else vc)]
+    tokens = [kv - 20, kv - q_len - window + 30, kv - q_len - window]     # the last is seen by none
+    for t in tokens:
+        at = (int(table[0, t // page]), 1, t % page)
+        cache[1][at][1], cache[2][at][1] = s, b
+        cache[0][at][gs // 8] = 0x11111111 * code - (1 << 32 if code > 7 else 0)     # eight channels at `code`
+    pos = torch.arange(kv - q_len, kv, device="cuda")
+    hit = torch.zeros(q_len, dtype=torch.bool, device="cuda")
+    for t in tokens:
+        hit |= (t <= pos) & (t > pos - window)
+    assert bool(hit.any()) and not bool(hit.all())
+    args = (q, cache, vc) if what == "k" else (q, kc, cache)
+    out, lse = attend(*args, table, kvs, cu, gs, q_len, window)
+    j = torch.arange(kv, device="cuda")
+    k, v = (rows64(c, table[0, j // page].long(), j % page, gs)[0] for c in args[1:])
+    want, bound = many_rows64(q, k, v, pos, window, d ** -0.5, U[dt])
+    check = (want.abs() + bound < 65504) & (~hit[:, None, None] if what == "k" else True)      # (outputs are binary16)
+    assert bool(check[~hit].all())
+    err = (out.double() - want).abs()
+    assert bool((err <= bound)[check].all()), f"{int((~(err <= bound))[check].sum())} outside"
+
+
+def test_f16_rows_of_the_largest_values_through_the_cache():
+    """Rows that span 0 to 65504 and -65504 to 65504, appended: their groups' last code is beyond binary16."""
+    hkv, d, gs, page, kv, q_len = 2, 64, 32, 32, 130, 60
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn(kv, hkv, d, generator=gen, device="cuda").half() for _ in range(2))
+    v[100, 1, 3], v[100, 1, 4], v[115, 1, 40], v[115, 1, 50] = 65504.0, 0.0, 65504.0, -65504.0
+    v[100, 1, 5:32] = v[100, 1, 5:32].abs()
+    v[100, 1, :3] = 1.0
+    kc, vc = (g4.gai4_kv_cache(5, hkv, page, d, gs, torch.float16) for _ in range(2))
+    g4.gai4_kv_append(k, v, torch.arange(kv, device="cuda"), kc, vc, group_size=gs)
+    q = torch.randn(q_len, 8, d, generator=gen, device="cuda").half()
+    out, _ = attend(q, kc, vc, i32([[0, 1, 2, 3, 4]]), [kv], [0, q_len], gs, q_len)
+    j = torch.arange(kv, device="cuda")
+    kk, vv = (rows64(c, j // page, j % page, gs)[0] for c in (kc, vc))
+    pos = torch.arange(kv - q_len, kv, device="cuda")
+    want, bound = many_rows64(q, kk, vv, pos, 0, d ** -0.5, U["f16"])
+    assert float(want[pos < 100].abs().max()) < 10 and bool((want.abs() + bound < 65504).all())
+    assert bool(((out.double() - want).abs() <= bound).all())
