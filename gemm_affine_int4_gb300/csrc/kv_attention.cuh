@@ -15,13 +15,14 @@
 //    operand is scaled by a power of two per row so that its largest element
 //    is near 2^13 (queries keep all their bits; 2^-4 more for the elements
 //    that meet bits 4..7); the powers of two leave in the score's factor.
-//  * The value side's p s is scaled by a power of two R that follows the
-//    largest |s| seen (accumulators are rescaled when it grows), so any range
-//    of scales works and binary16 has 38 bits of room. Rounding p s to 11 bits
-//    is the path's one rounding below 32 bits: its errors are independent from
-//    key to key, and bf16 / f16 outputs are rounded to 8 / 11 bits after it
-//    (4 requests of 131072 f16 tokens: 3.1e-4 of the outputs' size, against
-//    2.1e-4 for the output's rounding alone).
+//  * The value side's p s is scaled by a power of two R, one for each query row,
+//    that follows the largest |s| that the row sees (its accumulators are
+//    rescaled when it grows), so any range of scales works and binary16 has 38
+//    bits of room. Rounding p s to 11 bits is the path's one rounding below 32
+//    bits: its errors are independent from key to key, and bf16 / f16 outputs
+//    are rounded to 8 / 11 bits after it (4 requests of 131072 f16 tokens:
+//    3.1e-4 of the outputs' size, against 2.1e-4 for the output's rounding
+//    alone).
 //  * f32 queries and f32 p s are split in two binary16 parts (22 bits).
 //
 // Shape of the products (mma m16n8k16, tokens or value channels along M, query
@@ -136,6 +137,11 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 // two binary32 operations at once, on neighbouring registers
 __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
     asm("{\n .reg .b64 u, v;\n mov.b64 u, {%0, %1};\n mov.b64 v, {%2, %3};\n add.rn.f32x2 u, u, v;\n mov.b64 {%0, %1}, u;\n}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void mul2(float& x, float& y, float a, float b) {
+    asm("{\n .reg .b64 u, v;\n mov.b64 u, {%0, %1};\n mov.b64 v, {%2, %3};\n mul.rn.f32x2 u, u, v;\n mov.b64 {%0, %1}, u;\n}"
         : "+f"(x), "+f"(y)
         : "f"(a), "f"(b));
 }
@@ -390,14 +396,23 @@ __device__ __forceinline__ void producer(const KvAttnLaunch& p, Walk<C::NC, CUT>
     for (int i = issued > S ? issued - S : 0; i < issued; ++i) mbar_wait_drain(&full[i % S], (i / S) & 1, ctl.limit, ctl.status);
 }
 
+// Scales and biases (their bits) from which a group's middle, 8 s + b, may be
+// beyond binary32
+constexpr uint32_t kFarScale = 250u << 23, kFarBias = 253u << 23;   // 2^123, 2^126
+
 // per-warp running state of a unit
 template <class C>
 struct Acc {
     float o[C::D / 16][C::NT][4];   // O^T less sum p (b + 8 s): [value channel block][rows][..], in units of R 2^-14 and of 2^-24, 2^-20 (f32: 1)
     float ab[C::NG][C::NT][2];      // sum p (b + 8 s)
     float m[C::NT][2], l[C::NT][2];
-    int re;                         // exponent field of R
+    float inv[C::NT][2];            // 2^14 / R
+    uint32_t limit;                 // the least R of all columns, at most kFarScale (bits): scales up to it need no attention
 };
+
+// exponent field of R, a power of two of at least 2^-100
+__device__ __forceinline__ int r_exponent(float inv) { return 268 - (int)(__float_as_uint(inv) >> 23); }
+__device__ __forceinline__ float r_inverse(int e) { return __uint_as_float((uint32_t)(268 - e) << 23); }
 
 template <class C>
 __device__ __forceinline__ void clear(Acc<C>& a) {
@@ -416,7 +431,9 @@ __device__ __forceinline__ void clear(Acc<C>& a) {
 #pragma unroll
             for (int g = 0; g < C::NG; ++g) a.ab[g][n][e] = 0.f;
         }
-    a.re = 27;
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n) a.inv[n][0] = a.inv[n][1] = r_inverse(27);
+    a.limit = 0;
 }
 
 // query operand of one unit
@@ -562,10 +579,12 @@ __device__ __forceinline__ uint32_t value_codes(uint32_t w) {
     return d;
 }
 
-// Tokens (bits of `bad`) with groups of values that are not finite: the rows
-// that see such a token get NaN in the group's channels, and the group is
-// zeroed in the stage, so that 0 x NaN does not reach the rows that do not see
-// it, nor an infinite scale the others' R.
+// whether a value group has to be set apart: it, or its middle, is not finite
+__device__ __forceinline__ bool far_group(float s, float b) { return !(fabsf(fmaf(8.f, s, b)) < INFINITY); }
+
+// Tokens (bits of `bad`) with such groups: the rows that see one get NaN in the
+// group's channels, and the group is zeroed in the stage, so that 0 x NaN does
+// not reach the rows that do not see it.
 template <class C, bool CUT>
 __device__ __forceinline__ void set_apart(const uint8_t* stage, int sub, uint32_t bad, int tok0, const Walk<C::NC, CUT>& w,
                                           const KvAttnLaunch& p, Acc<C>& A) {
@@ -577,7 +596,7 @@ __device__ __forceinline__ void set_apart(const uint8_t* stage, int sub, uint32_
 #pragma unroll
     for (int k = 0; k < C::NG; ++k) {
         const float s = C::T::to_f32(vsc[k]), b = C::T::to_f32(vbi[k]);
-        if (fabsf(s) < INFINITY && fabsf(b) < INFINITY) continue;
+        if (!far_group(s, b)) continue;
         groups |= 1u << k;
         vsc[k] = vbi[k] = St(0);
     }
@@ -733,8 +752,8 @@ __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mas
             mx[n][c] = m;
             grew |= m > A.m[n][c];
         }
-    // whether R has to grow: the largest value scale of the tile (non-negative
-    // numbers, infinity and NaN are ordered as integers)
+    // whether some R has to grow: the largest value scale of the tile
+    // (non-negative numbers, infinity and NaN are ordered as integers)
     uint32_t smax = 0, bmax = 0;
     static_assert(kSub == 32, "a lane per token");
     {
@@ -747,8 +766,16 @@ __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mas
             bmax = max(bmax, __float_as_uint(b[k]) & 0x7fffffffu);
         }
     }
-    if (__any_sync(0xffffffffu, grew || smax > (uint32_t)A.re << 23 || bmax >= 0x7f800000u)) {
-        const uint32_t bad = __ballot_sync(0xffffffffu, max(smax, bmax) >= 0x7f800000u);
+    if (__any_sync(0xffffffffu, grew || smax > A.limit || bmax >= kFarBias)) {
+        bool far = false;
+        if (smax >= kFarScale || bmax >= kFarBias) {
+            float s[NG], b[NG];
+            load_groups<T, NG>(vsc + lane * NG * C::E, s);
+            load_groups<T, NG>(vbi + lane * NG * C::E, b);
+#pragma unroll
+            for (int k = 0; k < NG; ++k) far |= far_group(s[k], b[k]);
+        }
+        const uint32_t bad = __ballot_sync(0xffffffffu, far);
         if (bad != 0) {
             set_apart<C, CUT>(stage, sub, bad, tok0, w, p, A);
             float s[NG];
@@ -757,10 +784,42 @@ __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mas
 #pragma unroll
             for (int k = 0; k < NG; ++k) smax = max(smax, __float_as_uint(s[k]) & 0x7fffffffu);
         }
+        float down[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) down[n][0] = down[n][1] = 1.f;
         const uint32_t sb = __reduce_max_sync(0xffffffffu, smax);
-        const int ne = max(A.re, min((int)(sb >> 23) + ((sb & 0x7fffffu) != 0), 254));
-        const float down = A.re == ne ? 1.f : ex2((float)(A.re - ne));
-        A.re = ne;
+        if (sb > A.limit) {
+            // a column's R follows the scales of the tokens that it sees: in sub-tiles that not every row sees in full
+            // (up to the last cached token; scales are zero from there on), column by column
+            uint32_t big[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) big[n][0] = big[n][1] = sb;
+            if (tok0 < lo_max || min(tok0 + kSub, w.q.kv) > hi_min) {
+#pragma unroll 1
+                for (int col = 0; col < w.L.rows; ++col) {
+                    const long long pos = (long long)w.q.kv - w.q.qn + w.L.i0 + (w.L.first + col) / p.group;
+                    const int j = tok0 + lane;
+                    const uint32_t of = __reduce_max_sync(0xffffffffu, j <= pos && j >= lowest_key(p, pos) ? smax : 0u);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            if (col == n * 8 + 2 * t + c) big[n][c] = of;
+                }
+            }
+            int least = kFarScale >> 23;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int re = r_exponent(A.inv[n][c]);
+                    const int ne = max(re, (int)(big[n][c] >> 23) + ((big[n][c] & 0x7fffffu) != 0));
+                    down[n][c] = ex2((float)(re - ne));
+                    A.inv[n][c] = r_inverse(ne);
+                    least = min(least, ne);
+                }
+            A.limit = (uint32_t)__reduce_min_sync(0xffffffffu, least) << 23;
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -773,8 +832,8 @@ __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mas
                 for (int k = 0; k < NG; ++k) A.ab[k][n][c] *= f;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
-                    A.o[i][n][c] *= f * down;
-                    A.o[i][n][c + 2] *= f * down;
+                    A.o[i][n][c] *= f * down[n][c];
+                    A.o[i][n][c + 2] *= f * down[n][c];
                 }
             }
     }
@@ -798,27 +857,33 @@ __device__ __forceinline__ void tile(const uint8_t* stage, int sub, uint32_t mas
     // over a whole unit, with uncentred codes, 30 f32 requests were 2e-5 off.)
     // bf16 / f16: the sums of the codes as they are start at -8 sum p s, which
     // leaves a few 2^-24 of it. f32: the codes themselves are centred.
-    const float inv = __uint_as_float((uint32_t)(min(268 - A.re, 254)) << 23);   // 2^14 / R
     constexpr int kParts = C::kSplit ? 2 : 1;
     uint32_t P[kBlocks][kParts][NG][NT][2];
 #pragma unroll
     for (int mb = 0; mb < kBlocks; ++mb) {
-        float sc[2][NG], bi[2][NG];
+        float sc[2][NG], bi[2][NG], z[NT][4];   // z: p 2^14 / R (0 where s / R may be anything)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             load_groups<T, NG>(vsc + (16 * mb + tg + 8 * e) * NG * C::E, sc[e]);
             load_groups<T, NG>(vbi + (16 * mb + tg + 8 * e) * NG * C::E, bi[e]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                z[n][2 * e] = x[mb][n][2 * e];
+                z[n][2 * e + 1] = x[mb][n][2 * e + 1];
+                mul2(z[n][2 * e], z[n][2 * e + 1], A.inv[n][0], A.inv[n][1]);
+            }
         }
 #pragma unroll
         for (int k = 0; k < NG; ++k) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float mid = fmaf(8.f, sc[e][k], bi[e][k]), f = sc[e][k] * inv;
+                const float f = sc[e][k], mid = fmaf(8.f, f, bi[e][k]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) A.ab[k][n][c] = fmaf(x[mb][n][2 * e + c], mid, A.ab[k][n][c]);
-                    const float y0 = x[mb][n][2 * e] * f, y1 = x[mb][n][2 * e + 1] * f;
+                    float y0 = z[n][2 * e], y1 = z[n][2 * e + 1];
+                    mul2(y0, y1, f, f);
                     const uint32_t w = pack_f16(y0, y1);
                     P[mb][0][k][n][e] = transpose8(w);
                     if constexpr (C::kSplit) {
@@ -912,7 +977,6 @@ __device__ __forceinline__ void deposit(Acc<C>& A, uint8_t* buf) {
                 for (int k = 0; k < C::NG; ++k) A.ab[k][n][c] += __shfl_xor_sync(0xffffffffu, A.ab[k][n][c], s);
             }
         }
-    const float R = __uint_as_float((uint32_t)A.re << 23);
     constexpr float kLow = C::kSplit ? 1.f / 16384.f : 1024.f, kHigh = C::kSplit ? 1.f / 16384.f : 64.f;   // 2^-14 / the codes' unit
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -924,6 +988,7 @@ __device__ __forceinline__ void deposit(Acc<C>& A, uint8_t* buf) {
                 sl[warp * NC + col] = A.l[n][c];
             }
             float* dst = o + (warp * NC + col) * DP;
+            const float R = __uint_as_float((uint32_t)r_exponent(A.inv[n][c]) << 23);
             if constexpr (C::GS == 32) {
 #pragma unroll
                 for (int k = 0; k < C::NG; ++k) {   // channels 32 k + 8 (g >> 1) + 4 (g & 1) + 0..3

@@ -447,7 +447,8 @@ gai4_status gai4_kv_read(const uint32_t* packed, const void* scales, const void*
  * A row does not depend on tokens that it does not see, whatever their codes,
  * scales and biases hold. A scale or bias that is infinite or NaN makes the
  * rows that see it NaN: all of a row for keys (unless the score is -inf), the
- * group's channels for values.
+ * group's channels for values. (With few rows, or f32, a value group whose
+ * 8 s + b is beyond binary32 counts as infinite.)
  * bf16 / f16: with few rows per key/value head the codes enter the matrix unit
  * as they are and scales and biases are applied in binary32; with many rows
  * (max_q_len * q_heads / kv_heads above 32) keys, values and probabilities are

@@ -191,3 +191,51 @@ def test_f16_rows_of_the_largest_values_through_the_cache():
     want, bound = many_rows64(q, kk, vv, pos, 0, d ** -0.5, U["f16"])
     assert float(want[pos < 100].abs().max()) < 10 and bool((want.abs() + bound < 65504).all())
     assert bool(((out.double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("e", [40, 60, 100, 124])
+@pytest.mark.parametrize("dt,kv,q_len,window", [("bf16", 300, 4, 0), ("f32", 300, 3, 0), ("bf16", 300, 1, 50),
+                                                ("f32", 700, 4, 100), ("bf16", 5000, 4, 3000), ("f32", 400, 20, 0)])
+def test_large_scales_on_tokens_that_a_row_does_not_see(dt, kv, q_len, window, e):
+    """Finite value scales of 2^e, at a token that none sees and at one that only the later rows see."""
+    hkv, g, d, gs, page = 2, 2, 64, 32, 32
+    q, kc, vc, table, kvs, cu = problem([kv], [q_len], hkv, g, d, gs, page, dt, 97)
+    scales = vc[1].clone()
+    tokens = ([kv - 1] if q_len > 1 else []) + ([kv - q_len - window] if window else [])
+    for t in tokens:
+        scales[int(table[0, t // page]), 1, t % page, 1] = 2.0**e
+    vc = (vc[0], scales, vc[2])
+    out, lse = attend(q, kc, vc, table, kvs, cu, gs, q_len, window)
+    want, bound, rl, lb = attention64(q, kc, vc, table, kvs, cu, gs, d ** -0.5, window, dt)
+    # the row that sees such a token: eight times p s, rounded to 11 bits, where the code is 0
+    if q_len > 1:
+        bound[-1, g:] += 2.0 ** (e - 8)
+    compare(out, lse, (want, bound, rl, lb), torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda"))
+
+
+@pytest.mark.parametrize("s,b", [(2.0**126, 0.0), (2.0**125, 0.0), (2.0**127, -(2.0**127)), (2.0**124, 3.2e38), (0.5, 3.3e38)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_value_groups_at_the_end_of_the_range(dt, s, b):
+    """Few rows: a group whose middle, 8 s + b, is beyond binary32 counts as infinite, and only for the rows that see
+    its token; others are computed."""
+    hkv, g, d, gs, page, kv, q_len, window = 2, 2, 64, 32, 32, 500, 4, 100
+    q, kc, vc, table, kvs, cu = problem([kv], [q_len], hkv, g, d, gs, page, dt, 98)
+    ref = attention64(q, kc, vc, table, kvs, cu, gs, d ** -0.5, window, dt)
+    cache = [x.clone() for x in vc]
+    tokens = [kv - 2, kv - q_len - window, kv - q_len - window + 1]
+    for t in tokens:
+        at = (int(table[0, t // page]), 1, t % page, 1)
+        cache[1][at], cache[2][at] = s, b
+    out, lse = attend(q, kc, cache, table, kvs, cu, gs, q_len, window)
+    pos = torch.arange(kv - q_len, kv, device="cuda")
+    hit = torch.zeros(q.shape, dtype=torch.bool, device="cuda")
+    for t in tokens:
+        hit[(t <= pos) & (t > pos - window), g:, gs:] = True
+    assert bool(hit[2:, g:].any()) and not bool(hit[1].any())       # (the second row sees none of the three)
+    want, bound, _, _ = ref
+    assert bool(((out.double() - want).abs() <= bound)[~hit].all())
+    if 8 * s + b > 3.4028235e38:
+        assert bool(out[hit].isnan().all())
+    else:
+        want, bound, _, _ = attention64(q, kc, cache, table, kvs, cu, gs, d ** -0.5, window, dt)
+        assert bool(((out.double() - want).abs() <= bound)[want.abs() + bound < 3.3e38].all())
