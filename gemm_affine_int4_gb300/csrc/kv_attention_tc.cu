@@ -21,7 +21,7 @@
 // QK_1, so the commit of QK_i of a tile also says that PV_i of the tile
 // before it has finished: a softmax warp may then rescale O_i, which it does
 // only when a row's maximum has grown by more than 2^8 (P and the sum are
-// merely larger until then).
+// merely larger until then; f16 has room for it, see kAbove).
 //
 // Codes of a word come out of it as pairs (0, 4), (1, 5), (2, 6), (3, 7); that
 // order of the channels is kept in shared memory (queries are stored in it,
@@ -237,6 +237,13 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
 // power of two that values and keys carry (see above)
 template <bool BF>
 constexpr float kUndo = BF ? 1099511627776.f : 1.f;   // 2^40
+
+// Probabilities are taken relative to 2^-kAbove of a row's largest, so that
+// binary16 holds them from 2^15 (the maximum may lag by 2^8) down: all 11 bits to
+// 2^-21 of the largest, and multiples of 2^-31 of it below. Without it, many keys
+// beside one that takes nearly all were a sixth off at 1.4e-7 each.
+template <bool BF>
+constexpr float kAbove = BF ? 0.f : 7.f;
 
 // scale and bias of a group, in the forms that the codes need
 template <bool BF>
@@ -902,8 +909,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mx4[(e >> 1) & 3] = max3(mx4[(e >> 1) & 3], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
                 float mx = max3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3]));
                 mx *= f;
-                if (__any_sync(0xffffffffu, mx > m + 8.f || (m == -INFINITY && mx > m))) {
-                    const float mn = fmaxf(m, mx);
+                if (__any_sync(0xffffffffu, mx > m + (8.f + kAbove<BF>) || (m == -INFINITY && mx > m))) {
+                    const float mn = fmaxf(m, mx - kAbove<BF>);
                     const float a = m == -INFINITY ? 0.f : ex2(m - mn);
                     if (key0 > first_key) {
 #pragma unroll 1

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import gemm_affine_int4_gb300 as g4
-from kv_ref import U, attention64, rows64
+from kv_ref import DT, U, attention64, rows64
 from test_gpu_kv_cache import i32, problem
 
 pytestmark = pytest.mark.gpu
@@ -239,3 +239,28 @@ def test_value_groups_at_the_end_of_the_range(dt, s, b):
     else:
         want, bound, _, _ = attention64(q, kc, cache, table, kvs, cu, gs, d ** -0.5, window, dt)
         assert bool(((out.double() - want).abs() <= bound)[want.abs() + bound < 3.3e38].all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("q_len,batch", [(1, 3), (40, 300)])
+def test_one_key_far_above_many(dt, q_len, batch):
+    """A first key that takes nearly all of the softmax and has values of zero, and thousands of others of one score,
+    1.44e-7 of its probability each, whose values are one: their sum is the output. Requests share their pages, and are so
+    many that most units are whole. Beside the usual bound, many rows in f16: probabilities are multiples of 2^-31 of the
+    row's largest, so off by half of that for each key."""
+    d, gs, page, kv = 64, 64, 64, 5033
+    nb = -(-kv // page)
+    q = torch.full((batch * q_len, 2, d), 1.0, dtype=DT[dt], device="cuda")
+    kc, vc = (g4.gai4_kv_cache(nb, 1, page, d, gs, DT[dt]) for _ in range(2))
+    kc[2][0, 0, 0] = 1.96875              # scores of 0.125 * 64 * 1.96875 = 15.75 and 0
+    vc[2].fill_(1.0)
+    vc[2][0, 0, 0] = 0.0
+    table = torch.arange(nb, dtype=torch.int32, device="cuda").expand(batch, nb).contiguous()
+    out, lse = attend(q, kc, vc, table, [kv] * batch, [q_len * i for i in range(batch + 1)], gs, q_len)
+    want, bound, rl, lb = attention64(q[:q_len], kc, vc, table[:1], [kv], [0, q_len], gs, d ** -0.5, 0, dt, q_len > 16)
+    if dt == "f16" and q_len > 16:
+        bound = bound + kv * 2.0**-32
+    assert bool(((want > 7e-4) & (want < 8e-4)).all())
+    err = (out.double().view(batch, q_len, 2, d) - want).abs()
+    assert bool((err <= bound).all()), f"worst {float((err / bound).max()):.3g} of the bound"
+    assert bool(((lse.double().view(batch, q_len, 2) - rl).abs() <= lb).all())
