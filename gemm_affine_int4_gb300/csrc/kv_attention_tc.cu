@@ -874,8 +874,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int hi_min = live ? hi_key : 0x7fffffff, lo_max = lo_key;
             hi_min = __reduce_min_sync(0xffffffffu, hi_min);
             lo_max = __reduce_max_sync(0xffffffffu, lo_max);
-            // scores to powers of two; a tiny factor in the place of 0 keeps masked scores at -inf
-            const float f = fmaxf(fabsf(p.scale) * 1.4426950408889634f, 1e-30f) * kUndo<BF>;
+            // scores to powers of two; the least factor in the place of 0 keeps masked scores at -inf
+            const float f = fmaxf(fabsf(p.scale) * 1.4426950408889634f * kUndo<BF>, 1.4e-45f);
             const int first_key = (cur->t_first + cur->first()) * kKeys, end_key = (cur->t_first + cur->last()) * kKeys;
             const bool holes_here = holes(p, *cur, first_key, end_key, lane) != 0;
             for (int key0 = first_key; key0 < end_key; key0 += kKeys) {

@@ -264,3 +264,13 @@ def test_one_key_far_above_many(dt, q_len, batch):
     err = (out.double().view(batch, q_len, 2, d) - want).abs()
     assert bool((err <= bound).all()), f"worst {float((err / bound).max()):.3g} of the bound"
     assert bool(((lse.double().view(batch, q_len, 2) - rl).abs() <= lb).all())
+
+
+@pytest.mark.parametrize("e,scale", [(100, 2.0**-103), (100, -(2.0**-104)), (90, 0.0)])
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_extreme_queries_and_scales(q_len, e, scale):
+    q, kc, vc, table, kv, cu = problem([130, 64], [q_len] * 2, 2, 4, 64, 64, 16, "bf16", 61)
+    q = (q.float() * 2.0**e).bfloat16()
+    out, lse = attend(q, kc, vc, table, kv, cu, 64, q_len, scale=scale)
+    compare(out, lse, attention64(q, kc, vc, table, kv, cu, 64, scale, 0, "bf16", q_len > 1),
+            torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda"))
