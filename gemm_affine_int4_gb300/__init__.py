@@ -497,19 +497,22 @@ def gai4_kv_attention_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int
 
 
 def gai4_kv_attention(q, k_cache, v_cache, block_table, kv_lens, cu_q, group_size: int = 64, scale=None,
-                      window: int = 0, max_q_len: int = 1, out=None, lse=None, workspace=None, stream=None):
+                      window: int = 0, max_q_len: int | None = None, out=None, lse=None, workspace=None, stream=None):
     """Causal attention of q [tokens, q_heads, head_dim] (rows of one request
     after another, offsets cu_q [B + 1]) over each request's kv_lens[r] cached
     tokens, the new ones among them. scale defaults to head_dim ** -0.5;
     window > 0 keeps the last `window` positions; max_q_len, the most rows of a
-    request, guides the choice of kernel. lse, when given, float32 [tokens,
-    q_heads], takes the logarithms of the softmax sums. A workspace is
-    allocated here when none is given."""
+    request, guides the choice of kernel (left out, the requests' mean stands
+    for it: give it where prompts and single tokens share a call). lse, when
+    given, float32 [tokens, q_heads], takes the logarithms of the softmax sums.
+    A workspace is allocated here when none is given."""
     nb, h, page, d = _kv_shape(k_cache, group_size)
     _same_caches(k_cache, v_cache)
     n, hq, _ = q.shape
     B, width = block_table.shape
     T = k_cache[1].dtype
+    if max_q_len is None:
+        max_q_len = -(-n // max(B, 1))
     qs = _token_stride(q, hq, d, T, "q")
     _need(kv_lens.shape == (B,) and cu_q.shape == (B + 1,), "block_table [B, max_blocks], kv_lens [B], cu_q [B + 1]")
     if out is None:

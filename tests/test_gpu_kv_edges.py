@@ -274,3 +274,13 @@ def test_extreme_queries_and_scales(q_len, e, scale):
     out, lse = attend(q, kc, vc, table, kv, cu, 64, q_len, scale=scale)
     compare(out, lse, attention64(q, kc, vc, table, kv, cu, 64, scale, 0, "bf16", q_len > 1),
             torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda"))
+
+
+def test_prompts_without_a_stated_query_length():
+    """max_q_len left out: taken from the number of rows a request, so a prompt gets the kernel of many rows and single
+    tokens that of few."""
+    for kv, q_len, stated in (([300], [200], 200), ([300, 400], [1, 1], 1), ([90, 80], [80, 60], 70)):
+        q, kc, vc, table, kv, cu = problem(kv, q_len, 2, 4, 64, 32, 32, "bf16", 103)
+        a = g4.gai4_kv_attention(q, kc, vc, table, i32(kv), i32(cu), group_size=32)
+        b = g4.gai4_kv_attention(q, kc, vc, table, i32(kv), i32(cu), group_size=32, max_q_len=stated)
+        assert torch.equal(a, b)
