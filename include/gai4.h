@@ -392,8 +392,9 @@ gai4_status gai4_check_bounded_wait(int arrive, int64_t limit_cycles, int* statu
  *     info[0] pages missing           info[1] requests with more than max_blocks pages
  *     info[2] tokens over num_tokens  info[3] 1 if a length is negative, or free_count
  *                                     or the pages pushed do not fit free_capacity
- * No page may be in two requests' rows. kv_lens_out and free_count_out must
- * not alias kv_lens and free_count. 1 <= batch <= 8192; num_tokens >= 0.
+ * No page may be in two requests' rows. Outputs must not overlap the inputs
+ * (kv_lens_out and free_count_out in the place of kv_lens and free_count are
+ * refused). 1 <= batch <= 8192; num_tokens >= 0.
  * slots 8-byte aligned, the others 4-byte aligned. Nothing is read on the host.
  */
 gai4_status gai4_kv_plan(const int32_t* kv_lens, const int32_t* q_lens, int32_t* block_table, int64_t max_blocks,
@@ -436,27 +437,41 @@ gai4_status gai4_kv_read(const uint32_t* packed, const void* scales, const void*
  *     out[row, h] = sum_j softmax_j(scale * q[row, h] . k_j) v_j
  *     lse[row, h] = log sum_j exp(scale * q[row, h] . k_j)      (natural log)
  *   A row that sees nothing gives zeros and lse -inf, and so do the rows from
- *   cu_q[batch] to num_tokens.
+ *   cu_q[batch] to num_tokens. cu_q ascends; rows before cu_q[0] are neither
+ *   read nor written.
  *   q    T, row i, head h at q + i * q_token_stride + h * head_dim (strides in
  *        elements, >= q_heads * head_dim; aligned to the element size)
  *   out  T, likewise with out_token_stride; lse [num_tokens, q_heads] f32 or NULL
  *   block_table [batch, max_blocks] i32; entries outside [0, num_blocks) are
  *        never read from, and their tokens are left out.
  *   max_q_len: the largest number of query rows of a request as far as the
- *        host knows; it only guides the choice of kernel.
+ *        host knows; it only guides the choice of kernel, one for all requests.
+ *        A step of prompts and single tokens is faster, and its single tokens
+ *        are more exact, as two calls: requests 0 to n - 1 with the rows up to
+ *        cu_q[n], then the others with block_table, kv_lens and cu_q from n on.
+ * Outputs and workspace must not overlap the inputs or each other; scale is
+ * finite.
  * A row does not depend on tokens that it does not see, whatever their codes,
  * scales and biases hold. A scale or bias that is infinite or NaN makes the
  * rows that see it NaN: all of a row for keys (unless the score is -inf), the
  * group's channels for values. (With few rows, or f32, a value group whose
  * 8 s + b is beyond binary32 counts as infinite.)
- * bf16 / f16: with few rows per key/value head the codes enter the matrix unit
- * as they are and scales and biases are applied in binary32; with many rows
- * (max_q_len * q_heads / kv_heads above 32) keys, values and probabilities are
- * rounded once to T and multiplied on the tensor cores as in gai4_qmm_t; keys
- * are then at most 2^37 (f16: 65504) in magnitude, and bf16 values at most 2^37
- * (a scale of 2^35 or more counts as infinite). Softmax and sums are
- * binary32. f32: queries and probabilities enter as two binary16 parts, 22
- * bits. Results do not depend on the contents of the workspace, and repeat bit
+ * Softmax maxima and sums, and the sums over keys, are binary32. Before that
+ *  - f32, and bf16 / f16 with few rows per key/value head: codes enter the
+ *    matrix unit as they are, scales and biases are applied to its products.
+ *    Probability times value scale is rounded to 11 bits (f32: 22 bits, and so
+ *    are queries), and to multiples of 2^-37 of the largest value scale that the
+ *    row sees. The unit's own sums, over a row of keys or 32 tokens of values,
+ *    are truncated: f32 outputs are a few times as far off as those of a
+ *    computation in binary32 throughout.
+ *  - bf16 / f16 with many rows (max_q_len * q_heads / kv_heads above 32): keys,
+ *    values and probabilities are rounded once to T and multiplied on the
+ *    tensor cores as in gai4_qmm_t (f16 probabilities to multiples of 2^-31 of
+ *    the row's largest, if that is coarser), about twice the error of a
+ *    rounding of the outputs alone. Keys are at most 2^37 (f16: 65504) in
+ *    magnitude, bf16 values at most 2^37 (a scale of 2^35 or more counts as
+ *    infinite), and for bf16 `scale` is less than 2^80 in magnitude.
+ * Results do not depend on the contents of the workspace, and repeat bit
  * for bit. num_tokens * (q_heads / kv_heads) above 2^31 - 1 is UNSUPPORTED;
  * 1 <= batch < 2^27, page_size * max_blocks <= 2^31 - 4096.
  * workspace: 16-byte aligned, >= gai4_kv_attention_workspace_bytes(...).

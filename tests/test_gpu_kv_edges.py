@@ -284,3 +284,33 @@ def test_prompts_without_a_stated_query_length():
         a = g4.gai4_kv_attention(q, kc, vc, table, i32(kv), i32(cu), group_size=32)
         b = g4.gai4_kv_attention(q, kc, vc, table, i32(kv), i32(cu), group_size=32, max_q_len=stated)
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("g,q_len,window", [(33, 9, 0), (48, 40, 100), (71, 21, 0), (300, 5, 0), (300, 1, 64), (1000, 3, 0)])
+def test_many_query_heads_per_key_head(dt, g, q_len, window):
+    kv = [150, 700, 3]
+    q, kc, vc, table, kv, cu = problem(kv, [q_len, q_len, 1], 1, g, 64, 32, 32, dt, 101)
+    out, lse = attend(q, kc, vc, table, kv, cu, 32, q_len, window)
+    compare(out, lse, attention64(q, kc, vc, table, kv, cu, 32, 64 ** -0.5, window, dt, True),
+            torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda"))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_a_step_of_single_tokens_and_a_prompt_as_two_calls(dt):
+    """The second call has the tables and offsets of the later requests, and leaves the first one's rows alone."""
+    kv, q_lens = [90, 700, 1, 400, 60], [1, 1, 1, 150, 60]
+    q, kc, vc, table, kv, cu = problem(kv, q_lens, 2, 4, 64, 32, 32, dt, 105)
+    q = torch.cat([q, q[:2]])          # two rows of no request
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 5.0, device="cuda")
+    kvt, cut = i32(kv), i32(cu)
+    g4.gai4_kv_attention(q[:3], kc, vc, table[:3], kvt[:3], cut[:4], group_size=32, max_q_len=1, out=out[:3], lse=lse[:3])
+    first = out.clone(), lse.clone()
+    assert bool((out[3:] == 7.0).all()) and bool((lse[3:] == 5.0).all())
+    g4.gai4_kv_attention(q, kc, vc, table[3:], kvt[3:], cut[3:], group_size=32, max_q_len=150, out=out, lse=lse)
+    assert torch.equal(out[:3], first[0][:3]) and torch.equal(lse[:3], first[1][:3])
+    assert bool((out[-2:] == 0.0).all()) and bool((lse[-2:] == -np.inf).all())
+    for many, rows in ((False, slice(0, 3)), (True, slice(3, cu[-1]))):
+        want, bound, rl, lb = attention64(q[:cu[-1]], kc, vc, table, kv, cu, 32, 64 ** -0.5, 0, dt, many)
+        assert bool(((out[rows].double() - want[rows]).abs() <= bound[rows]).all())
+        assert bool(((lse[rows].double() - rl[rows]).abs() <= lb[rows]).all())
