@@ -31,7 +31,7 @@
 // the power leaves through f and through the last division. Keys and values
 // from 2^-86 to 2^37 keep all their bits.
 // f16: codes by the offset of 1024, then fma(c, s, b); keys up to 65504. Value
-// groups that may have larger values are multiplied apart, in binary32.
+// groups that reach beyond it are multiplied apart, in binary32.
 //
 // Work split: a unit is (request, block of 256 rows, key/value head); all
 // units lie on one line, each with places in proportion to its key tiles (and
@@ -290,13 +290,11 @@ template <bool BF>
 __device__ __forceinline__ uint32_t too_wide(uint32_t s, uint32_t b) {
     return ((s | b << 16) & 0x7fff7fffu) + (BF ? 0x00802F00u : 0x04000400u);
 }
-// The same signs for values that the tensor cores do not multiply: those, and
-// f16 groups with |s| >= 2048 or |b| >= 32768. Below, |15 s + b| is less than
-// 65504, so no code expands to an infinity. (A test of the sum itself would be
-// exact, but not as short, and every tile of values goes through it.)
-template <bool BF>
-__device__ __forceinline__ uint32_t set_apart(uint32_t s, uint32_t b) {
-    return BF ? too_wide<BF>(s, b) : ((s | b << 16) & 0x7fff7fffu) + 0x08001800u;
+// f16: groups whose values cannot all be expanded, two of them, a sign bit for
+// each in its half: those, and finite ones whose last code, 15 s + b, is rounded
+// to infinity (the others lie between that and b).
+__device__ __forceinline__ uint32_t too_large(uint32_t s0, uint32_t b0, uint32_t s1, uint32_t b1) {
+    return (fma2<false>(s0 | s1 << 16, 0x4B804B80u, b0 | b1 << 16) & 0x7fff7fffu) + 0x04000400u;
 }
 
 // columns of tensor memory (128 for each M tile)
@@ -749,13 +747,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // 0 x NaN: zeros in their place, and the softmax warps add to the outputs that need it what was
                     // left out.
                     uint32_t wide = 0;
+                    if constexpr (BF) {
 #pragma unroll
-                    for (int x = 0; x < D / 32; ++x) wide |= set_apart<BF>(scale[x], bias[x]);
-                    if (side && (wide & 0x80008000u)) {
+                        for (int x = 0; x < D / 32; ++x) wide |= too_wide<BF>(scale[x], bias[x]);
+                        if (side && (wide & 0x80008000u)) {
 #pragma unroll
-                        for (int x = 0; x < D / 32; ++x)
-                            if (set_apart<BF>(scale[x], bias[x]) & 0x80008000u) scale[x] = bias[x] = 0;
-                        wide_values = 1;
+                            for (int x = 0; x < D / 32; ++x)
+                                if (too_wide<BF>(scale[x], bias[x]) & 0x80008000u) scale[x] = bias[x] = 0;
+                            wide_values = 1;
+                        }
+                    } else {
+                        if (side) {
+#pragma unroll
+                            for (int x = 0; x < D / 32; x += 2) wide |= too_large(scale[x], bias[x], scale[x + 1], bias[x + 1]);
+                            if (wide & 0x80008000u) {
+#pragma unroll
+                                for (int x = 0; x < D / 32; ++x)
+                                    if (too_large(scale[x], bias[x], 0u, 0u) & 0x8000u) scale[x] = bias[x] = 0;
+                                wide_values = 1;
+                            }
+                        }
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ring_empty[s]);
@@ -986,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int g = 0; g < ng; ++g) {
                         const uint32_t s = vs[line * ng + g], b = vb[line * ng + g];
                         if (too_wide<BF>(s, b) & 0x80008000u) groups |= 1u << g;
-                        else if (set_apart<BF>(s, b) & 0x80008000u) large |= 1u << g;
+                        else if (!BF && (too_large(s, b, 0u, 0u) & 0x8000u)) large |= 1u << g;
                     }
                 }
 #pragma unroll 1
@@ -999,18 +1010,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t add = __shfl_sync(0xffffffffu, large, o);
                         if (add == 0) continue;
                         const long long at = __shfl_sync(0xffffffffu, line, o);
-                        auto code = [&](const uint32_t* w, int d) { return (w[at * (D / 8) + (d >> 3)] >> (4 * (d & 7))) & 15u; };
                         float prob = 0.f;
                         if (sees) {
                             const uint16_t* q = static_cast<const uint16_t*>(p.q) + (rq_q0 + tok) * p.q_stride + (long long)head * D;
                             float dot = 0.f;
-#pragma unroll 1
-                            for (int d = 0; d < D; ++d) {
-                                const long long g = at * ng + (d >> gs_log2);
-                                const __half k = __hfma(__ushort2half_rn((unsigned short)code(p.k.packed, d)),
-                                                        __ushort_as_half(static_cast<const uint16_t*>(p.k.scales)[g]),
-                                                        __ushort_as_half(static_cast<const uint16_t*>(p.k.biases)[g]));
-                                dot = fmaf(F16::to_f32(q[d]), __half2float(k), dot);
+#pragma unroll 4
+                            for (int c = 0; c < D / 8; ++c) {
+                                const long long g = at * ng + ((8 * c) >> gs_log2);
+                                const __half ks = __ushort_as_half(static_cast<const uint16_t*>(p.k.scales)[g]);
+                                const __half kb = __ushort_as_half(static_cast<const uint16_t*>(p.k.biases)[g]);
+                                const uint32_t w = p.k.packed[at * (D / 8) + c];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const __half k = __hfma(__ushort2half_rn((unsigned short)((w >> (4 * e)) & 15u)), ks, kb);
+                                    dot = fmaf(F16::to_f32(q[8 * c + e]), __half2float(k), dot);
+                                }
                             }
                             prob = ex2(fmaf(dot, p.scale * 1.4426950408889634f, m == -INFINITY ? 0.f : -m));
                         }
@@ -1019,12 +1033,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const int g = (8 * c) >> gs_log2;
                             if (!((add >> g) & 1u)) continue;
                             const float s = F16::to_f32(vs[at * ng + g]), b = F16::to_f32(vb[at * ng + g]);
+                            const uint32_t w = p.v.packed[at * (D / 8) + c];
                             uint32_t y[8];
                             tmem_ld8(o_tm + 8 * c, y);
                             tmem_ld_wait();
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {   // (channels in the order 0 4 1 5 2 6 3 7)
-                                const float v = fmaf(s, (float)code(p.v.packed, 8 * c + (e >> 1) + 4 * (e & 1)), b);
+                                const float v = fmaf(s, (float)((w >> (4 * ((e >> 1) + 4 * (e & 1)))) & 15u), b);
                                 if (sees) y[e] = __float_as_uint(fmaf(prob, v, __uint_as_float(y[e])));
                             }
                             tmem_st8(o_tm + 8 * c, y);
