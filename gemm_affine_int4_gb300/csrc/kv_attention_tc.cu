@@ -980,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (mine && wide_values) {
             const int row = row0 + i * 128 + r, pl = p.sh.page_log2, ng = D >> gs_log2;
             const bool live = row < rows;
-            const int tok = live ? row / p.group : 0, head = h * p.group + (live ? row - tok * p.group : 0);
+            const int tok = live ? row / p.group : 0;
             const long long pos = live ? (long long)cur->q.kv - cur->q.qn + tok : -1;
             const long long lo = p.window > 0 ? pos - p.window + 1 : 0;
             const int end = min((cur->t_first + cur->last()) * kKeys, cur->q.kv);
@@ -1012,21 +1012,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const long long at = __shfl_sync(0xffffffffu, line, o);
                         float prob = 0.f;
                         if (sees) {
-                            const uint16_t* q = static_cast<const uint16_t*>(p.q) + (rq_q0 + tok) * p.q_stride + (long long)head * D;
-                            float dot = 0.f;
+                            float dot = 0.f;                // (the queries are still in their tile)
 #pragma unroll 4
                             for (int c = 0; c < D / 8; ++c) {
                                 const long long g = at * ng + ((8 * c) >> gs_log2);
-                                const __half ks = __ushort_as_half(static_cast<const uint16_t*>(p.k.scales)[g]);
-                                const __half kb = __ushort_as_half(static_cast<const uint16_t*>(p.k.biases)[g]);
-                                const uint32_t w = p.k.packed[at * (D / 8) + c];
+                                const uint4 k = expand<BF>(p.k.packed[at * (D / 8) + c],
+                                                           Group<BF>(static_cast<const uint16_t*>(p.k.scales)[g],
+                                                                     static_cast<const uint16_t*>(p.k.biases)[g]));
+                                const uint4 q = *reinterpret_cast<const uint4*>(chunk_at(r, c));
+                                const uint32_t kw[4] = {k.x, k.y, k.z, k.w}, qw[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const __half k = __hfma(__ushort2half_rn((unsigned short)((w >> (4 * e)) & 15u)), ks, kb);
-                                    dot = fmaf(F16::to_f32(q[8 * c + e]), __half2float(k), dot);
+                                for (int e = 0; e < 4; ++e) {
+                                    dot = fmaf(T::to_f32((uint16_t)qw[e]), T::to_f32((uint16_t)kw[e]), dot);
+                                    dot = fmaf(T::to_f32((uint16_t)(qw[e] >> 16)), T::to_f32((uint16_t)(kw[e] >> 16)), dot);
                                 }
                             }
-                            prob = ex2(fmaf(dot, p.scale * 1.4426950408889634f, m == -INFINITY ? 0.f : -m));
+                            prob = ex2(fmaf(dot, fabsf(p.scale) * 1.4426950408889634f, m == -INFINITY ? 0.f : -m));
                         }
 #pragma unroll 1
                         for (int c = 0; c < D / 8; ++c) {
