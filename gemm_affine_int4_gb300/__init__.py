@@ -503,9 +503,10 @@ def gai4_kv_attention(q, k_cache, v_cache, block_table, kv_lens, cu_q, group_siz
     tokens, the new ones among them. scale defaults to head_dim ** -0.5;
     window > 0 keeps the last `window` positions; max_q_len, the most rows of a
     request, guides the choice of kernel (left out, the requests' mean stands
-    for it: give it where prompts and single tokens share a call). lse, when
-    given, float32 [tokens, q_heads], takes the logarithms of the softmax sums.
-    A workspace is allocated here when none is given."""
+    for it: give it where prompts and single tokens share a call; 0 takes the
+    kernel for few rows, which rounds less, for everything). lse, when given,
+    float32 [tokens, q_heads], takes the logarithms of the softmax sums. A
+    workspace is allocated here when none is given."""
     nb, h, page, d = _kv_shape(k_cache, group_size)
     _same_caches(k_cache, v_cache)
     n, hq, _ = q.shape

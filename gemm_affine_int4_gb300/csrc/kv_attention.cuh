@@ -43,11 +43,12 @@
 // O) records in the workspace, which a second kernel joins in order; its
 // launch overlaps the first. No sum depends on timing: results repeat.
 //
-// What bounds it: instruction issue (58 % of the cycles; the rest are waits
-// within the two consumer warps that an SMSP has). 4 requests of 90001 to
-// 131072 tokens, 8 key/value heads of 128 f16 values, 8 query heads each (494
-// MB): 114 us, 4.3 TB/s; with the loads alone 83 us, with the products alone
-// 111. 48 requests of up to 4500 tokens (126 MB): 43 us.
+// What bounds it: dependent instructions. The two or three consumer warps of an
+// SMSP issue in 59 % of its cycles, and each mostly waits for its own last
+// result. 4 requests of 90001 to 131072 tokens, 8 key/value heads of 128 f16
+// values, 8 query heads each (494 MB): 113 us, 4.4 TB/s; with the loads alone 83
+// us, with the products alone 111 (of 114 at the time). 48 requests of up to
+// 4500 tokens (126 MB): 43 us.
 #pragma once
 
 #include <math.h>
@@ -71,7 +72,9 @@ constexpr int kBlocks = kSub / 16;              // 16-token blocks of a sub-tile
 // not cut / cut, in us, at 8 key/value heads of 128 and 4 query heads each: one request of 60 tokens 6.4/9.0, of 300
 // 8.3/8.9, of 500 9.7/9.3, of 1000 12.6/10.4; 16 requests of 500 11.6/13.1, of
 // 1000 15.6/14.5; 64 of 500 20.8/24.1, of 1000 30.2/32.1, of 2000 46.9/42.5.
-// The host's part of a call falls by 2.5 us as well.
+// The host's part of a call falls by 2.5 us as well. (The width stands for the
+// requests' lengths, which the host does not know: under a wide table short
+// requests are cut.)
 constexpr int kWholeTokens = 512;
 // What the start and join of a unit cost, in tiles (see Walk). Measured with 2,
 // 4, 6 and 9: 48 ragged requests of up to 4500 tokens 52.7, 45.8, 42.2, 42.3

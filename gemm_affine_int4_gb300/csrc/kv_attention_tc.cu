@@ -48,9 +48,10 @@
 // products take at least 2050, a row's softmax 2500 beside its neighbours), and
 // shared memory: Q K^T alone reads its full 128 bytes a cycle. A prompt of 8192 bf16 tokens, 8
 // key/value heads of 128, 4 query heads each (550 GFLOP below the diagonal):
-// 460 us, 1.2 PFLOP/s; without the exponentials 446, without the expansion 439,
-// without both 405. Six prompts' chunks of 333 to 1500 rows behind up to 7000
-// tokens: 336 us. Tensor pipe 53 % of the cycles.
+// 465 us, 1.2 PFLOP/s (f16 497); when it took 460, without the exponentials 446,
+// without the expansion 439, without both 405. Six prompts' chunks of 333 to
+// 1500 rows behind up to 7000 tokens: 331 us (f16 355). Tensor pipe 53 % of the
+// cycles.
 // Slower, and not kept: two warps that issue products (641 us at the time, with
 // one 456), eight warps that expand (532), 64-key tiles with the queries in
 // tensor memory (536), any further unrolling (the instruction cache), two
@@ -320,7 +321,8 @@ __host__ __device__ constexpr size_t meta_bytes(int ctas) { return ((size_t)ctas
 struct Req {
     int q0, qn, kv;
     int nblk;               // blocks of 256 rows
-    int places, more;       // places of the units of block 0, and how many more each later block's have
+    int places, more;       // places of the units of block 0, and how many more each later block's have (rounded
+                            // down: 0 above 32 query heads, where later blocks count too little)
 };
 __device__ __forceinline__ Req request(const KvAttnLaunch& p, int r) {
     Req q;
@@ -745,7 +747,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     // Values that are not finite once expanded would reach the rows that do not see their token, as
                     // 0 x NaN: zeros in their place, and the softmax warps add to the outputs that need it what was
-                    // left out.
+                    // left out. (f16: the exact test for values only, 497 us for the prompt; for keys as well 504, with
+                    // the values saturated here instead 516.)
                     uint32_t wide = 0;
                     if constexpr (BF) {
 #pragma unroll

@@ -449,6 +449,7 @@ gai4_status gai4_kv_read(const uint32_t* packed, const void* scales, const void*
  *        A step of prompts and single tokens is faster, and its single tokens
  *        are more exact, as two calls: requests 0 to n - 1 with the rows up to
  *        cu_q[n], then the others with block_table, kv_lens and cu_q from n on.
+ *        0 takes the kernel for few rows, which rounds less, for everything.
  * Outputs and workspace must not overlap the inputs or each other; scale is
  * finite.
  * A row does not depend on tokens that it does not see, whatever their codes,
