@@ -65,6 +65,14 @@ SIGNATURES = {
     "gai4_kv_attention": ([_P, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _P, _I64, _P, _I, _I, _I64, _I64, _I64,
                            _I64, _I64, _I, _I64, _I, ctypes.c_float, _I64, _P, ctypes.c_size_t, _P], _I),
     "gai4_kv_attention_workspace_bytes": ([_I64, _I64, _I, _I], ctypes.c_size_t),
+    "gai4_rope_inv_freq": ([_P, _P, _I, ctypes.c_double, _I, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                            ctypes.c_double], _I),
+    "gai4_rope": ([_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, ctypes.c_float, _I, _I64, _I64, _I64, _I, _I, _I, _P],
+                  _I),
+    "gai4_rms_norm": ([_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I, _I64, _I64, ctypes.c_float, _P], _I),
+    "gai4_quantize_x_fp8": ([_P, _I64, _P, _P, _I, _I64, _I64, _P], _I),
+    "gai4_quantize_fp8": ([_P, _P, _P, _I, _I64, _I64, _P], _I),
+    "gai4_fp8_mm_t": ([_P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _P], _I),
 }
 
 
@@ -542,6 +550,202 @@ def gai4_kv_attention(q, k_cache, v_cache, block_table, kv_lens, cu_q, group_siz
         q.data_ptr(), qs, kp, ksc, kb, vp, vsc, vb, table, width, lens, cu, out.data_ptr(), os_, lse_ptr, _dtype(q),
         group_size, B, n, max_q_len, hq, h, d, nb, page, d ** -0.5 if scale is None else scale, window, ws, nbytes,
         _stream_handle(stream, q)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# around the attention: rotary positions, norm, e4m3 with block scales. e4m3
+# tensors are torch.float8_e4m3fn (or uint8 with the same bytes) [rows, K] with
+# float32 scales, [M, ceil(K / 128)] for activations and
+# [ceil(N / 128), ceil(K / 128)] for weights.
+# ---------------------------------------------------------------------------
+_E4M3 = torch.float8_e4m3fn
+_FP8_BLOCK = 128
+_ROPE_SCALING = {None: 0, "linear": 1, "ntk": 2, "yarn": 3, "smooth": 4}
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _launch(name: str, fn, t: torch.Tensor, *args):
+    """Calls `fn` with the tensors' device current."""
+    i = t.get_device()
+    if i == _get_device():
+        st = fn(*args)
+    else:
+        with torch.cuda.device(i):
+            st = fn(*args)
+    if st != GAI4_OK:
+        raise Gai4Error(name, st)
+
+
+def _together(*tensors):
+    """All on one CUDA device."""
+    i = tensors[0].get_device()
+    for t in tensors:
+        if not t.is_cuda or t.get_device() != i:
+            raise ValueError("gai4: tensors must live on one CUDA device")
+
+
+def _row_stride(t: torch.Tensor, what: str) -> int:
+    """Row stride of [rows, cols] with contiguous columns."""
+    rows, cols = t.shape
+    _need(t.stride(1) == 1 or cols == 1, f"{what}: columns must be contiguous")
+    return t.stride(0) if rows > 1 else cols
+
+
+def _e4m3(t: torch.Tensor):
+    _need(t.dtype == _E4M3 or t.dtype == torch.uint8, "codes must be float8_e4m3fn (or uint8)")
+
+
+def gai4_rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                       original_len: float = 0.0, low: float = 1.0, high: float | None = None, device="cuda"):
+    """(inv_freq float64 [rot_dim / 2], mscale) for gai4_rope. scaling: None,
+    "linear", "ntk", "yarn" or "smooth"; high defaults to 32 (yarn) or 4."""
+    _need(scaling in _ROPE_SCALING, f"unknown scaling {scaling!r}")
+    host = torch.empty(max(rot_dim // 2, 1), dtype=torch.float64)
+    mscale = ctypes.c_float()
+    if high is None:
+        high = 4.0 if scaling == "smooth" else 32.0
+    _check("gai4_rope_inv_freq", lib().gai4_rope_inv_freq(host.data_ptr(), ctypes.addressof(mscale), rot_dim, base,
+                                                          _ROPE_SCALING[scaling], factor, original_len, low, high))
+    return host.to(device), mscale.value
+
+
+def gai4_rope(q, k, positions, inv_freq, interleaved: bool = False, mscale: float = 1.0, q_out=None, k_out=None,
+              stream=None):
+    """Rotary positions of query and key rows [tokens, heads, head_dim] (any
+    token stride; k may be None): the first 2 * len(inv_freq) channels of each
+    head, halves or, interleaved, neighbours as pairs, turn by
+    positions[token] * inv_freq[pair]. positions int32 [tokens], inv_freq
+    float64. New tensors unless q_out, k_out are given; q and k themselves are
+    allowed. Returns (q_out, k_out)."""
+    n, hq, d = q.shape
+    T = q.dtype
+    _need(positions.shape == (n,) and positions.dtype == torch.int32, "positions must be int32 [tokens]")
+    _need(inv_freq.dim() == 1 and inv_freq.dtype == torch.float64, "inv_freq must be float64 [rot_dim / 2]")
+    hk = 0 if k is None else k.shape[1]
+    qs = _token_stride(q, hq, d, T, "q")
+    if q_out is None:
+        q_out = _empty((n, hq, d), T, q.device, stream)
+    _need(q_out.shape[0] == n, "q_out must have a row for each row of q")
+    qo = _token_stride(q_out, hq, d, T, "q_out")
+    kp = ks = kop = ko = 0
+    if k is not None:
+        _need(k.shape[0] == n, "q and k must have the same rows")
+        ks = _token_stride(k, hk, d, T, "k")
+        if k_out is None:
+            k_out = _empty((n, hk, d), T, k.device, stream)
+        _need(k_out.shape[0] == n, "k_out must have a row for each row of k")
+        ko = _token_stride(k_out, hk, d, T, "k_out")
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+        _together(q, k, k_out)
+    _together(q, q_out, positions, inv_freq)
+    pos, freq = _addr(positions, inv_freq)
+    _launch("gai4_rope", lib().gai4_rope, q, q.data_ptr(), qs, q_out.data_ptr(), qo, kp, ks, kop, ko, pos, freq, mscale,
+            _dtype(q), n, hq, hk, d, 2 * inv_freq.shape[0], 1 if interleaved else 0, _stream_handle(stream, q))
+    return q_out, k_out
+
+
+class Normed(NamedTuple):
+    """What gai4_rms_norm returns; None where it was not asked for."""
+    out: torch.Tensor | None        # [rows, cols] of x's type
+    residual: torch.Tensor | None   # x + residual
+    codes: torch.Tensor | None      # float8_e4m3fn [rows, cols]
+    scales: torch.Tensor | None     # float32 [rows, ceil(cols / 128)]
+
+
+def gai4_rms_norm(x, gain=None, eps: float = 1e-6, residual=None, fp8: bool = False, out=None, residual_out=None,
+                  codes=None, scales=None, stream=None) -> Normed:
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * gain for rows x
+    [rows, cols] (any row stride). With residual the sum h comes back too. With
+    fp8 y comes back as e4m3 codes and scales, and in x's type only where `out`
+    is given; residual_out may be `residual` itself."""
+    rows, cols = x.shape
+    T = x.dtype
+    xs = _row_stride(x, "x")
+    used = [x]
+    rp = rs = gp = op = rop = cp = sp = 0
+    if residual is not None:
+        _need(residual.shape == (rows, cols) and residual.dtype == T, "residual must have x's shape and type")
+        rp, rs = residual.data_ptr(), _row_stride(residual, "residual")
+        if residual_out is None:
+            residual_out = _empty((rows, cols), T, x.device, stream)
+        used.append(residual)
+    if gain is not None:
+        _need(gain.shape == (cols,) and gain.dtype == T, "gain must be [cols] of x's type")
+        gp, = _addr(gain)
+        used.append(gain)
+    if out is None and not fp8:
+        out = _empty((rows, cols), T, x.device, stream)
+    for t in (out, residual_out):
+        if t is not None:
+            _need(t.shape == (rows, cols) and t.dtype == T, "outputs must have x's shape and type")
+            used.append(t)
+    if out is not None:
+        op, = _addr(out)
+    if residual_out is not None:
+        rop, = _addr(residual_out)
+    if fp8:
+        codes, scales = _fp8_outputs(codes, scales, rows, cols, rows, x.device, stream)
+        cp, sp = _addr(codes, scales)
+        used += [codes, scales]
+    else:
+        _need(codes is None and scales is None, "codes and scales are outputs of fp8=True")
+    _together(*used)
+    _launch("gai4_rms_norm", lib().gai4_rms_norm, x, x.data_ptr(), xs, rp, rs, gp, op, rop, cp, sp, _dtype(x), rows,
+            cols, eps, _stream_handle(stream, x))
+    return Normed(out, residual_out, codes, scales)
+
+
+def _fp8_outputs(codes, scales, rows, cols, scale_rows, device, stream):
+    if codes is None:
+        codes = _empty((rows, cols), _E4M3, device, stream)
+    if scales is None:
+        scales = _empty((scale_rows, -(-cols // _FP8_BLOCK)), torch.float32, device, stream)
+    _e4m3(codes)
+    _need(codes.shape == (rows, cols) and scales.shape == (scale_rows, -(-cols // _FP8_BLOCK)) and
+          scales.dtype == torch.float32, "codes [rows, cols], scales float32, one for each block of 128")
+    return codes, scales
+
+
+def gai4_quantize_x_fp8(x, codes=None, scales=None, stream=None):
+    """Activations x [M, K] (any row stride) -> (codes e4m3 [M, K], scales
+    float32 [M, ceil(K / 128)])."""
+    M, K = x.shape
+    xs = _row_stride(x, "x")
+    codes, scales = _fp8_outputs(codes, scales, M, K, M, x.device, stream)
+    _together(x, codes, scales)
+    _launch("gai4_quantize_x_fp8", lib().gai4_quantize_x_fp8, x, x.data_ptr(), xs, *_addr(codes, scales), _dtype(x), M, K,
+            _stream_handle(stream, x))
+    return codes, scales
+
+
+def gai4_quantize_fp8(w, codes=None, scales=None, stream=None):
+    """Weights w [N, K] -> (codes e4m3 [N, K], scales float32 [ceil(N / 128),
+    ceil(K / 128)])."""
+    N, K = w.shape
+    codes, scales = _fp8_outputs(codes, scales, N, K, -(-N // _FP8_BLOCK), w.device, stream)
+    _together(w, codes, scales)
+    wp, cp, sp = _addr(w, codes, scales)
+    _launch("gai4_quantize_fp8", lib().gai4_quantize_fp8, w, wp, cp, sp, _dtype(w), N, K, _stream_handle(stream, w))
+    return codes, scales
+
+
+def gai4_fp8_mm_t(w_codes, w_scales, x_codes, x_scales, out=None, dtype=torch.bfloat16, stream=None):
+    """out[m, n] = sum_k (x_codes x_scales)[m, k] (w_codes w_scales)[n, k] in
+    `dtype` (or out's type); K a multiple of 16."""
+    N, K = w_codes.shape
+    M, B = x_codes.shape[0], -(-K // _FP8_BLOCK)
+    _e4m3(w_codes)
+    _e4m3(x_codes)
+    _need(x_codes.shape == (M, K) and x_scales.shape == (M, B) and w_scales.shape == (-(-N // _FP8_BLOCK), B) and
+          x_scales.dtype == torch.float32 and w_scales.dtype == torch.float32,
+          "codes [N, K] and [M, K], scales float32 [ceil(N / 128), ceil(K / 128)] and [M, ceil(K / 128)]")
+    if out is None:
+        out = _empty((M, N), dtype, x_codes.device, stream)
+    _need(out.shape == (M, N), "out must be [M, N]")
+    _together(w_codes, w_scales, x_codes, x_scales, out)
+    w, ws, x, xs, o = _addr(w_codes, w_scales, x_codes, x_scales, out)
+    _launch("gai4_fp8_mm_t", lib().gai4_fp8_mm_t, out, w, ws, x, xs, o, _dtype(out), M, N, K, _stream_handle(stream, out))
     return out
 
 

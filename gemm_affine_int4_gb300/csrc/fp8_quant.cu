@@ -1,0 +1,133 @@
+// fp8_quant.cu -- activations and weights into e4m3 (internal).
+//
+// Activations: a scale for each 128 consecutive elements of a row. Weights: a
+// scale for each block of 128 rows x 128 columns. Both read every value once
+// and write a byte for it: bound by HBM (16-bit inputs 3 bytes a value, binary32
+// 5), for a few rows by the launch.
+#include "fp8_quant.cuh"
+#include "internal.h"
+
+namespace gai4 {
+
+namespace {
+
+using namespace fp8;
+
+constexpr int kThreads = 256;
+
+// 16 lanes hold a group, 8 elements each. A thread takes kUnits such eights, a
+// block's width apart, all of them loaded before the first is used. `units`:
+// eights of a row, rounded up to whole groups.
+template <typename T, bool VEC, int kUnits>
+__global__ void __launch_bounds__(kThreads) quantize_x_fp8_kernel(const typename T::storage* __restrict__ x,
+                                                                  int64_t x_stride, uint8_t* __restrict__ codes,
+                                                                  float* __restrict__ scales, int64_t rows,
+                                                                  int64_t cols, int64_t units) {
+    pdl_launch_dependents();
+    pdl_wait();   // the kernels before this one are complete: global memory may be read
+    const int64_t total = rows * units;
+    const int64_t first = (int64_t)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
+    float v[kUnits][8];
+    int64_t row[kUnits], col[kUnits];
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j) {
+        const int64_t u = first + j * kThreads;
+        row[j] = u < 0x7fffffff ? (int64_t)((uint32_t)u / (uint32_t)units) : u / units;
+        col[j] = (u - row[j] * units) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
+        if (u < total && col[j] < cols) load8<T, VEC>(x + row[j] * x_stride + col[j], cols - col[j], v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j) {
+        const Scale s = scale_of(group_max(amax8(v[j])));
+        if (first + j * kThreads >= total) continue;
+        if (col[j] < cols) store_codes8<VEC>(codes + row[j] * cols + col[j], cols - col[j], codes8(v[j], s));
+        if ((threadIdx.x & 15) == 0) scales[row[j] * (units / 16) + col[j] / kGroup] = scale_value(s);
+    }
+}
+
+// One block of 128 x 128 a CTA: thread t holds columns 8 (t % 16) on of the
+// rows t / 16 + 16 j, in registers from the maximum to the codes.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(const typename T::storage* __restrict__ w,
+                                                                uint8_t* __restrict__ codes,
+                                                                float* __restrict__ scales, int64_t N, int64_t K) {
+    // no programmatic launch: what this kernel writes may be read as weights
+    pdl_wait();
+    __shared__ uint32_t part[kThreads / 32];
+    const int64_t k = (int64_t)blockIdx.x * kGroup + (threadIdx.x & 15) * 8;
+    const int64_t n0 = (int64_t)blockIdx.y * kGroup + (threadIdx.x >> 4);
+    float v[8][8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
+        if (n0 + 16 * j < N && k < K) load8<T, VEC>(w + (n0 + 16 * j) * K + k, K - k, v[j]);
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, amax8(v[j]));
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) m = max(m, part[i]);
+    const Scale s = scale_of(m);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (n0 + 16 * j < N && k < K) store_codes8<VEC>(codes + (n0 + 16 * j) * K + k, K - k, codes8(v[j], s));
+    if (threadIdx.x == 0) scales[blockIdx.y * (int64_t)gridDim.x + blockIdx.x] = scale_value(s);
+}
+
+bool vec_ok(const void* p, int64_t stride, int64_t cols, int elem, const void* codes) {
+    return cols % 8 == 0 && (uintptr_t)p % 16 == 0 && (stride * elem) % 16 == 0 && (uintptr_t)codes % 8 == 0;
+}
+
+template <typename T>
+cudaError_t x_launch(const void* x, int64_t x_stride, uint8_t* codes, float* scales, int64_t rows, int64_t cols,
+                     cudaStream_t s) {
+    const auto* p = static_cast<const typename T::storage*>(x);
+    const int64_t units = (cols + kGroup - 1) / kGroup * 16, total = rows * units;
+    const bool vec = vec_ok(x, x_stride, cols, T::kBytes, codes);
+    // few values: one eight a thread, on as many SMs as there are
+    if (total <= (int64_t)num_sms() * 4 * kThreads) {
+        const dim3 grid((unsigned)((total + kThreads - 1) / kThreads));
+        return launch_pdl(vec ? quantize_x_fp8_kernel<T, true, 1> : quantize_x_fp8_kernel<T, false, 1>, grid,
+                          dim3(kThreads), 0, s, p, x_stride, codes, scales, rows, cols, units);
+    }
+    const int64_t blocks = (total + 4 * kThreads - 1) / (4 * kThreads);
+    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    return launch_pdl(vec ? quantize_x_fp8_kernel<T, true, 4> : quantize_x_fp8_kernel<T, false, 4>,
+                      dim3((unsigned)blocks), dim3(kThreads), 0, s, p, x_stride, codes, scales, rows, cols, units);
+}
+
+template <typename T>
+cudaError_t w_launch(const void* w, uint8_t* codes, float* scales, int64_t N, int64_t K, cudaStream_t s) {
+    const auto* p = static_cast<const typename T::storage*>(w);
+    const dim3 grid((unsigned)((K + kGroup - 1) / kGroup), (unsigned)((N + kGroup - 1) / kGroup));
+    return launch_pdl(vec_ok(w, K, K, T::kBytes, codes) ? quantize_fp8_kernel<T, true> : quantize_fp8_kernel<T, false>,
+                      grid, dim3(kThreads), 0, s, p, codes, scales, N, K);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_x_fp8(const void* x, int64_t x_stride, uint8_t* codes, float* scales, int dtype,
+                                  int64_t rows, int64_t cols, cudaStream_t s) {
+    switch (dtype) {
+    case GAI4_F16: return x_launch<F16>(x, x_stride, codes, scales, rows, cols, s);
+    case GAI4_F32: return x_launch<F32>(x, x_stride, codes, scales, rows, cols, s);
+    default: return x_launch<BF16>(x, x_stride, codes, scales, rows, cols, s);
+    }
+}
+
+cudaError_t launch_quantize_fp8(const void* w, uint8_t* codes, float* scales, int dtype, int64_t N, int64_t K,
+                                cudaStream_t s) {
+    switch (dtype) {
+    case GAI4_F16: return w_launch<F16>(w, codes, scales, N, K, s);
+    case GAI4_F32: return w_launch<F32>(w, codes, scales, N, K, s);
+    default: return w_launch<BF16>(w, codes, scales, N, K, s);
+    }
+}
+
+}  // namespace gai4

@@ -185,6 +185,44 @@ cudaError_t launch_kv_attention_f32(const KvAttnLaunch& L, cudaStream_t s);
 cudaError_t launch_kv_attention_tc(const KvAttnLaunch& L, cudaStream_t s);
 size_t kv_attention_tc_workspace(int d);
 
+// rotary positions (rope.cu)
+struct RopeLaunch {
+    const void* in[2];   // query and key rows; heads 0: none
+    void* out[2];
+    int64_t in_stride[2], out_stride[2];
+    int heads[2];
+    const int32_t* positions;
+    const double* inv_freq;
+    float mscale;
+    int64_t tokens;
+    int head_dim, rot_dim, interleaved, dtype;
+};
+cudaError_t launch_rope(const RopeLaunch& L, cudaStream_t s);
+
+// root-mean-square norm (norm.cu)
+cudaError_t launch_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t r_stride, const void* gain,
+                            void* out, void* residual_out, uint8_t* codes, float* scales, int dtype, int64_t rows,
+                            int64_t cols, float eps, cudaStream_t s);
+
+// activations and weights into e4m3 (fp8_quant.cu)
+cudaError_t launch_quantize_x_fp8(const void* x, int64_t x_stride, uint8_t* codes, float* scales, int dtype,
+                                  int64_t rows, int64_t cols, cudaStream_t s);
+cudaError_t launch_quantize_fp8(const void* w, uint8_t* codes, float* scales, int dtype, int64_t N, int64_t K,
+                                cudaStream_t s);
+
+// product of e4m3 operands with block scales (fp8_mm.cu)
+struct Fp8MmLaunch {
+    const uint8_t* w;        // [N, K]
+    const float* w_scales;   // [ceil(N / 128), ceil(K / 128)]
+    const uint8_t* x;        // [M, K]
+    const float* x_scales;   // [M, ceil(K / 128)]
+    void* out;               // [M, N]
+    int64_t M, N, K;
+    int* status;
+    long long spin_limit;
+};
+cudaError_t launch_fp8_mm(const Fp8MmLaunch& L, int dtype, cudaStream_t s);
+
 int* status_ptr();  // device status word of the current device
 int num_sms();  // SM count of the current device (cached)
 

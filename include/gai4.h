@@ -490,6 +490,115 @@ gai4_status gai4_kv_attention(const void* q, int64_t q_token_stride, const uint3
  * arguments that gai4_kv_attention refuses. */
 size_t gai4_kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int head_dim, gai4_dtype dtype);
 
+/* ===========================================================================
+ * Around the attention: rotary positions, norm, 8-bit floating point
+ *
+ * e4m3 with block scales: codes are bytes, each an e4m3 value (4 exponent
+ * bits, 3 mantissa bits, largest 448, 0x7f and 0xff NaN); a scale (float)
+ * belongs to a block of 128 columns, the last of a row shorter where K is not a
+ * multiple of 128, so a row has B = ceil(K / 128) of them.
+ *   activations  codes [M, K], scales [M, B]: 1 x 128
+ *   weights      codes [N, K], scales [ceil(N / 128), B]: 128 x 128
+ * The represented value is code * scale. Quantization takes, of the block's
+ * values v,
+ *   a = max(max |v|, 2^-100),  scale = RN(a / 448),
+ *   code = the e4m3 value nearest to q, ties to even, q = RN(448 v / a)
+ * (for float inputs 448 v is rounded first). A block that holds an infinity or
+ * a NaN represents NaN throughout.
+ * (No counterpart on the pages; an addition of this library.)
+ * ======================================================================== */
+
+enum {
+    GAI4_ROPE_NONE = 0,
+    GAI4_ROPE_LINEAR = 1,   /* every frequency divided by `factor` */
+    GAI4_ROPE_NTK = 2,      /* the base times factor^(rot_dim / (rot_dim - 2)) */
+    GAI4_ROPE_YARN = 3,     /* pairs that make fewer than `low` turns over original_len positions divided, those with
+                               more than `high` kept, a ramp over the pairs between; mscale = 0.1 ln(factor) + 1 */
+    GAI4_ROPE_SMOOTH = 4    /* likewise with a ramp over the turns, mscale = 1 */
+};
+
+/*
+ * gai4_rope_inv_freq -- angles per position of the rot_dim / 2 pairs:
+ *   inv_freq[i] = base^(-2 i / rot_dim), scaled for contexts longer than
+ *   original_len by one of the rules above (factor >= 1; low, high: 1 and 32
+ *   are usual for YARN, 1 and 4 for SMOOTH; ignored by rules that lack them).
+ * inv_freq and mscale are HOST memory; nothing runs on the device.
+ */
+gai4_status gai4_rope_inv_freq(double* inv_freq, float* mscale, int rot_dim, double base, int scaling, double factor,
+                               double original_len, double low, double high);
+
+/*
+ * gai4_rope -- rotary positions of query and key rows: the first rot_dim
+ * channels of a head, as pairs (i, i + rot_dim / 2) or, interleaved != 0,
+ * (2 i, 2 i + 1), turn by the angle t = positions[token] * inv_freq[i]:
+ *   a' = mscale (a cos t - b sin t)     b' = mscale (b cos t + a sin t)
+ * The other channels are copied.
+ *   q, k  T, row i, head h at q + i * q_token_stride + h * head_dim (strides in
+ *         elements, >= heads * head_dim; aligned to the element size); heads 0:
+ *         there are none, pointers and strides are ignored
+ *   q_out, k_out  likewise; they may be q and k themselves (same stride), and
+ *         must not overlap the inputs or each other otherwise
+ *   positions [num_tokens] i32, any value: a negative one turns back
+ *   inv_freq [rot_dim / 2] double (device, 8-byte aligned): any value. The
+ *         angle's whole turns are taken off exactly, so far positions lose
+ *         nothing.
+ * rot_dim even, 2 .. head_dim; head_dim up to 1024. Every row is turned, those
+ * behind a step's last token (position 0 in gai4_kv_plan's positions) too.
+ */
+gai4_status gai4_rope(const void* q, int64_t q_token_stride, void* q_out, int64_t q_out_token_stride, const void* k,
+                      int64_t k_token_stride, void* k_out, int64_t k_out_token_stride, const int32_t* positions,
+                      const double* inv_freq, float mscale, gai4_dtype dtype, int64_t num_tokens, int64_t q_heads,
+                      int64_t kv_heads, int head_dim, int rot_dim, int interleaved, void* stream);
+
+/*
+ * gai4_rms_norm -- root-mean-square norm of rows, with the residual's addition
+ * and the result in T, in e4m3, or both:
+ *   h = x + residual        y = h / sqrt(sum_c h_c^2 / cols + eps) * gain
+ *   x, residual (or NULL)  T, rows x_row_stride and residual_row_stride apart
+ *         (elements, >= cols); gain [cols] T or NULL (ones)
+ *   residual_out [rows, cols] T or NULL: h, rounded
+ *   out [rows, cols] T or NULL: y, rounded
+ *   codes [rows, cols] and scales [rows, ceil(cols / 128)], or both NULL: y as
+ *         activations in e4m3 (not rounded to T in between)
+ * h, the sum and y are binary32; a sum of squares beyond it (|h| above 1e19)
+ * counts as infinite. Any cols >= 1. out or residual_out (not both) may be x or
+ * residual where those are contiguous; outputs must not overlap the inputs or
+ * each other otherwise.
+ */
+gai4_status gai4_rms_norm(const void* x, int64_t x_row_stride, const void* residual, int64_t residual_row_stride,
+                          const void* gain, void* out, void* residual_out, uint8_t* codes, float* scales,
+                          gai4_dtype dtype, int64_t rows, int64_t cols, float eps, void* stream);
+
+/*
+ * gai4_quantize_x_fp8 -- activations x [M, K] T (rows x_row_stride >= K
+ * elements apart) into e4m3 with a scale for each 1 x 128; any K >= 1. Outputs
+ * must not overlap x.
+ */
+gai4_status gai4_quantize_x_fp8(const void* x, int64_t x_row_stride, uint8_t* codes, float* scales, gai4_dtype dtype,
+                                int64_t M, int64_t K, void* stream);
+
+/*
+ * gai4_quantize_fp8 -- weights w [N, K] T (contiguous) into e4m3 with a scale
+ * for each 128 x 128; any N (up to 8388480) and K >= 1. Outputs must not
+ * overlap w.
+ */
+gai4_status gai4_quantize_fp8(const void* w, uint8_t* codes, float* scales, gai4_dtype dtype, int64_t N, int64_t K,
+                              void* stream);
+
+/*
+ * gai4_fp8_mm_t -- product of e4m3 activations with e4m3 weights:
+ *   out[m, n] = sum_b x_scales[m, b] w_scales[n / 128, b] sum_{k in block b} x[m, k] w[n, k]
+ *   w_codes [N, K], x_codes [M, K] (16-byte aligned), scales as above (finite,
+ *   the products of a row's and a column's scales within binary32's range);
+ *   out [M, N] T. Any M >= 0 and N >= 1; K a multiple of 16 (UNSUPPORTED
+ *   otherwise). Codes of a NaN make the outputs that read them NaN.
+ * Sums within a block are the tensor cores' (products exact), sums over blocks
+ * binary32; one rounding to T at the end. Results repeat bit for bit; those of
+ * a row may depend in the last bits on how many rows the call has.
+ */
+gai4_status gai4_fp8_mm_t(const uint8_t* w_codes, const float* w_scales, const uint8_t* x_codes, const float* x_scales,
+                          void* out, gai4_dtype dtype, int64_t M, int64_t N, int64_t K, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
