@@ -345,16 +345,46 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     cluster_wait();
 }
 
-static bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int box_rows) {
+template <typename... KArgs, typename... Args>
+static cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, unsigned cluster,
+                                  cudaStream_t stream, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+static bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* p, int64_t rows, int64_t cols, int64_t pitch,
+                   int box_rows, int box_cols, CUtensorMapSwizzle swizzle) {
     auto fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)cols};
-    const cuuint32_t box[2] = {(cuuint32_t)kBlock, (cuuint32_t)box_rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)pitch};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     const cuuint32_t one[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, box, one,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(map, type, 2, const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// e4m3 rows as an operand: boxes of 128 columns
+static bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int box_rows) {
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, rows, cols, cols, box_rows, kBlock, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// outputs: boxes of 32 rows of 64 bytes
+template <typename T>
+static bool make_out_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols) {
+    const CUtensorMapDataType type = T::kBytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    return encode(map, type, p, rows, cols, cols * T::kBytes, 32, 64 / T::kBytes, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 template <typename T, int MT>
@@ -371,21 +401,365 @@ static cudaError_t few_launch(const Fp8MmLaunch& L, cudaStream_t s) {
     int split = (int)std::min<int64_t>({8, blocks, std::max<int64_t>(1, 2 * (int64_t)num_sms() / (tiles * chunks))});
     if (tiles * chunks * split > 0x7fffffff) return cudaErrorInvalidConfiguration;
     const FewArgs a{L.w_scales, L.x_scales, L.out, L.M, L.N, blocks, (int)chunks, split, L.status, L.spin_limit};
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * chunks * split));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)split;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, few_kernel<T, MT>, w_map, x_map, a);
+    return launch_cluster(few_kernel<T, MT>, (unsigned)(tiles * chunks * split), kThreads, C::kSmem, (unsigned)split, s,
+                          w_map, x_map, a);
+}
+
+// ---------------------------------------------------------------------------
+// Many tokens. Two CTAs on neighbouring SMs share a tile of 256 tokens x NT
+// weight rows (cta_group::2): each brings 128 tokens and half of the weight
+// rows into its shared memory, and the products read both halves, so a block of
+// K costs an SM (128 + NT / 2) x 128 bytes of loads for 128 x NT x 128 products.
+// The pairs walk over the tiles, with the ring and the tensor memory buffers
+// running on from tile to tile.
+//
+//   warp 0      TMA producer of the CTA's halves; both halves report to the first CTA
+//   warp 1      (first CTA) issues the products for the pair
+//   warp 2      scales of the CTA's tokens and of the tile's weight blocks into
+//               shared memory, kBatch blocks of K at a time
+//   warp 3      allocates tensor memory, lets the next kernel start
+//   warps 4-19  thread = token, a quarter of the tile's columns:
+//               sum[n] += D[n] * (sx sw), one factor for all of them; in the end
+//               rows of 64 bytes through shared memory and TMA stores
+// ---------------------------------------------------------------------------
+constexpr int kSumWarps = 16;
+constexpr int kPairThreads = 32 * (4 + kSumWarps);
+constexpr int kPairRows = 256;
+// 640 threads x 96 registers: 128 x 32 + 512 x 112
+constexpr int kControlRegs = 32, kSumRegs = 112;
+constexpr int kOutBox = 32 * 64;   // bytes: 32 rows of 64
+
+template <int NT>
+struct Many {
+    static constexpr int kStage = kTile * kBlock + NT / 2 * kBlock;   // of one CTA
+    static constexpr int kStages = NT == 256 ? 5 : 7;
+    static constexpr int kBufs = 512 / NT;
+    static constexpr int kCols = NT / 4;   // of a thread
+    static constexpr size_t kSmem = (size_t)kStages * kStage + kSumWarps * kOutBox + 1024;
+};
+
+struct ManyArgs {
+    const float* w_scales;
+    const float* x_scales;
+    void* out;
+    int64_t M, N;
+    int blocks;                 // of K
+    int tiles_m, tiles_n;
+    int pairs;
+    int aligned;                // rows of out start on 16-byte boundaries: out_map is there
+    int* status;
+    long long spin_limit;
+};
+
+// tiles in strips of 8 tiles of tokens: the pairs' operands of a moment stay in L2
+__device__ __forceinline__ void tile_at(const ManyArgs& a, int t, int& tm, int& tn) {
+    constexpr int kStrip = 8;
+    const int strip = t / (kStrip * a.tiles_n), first = strip * kStrip;
+    const int height = min(kStrip, a.tiles_m - first), r = t - first * a.tiles_n;
+    tm = first + r % height;
+    tn = r / height;
+}
+
+__device__ __forceinline__ void pair_load(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// as block_products, for both CTAs of the pair; the commits reach both
+__device__ __forceinline__ void pair_products(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t id, uint64_t* slot_free,
+                                              uint64_t* done) {
+    asm volatile(
+        "{\n .reg .pred e, z, o;\n .reg .b32 r, t, u;\n .reg .b64 x, y;\n .reg .b16 m;\n elect.sync r|e, 0xffffffff;\n"
+        " setp.ne.b32 z, 0, 0;\n setp.eq.b32 o, 0, 0;\n mov.b16 m, 3;\n"
+        " mov.b64 x, {%1, %4};\n mov.b64 y, {%2, %4};\n"
+        " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], x, y, %3, z;\n"
+        " add.u32 u, %1, 2;\n mov.b64 x, {u, %4};\n add.u32 t, %2, 2;\n mov.b64 y, {t, %4};\n"
+        " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], x, y, %3, o;\n"
+        " add.u32 u, %1, 4;\n mov.b64 x, {u, %4};\n add.u32 t, %2, 4;\n mov.b64 y, {t, %4};\n"
+        " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], x, y, %3, o;\n"
+        " add.u32 u, %1, 6;\n mov.b64 x, {u, %4};\n add.u32 t, %2, 6;\n mov.b64 y, {t, %4};\n"
+        " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], x, y, %3, o;\n"
+        " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%5], m;\n"
+        " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%6], m;\n}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(id), "r"(kDescHi), "r"(smem_u32(slot_free)), "r"(smem_u32(done))
+        : "memory");
+}
+
+__device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n"
+                 "cp.async.bulk.commit_group;" ::"l"(map),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_constant__ CUtensorMap w_map,
+                                                               const __grid_constant__ CUtensorMap x_map,
+                                                               const __grid_constant__ CUtensorMap out_map,
+                                                               const __grid_constant__ ManyArgs a) {
+    using C = Many<NT>;
+    extern __shared__ uint8_t dyn[];
+    __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], d_full[C::kBufs], d_empty[C::kBufs];
+    __shared__ __align__(8) uint64_t s_full[2], s_empty[2];
+    __shared__ __align__(8) uint64_t tmem_ready;
+    __shared__ float sx[2][kBatch][kTile + 4], sw[2][kBatch][2];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    __shared__ int loads, products;   // issued
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)(blockIdx.x & 1u), pair = (int)(blockIdx.x >> 1);
+    const int tiles = a.tiles_m * a.tiles_n;
+    const Ctl ctl{a.status, a.spin_limit, &abort_flag};
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < C::kBufs; ++i) {
+            mbar_init(&d_full[i], 1);
+            mbar_init(&d_empty[i], 2 * kSumWarps);   // of both CTAs
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 32);
+            mbar_init(&s_empty[i], kSumWarps);
+        }
+        mbar_init(&tmem_ready, 2);
+        abort_flag = loads = products = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    cluster_arrive();   // the other CTA reports to these barriers
+    cluster_wait();
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+        if (warp == 0) {
+            if (lane == 0) {
+                int g = 0, slot = 0;
+                uint32_t phase = 1;   // (the first round finds every slot free)
+                bool ok = true;
+                for (int t = pair; ok && t < tiles; t += a.pairs) {
+                    int tm, tn;
+                    tile_at(a, t, tm, tn);
+                    const int m = tm * kPairRows + rank * kTile, n = tn * NT + rank * (NT / 2);
+                    for (int kb = 0; kb < a.blocks; ++kb, ++g) {
+                        if (g >= C::kStages && !mbar_wait(&empty[slot], phase, ctl)) {
+                            ok = false;
+                            break;
+                        }
+                        uint8_t* st = ring + slot * C::kStage;
+                        const uint32_t bar = mapa(smem_u32(&full[slot]), 0);
+                        if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * C::kStage);
+                        pair_load(st + kTile * kBlock, &w_map, bar, kb * kBlock, n);
+                        if (g == 0) pdl_wait();   // (weights may be read before)
+                        pair_load(st, &x_map, bar, kb * kBlock, m);
+                        loads = g + 1;
+                        if (++slot == C::kStages) {
+                            slot = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            if (rank == 0) {
+                bool ok = warp_wait(&tmem_ready, 0, ctl);
+                fence_after();
+                const uint32_t tmem = tmem_slot;
+                int g = 0, slot = 0;
+                uint32_t phase = 0;
+                for (int t = pair; ok && t < tiles; t += a.pairs)
+                    for (int kb = 0; kb < a.blocks; ++kb, ++g) {
+                        const int buf = g % C::kBufs;
+                        ok = warp_wait(&full[slot], phase, ctl) &&
+                             (g < C::kBufs || warp_wait(&d_empty[buf], (uint32_t)(g / C::kBufs - 1) & 1u, ctl));
+                        if (!ok) break;
+                        fence_after();
+                        const uint32_t st = smem_u32(ring + slot * C::kStage);
+                        pair_products(tmem + buf * NT, desc_lo(st), desc_lo(st + kTile * kBlock), idesc(kPairRows, NT),
+                                      &empty[slot], &d_full[buf]);
+                        if (lane == 0) products = g + 1;
+                        if (++slot == C::kStages) {
+                            slot = 0;
+                            phase ^= 1u;
+                        }
+                    }
+            }
+        } else if (warp == 2) {
+            pdl_wait();
+            const int w_rows = (int)((a.N + kBlock - 1) / kBlock);
+            int j = 0;
+            bool ok = true;
+            for (int t = pair; ok && t < tiles; t += a.pairs) {
+                int tm, tn;
+                tile_at(a, t, tm, tn);
+                // lanes: 8 blocks of K by 4 tokens
+                const int64_t m = (int64_t)tm * kPairRows + rank * kTile + (lane >> 3);
+                const int wr = (int)((int64_t)tn * NT / kBlock) + (lane >> 3);
+                for (int k0 = 0; k0 < a.blocks; k0 += kBatch, ++j) {
+                    const int kb = k0 + (lane & 7);
+                    const bool in = kb < a.blocks;
+                    if (j >= 2 && !(ok = warp_wait(&s_empty[j & 1], (uint32_t)(j / 2 - 1) & 1u, ctl))) break;
+                    const float* from = a.x_scales + m * a.blocks + kb;
+                    float* to = &sx[j & 1][lane & 7][lane >> 3];
+                    const int rows = in ? (int)max((int64_t)0, min((int64_t)kTile, a.M - m)) : 0;
+#pragma unroll 8
+                    for (int r = 0; r < kTile; r += 4) to[r] = r < rows ? from[(int64_t)r * a.blocks] : 0.f;
+                    if (lane < 16)
+                        sw[j & 1][lane & 7][lane >> 3] = in && wr < w_rows ? a.w_scales[(int64_t)wr * a.blocks + kb] : 0.f;
+                    mbar_arrive(&s_full[j & 1]);
+                }
+            }
+        } else {
+            // (the order of these: see few_kernel)
+            pdl_wait();
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot))
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+            fence_before();
+            pdl_launch_dependents();
+            // both CTAs' columns are there before the first product
+            if (lane < 2) arrive_at(mapa(smem_u32(&tmem_ready), lane));
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+        using S = typename T::storage;
+        const int quarter = (warp - 4) >> 2;
+        const int row = (warp & 3) * 32 + lane;
+        const int half = quarter * C::kCols / kBlock;   // weight block of the tile
+        bool ok = warp_wait(&tmem_ready, 0, ctl);
+        fence_after();
+        const uint32_t mine = tmem_slot + ((uint32_t)(warp & 3) << 21) + quarter * C::kCols;
+        const uint32_t box = smem_u32(ring + C::kStages * C::kStage + (warp - 4) * kOutBox);
+        pdl_wait();   // (every thread that writes outputs)
+        int g = 0, j = 0;
+        for (int t = pair; ok && t < tiles; t += a.pairs) {
+            float sum[C::kCols];
+#pragma unroll
+            for (int i = 0; i < C::kCols; ++i) sum[i] = 0.f;
+            for (int kb = 0; kb < a.blocks; ++kb, ++g) {
+                const int buf = g % C::kBufs, at_batch = kb % kBatch;
+                if (at_batch == 0 && !(ok = warp_wait(&s_full[j & 1], (uint32_t)(j / 2) & 1u, ctl))) break;
+                const float s = sx[j & 1][at_batch][row] * sw[j & 1][at_batch][half];
+                if (!(ok = warp_wait(&d_full[buf], (uint32_t)(g / C::kBufs) & 1u, ctl))) break;
+                fence_after();
+                const uint32_t at = mine + buf * NT;
+                uint32_t d[2][16];
+                tmem_ld16(at, d[0]);
+#pragma unroll
+                for (int c = 0; c < C::kCols / 16; ++c) {
+                    tmem_ld_wait();
+                    if (c + 1 < C::kCols / 16) {
+                        tmem_ld16(at + 16 * (c + 1), d[(c + 1) & 1]);
+                    } else {
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_at(mapa(smem_u32(&d_empty[buf]), 0));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2)
+                        fma2(sum[16 * c + i], sum[16 * c + i + 1], d[c & 1][i], d[c & 1][i + 1], s, s);
+                }
+                if (at_batch == kBatch - 1 || kb == a.blocks - 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_empty[j & 1]);
+                    ++j;
+                }
+            }
+            if (!ok) break;
+            int tm, tn;
+            tile_at(a, t, tm, tn);
+            const int64_t m0 = (int64_t)tm * kPairRows + rank * kTile + (warp & 3) * 32;
+            const int64_t n0 = (int64_t)tn * NT + quarter * C::kCols;
+            if (m0 >= a.M || n0 >= a.N) continue;
+            if (a.aligned) {
+                // 64 bytes of the warp's 32 rows at a time, 64-byte swizzled; what lies
+                // beyond the matrix is cut off by the store
+                constexpr int kEach = 64 / T::kBytes;
+#pragma unroll
+                for (int c = 0; c < C::kCols; c += kEach) {
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if constexpr (T::kBytes == 4)
+                                w[i] = __float_as_uint(sum[c + 4 * k + i]);
+                            else
+                                w[i] = (uint32_t)T::from_f32(sum[c + 8 * k + 2 * i]) |
+                                       (uint32_t)T::from_f32(sum[c + 8 * k + 2 * i + 1]) << 16;
+                        }
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         box + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4)),
+                                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                     : "memory");
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0 && n0 + c < a.N) store_box(&out_map, box, (int)(n0 + c), (int)m0);
+                }
+            } else if (m0 + lane < a.M) {
+                S* out = static_cast<S*>(a.out) + (m0 + lane) * a.N + n0;
+                const int cols = (int)min((int64_t)C::kCols, a.N - n0);
+#pragma unroll
+                for (int c = 0; c < C::kCols; ++c)
+                    if (c < cols) out[c] = T::from_f32(sum[c]);
+            }
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
+    }
+
+    // What was issued lands before the CTAs leave; without a time-out it has.
+    __syncthreads();
+    if (abort_flag && rank == 0 && threadIdx.x == 0) {
+        for (int i = 0; i < min(loads, C::kStages); ++i)
+            mbar_wait_drain(&full[i], (uint32_t)((loads - 1 - i) / C::kStages) & 1u, a.spin_limit, a.status);
+        for (int i = 0; i < min(products, C::kBufs); ++i)
+            mbar_wait_drain(&d_full[i], (uint32_t)((products - 1 - i) / C::kBufs) & 1u, a.spin_limit, a.status);
+    }
+    fence_before();
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    fence_after();
+    if (warp == 3)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem_slot) : "memory");
+    cluster_arrive();
+    cluster_wait();
+}
+
+template <typename T, int NT>
+static cudaError_t many_launch(const Fp8MmLaunch& L, cudaStream_t s) {
+    using C = Many<NT>;
+    const int aligned = (L.N * T::kBytes) % 16 == 0 && (uintptr_t)L.out % 16 == 0;
+    CUtensorMap w_map, x_map, out_map = {};
+    if (!make_map(&w_map, L.w, L.N, L.K, NT / 2) || !make_map(&x_map, L.x, L.M, L.K, kTile) ||
+        (aligned && !make_out_map<T>(&out_map, L.out, L.M, L.N)))
+        return cudaErrorInvalidValue;
+    static bool done[64];
+    cudaError_t e = allow_smem_once(many_kernel<T, NT>, C::kSmem, done);
+    if (e != cudaSuccess) return e;
+    const int64_t tm = (L.M + kPairRows - 1) / kPairRows, tn = (L.N + NT - 1) / NT;
+    if (tm * tn > 0x7fffffff - 4096) return cudaErrorInvalidConfiguration;
+    const int pairs = (int)std::min<int64_t>(tm * tn, num_sms() / 2);
+    const ManyArgs a{L.w_scales, L.x_scales, L.out, L.M, L.N, (int)((L.K + kBlock - 1) / kBlock), (int)tm, (int)tn, pairs,
+                     aligned, L.status, L.spin_limit};
+    return launch_cluster(many_kernel<T, NT>, 2 * (unsigned)pairs, kPairThreads, C::kSmem, 2, s, w_map, x_map, out_map, a);
 }
 
 template <typename T>
@@ -393,7 +767,10 @@ static cudaError_t typed(const Fp8MmLaunch& L, cudaStream_t s) {
     if (L.M <= 16) return few_launch<T, 16>(L, s);
     if (L.M <= 32) return few_launch<T, 32>(L, s);
     if (L.M <= 64) return few_launch<T, 64>(L, s);
-    return few_launch<T, 128>(L, s);
+    if (L.M <= 128) return few_launch<T, 128>(L, s);
+    const int64_t tm = (L.M + kPairRows - 1) / kPairRows, pairs = num_sms() / 2;
+    const int64_t wide = (tm * ((L.N + 255) / 256) + pairs - 1) / pairs * 2, narrow = (tm * ((L.N + 127) / 128) + pairs - 1) / pairs;
+    return narrow < wide ? many_launch<T, 128>(L, s) : many_launch<T, 256>(L, s);
 }
 
 }  // namespace fp8mm
