@@ -67,14 +67,24 @@ __device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t* v) {
         : "memory");
 }
 
-// (a, b) += (x * s, y * t): one packed instruction
-__device__ __forceinline__ void fma2(float& a, float& b, uint32_t x, uint32_t y, float s, float t) {
-    asm("{\n .reg .b64 u, v, w;\n mov.b64 u, {%2, %3};\n mov.b64 v, {%4, %5};\n mov.b64 w, {%0, %1};\n"
-        " fma.rn.f32x2 w, u, v, w;\n mov.b64 {%0, %1}, w;\n}"
-        : "+f"(a), "+f"(b)
-        : "r"(x), "r"(y), "f"(s), "f"(t));
+__device__ __forceinline__ float lds1(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
 }
 
+// two values in T's 16 bits, `lo` in the low half
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    uint32_t r;
+    if constexpr (T::kIsBF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float as_f32(uint32_t v) { return __uint_as_float(v); }
 __device__ __forceinline__ float4 lds4(const float* p) {
     float4 v;
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -289,8 +299,10 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
 #pragma unroll
                 for (int t = 0; t < 16; t += 4) {
                     const float4 s = lds4(sc + 16 * c + t);
-                    fma2(sum[16 * c + t], sum[16 * c + t + 1], d[c & 1][t], d[c & 1][t + 1], s.x, s.y);
-                    fma2(sum[16 * c + t + 2], sum[16 * c + t + 3], d[c & 1][t + 2], d[c & 1][t + 3], s.z, s.w);
+                    sum[16 * c + t] = fmaf(as_f32(d[c & 1][t]), s.x, sum[16 * c + t]);
+                    sum[16 * c + t + 1] = fmaf(as_f32(d[c & 1][t + 1]), s.y, sum[16 * c + t + 1]);
+                    sum[16 * c + t + 2] = fmaf(as_f32(d[c & 1][t + 2]), s.z, sum[16 * c + t + 2]);
+                    sum[16 * c + t + 3] = fmaf(as_f32(d[c & 1][t + 3]), s.w, sum[16 * c + t + 3]);
                 }
             }
             fence_before();
@@ -380,11 +392,12 @@ static bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* p, in
 static bool make_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int box_rows) {
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, rows, cols, cols, box_rows, kBlock, CU_TENSOR_MAP_SWIZZLE_128B);
 }
-// outputs: boxes of 32 rows of 64 bytes
+// outputs: boxes of 32 rows of `bytes`
 template <typename T>
-static bool make_out_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols) {
+static bool make_out_map(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int bytes) {
     const CUtensorMapDataType type = T::kBytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
-    return encode(map, type, p, rows, cols, cols * T::kBytes, 32, 64 / T::kBytes, CU_TENSOR_MAP_SWIZZLE_64B);
+    return encode(map, type, p, rows, cols, cols * T::kBytes, 32, bytes / T::kBytes,
+                  bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 template <typename T, int MT>
@@ -413,29 +426,35 @@ static cudaError_t few_launch(const Fp8MmLaunch& L, cudaStream_t s) {
 // The pairs walk over the tiles, with the ring and the tensor memory buffers
 // running on from tile to tile.
 //
-//   warp 0      TMA producer of the CTA's halves; both halves report to the first CTA
-//   warp 1      (first CTA) issues the products for the pair
-//   warp 2      scales of the CTA's tokens and of the tile's weight blocks into
-//               shared memory, kBatch blocks of K at a time
-//   warp 3      allocates tensor memory, lets the next kernel start
-//   warps 4-19  thread = token, a quarter of the tile's columns:
-//               sum[n] += D[n] * (sx sw), one factor for all of them; in the end
-//               rows of 64 bytes through shared memory and TMA stores
+//   warp 0      TMA producer of the CTA's weight rows
+//   warp 2      TMA producer of its tokens; copies the scales of the tokens and of
+//               the tile's weight blocks, kBatch blocks of K at a time
+//   warps 1, 3  (first CTA) issue the products for the pair, each with half of the
+//               weight rows (warp 3 also allocates tensor memory and lets the next
+//               kernel start)
+//   warps 4-11  thread = token, half of the tile's columns (one product's):
+//               sum[n] += D[n] * (sx sw), one factor for all of them
+// Two producers and two issuers, since a block of K is 512 cycles of products,
+// and waits, a load and an issue take a warp some 150 to 250 cycles each.
 // ---------------------------------------------------------------------------
-constexpr int kSumWarps = 16;
+constexpr int kSumWarps = 8;
 constexpr int kPairThreads = 32 * (4 + kSumWarps);
 constexpr int kPairRows = 256;
-// 640 threads x 96 registers: 128 x 32 + 512 x 112
-constexpr int kControlRegs = 32, kSumRegs = 112;
-constexpr int kOutBox = 32 * 64;   // bytes: 32 rows of 64
+// 384 threads x 168 registers = 128 x 72 + 256 x 216
+constexpr int kControlRegs = 72, kSumRegs = 216;
+
+constexpr int kOutBox = 32 * 128;   // bytes of a warp: 32 rows of 128
 
 template <int NT>
 struct Many {
     static constexpr int kStage = kTile * kBlock + NT / 2 * kBlock;   // of one CTA
-    static constexpr int kStages = NT == 256 ? 5 : 7;
-    static constexpr int kBufs = 512 / NT;
-    static constexpr int kCols = NT / 4;   // of a thread
+    static constexpr int kStages = NT == 256 ? 5 : 6;
+    static constexpr int kCols = NT / 2;        // columns of a product, and of a thread
+    static constexpr int kPart = NT / 4;        // of them from one CTA's weight rows
+    static constexpr int kBufs = 2;             // of each half
+    static constexpr int kOutBytes = NT == 256 ? 128 : 96;   // of a row in a stored box
     static constexpr size_t kSmem = (size_t)kStages * kStage + kSumWarps * kOutBox + 1024;
+    static_assert(2 * kBufs * kCols <= 512 && kPart * kBlock % 1024 == 0 && kPart % 16 == 0, "");
 };
 
 struct ManyArgs {
@@ -452,19 +471,29 @@ struct ManyArgs {
 };
 
 // tiles in strips of 8 tiles of tokens: the pairs' operands of a moment stay in L2
+constexpr int kStrip = 8;
 __device__ __forceinline__ void tile_at(const ManyArgs& a, int t, int& tm, int& tn) {
-    constexpr int kStrip = 8;
     const int strip = t / (kStrip * a.tiles_n), first = strip * kStrip;
     const int height = min(kStrip, a.tiles_m - first), r = t - first * a.tiles_n;
     tm = first + r % height;
     tn = r / height;
 }
 
-__device__ __forceinline__ void pair_load(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+// Both CTAs' loads report to the first CTA's barrier. Issued by a converged
+// warp, one lane of which is elected.
+__device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
-        "[%4];" ::"r"(smem_u32(dst)),
+        "{\n .reg .pred e;\n .reg .b32 r;\n elect.sync r|e, 0xffffffff;\n"
+        " @e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
+        "[%4];\n}" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void expect_warp(uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n .reg .pred e;\n .reg .b32 r;\n elect.sync r|e, 0xffffffff;\n"
+        " @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}" ::"r"(bar),
+        "r"(bytes)
         : "memory");
 }
 
@@ -492,11 +521,60 @@ __device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
+// column within the tile of column c of a product: NT / 4 columns are weight
+// rows of the first CTA, the others of the second, NT / 2 further
+template <int NT>
+__device__ __forceinline__ int column(int half, int c) {
+    return c / (NT / 4) * (NT / 2) + half * (NT / 4) + c % (NT / 4);
+}
+
 __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, int x, int y) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n"
                  "cp.async.bulk.commit_group;" ::"l"(map),
                  "r"(x), "r"(y), "r"(src)
                  : "memory");
+}
+
+// Whether both barriers' phases are over, asked for together: an answer takes
+// some 100 cycles. (It may wait a while for them.)
+__device__ __forceinline__ bool both_ready(uint32_t bar, uint32_t phase, uint32_t bar2, uint32_t phase2) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p, q;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n and.pred p, p, q;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(phase), "r"(bar2), "r"(phase2)
+        : "memory");
+    return ok != 0;
+}
+// at once
+__device__ __forceinline__ bool is_ready(uint32_t bar, uint32_t phase) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(phase)
+        : "memory");
+    return ok != 0;
+}
+
+// Scales of kBatch blocks of K, from kb on, by a warp: rows m on of the
+// activations, block rows wr and wr + 1 of the weights; zeros outside. The
+// copies' completion arrives at `bar` (32 arrivals).
+__device__ __forceinline__ void copy4(float* to, const float* from, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(in ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_scales(const ManyArgs& a, int m, int wr, int w_rows, int kb, float (*sx)[kTile + 4],
+                                            float (*sw)[2], uint64_t* bar) {
+    const int lane = threadIdx.x & 31, k = lane & 7, i = lane >> 3;   // 8 blocks by 4 rows
+    const bool in = kb + k < a.blocks;
+    const int rows = in ? (int)min((int64_t)kTile, a.M - m) - i : 0;
+    const float* from = in ? a.x_scales + (int64_t)(m + i) * a.blocks + kb + k : a.x_scales;
+#pragma unroll 4
+    for (int r = 0; r < kTile; r += 4) copy4(&sx[k][r + i], r < rows ? from + (int64_t)r * a.blocks : a.x_scales, r < rows);
+    const bool w_in = in && i < 2 && wr + i < w_rows;
+    if (i < 2) copy4(&sw[k][i], w_in ? a.w_scales + (int64_t)(wr + i) * a.blocks + kb + k : a.w_scales, w_in);
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 template <typename T, int NT>
@@ -506,13 +584,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
                                                                const __grid_constant__ ManyArgs a) {
     using C = Many<NT>;
     extern __shared__ uint8_t dyn[];
-    __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], d_full[C::kBufs], d_empty[C::kBufs];
+    __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], d_full[2][C::kBufs], d_empty[2][C::kBufs];
     __shared__ __align__(8) uint64_t s_full[2], s_empty[2];
     __shared__ __align__(8) uint64_t tmem_ready;
     __shared__ float sx[2][kBatch][kTile + 4], sw[2][kBatch][2];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
-    __shared__ int loads, products;   // issued
+    __shared__ int loads, products[2];   // issued
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -523,18 +601,18 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], 2);   // both halves' products
         }
-        for (int i = 0; i < C::kBufs; ++i) {
-            mbar_init(&d_full[i], 1);
-            mbar_init(&d_empty[i], 2 * kSumWarps);   // of both CTAs
+        for (int i = 0; i < 2 * C::kBufs; ++i) {
+            mbar_init(&d_full[0][i], 1);
+            mbar_init(&d_empty[0][i], kSumWarps);   // half of each CTA's
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 32);
             mbar_init(&s_empty[i], kSumWarps);
         }
         mbar_init(&tmem_ready, 2);
-        abort_flag = loads = products = 0;
+        abort_flag = loads = products[0] = products[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -543,183 +621,213 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+        const uint32_t lead = mapa(smem_u32(full), 0);   // the first CTA's barriers
         if (warp == 0) {
-            if (lane == 0) {
-                int g = 0, slot = 0;
-                uint32_t phase = 1;   // (the first round finds every slot free)
-                bool ok = true;
-                for (int t = pair; ok && t < tiles; t += a.pairs) {
-                    int tm, tn;
-                    tile_at(a, t, tm, tn);
-                    const int m = tm * kPairRows + rank * kTile, n = tn * NT + rank * (NT / 2);
-                    for (int kb = 0; kb < a.blocks; ++kb, ++g) {
-                        if (g >= C::kStages && !mbar_wait(&empty[slot], phase, ctl)) {
-                            ok = false;
-                            break;
-                        }
-                        uint8_t* st = ring + slot * C::kStage;
-                        const uint32_t bar = mapa(smem_u32(&full[slot]), 0);
-                        if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * C::kStage);
-                        pair_load(st + kTile * kBlock, &w_map, bar, kb * kBlock, n);
-                        if (g == 0) pdl_wait();   // (weights may be read before)
-                        pair_load(st, &x_map, bar, kb * kBlock, m);
-                        loads = g + 1;
-                        if (++slot == C::kStages) {
-                            slot = 0;
-                            phase ^= 1u;
-                        }
-                    }
-                }
-            }
-            __syncwarp();
-        } else if (warp == 1) {
-            if (rank == 0) {
-                bool ok = warp_wait(&tmem_ready, 0, ctl);
-                fence_after();
-                const uint32_t tmem = tmem_slot;
-                int g = 0, slot = 0;
-                uint32_t phase = 0;
-                for (int t = pair; ok && t < tiles; t += a.pairs)
-                    for (int kb = 0; kb < a.blocks; ++kb, ++g) {
-                        const int buf = g % C::kBufs;
-                        ok = warp_wait(&full[slot], phase, ctl) &&
-                             (g < C::kBufs || warp_wait(&d_empty[buf], (uint32_t)(g / C::kBufs - 1) & 1u, ctl));
-                        if (!ok) break;
-                        fence_after();
-                        const uint32_t st = smem_u32(ring + slot * C::kStage);
-                        pair_products(tmem + buf * NT, desc_lo(st), desc_lo(st + kTile * kBlock), idesc(kPairRows, NT),
-                                      &empty[slot], &d_full[buf]);
-                        if (lane == 0) products = g + 1;
-                        if (++slot == C::kStages) {
-                            slot = 0;
-                            phase ^= 1u;
-                        }
-                    }
-            }
-        } else if (warp == 2) {
-            pdl_wait();
-            const int w_rows = (int)((a.N + kBlock - 1) / kBlock);
-            int j = 0;
+            const uint32_t to = smem_u32(ring) + kTile * kBlock;
+            int slot = 0, g = 0;
+            uint32_t phase = 1;   // (the first round finds every slot free)
             bool ok = true;
             for (int t = pair; ok && t < tiles; t += a.pairs) {
                 int tm, tn;
                 tile_at(a, t, tm, tn);
-                // lanes: 8 blocks of K by 4 tokens
-                const int64_t m = (int64_t)tm * kPairRows + rank * kTile + (lane >> 3);
-                const int wr = (int)((int64_t)tn * NT / kBlock) + (lane >> 3);
-                for (int k0 = 0; k0 < a.blocks; k0 += kBatch, ++j) {
-                    const int kb = k0 + (lane & 7);
-                    const bool in = kb < a.blocks;
-                    if (j >= 2 && !(ok = warp_wait(&s_empty[j & 1], (uint32_t)(j / 2 - 1) & 1u, ctl))) break;
-                    const float* from = a.x_scales + m * a.blocks + kb;
-                    float* to = &sx[j & 1][lane & 7][lane >> 3];
-                    const int rows = in ? (int)max((int64_t)0, min((int64_t)kTile, a.M - m)) : 0;
-#pragma unroll 8
-                    for (int r = 0; r < kTile; r += 4) to[r] = r < rows ? from[(int64_t)r * a.blocks] : 0.f;
-                    if (lane < 16)
-                        sw[j & 1][lane & 7][lane >> 3] = in && wr < w_rows ? a.w_scales[(int64_t)wr * a.blocks + kb] : 0.f;
-                    mbar_arrive(&s_full[j & 1]);
+                const int n = tn * NT + rank * (NT / 2);
+                for (int kb = 0; kb < a.blocks; ++kb, ++g) {
+                    if (g >= C::kStages && !(ok = warp_wait(&empty[slot], phase, ctl))) break;
+                    if (rank == 0) expect_warp(smem_u32(&full[slot]), 2 * C::kStage);
+                    pair_load(to + slot * C::kStage, &w_map, lead + 8 * slot, kb * kBlock, n);
+                    if (lane == 0) loads = g + 1;
+                    if (++slot == C::kStages) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        } else if (warp == 2) {
+            pdl_wait();
+            const uint32_t to = smem_u32(ring);
+            const int w_rows = (int)((a.N + kBlock - 1) / kBlock);
+            int slot = 0, g = 0, j = 0;
+            uint32_t phase = 1;
+            bool ok = true;
+            for (int t = pair; ok && t < tiles; t += a.pairs) {
+                int tm, tn;
+                tile_at(a, t, tm, tn);
+                const int m = tm * kPairRows + rank * kTile;
+                for (int kb = 0; kb < a.blocks; ++kb, ++g) {
+                    if (kb % kBatch == 0) {
+                        if (j >= 2 && !(ok = warp_wait(&s_empty[j & 1], (uint32_t)(j / 2 - 1) & 1u, ctl))) break;
+                        copy_scales(a, m, (int)((int64_t)tn * NT / kBlock), w_rows, kb, sx[j & 1], sw[j & 1], &s_full[j & 1]);
+                        ++j;
+                    }
+                    if (g >= C::kStages && !(ok = warp_wait(&empty[slot], phase, ctl))) break;
+                    pair_load(to + slot * C::kStage, &x_map, lead + 8 * slot, kb * kBlock, m);
+                    if (++slot == C::kStages) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
         } else {
-            // (the order of these: see few_kernel)
-            pdl_wait();
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot))
-                         : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-            fence_before();
-            pdl_launch_dependents();
-            // both CTAs' columns are there before the first product
-            if (lane < 2) arrive_at(mapa(smem_u32(&tmem_ready), lane));
-            __syncwarp();
+            if (warp == 3) {
+                // (the order of these: see few_kernel)
+                pdl_wait();
+                asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot))
+                             : "memory");
+                asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+                fence_before();
+                pdl_launch_dependents();
+                // both CTAs' columns are there before the first product
+                if (lane < 2) arrive_at(mapa(smem_u32(&tmem_ready), lane));
+                __syncwarp();
+            }
+            if (rank == 0) {
+                bool ok = warp_wait(&tmem_ready, 0, ctl);
+                fence_after();
+                const uint32_t tmem = tmem_slot, from = smem_u32(ring);
+                // warp 1 takes the first half of both CTAs' weight rows, warp 3 the second
+                const int half = warp >> 1;
+                const int total = (tiles - pair + a.pairs - 1) / a.pairs * a.blocks;
+                int slot = 0, buf = 0;
+                uint32_t phase = 0, d_phase = 1;
+                for (int g = 0; ok && g < total; ++g) {
+                    // (the first round finds every buffer free: a barrier's phase before its first is over)
+                    if (!__all_sync(0xffffffffu, both_ready(smem_u32(&full[slot]), phase, smem_u32(&d_empty[half][buf]), d_phase)) &&
+                        !(ok = warp_wait(&full[slot], phase, ctl) && warp_wait(&d_empty[half][buf], d_phase, ctl)))
+                        break;
+                    fence_after();
+                    const uint32_t st = desc_lo(from + slot * C::kStage);
+                    pair_products(tmem + (2 * buf + half) * C::kCols, st, st + (kTile * kBlock + half * C::kPart * kBlock >> 4),
+                                  idesc(kPairRows, C::kCols), &empty[slot], &d_full[half][buf]);
+                    if (lane == 0) products[half] = g + 1;
+                    if (++slot == C::kStages) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
+                    if (++buf == C::kBufs) {
+                        buf = 0;
+                        d_phase ^= 1u;
+                    }
+                }
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
         using S = typename T::storage;
-        const int quarter = (warp - 4) >> 2;
+        constexpr int kPart = C::kPart, kChunk = 16;
+        const int half = (warp - 4) >> 2;
         const int row = (warp & 3) * 32 + lane;
-        const int half = quarter * C::kCols / kBlock;   // weight block of the tile
         bool ok = warp_wait(&tmem_ready, 0, ctl);
         fence_after();
-        const uint32_t mine = tmem_slot + ((uint32_t)(warp & 3) << 21) + quarter * C::kCols;
-        const uint32_t box = smem_u32(ring + C::kStages * C::kStage + (warp - 4) * kOutBox);
+        const uint32_t mine = tmem_slot + ((uint32_t)(warp & 3) << 21) + half * C::kCols;
+        const uint32_t sx_at = smem_u32(&sx[0][0][row]), sw_at = smem_u32(&sw[0][0][0]);
+        const uint32_t filled = smem_u32(&d_full[half][0]), released = mapa(smem_u32(&d_empty[half][0]), 0);
+        const uint32_t box = smem_u32(ring) + C::kStages * C::kStage + (warp - 4) * kOutBox;
         pdl_wait();   // (every thread that writes outputs)
-        int g = 0, j = 0;
+        int buf = 0, batch = 0;
+        uint32_t d_phase = 0, s_phase = 0;
+        bool ready = false;   // the next buffer is known to be filled
         for (int t = pair; ok && t < tiles; t += a.pairs) {
             float sum[C::kCols];
 #pragma unroll
             for (int i = 0; i < C::kCols; ++i) sum[i] = 0.f;
-            for (int kb = 0; kb < a.blocks; ++kb, ++g) {
-                const int buf = g % C::kBufs, at_batch = kb % kBatch;
-                if (at_batch == 0 && !(ok = warp_wait(&s_full[j & 1], (uint32_t)(j / 2) & 1u, ctl))) break;
-                const float s = sx[j & 1][at_batch][row] * sw[j & 1][at_batch][half];
-                if (!(ok = warp_wait(&d_full[buf], (uint32_t)(g / C::kBufs) & 1u, ctl))) break;
-                fence_after();
-                const uint32_t at = mine + buf * NT;
-                uint32_t d[2][16];
-                tmem_ld16(at, d[0]);
-#pragma unroll
-                for (int c = 0; c < C::kCols / 16; ++c) {
-                    tmem_ld_wait();
-                    if (c + 1 < C::kCols / 16) {
-                        tmem_ld16(at + 16 * (c + 1), d[(c + 1) & 1]);
-                    } else {
-                        fence_before();
-                        __syncwarp();
-                        if (lane == 0) arrive_at(mapa(smem_u32(&d_empty[buf]), 0));
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2)
-                        fma2(sum[16 * c + i], sum[16 * c + i + 1], d[c & 1][i], d[c & 1][i + 1], s, s);
-                }
-                if (at_batch == kBatch - 1 || kb == a.blocks - 1) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s_empty[j & 1]);
-                    ++j;
-                }
-            }
-            if (!ok) break;
             int tm, tn;
             tile_at(a, t, tm, tn);
+            uint32_t second = 0;   // chunks in the second weight block that the tile touches
+            if constexpr (NT != 256) {
+#pragma unroll
+                for (int c = 0; c < C::kCols / kChunk; ++c)
+                    second |= (tn * NT % kBlock + column<NT>(half, kChunk * c)) / kBlock << c;
+            }
+            for (int k0 = 0; ok && k0 < a.blocks; k0 += kBatch) {
+                if (!(ok = warp_wait(&s_full[batch], s_phase, ctl))) break;
+                const int n = min(kBatch, a.blocks - k0);
+                uint32_t xs = sx_at + batch * (kBatch * (kTile + 4) * 4), ws = sw_at + batch * (kBatch * 8);
+                float x = lds1(xs), w0 = lds1(ws), w1 = lds1(ws + 4);
+                for (int k = 0; k < n; ++k) {
+                    if (!ready && !(ok = warp_wait(&d_full[half][buf], d_phase, ctl))) break;
+                    fence_after();
+                    const uint32_t at = mine + buf * NT;
+                    const float s0 = x * w0, s1 = x * w1;
+                    uint32_t d[2][kChunk];
+                    tmem_ld16(at, d[0]);
+#pragma unroll
+                    for (int c = 0; c < C::kCols / kChunk; ++c) {
+                        tmem_ld_wait();
+                        if (c + 1 < C::kCols / kChunk) {
+                            tmem_ld16(at + kChunk * (c + 1), d[(c + 1) & 1]);
+                        } else {
+                            // the buffer goes back, and what the next block needs is
+                            // asked for, before the last products
+                            fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive_at(released + 8 * buf);
+                            if (++buf == C::kBufs) {
+                                buf = 0;
+                                d_phase ^= 1u;
+                            }
+                            ready = is_ready(filled + 8 * buf, d_phase);
+                            if (k + 1 < n) {
+                                xs += (kTile + 4) * 4;
+                                ws += 8;
+                            }
+                            x = lds1(xs);
+                            w0 = lds1(ws);
+                            w1 = lds1(ws + 4);
+                        }
+                        // the weight block of 16 columns: that of their CTA's rows, or by place
+                        const float f = NT == 256 ? (kChunk * c < kPart ? s0 : s1) : (second >> c & 1) ? s1 : s0;
+#pragma unroll
+                        for (int i = 0; i < kChunk; ++i)
+                            sum[kChunk * c + i] = fmaf(as_f32(d[c & 1][i]), f, sum[kChunk * c + i]);
+                    }
+                    ready = __all_sync(0xffffffffu, ready);
+                }
+                if (lane == 0) mbar_arrive(&s_empty[batch]);   // (what was read last has arrived: the vote)
+                batch ^= 1;
+                if (batch == 0) s_phase ^= 1u;
+            }
+            if (!ok) break;
             const int64_t m0 = (int64_t)tm * kPairRows + rank * kTile + (warp & 3) * 32;
-            const int64_t n0 = (int64_t)tn * NT + quarter * C::kCols;
-            if (m0 >= a.M || n0 >= a.N) continue;
+            if (m0 >= a.M) continue;
             if (a.aligned) {
-                // 64 bytes of the warp's 32 rows at a time, 64-byte swizzled; what lies
-                // beyond the matrix is cut off by the store
-                constexpr int kEach = 64 / T::kBytes;
+                // 128 (96) bytes of the warp's rows at a time through shared memory;
+                // what lies beyond the matrix is cut off by the store. Rows of 128
+                // bytes are swizzled, those of 96 spread over the banks as they are.
+                constexpr int kEach = C::kOutBytes / T::kBytes;
 #pragma unroll
                 for (int c = 0; c < C::kCols; c += kEach) {
+                    const int64_t n = (int64_t)tn * NT + column<NT>(half, c);
+                    if (n >= a.N) continue;
                     if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                     __syncwarp();
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int i = 0; i < C::kOutBytes / 16; ++i) {
                         uint32_t w[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int j = 0; j < 4; ++j) {
                             if constexpr (T::kBytes == 4)
-                                w[i] = __float_as_uint(sum[c + 4 * k + i]);
+                                w[j] = __float_as_uint(sum[c + 4 * i + j]);
                             else
-                                w[i] = (uint32_t)T::from_f32(sum[c + 8 * k + 2 * i]) |
-                                       (uint32_t)T::from_f32(sum[c + 8 * k + 2 * i + 1]) << 16;
+                                w[j] = pack16<T>(sum[c + 8 * i + 2 * j], sum[c + 8 * i + 2 * j + 1]);
                         }
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         box + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4)),
+                        const int piece = C::kOutBytes == 128 ? i ^ (lane & 7) : i;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * C::kOutBytes + (piece << 4)),
                                      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                                      : "memory");
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (lane == 0 && n0 + c < a.N) store_box(&out_map, box, (int)(n0 + c), (int)m0);
+                    if (lane == 0) store_box(&out_map, box, (int)n, (int)m0);
                 }
             } else if (m0 + lane < a.M) {
-                S* out = static_cast<S*>(a.out) + (m0 + lane) * a.N + n0;
-                const int cols = (int)min((int64_t)C::kCols, a.N - n0);
 #pragma unroll
-                for (int c = 0; c < C::kCols; ++c)
-                    if (c < cols) out[c] = T::from_f32(sum[c]);
+                for (int c = 0; c < C::kCols; ++c) {
+                    const int64_t n = (int64_t)tn * NT + column<NT>(half, c);
+                    if (n < a.N) static_cast<S*>(a.out)[(m0 + lane) * a.N + n] = T::from_f32(sum[c]);
+                }
             }
         }
+        __syncwarp();
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         __syncwarp();
     }
@@ -729,8 +837,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
     if (abort_flag && rank == 0 && threadIdx.x == 0) {
         for (int i = 0; i < min(loads, C::kStages); ++i)
             mbar_wait_drain(&full[i], (uint32_t)((loads - 1 - i) / C::kStages) & 1u, a.spin_limit, a.status);
-        for (int i = 0; i < min(products, C::kBufs); ++i)
-            mbar_wait_drain(&d_full[i], (uint32_t)((products - 1 - i) / C::kBufs) & 1u, a.spin_limit, a.status);
+        for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < min(products[h], C::kBufs); ++i)
+                mbar_wait_drain(&d_full[h][i], (uint32_t)((products[h] - 1 - i) / C::kBufs) & 1u, a.spin_limit, a.status);
     }
     fence_before();
     __syncthreads();
@@ -749,7 +858,7 @@ static cudaError_t many_launch(const Fp8MmLaunch& L, cudaStream_t s) {
     const int aligned = (L.N * T::kBytes) % 16 == 0 && (uintptr_t)L.out % 16 == 0;
     CUtensorMap w_map, x_map, out_map = {};
     if (!make_map(&w_map, L.w, L.N, L.K, NT / 2) || !make_map(&x_map, L.x, L.M, L.K, kTile) ||
-        (aligned && !make_out_map<T>(&out_map, L.out, L.M, L.N)))
+        (aligned && !make_out_map<T>(&out_map, L.out, L.M, L.N, C::kOutBytes)))
         return cudaErrorInvalidValue;
     static bool done[64];
     cudaError_t e = allow_smem_once(many_kernel<T, NT>, C::kSmem, done);
@@ -769,8 +878,8 @@ static cudaError_t typed(const Fp8MmLaunch& L, cudaStream_t s) {
     if (L.M <= 64) return few_launch<T, 64>(L, s);
     if (L.M <= 128) return few_launch<T, 128>(L, s);
     const int64_t tm = (L.M + kPairRows - 1) / kPairRows, pairs = num_sms() / 2;
-    const int64_t wide = (tm * ((L.N + 255) / 256) + pairs - 1) / pairs * 2, narrow = (tm * ((L.N + 127) / 128) + pairs - 1) / pairs;
-    return narrow < wide ? many_launch<T, 128>(L, s) : many_launch<T, 256>(L, s);
+    const auto rounds = [&](int nt) { return (tm * ((L.N + nt - 1) / nt) + pairs - 1) / pairs; };
+    return rounds(192) * 12 < rounds(256) * 13 ? many_launch<T, 192>(L, s) : many_launch<T, 256>(L, s);
 }
 
 }  // namespace fp8mm
