@@ -46,14 +46,18 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
 
 // Allows a kernel `bytes` of dynamic shared memory, once per kernel and device
 // (the attribute call costs a microsecond of every launch otherwise). `done`
-// is a static array of the caller, one entry per device.
+// is a static array of the caller, one entry per device. `carveout`: the share
+// of an SM's memory that is shared memory, in percent, where several CTAs are to
+// find room.
 template <typename Kernel>
-inline cudaError_t allow_smem_once(Kernel kernel, size_t bytes, bool (&done)[64]) {
+inline cudaError_t allow_smem_once(Kernel kernel, size_t bytes, bool (&done)[64], int carveout = -1) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && carveout >= 0)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, carveout);
     if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
     return e;
 }

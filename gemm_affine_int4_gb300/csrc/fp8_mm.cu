@@ -101,39 +101,100 @@ __device__ __forceinline__ uint32_t mapa(uint32_t a, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
     return r;
 }
-__device__ __forceinline__ float ld_cluster(uint32_t a) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
+
+// Issued by a converged warp, one lane of which is elected: a barrier's bytes
+// to come, and a load that reports to it.
+__device__ __forceinline__ void expect_warp(uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n .reg .pred e;\n .reg .b32 r;\n elect.sync r|e, 0xffffffff;\n"
+        " @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}" ::"r"(bar),
+        "r"(bytes)
+        : "memory");
+}
+
+__device__ __forceinline__ void load_warp(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "{\n .reg .pred e;\n .reg .b32 r;\n elect.sync r|e, 0xffffffff;\n"
+        " @e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n}" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+// Whether both barriers' phases are over, asked for together: an answer takes
+// some 100 cycles. (It may wait a while for them.)
+__device__ __forceinline__ bool both_ready(uint32_t bar, uint32_t phase, uint32_t bar2, uint32_t phase2) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p, q;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n and.pred p, p, q;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(phase), "r"(bar2), "r"(phase2)
+        : "memory");
+    return ok != 0;
+}
+// at once
+__device__ __forceinline__ bool is_ready(uint32_t bar, uint32_t phase) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(phase)
+        : "memory");
+    return ok != 0;
+}
+
+// four bytes from global memory, or zeros
+__device__ __forceinline__ void copy4(float* to, const float* from, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(in ? 4 : 0) : "memory");
+}
+// four values into shared memory of the cluster; 16 bytes are counted at `bar`
+__device__ __forceinline__ void send4(uint32_t to, uint32_t bar, float x, float y, float z, float w) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+                 "f"(x), "f"(y), "f"(z), "f"(w), "r"(bar)
+                 : "memory");
 }
 
 // ---------------------------------------------------------------------------
 // Few tokens. The 128 weight rows of a tile are the M dimension of the product
 // and MT tokens its N dimension; a cluster of up to 8 CTAs shares a tile, each
-// CTA with a part of the blocks of K, and joins its sums through distributed
-// shared memory in a fixed order: no workspace, no second launch.
+// CTA with a part of the blocks of K. No workspace, no second launch: the CTAs
+// send their sums to the cluster's shared memory (four tokens of a row at a
+// time, to the CTA that joins them), where a barrier counts the bytes, and a
+// CTA that has sent its own and joins none is done.
 //
 //   warp 0     TMA producer: a block of weights [128 x 128] and of tokens [MT x 128] a stage
 //   warp 1     issues the products, into tensor memory buffers of MT columns in turn
-//   warp 2     sx[m, b] * sw[b] of the tile's tokens into shared memory, kBatch blocks at a time
-//   warp 3     allocates tensor memory, lets the next kernel start
-//   warps 4-7  thread = weight row: sum[m] += D[m] * scale[m]
+//   warp 2     sx[m, b] * sw[b] of the tile's tokens into shared memory, four blocks at a time
+//   warp 3     takes and frees tensor memory, lets the next kernel start
+//   warps 4-7  thread = weight row: sum[m] += D[m] * scale[m]; join
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;
-constexpr int kBatch = 8;
+constexpr int kFewBatch = 4, kFewBatches = 3;
 constexpr int kThreads = 256;
+constexpr int kMostSplit = 8;
+
+// the CTAs that may share a tile
+constexpr int kSplits[] = {1, 2, 3, 4, 6, 8};
+// groups of four tokens that a CTA of `split` joins at most
+constexpr int groups_of(int mt, int split) { return (mt / 4 + split - 1) / split; }
+constexpr int most_groups(int mt) {
+    int most = 0;
+    for (int s : kSplits) most = s > 1 && s * groups_of(mt, s) > most ? s * groups_of(mt, s) : most;
+    return most;
+}
 
 template <int MT>
 struct Few {
     static constexpr int kStage = kTile * kBlock + MT * kBlock;
-    // two CTAs an SM
-    static constexpr int kStages = MT == 16 ? 6 : MT == 32 ? 5 : MT == 64 ? 4 : 3;
+    // two CTAs an SM (113 KB each), of the widest one
+    static constexpr int kPerSm = MT == 128 ? 1 : 2;
+    static constexpr int kStages = MT == 16 ? 5 : MT == 32 ? 4 : MT == 64 ? 3 : 4;
     static constexpr int kBufs = MT == 128 ? 2 : 4;
     static constexpr int kCols = kBufs * MT;   // 64, 128, 256, 256
     static constexpr int kPitch = MT + 4;      // floats of a block's scales
-    static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
+    static constexpr int kJoin = most_groups(MT) * kTile * 16;   // bytes
+    static constexpr size_t kSmem = (size_t)kStages * kStage + kJoin + 1024;
     static_assert(kCols <= 256, "two CTAs share an SM's 512 columns");
-    static_assert(kStages * kStage >= kTile * MT * 4, "the ring takes the sums at the end");
 };
 
 struct FewArgs {
@@ -148,7 +209,7 @@ struct FewArgs {
     long long spin_limit;
 };
 
-// a share of warps 0-3 goes to warps 4-7: 128 x 56 + 128 x 200 = 256 x 128
+// a share of the registers of warps 0-3 goes to warps 4-7: 128 x 56 + 128 x 200 = 256 x 128
 template <int MT>
 __device__ __forceinline__ void give_registers() {
     if constexpr (MT == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -161,13 +222,14 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     using C = Few<MT>;
     extern __shared__ uint8_t dyn[];
     __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], d_full[C::kBufs], d_empty[C::kBufs];
-    __shared__ __align__(8) uint64_t s_full[2], s_empty[2];
-    __shared__ __align__(16) float scales[2][kBatch][C::kPitch];
-    __shared__ __align__(8) uint64_t tmem_ready;
+    __shared__ __align__(8) uint64_t s_full[kFewBatches], s_empty[kFewBatches];
+    __shared__ __align__(8) uint64_t tmem_ready, tmem_done, joined;
+    __shared__ __align__(16) float scales[kFewBatches][kFewBatch][C::kPitch];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ int loads, products;   // issued
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
+    uint8_t* join = ring + C::kStages * C::kStage;   // [sender][group][row] of four sums
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)(blockIdx.x % (unsigned)a.split);
@@ -177,6 +239,9 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     const int64_t n0 = (int64_t)tile * kTile;
     const int b0 = (int)((int64_t)a.blocks * rank / a.split), b1 = (int)((int64_t)a.blocks * (rank + 1) / a.split);
     const int count = b1 - b0;
+    const int live = (int)min((int64_t)MT, a.M - m0);   // tokens of this chunk
+    const int groups = (live + 3) / 4;
+    const int own = groups > rank ? (groups - rank + a.split - 1) / a.split : 0;   // groups rank, rank + split, ...
     const Ctl ctl{a.status, a.spin_limit, &abort_flag};
 
     if (threadIdx.x == 0) {
@@ -188,85 +253,120 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
             mbar_init(&d_full[i], 1);
             mbar_init(&d_empty[i], 4);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kFewBatches; ++i) {
             mbar_init(&s_full[i], 32);
             mbar_init(&s_empty[i], 4);
         }
         mbar_init(&tmem_ready, 1);
+        mbar_init(&tmem_done, 4);
+        mbar_init(&joined, 1);
         abort_flag = loads = products = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        if (a.split > 1 && own > 0) mbar_arrive_expect_tx(&joined, (uint32_t)(a.split * own * kTile * 16));
     }
     __syncthreads();
+    if (a.split > 1) cluster_arrive();   // (waited for before the first sum is sent)
 
     using S = typename T::storage;
     S* out = static_cast<S*>(a.out);
-    const int row = threadIdx.x & 127;
-    const int64_t n = n0 + row;
-    const int live = (int)min((int64_t)MT, a.M - m0);   // tokens of this chunk
-    float* mine = reinterpret_cast<float*>(ring);       // the CTA's sums in the end, [token][row]
+    bool freed = false;   // (of warp 3)
 
-    // 128 sums a thread: the registers go to the warps that hold them
     if (warp == 0) {
         give_registers<MT>();
-        if (lane == 0) {
-            // the first stages' weights before the kernels ahead of this one have finished
-            const int first = min(count, C::kStages);
-            for (int i = 0; i < first; ++i) {
-                mbar_arrive_expect_tx(&full[i], C::kStage);
-                tma_load_2d(ring + i * C::kStage, &w_map, &full[i], (b0 + i) * kBlock, (int)n0);
-            }
-            pdl_wait();
-            loads = first;
-            for (int i = 0; i < first; ++i)
-                tma_load_2d(ring + i * C::kStage + kTile * kBlock, &x_map, &full[i], (b0 + i) * kBlock, (int)m0);
-            for (int i = first; i < count; ++i) {
-                const int slot = i % C::kStages;
-                if (!mbar_wait(&empty[slot], (uint32_t)(i / C::kStages - 1) & 1u, ctl)) break;
-                uint8_t* st = ring + slot * C::kStage;
-                mbar_arrive_expect_tx(&full[slot], C::kStage);
-                tma_load_2d(st, &w_map, &full[slot], (b0 + i) * kBlock, (int)n0);
-                tma_load_2d(st + kTile * kBlock, &x_map, &full[slot], (b0 + i) * kBlock, (int)m0);
-                loads = i + 1;
+        // the first stages' weights before the kernels ahead of this one have finished
+        const uint32_t to = smem_u32(ring);
+        const int first = min(count, C::kStages);
+        for (int i = 0; i < first; ++i) {
+            expect_warp(smem_u32(&full[i]), C::kStage);
+            load_warp(to + i * C::kStage, &w_map, smem_u32(&full[i]), (b0 + i) * kBlock, (int)n0);
+        }
+        pdl_wait();
+        if (lane == 0) loads = first;
+        for (int i = 0; i < first; ++i)
+            load_warp(to + i * C::kStage + kTile * kBlock, &x_map, smem_u32(&full[i]), (b0 + i) * kBlock, (int)m0);
+        int slot = 0;
+        uint32_t phase = 0;
+        for (int i = first; i < count; ++i) {
+            if (!warp_wait(&empty[slot], phase, ctl)) break;
+            const uint32_t st = to + slot * C::kStage;
+            expect_warp(smem_u32(&full[slot]), C::kStage);
+            load_warp(st, &w_map, smem_u32(&full[slot]), (b0 + i) * kBlock, (int)n0);
+            load_warp(st + kTile * kBlock, &x_map, smem_u32(&full[slot]), (b0 + i) * kBlock, (int)m0);
+            if (lane == 0) loads = i + 1;
+            if (++slot == C::kStages) {
+                slot = 0;
+                phase ^= 1u;
             }
         }
-        __syncwarp();
     } else if (warp == 1) {
         give_registers<MT>();
         const bool ready = warp_wait(&tmem_ready, 0, ctl);
         fence_after();
-        const uint32_t tmem = tmem_slot;
+        const uint32_t tmem = tmem_slot, from = smem_u32(ring);
+        int slot = 0, buf = 0;
+        uint32_t phase = 0, d_phase = 1;   // (the first round finds every buffer free)
         for (int i = 0; ready && i < count; ++i) {
-            const int slot = i % C::kStages, buf = i % C::kBufs;
-            if (i >= C::kBufs && !warp_wait(&d_empty[buf], (uint32_t)(i / C::kBufs - 1) & 1u, ctl)) break;
-            if (!warp_wait(&full[slot], (uint32_t)(i / C::kStages) & 1u, ctl)) break;
+            if (!__all_sync(0xffffffffu, both_ready(smem_u32(&full[slot]), phase, smem_u32(&d_empty[buf]), d_phase)) &&
+                !(warp_wait(&full[slot], phase, ctl) && warp_wait(&d_empty[buf], d_phase, ctl)))
+                break;
             fence_after();
-            const uint32_t st = smem_u32(ring + slot * C::kStage);
-            block_products(tmem + buf * MT, desc_lo(st), desc_lo(st + kTile * kBlock), idesc(kTile, MT), &empty[slot],
-                           &d_full[buf]);
+            const uint32_t st = desc_lo(from + slot * C::kStage);
+            block_products(tmem + buf * MT, st, st + (kTile * kBlock >> 4), idesc(kTile, MT), &empty[slot], &d_full[buf]);
             if (lane == 0) products = i + 1;
+            if (++slot == C::kStages) {
+                slot = 0;
+                phase ^= 1u;
+            }
+            if (++buf == C::kBufs) {
+                buf = 0;
+                d_phase ^= 1u;
+            }
         }
     } else if (warp == 2) {
         give_registers<MT>();
         pdl_wait();
-        const float* sw = a.w_scales + (int64_t)tile * a.blocks;
-        for (int j = 0; j * kBatch < count; ++j) {
-            // lanes: 8 blocks of K by 4 tokens
-            const int kb = b0 + j * kBatch + (lane & 7);
-            const bool in = kb < b1;
-            const float w = in ? sw[kb] : 0.f;
-            if (j >= 2 && !warp_wait(&s_empty[j & 1], (uint32_t)(j / 2 - 1) & 1u, ctl)) break;
-            const float* sx = a.x_scales + (m0 + (lane >> 3)) * a.blocks + kb;
-            float* to = &scales[j & 1][lane & 7][lane >> 3];
+        // Lanes: 4 blocks of K by 8 tokens. A batch is copied while the one before
+        // it lands and is multiplied in place.
+        const int k = lane & 3, i0 = lane >> 2;
+        const int batches = (count + kFewBatch - 1) / kFewBatch;
+        const float* sw = a.w_scales + (int64_t)tile * a.blocks + b0 + k;
+        const float* sx = a.x_scales + (m0 + i0) * a.blocks + b0 + k;
+        const auto start = [&](int j) {
+            const bool in = j * kFewBatch + k < count;
+            float* to = &scales[j % kFewBatches][k][i0];
 #pragma unroll 4
-            for (int t = 0; t < MT / 4; ++t)
-                to[4 * t] = in && 4 * t + (lane >> 3) < live ? sx[(int64_t)(4 * t) * a.blocks] * w : 0.f;
-            mbar_arrive(&s_full[j & 1]);
+            for (int t = 0; t < MT; t += 8) {
+                const bool there = in && t + i0 < live;
+                copy4(to + t, there ? sx + (int64_t)t * a.blocks + j * kFewBatch : a.x_scales, there);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            return in ? sw[j * kFewBatch] : 0.f;
+        };
+        float w = start(0);
+        for (int j = 0; j < batches; ++j) {
+            float next = 0.f;
+            if (j + 1 < batches) {
+                const int n = j + 1;
+                if (n >= kFewBatches &&
+                    !warp_wait(&s_empty[n % kFewBatches], (uint32_t)(n / kFewBatches - 1) & 1u, ctl))
+                    break;
+                next = start(n);
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            } else {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            }
+            float* mine = &scales[j % kFewBatches][k][i0];
+#pragma unroll 4
+            for (int t = 0; t < MT; t += 8) mine[t] *= w;
+            mbar_arrive(&s_full[j % kFewBatches]);
+            w = next;
         }
     } else if (warp == 3) {
         give_registers<MT>();
-        // Tensor memory is taken after the kernels before this one have
-        // finished, and the next one may start after it is taken: of two
-        // kernels on an SM, none holds columns that the other needs to end.
+        // Tensor memory is taken after the kernels before this one have finished,
+        // and the next one may start after it is taken; and it is free again
+        // before the cluster's CTAs wait for each other's sums. So no CTA holds
+        // columns while it waits for one that may need them.
         pdl_wait();
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
                      "r"(C::kCols)
@@ -275,27 +375,41 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
         fence_before();
         pdl_launch_dependents();
         if (lane == 0) mbar_arrive(&tmem_ready);
+        if (warp_wait(&tmem_done, 0, ctl)) {
+            fence_after();
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_slot), "r"(C::kCols) : "memory");
+            freed = true;
+        }
     } else {
         if constexpr (MT == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        const bool ready = warp_wait(&tmem_ready, 0, ctl);
+        const int row = threadIdx.x & 127;
+        const int64_t n = n0 + row;
+        bool ok = warp_wait(&tmem_ready, 0, ctl);
         fence_after();
-        const uint32_t tmem = tmem_slot;
-        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+        const uint32_t lanes = tmem_slot + ((uint32_t)(warp & 3) << 21);
         float sum[MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m) sum[m] = 0.f;
-        for (int i = 0; ready && i < count; ++i) {
-            const int buf = i % C::kBufs, j = i / kBatch;
-            if (i % kBatch == 0 && !warp_wait(&s_full[j & 1], (uint32_t)(j / 2) & 1u, ctl)) break;
-            if (!warp_wait(&d_full[buf], (uint32_t)(i / C::kBufs) & 1u, ctl)) break;
+        int buf = 0, batch = 0;
+        uint32_t d_phase = 0, s_phase = 0;
+        for (int i = 0; ok && i < count; ++i) {
+            const int k = i % kFewBatch;
+            if (k == 0 && !(ok = warp_wait(&s_full[batch], s_phase, ctl))) break;
+            if (!(ok = warp_wait(&d_full[buf], d_phase, ctl))) break;
             fence_after();
-            const float* sc = scales[j & 1][i % kBatch];
+            const float* sc = scales[batch][k];
             uint32_t d[2][16];
             tmem_ld16(lanes + buf * MT, d[0]);
 #pragma unroll
             for (int c = 0; c < MT / 16; ++c) {
                 tmem_ld_wait();
-                if (c + 1 < MT / 16) tmem_ld16(lanes + buf * MT + 16 * (c + 1), d[(c + 1) & 1]);
+                if (c + 1 < MT / 16) {
+                    tmem_ld16(lanes + buf * MT + 16 * (c + 1), d[(c + 1) & 1]);
+                } else {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&d_empty[buf]);
+                }
 #pragma unroll
                 for (int t = 0; t < 16; t += 4) {
                     const float4 s = lds4(sc + 16 * c + t);
@@ -305,13 +419,22 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
                     sum[16 * c + t + 3] = fmaf(as_f32(d[c & 1][t + 3]), s.w, sum[16 * c + t + 3]);
                 }
             }
-            fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&d_empty[buf]);
-                if (i % kBatch == kBatch - 1) mbar_arrive(&s_empty[j & 1]);
+            if (++buf == C::kBufs) {
+                buf = 0;
+                d_phase ^= 1u;
+            }
+            if (k == kFewBatch - 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_empty[batch]);
+                if (++batch == kFewBatches) {
+                    batch = 0;
+                    s_phase ^= 1u;
+                }
             }
         }
+        fence_before();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&tmem_done);
         pdl_wait();   // (every thread that writes outputs)
         if (a.split == 1) {
             if (n < a.N) {
@@ -320,16 +443,51 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
                     if (m < live) out[(m0 + m) * a.N + n] = T::from_f32(sum[m]);
             }
         } else {
-            // (the last products have been waited for: the ring is free)
+            cluster_wait();   // every CTA's barriers are there
+            const int slots = groups_of(MT, a.split);
+            const uint32_t at = smem_u32(join) + (uint32_t)(rank * slots * kTile + row) * 16;
+            int to = 0;
+            uint32_t place = at;
 #pragma unroll
-            for (int m = 0; m < MT; ++m) mine[m * kTile + row] = sum[m];
+            for (int q = 0; q < MT / 4; ++q) {
+                if (4 * q < live)
+                    send4(mapa(place, to), mapa(smem_u32(&joined), to), sum[4 * q], sum[4 * q + 1], sum[4 * q + 2], sum[4 * q + 3]);
+                if (++to == a.split) {
+                    to = 0;
+                    place += kTile * 16;
+                }
+            }
+            // what this CTA joins, in the order of the ranks
+            if (own > 0 && warp_wait(&joined, 0, ctl)) {
+                for (int q = 0; q < own; ++q) {
+                    const float* from = reinterpret_cast<const float*>(join) + (q * kTile + row) * 4;
+                    float4 s = lds4(from);
+                    for (int r = 1; r < a.split; ++r) {
+                        const float4 v = lds4(from + r * slots * kTile * 4);
+                        s.x += v.x;
+                        s.y += v.y;
+                        s.z += v.z;
+                        s.w += v.w;
+                    }
+                    const int m = 4 * (q * a.split + rank);
+                    if (n < a.N) {
+                        S* o = out + (m0 + m) * a.N + n;
+                        o[0] = T::from_f32(s.x);
+                        if (m + 1 < live) o[a.N] = T::from_f32(s.y);
+                        if (m + 2 < live) o[2 * a.N] = T::from_f32(s.z);
+                        if (m + 3 < live) o[3 * a.N] = T::from_f32(s.w);
+                    }
+                }
+            }
         }
     }
 
-    // What was issued lands before the CTA leaves. Without a time-out it has:
-    // the commit of the last products was waited for above.
+    // What was issued lands before the CTA leaves; without a time-out it has: the
+    // commit of the last products was waited for above, and so were the sums sent
+    // to this CTA.
     __syncthreads();
-    if (abort_flag && threadIdx.x == 0) {
+    if (!abort_flag) return;
+    if (threadIdx.x == 0) {
         for (int i = 0; i < min(loads, C::kStages); ++i)
             mbar_wait_drain(&full[i], (uint32_t)((loads - 1 - i) / C::kStages) & 1u, a.spin_limit, a.status);
         for (int i = 0; i < min(products, C::kBufs); ++i)
@@ -338,23 +496,13 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     fence_before();
     __syncthreads();
     fence_after();
-    // (before the cluster's CTAs wait for each other: a CTA that holds tensor
-    // memory waits for none of them)
-    if (warp == 3)
+    if (warp == 3 && !freed)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_slot), "r"(C::kCols) : "memory");
-
-    if (a.split == 1) return;
-    pdl_wait();
-    // token m is joined by rank m % split, in the order of the ranks
-    cluster_arrive();
-    cluster_wait();
-    for (int m = rank + a.split * (int)(threadIdx.x >> 7); m < live; m += 2 * a.split) {
-        float s = 0.f;
-        for (int r = 0; r < a.split; ++r) s += ld_cluster(mapa(smem_u32(mine + m * kTile + row), r));
-        if (n < a.N) out[(m0 + m) * a.N + n] = T::from_f32(s);
+    if (a.split > 1) {   // sums may still be on their way here: until the others have sent theirs, or left
+        if (warp < 4) cluster_wait();
+        cluster_arrive();
+        cluster_wait();
     }
-    cluster_arrive();   // no CTA leaves while another reads its sums
-    cluster_wait();
 }
 
 template <typename... KArgs, typename... Args>
@@ -400,20 +548,77 @@ static bool make_out_map(CUtensorMap* map, const void* p, int64_t rows, int64_t 
                   bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+// How many clusters of a size find SMs of their own (a cluster lies within a part
+// of the GPU, so not every SM takes part in large ones).
+template <typename T, int MT>
+static int clusters_at_once(int split) {
+    static int known[64][kMostSplit + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (known[dev][split] > 0) return known[dev][split];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)split);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Few<MT>::kSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)split;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, few_kernel<T, MT>, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = std::max(1, num_sms() / split);
+    }
+    return known[dev][split] = n;
+}
+
+// The split that should end first, and when, in units of 10 ns: 3 us for a start
+// and an end; 0.4 us (128 tokens: 0.52) a block of K of a CTA that has an SM to
+// itself, 0.56 us where two share one, and 1.3 us since the next call's CTAs then
+// find no room to load their weights early; or HBM at 6.2 TB/s. Measured in us,
+// split 1, 2, 3, 4, 6, 8:
+//   1 x 4096 x 4096     10.2   7.0   5.5   5.4   6.3   6.8
+//   64 x 2048 x 2048     9.0   6.9   6.0   5.2   4.8   6.4
+//   16 x 14336 x 5120   16.2  16.0  16.2  16.0  17.3  19.9
+//   33 x 5120 x 14336   42.7  24.6  18.7  20.3  16.9  21.0
+//   56 x 5120 x 17408   51.6  29.6  22.9  23.6  19.9  24.6
+//   16 x 256 x 16384    33.9  18.2  13.0  10.2   7.7   6.4
+template <typename T, int MT>
+static int64_t few_plan(const Fp8MmLaunch& L, int* split) {
+    using C = Few<MT>;
+    const int64_t clusters = (L.N + kTile - 1) / kTile * ((L.M + MT - 1) / MT);
+    const int64_t blocks = (L.K + kBlock - 1) / kBlock, hbm = L.N * L.K / 62000;
+    int64_t best = -1;
+    for (int n : kSplits) {
+        if (n > blocks) break;
+        const int64_t alone = clusters_at_once<T, MT>(n), each = (blocks + n - 1) / n;
+        const int64_t rounds = (clusters + alone * C::kPerSm - 1) / (alone * C::kPerSm);
+        const int64_t cost = clusters <= alone ? 300 + std::max((MT == 128 ? 52 : 40) * each, hbm)
+                                               : 430 * rounds + std::max((MT == 128 ? 52 : 56) * each * rounds, hbm);
+        if (best < 0 || cost < best) {
+            best = cost;
+            *split = n;
+        }
+    }
+    return best;
+}
+
 template <typename T, int MT>
 static cudaError_t few_launch(const Fp8MmLaunch& L, cudaStream_t s) {
     using C = Few<MT>;
     CUtensorMap w_map, x_map;
     if (!make_map(&w_map, L.w, L.N, L.K, kTile) || !make_map(&x_map, L.x, L.M, L.K, MT)) return cudaErrorInvalidValue;
     static bool done[64];
-    cudaError_t e = allow_smem_once(few_kernel<T, MT>, C::kSmem, done);
+    cudaError_t e = allow_smem_once(few_kernel<T, MT>, C::kSmem, done, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
+    int split = 1;
+    few_plan<T, MT>(L, &split);
     const int64_t tiles = (L.N + kTile - 1) / kTile, chunks = (L.M + MT - 1) / MT;
-    const int blocks = (int)((L.K + kBlock - 1) / kBlock);
-    // as many CTAs as two an SM hold
-    int split = (int)std::min<int64_t>({8, blocks, std::max<int64_t>(1, 2 * (int64_t)num_sms() / (tiles * chunks))});
     if (tiles * chunks * split > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    const FewArgs a{L.w_scales, L.x_scales, L.out, L.M, L.N, blocks, (int)chunks, split, L.status, L.spin_limit};
+    const FewArgs a{L.w_scales, L.x_scales, L.out, L.M, L.N, (int)((L.K + kBlock - 1) / kBlock), (int)chunks, split,
+                    L.status, L.spin_limit};
     return launch_cluster(few_kernel<T, MT>, (unsigned)(tiles * chunks * split), kThreads, C::kSmem, (unsigned)split, s,
                           w_map, x_map, a);
 }
@@ -440,6 +645,7 @@ static cudaError_t few_launch(const Fp8MmLaunch& L, cudaStream_t s) {
 constexpr int kSumWarps = 8;
 constexpr int kPairThreads = 32 * (4 + kSumWarps);
 constexpr int kPairRows = 256;
+constexpr int kBatch = 8;
 // 384 threads x 168 registers = 128 x 72 + 256 x 216
 constexpr int kControlRegs = 72, kSumRegs = 216;
 
@@ -489,14 +695,6 @@ __device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap* map, 
         "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ void expect_warp(uint32_t bar, uint32_t bytes) {
-    asm volatile(
-        "{\n .reg .pred e;\n .reg .b32 r;\n elect.sync r|e, 0xffffffff;\n"
-        " @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}" ::"r"(bar),
-        "r"(bytes)
-        : "memory");
-}
-
 // as block_products, for both CTAs of the pair; the commits reach both
 __device__ __forceinline__ void pair_products(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t id, uint64_t* slot_free,
                                               uint64_t* done) {
@@ -535,35 +733,9 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, 
                  : "memory");
 }
 
-// Whether both barriers' phases are over, asked for together: an answer takes
-// some 100 cycles. (It may wait a while for them.)
-__device__ __forceinline__ bool both_ready(uint32_t bar, uint32_t phase, uint32_t bar2, uint32_t phase2) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p, q;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n and.pred p, p, q;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(phase), "r"(bar2), "r"(phase2)
-        : "memory");
-    return ok != 0;
-}
-// at once
-__device__ __forceinline__ bool is_ready(uint32_t bar, uint32_t phase) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(phase)
-        : "memory");
-    return ok != 0;
-}
-
 // Scales of kBatch blocks of K, from kb on, by a warp: rows m on of the
 // activations, block rows wr and wr + 1 of the weights; zeros outside. The
 // copies' completion arrives at `bar` (32 arrivals).
-__device__ __forceinline__ void copy4(float* to, const float* from, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(in ? 4 : 0) : "memory");
-}
 __device__ __forceinline__ void copy_scales(const ManyArgs& a, int m, int wr, int w_rows, int kb, float (*sx)[kTile + 4],
                                             float (*sw)[2], uint64_t* bar) {
     const int lane = threadIdx.x & 31, k = lane & 7, i = lane >> 3;   // 8 blocks by 4 rows
@@ -871,15 +1043,25 @@ static cudaError_t many_launch(const Fp8MmLaunch& L, cudaStream_t s) {
     return launch_cluster(many_kernel<T, NT>, 2 * (unsigned)pairs, kPairThreads, C::kSmem, 2, s, w_map, x_map, out_map, a);
 }
 
+// The pairs take 3.5 us and 0.455 us a block of K and round of tiles with 256
+// weight rows, 0.42 us with 192 (8192 x 14336 x 5120: 24 rounds in 437 us, 32 in
+// 539; 1111 x 5000 x 14416: 2 rounds in 110, 2 in 101). They are taken from 65
+// tokens on where that is less than few_plan's time for 128 at once; few / many
+// in us: 128 x 4096 x 4096 10.3 / 17.8, 256 x 4096 x 4096 14.0 / 18.0, 512 x 4096
+// x 4096 19.8 / 18.3, 256 x 14336 x 5120 48 / 24, 512 x 1024 x 8192 13.5 / 31.
 template <typename T>
 static cudaError_t typed(const Fp8MmLaunch& L, cudaStream_t s) {
     if (L.M <= 16) return few_launch<T, 16>(L, s);
     if (L.M <= 32) return few_launch<T, 32>(L, s);
     if (L.M <= 64) return few_launch<T, 64>(L, s);
-    if (L.M <= 128) return few_launch<T, 128>(L, s);
-    const int64_t tm = (L.M + kPairRows - 1) / kPairRows, pairs = num_sms() / 2;
-    const auto rounds = [&](int nt) { return (tm * ((L.N + nt - 1) / nt) + pairs - 1) / pairs; };
-    return rounds(192) * 12 < rounds(256) * 13 ? many_launch<T, 192>(L, s) : many_launch<T, 256>(L, s);
+    const int64_t tm = (L.M + kPairRows - 1) / kPairRows, pairs = num_sms() / 2, blocks = (L.K + kBlock - 1) / kBlock;
+    const auto cost = [&](int nt, int64_t each) {
+        return 3500 + (tm * ((L.N + nt - 1) / nt) + pairs - 1) / pairs * blocks * each;   // ns
+    };
+    const int64_t wide = cost(256, 455), narrow = cost(192, 420);
+    int split;
+    if (10 * few_plan<T, 128>(L, &split) <= std::min(wide, narrow)) return few_launch<T, 128>(L, s);
+    return narrow < wide ? many_launch<T, 192>(L, s) : many_launch<T, 256>(L, s);
 }
 
 }  // namespace fp8mm
