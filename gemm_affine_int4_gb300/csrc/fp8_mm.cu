@@ -551,10 +551,8 @@ static bool make_out_map(CUtensorMap* map, const void* p, int64_t rows, int64_t 
 // How many clusters of a size find SMs of their own (a cluster lies within a part
 // of the GPU, so not every SM takes part in large ones).
 template <typename T, int MT>
-static int clusters_at_once(int split) {
+static int clusters_at_once(int dev, int split) {
     static int known[64][kMostSplit + 1];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     if (known[dev][split] > 0) return known[dev][split];
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)split);
@@ -593,7 +591,7 @@ static int64_t few_plan(const Fp8MmLaunch& L, int* split) {
     int64_t best = -1;
     for (int n : kSplits) {
         if (n > blocks) break;
-        const int64_t alone = clusters_at_once<T, MT>(n), each = (blocks + n - 1) / n;
+        const int64_t alone = clusters_at_once<T, MT>(L.device, n), each = (blocks + n - 1) / n;
         const int64_t rounds = (clusters + alone * C::kPerSm - 1) / (alone * C::kPerSm);
         const int64_t cost = clusters <= alone ? 300 + std::max((MT == 128 ? 52 : 40) * each, hbm)
                                                : 430 * rounds + std::max((MT == 128 ? 52 : 56) * each * rounds, hbm);

@@ -220,6 +220,7 @@ struct Fp8MmLaunch {
     int64_t M, N, K;
     int* status;
     long long spin_limit;
+    int device;              // the current one, below 64
 };
 cudaError_t launch_fp8_mm(const Fp8MmLaunch& L, int dtype, cudaStream_t s);
 

@@ -163,8 +163,8 @@ gai4_status gai4_fp8_mm_t(const uint8_t* w_codes, const float* w_scales, const u
     if (!aligned_to(w_codes, 16) || !aligned_to(x_codes, 16) || !aligned_to(w_scales, 4) || !aligned_to(x_scales, 4) ||
         !aligned_to(out, elem_bytes(dtype)))
         return GAI4_ERR_MISALIGNED;
-    Fp8MmLaunch L{w_codes, w_scales, x_codes, x_scales, out, M, N, K, status_ptr(), 2000000000LL};   // ~1 s a wait
-    if (!L.status) return GAI4_ERR_CUDA;
+    Fp8MmLaunch L{w_codes, w_scales, x_codes, x_scales, out, M, N, K, status_ptr(), 2000000000LL, 0};   // ~1 s a wait
+    if (!L.status || cudaGetDevice(&L.device) != cudaSuccess || L.device >= 64) return GAI4_ERR_CUDA;
     return done(launch_fp8_mm(L, dtype, (cudaStream_t)stream));
 }
 
