@@ -96,6 +96,17 @@ struct F32 {
     __device__ __forceinline__ static float from_f32(float f) { return f; }
 };
 
+// two values in T's 16 bits, `lo` in the low half
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    uint32_t r;
+    if constexpr (T::kIsBF16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // ---------------------------------------------------------------------------
 // mixed-precision multiply-add: binary32 += T16 x T16 with a half-word select
 // (sm_100+ fma.rn.f32.{bf16,f16}); HA / HB pick the low (0) or high (1) half

@@ -73,17 +73,6 @@ __device__ __forceinline__ float lds1(uint32_t a) {
     return v;
 }
 
-// two values in T's 16 bits, `lo` in the low half
-template <typename T>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
-    uint32_t r;
-    if constexpr (T::kIsBF16)
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 __device__ __forceinline__ float as_f32(uint32_t v) { return __uint_as_float(v); }
 __device__ __forceinline__ float4 lds4(const float* p) {
     float4 v;

@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(const typename T
                                                                 float* __restrict__ scales, int64_t N, int64_t K) {
     // no programmatic launch: what this kernel writes may be read as weights
     pdl_wait();
-    __shared__ uint32_t part[kThreads / 32];
+    __shared__ float part[kThreads / 32];
     const int64_t k = (int64_t)blockIdx.x * kGroup + (threadIdx.x & 15) * 8;
     const int64_t n0 = (int64_t)blockIdx.y * kGroup + (threadIdx.x >> 4);
     float v[8][8];
@@ -65,14 +65,15 @@ __global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(const typename T
         for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
         if (n0 + 16 * j < N && k < K) load8<T, VEC>(w + (n0 + 16 * j) * K + k, K - k, v[j]);
     }
-    uint32_t m = 0;
+    float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, amax8(v[j]));
-    m = __reduce_max_sync(0xffffffffu, m);
+    for (int j = 0; j < 8; ++j) m = max_abs(m, amax8(v[j]));
+    m = group_max(m);
+    m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, 16));
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) m = max(m, part[i]);
+    for (int i = 0; i < kThreads / 32; ++i) m = max_abs(m, part[i]);
     const Scale s = scale_of(m);
 #pragma unroll
     for (int j = 0; j < 8; ++j)

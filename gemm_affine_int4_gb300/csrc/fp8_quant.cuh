@@ -17,31 +17,33 @@ namespace fp8 {
 constexpr int kGroup = 128;
 constexpr float kLeastMax = 7.888609052210118e-31f;   // 2^-100
 
-// |v| as an integer that grows with it; infinities above every number, NaN
-// above infinities (a maximum of these does not lose a NaN)
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// the larger magnitude; a NaN stays one
+__device__ __forceinline__ float max_abs(float a, float b) {
+    float r;
+    asm("{\n .reg .f32 x, y;\n abs.f32 x, %1;\n abs.f32 y, %2;\n max.NaN.f32 %0, x, y;\n}" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
 struct Scale {
-    float amax;   // at least 2^-100; infinite or NaN if the group holds such a value
+    float part;   // amax / 512, amax at least 2^-100 (infinite or NaN if the group holds such a value)
     float rcp;
 };
-__device__ __forceinline__ Scale scale_of(uint32_t amax_bits) {
-    const uint32_t least = __float_as_uint(kLeastMax);
+__device__ __forceinline__ Scale scale_of(float amax) {
     Scale s;
-    s.amax = __uint_as_float(amax_bits < least ? least : amax_bits);
-    s.rcp = __frcp_rn(s.amax);
+    s.part = max_abs(amax, kLeastMax) * 0x1p-9f;
+    s.rcp = __frcp_rn(s.part);
     return s;
 }
-__device__ __forceinline__ float scale_value(const Scale& s) { return __fdiv_rn(s.amax, 448.0f); }
+__device__ __forceinline__ float scale_value(const Scale& s) { return __fdiv_rn(s.part, 0.875f); }
 
 // 448 x / amax, rounded to nearest: c = 448 x 2^-9 (exact for 16-bit x, no
-// overflow), a first quotient from the correctly rounded reciprocal, and one
-// correction by its exact residual. If amax is infinite or NaN the residual is
-// NaN, and with it every code of the group.
+// overflow), a first quotient by amax 2^-9 from its correctly rounded
+// reciprocal, and one correction by the exact residual. If amax is infinite or
+// NaN the residual is NaN, and with it every code of the group.
 __device__ __forceinline__ float quotient(float x, const Scale& s) {
     const float c = x * 0.875f;
     const float t = c * s.rcp;
-    return fmaf(fmaf(-t, s.amax, c), s.rcp, t) * 512.0f;
+    return fmaf(fmaf(-t, s.part, c), s.rcp, t);
 }
 
 // two codes, `lo` in the low byte
@@ -51,12 +53,18 @@ __device__ __forceinline__ uint32_t codes2(float lo, float hi) {
     return r;
 }
 
-// 8 values -> 8 codes
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], const Scale& s) {
+// 8 quotients -> 8 codes
+__device__ __forceinline__ uint2 codes8(const float (&q)[8]) {
     uint32_t h[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = codes2(quotient(v[2 * i], s), quotient(v[2 * i + 1], s));
+    for (int i = 0; i < 4; ++i) h[i] = codes2(q[2 * i], q[2 * i + 1]);
     return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+}
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], const Scale& s) {
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = quotient(v[i], s);
+    return codes8(q);
 }
 
 // ---------------------------------------------------------------------------
@@ -64,25 +72,52 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], const Scale& s) {
 // row's end at `left` elements (VEC false)
 // ---------------------------------------------------------------------------
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const typename T::storage* p, int64_t left, float (&v)[8]) {
-    if constexpr (VEC) {
-        if constexpr (T::kBytes == 4) {
+struct Eight {
+    // as loaded: 16 bytes of 16-bit elements, or values
+    static constexpr bool kPacked = VEC && T::kBytes == 2;
+    uint4 w;
+    float v[kPacked ? 1 : 8];
+
+    __device__ __forceinline__ void load(const typename T::storage* p, int64_t left) {
+        if constexpr (kPacked) {
+            w = *reinterpret_cast<const uint4*>(p);
+        } else if constexpr (VEC) {
             const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
             v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
             v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
         } else {
-            const uint4 a = *reinterpret_cast<const uint4*>(p);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < left ? T::to_f32(p[i]) : 0.f;
+        }
+    }
+    __device__ __forceinline__ void zero() {
+        if constexpr (kPacked) {
+            w = make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        }
+    }
+    __device__ __forceinline__ void values(float (&to)[8]) const {
+        if constexpr (kPacked) {
+            const uint32_t h[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                v[2 * i] = T::to_f32((uint16_t)(w[i] & 0xffffu));
-                v[2 * i + 1] = T::to_f32((uint16_t)(w[i] >> 16));
+                to[2 * i] = T::to_f32((uint16_t)(h[i] & 0xffffu));
+                to[2 * i + 1] = T::to_f32((uint16_t)(h[i] >> 16));
             }
-        }
-    } else {
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < left ? T::to_f32(p[i]) : 0.f;
+            for (int i = 0; i < 8; ++i) to[i] = v[i];
+        }
     }
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const typename T::storage* p, int64_t left, float (&v)[8]) {
+    Eight<T, VEC> e;
+    e.load(p, left);
+    e.values(v);
 }
 
 template <typename T, bool VEC>
@@ -94,8 +129,7 @@ __device__ __forceinline__ void store8(typename T::storage* p, int64_t left, con
         } else {
             uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = (uint32_t)T::from_f32(v[2 * i]) | (uint32_t)T::from_f32(v[2 * i + 1]) << 16;
+            for (int i = 0; i < 4; ++i) w[i] = pack16<T>(v[2 * i], v[2 * i + 1]);
             *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     } else {
@@ -116,16 +150,16 @@ __device__ __forceinline__ void store_codes8(uint8_t* p, int64_t left, uint2 c) 
     }
 }
 
-__device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {
-    uint32_t m = 0;
+__device__ __forceinline__ float amax8(const float (&v)[8]) {
+    float m = max_abs(v[0], v[1]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+    for (int i = 2; i < 8; ++i) m = max_abs(m, v[i]);
     return m;
 }
 // over the 16 lanes that hold a group
-__device__ __forceinline__ uint32_t group_max(uint32_t m) {
+__device__ __forceinline__ float group_max(float m) {
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 8; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;
 }
 

@@ -4,11 +4,18 @@
 // scale for each 128 elements (fp8_quant.cuh). Sums, h and y are binary32; y is
 // rounded once.
 //
+// A group's codes are those of p = h * gain: y / max |y| = p / max |p|, the root
+// of the row divides out, and only the scales wait for it. So codes and the new
+// residual are written while the row's sum is still being taken, and the codes
+// do not carry its rounding.
+//
 // Each value is read once and written once, so a long input is bound by HBM and
 // a few rows by the latency of a load, the sum across the row and a store. A
-// row is held in registers between the sum and the outputs: `warps` warps take
-// a row, a thread kUnits eights of it, a row's width of threads apart (16 lanes
-// hold a group of 128). Rows too long for that are read a second time.
+// row belongs to some warps; a thread takes kUnits eights of it, a row's width of
+// threads apart (16 lanes hold a group of 128), and keeps p for y in T. Rows too
+// long for that are read a second time.
+#include <algorithm>
+
 #include "fp8_quant.cuh"
 #include "internal.h"
 
@@ -34,59 +41,93 @@ struct NormArgs {
     float eps;
 };
 
-// 8 values of h, zeros past the row's end
+// an eight of a row's inputs, and of the gain, as loaded
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_h(const NormArgs& a, int64_t row, int64_t col, float (&h)[8]) {
-    using S = typename T::storage;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = 0.f;
-    if (col >= a.cols) return;
-    load8<T, VEC>(static_cast<const S*>(a.x) + row * a.x_stride + col, a.cols - col, h);
-    if (a.residual) {
-        float r[8];
-        load8<T, VEC>(static_cast<const S*>(a.residual) + row * a.r_stride + col, a.cols - col, r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] += r[i];
+struct Inputs {
+    Eight<T, VEC> x, r;
+    __device__ __forceinline__ void load(const NormArgs& a, int64_t row, int64_t col) {
+        using S = typename T::storage;
+        if (row < a.rows && col < a.cols) {
+            x.load(static_cast<const S*>(a.x) + row * a.x_stride + col, a.cols - col);
+            if (a.residual) r.load(static_cast<const S*>(a.residual) + row * a.r_stride + col, a.cols - col);
+        } else {
+            x.zero();
+            r.zero();
+        }
     }
+};
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_gain(const NormArgs& a, int64_t col, Eight<T, VEC>& g) {
+    if (a.gain && col < a.cols)
+        g.load(static_cast<const typename T::storage*>(a.gain) + col, a.cols - col);
+    else
+        g.zero();
 }
 
-// writes the row's 8 values; every lane of the warp calls it
+// What can be done with an eight of the row before its root is known: p, and
+// the largest |p| of the group (with codes). Returns the sum of squares of h.
+// Every lane of the warp calls it.
 template <typename T, bool VEC>
-__device__ __forceinline__ void finish8(const NormArgs& a, int64_t row, int64_t col, float inv, float (&h)[8]) {
+__device__ __forceinline__ float begin8(const NormArgs& a, const Inputs<T, VEC>& from, const Eight<T, VEC>& gain,
+                                        int64_t row, int64_t col, bool write, float (&p)[8], float& amax) {
     using S = typename T::storage;
     const bool in = row < a.rows && col < a.cols;
     const int64_t left = a.cols - col, at = row * a.cols + col;
-    if (in && a.residual_out) store8<T, VEC>(static_cast<S*>(a.residual_out) + at, left, h);
-    float g[8];
+    float sum = 0.f;
+    from.x.values(p);
+    if (a.residual) {
+        float r[8];
+        from.r.values(r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = 1.f;
-    if (in && a.gain) load8<T, VEC>(static_cast<const S*>(a.gain) + col, left, g);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = h[i] * inv * g[i];
-    if (in && a.out) store8<T, VEC>(static_cast<S*>(a.out) + at, left, h);
-    if (a.codes) {   // (uniform)
-        const Scale s = scale_of(group_max(amax8(h)));
-        if (in) store_codes8<VEC>(a.codes + at, left, codes8(h, s));
-        if (in && (threadIdx.x & 15) == 0)
-            a.scales[row * ((a.cols + kGroup - 1) / kGroup) + col / kGroup] = scale_value(s);
+        for (int i = 0; i < 8; ++i) p[i] += r[i];
     }
-}
-
-__device__ __forceinline__ float sum_squares(const float (&h)[8]) {
-    float s = 0.f;
+    if (write && in && a.residual_out) store8<T, VEC>(static_cast<S*>(a.residual_out) + at, left, p);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(h[i], h[i], s);
-    return s;
+    for (int i = 0; i < 8; ++i) sum = fmaf(p[i], p[i], sum);
+    if (a.gain) {
+        float g[8];
+        gain.values(g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] *= g[i];
+    }
+    if (write && a.codes) {   // (uniform)
+        amax = max_abs(group_max(amax8(p)), kLeastMax);
+        const float f = __fdiv_rn(448.0f, amax);
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = p[i] * f;
+        if (in) store_codes8<VEC>(a.codes + at, left, codes8(q));
+    }
+    return sum;
 }
 
-// sum over the `warps` warps of a row (threadIdx.y: the row of the block)
-__device__ __forceinline__ float row_sum(float s, int warps, float (*part)[kMaxWarps]) {
-    s = warp_sum(s);
-    if (warps == 1) return s;
-    if ((threadIdx.x & 31) == 0) part[threadIdx.y][threadIdx.x >> 5] = s;
-    __syncthreads();
+// and after it is: y in T, scales
+template <typename T, bool VEC>
+__device__ __forceinline__ void end8(const NormArgs& a, int64_t row, int64_t col, float inv, const float (&p)[8], float amax) {
+    using S = typename T::storage;
+    if (row >= a.rows || col >= a.cols) return;
+    if (a.out) {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = p[i] * inv;
+        store8<T, VEC>(static_cast<S*>(a.out) + row * a.cols + col, a.cols - col, y);
+    }
+    if (a.codes && (threadIdx.x & 15) == 0)
+        a.scales[row * ((a.cols + kGroup - 1) / kGroup) + col / kGroup] = __fdiv_rn(inv * amax, 448.0f);
+}
+
+// sum over a row's threads: blockDim.x of them, 16 or whole warps (threadIdx.y:
+// the row of the block)
+__device__ __forceinline__ float row_sum(float s, float (*part)[kMaxWarps]) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (blockDim.x == 16) return s;
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    if (blockDim.x == 32) return s;
     const int lane = threadIdx.x & 31;
-    return warp_sum(lane < warps ? part[threadIdx.y][lane] : 0.f);
+    if (lane == 0) part[threadIdx.y][threadIdx.x >> 5] = s;
+    __syncthreads();
+    return warp_sum(lane < blockDim.x / 32 ? part[threadIdx.y][lane] : 0.f);
 }
 
 // 1 / sqrt(mean + eps)
@@ -94,48 +135,68 @@ __device__ __forceinline__ float inverse_root(float sum, const NormArgs& a) {
     return __frsqrt_rn(__fdiv_rn(sum, (float)a.cols) + a.eps);
 }
 
-// blockDim = (32 * warps, rows a block); kUnits eights a thread cover the row
-template <typename T, bool VEC, int kUnits>
-__global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ NormArgs a) {
+// blockDim = (threads a row, rows a block); kUnits eights a thread cover the
+// row. With LOOP a block takes rows gridDim.x * blockDim.y apart: the gain is
+// read once, and a row is read while the one before it is summed and written.
+// An output in the place of an input: an eight is written by the thread that has
+// read it.
+template <typename T, bool VEC, int kUnits, bool LOOP>
+__global__ void __launch_bounds__(kUnits == 4 ? 512 : 1024) rms_norm_kernel(const __grid_constant__ NormArgs a) {
     pdl_launch_dependents();
     pdl_wait();   // the kernels before this one are complete: global memory may be read
-    __shared__ float part[32][kMaxWarps];
-    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    float h[kUnits][8];
-    float s = 0.f;
+    __shared__ float part[2][16][kMaxWarps];
+    Inputs<T, VEC> in[kUnits];
+    Eight<T, VEC> gain[kUnits];
+    const int col0 = threadIdx.x * 8, step = blockDim.x * 8;
+    int64_t first = (int64_t)blockIdx.x * blockDim.y;   // row of the block's first threads
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-        const int64_t col = ((int64_t)j * blockDim.x + threadIdx.x) * 8;
-        load_h<T, VEC>(a, row, row < a.rows ? col : a.cols, h[j]);
-    }
+    for (int j = 0; j < kUnits; ++j) in[j].load(a, first + threadIdx.y, col0 + j * step);
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) s += sum_squares(h[j]);
-    const float inv = inverse_root(row_sum(s, blockDim.x / 32, part), a);
+    for (int j = 0; j < kUnits; ++j) load_gain<T, VEC>(a, col0 + j * step, gain[j]);
+    int turn = 0;
+    do {
+        const int64_t row = first + threadIdx.y;
+        first += (int64_t)gridDim.x * blockDim.y;
+        float p[kUnits][8], amax[kUnits], s = 0.f;
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j)
-        finish8<T, VEC>(a, row, ((int64_t)j * blockDim.x + threadIdx.x) * 8, inv, h[j]);
+        for (int j = 0; j < kUnits; ++j) {
+            amax[j] = 0.f;
+            s += begin8<T, VEC>(a, in[j], gain[j], row, col0 + j * step, true, p[j], amax[j]);
+        }
+        if constexpr (LOOP) {
+#pragma unroll
+            for (int j = 0; j < kUnits; ++j) in[j].load(a, first + threadIdx.y, col0 + j * step);
+        }
+        const float inv = inverse_root(row_sum(s, part[turn]), a);
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j) end8<T, VEC>(a, row, col0 + j * step, inv, p[j], amax[j]);
+        turn ^= 1;
+    } while (LOOP && first < a.rows);
 }
 
-// rows of any length, one a block, read twice (the outputs may lie on the
-// inputs: an eight is read again by the thread that writes it, before it does)
+// rows of any length, one a block, read twice (nothing is written in between:
+// outputs may lie on inputs)
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const __grid_constant__ NormArgs a) {
     pdl_launch_dependents();
     pdl_wait();
     __shared__ float part[1][kMaxWarps];
     const int64_t row = blockIdx.x;
-    float s = 0.f;
+    Inputs<T, VEC> in;
+    Eight<T, VEC> gain;
+    float p[8], amax = 0.f, s = 0.f;
     for (int64_t col = (int64_t)threadIdx.x * 8; col < a.cols; col += (int64_t)blockDim.x * 8) {
-        float h[8];
-        load_h<T, VEC>(a, row, col, h);
-        s += sum_squares(h);
+        in.load(a, row, col);
+        load_gain<T, VEC>(a, col, gain);
+        s += begin8<T, VEC>(a, in, gain, row, col, false, p, amax);
     }
-    const float inv = inverse_root(row_sum(s, blockDim.x / 32, part), a);
+    const float inv = inverse_root(row_sum(s, part), a);
     for (int64_t at = 0; at < a.cols; at += (int64_t)blockDim.x * 8) {
         const int64_t col = at + (int64_t)threadIdx.x * 8;
-        float h[8];
-        load_h<T, VEC>(a, row, col, h);
-        finish8<T, VEC>(a, row, col, inv, h);
+        in.load(a, row, col);
+        load_gain<T, VEC>(a, col, gain);
+        begin8<T, VEC>(a, in, gain, row, col, true, p, amax);
+        end8<T, VEC>(a, row, col, inv, p, amax);
     }
 }
 
@@ -143,20 +204,31 @@ template <typename T, bool VEC>
 cudaError_t norm_launch(const NormArgs& a, cudaStream_t s) {
     const int64_t eights = (a.cols + 7) / 8;
     const int64_t wide = (eights + 31) / 32;   // warps that take the row at one eight a thread
-    if (wide > kMaxWarps * 4) {
+    if (wide > kMaxWarps * 2)
         return launch_pdl(rms_norm_long_kernel<T, VEC>, dim3((unsigned)a.rows), dim3(1024), 0, s, a);
-    }
-    // Few rows: as many threads a row as it has eights. Many rows: fewer
-    // threads with more eights each, so that more rows are under way.
+    // Few rows: as many threads a row as it has eights. Many rows: two eights a
+    // thread, so that more is on its way (20011 x 5120, bf16, residual and codes:
+    // 158 us with one, 130 with two), and blocks that take row after row (122 us).
+    // Those pay off for 16-bit rows only: 10000 x 5120 in f32 takes 96 us without,
+    // 134 with, as registers run out. Without a residual half as much is read at a
+    // time: four eights (80 us, two 87).
     const bool few = a.rows <= 2 * num_sms();
-    int units = few ? 1 : wide > 4 ? 4 : wide > 1 ? 2 : 1;
-    while ((wide + units - 1) / units > kMaxWarps) units *= 2;
-    const int warps = (int)((wide + units - 1) / units);
-    const int per = few ? 1 : warps >= 8 ? 1 : 8 / warps;
-    const dim3 block(32 * warps, per);
-    const dim3 grid((unsigned)((a.rows + per - 1) / per));
-    auto* k = units == 1 ? rms_norm_kernel<T, VEC, 1> : units == 2 ? rms_norm_kernel<T, VEC, 2> : rms_norm_kernel<T, VEC, 4>;
-    return launch_pdl(k, grid, block, 0, s, a);
+    const bool loop = !few && T::kBytes == 2 && VEC && wide > 1;
+    int units = few || wide == 1 ? 1 : loop && !a.residual && wide > 4 ? 4 : 2;
+    if (units == 1 && wide > kMaxWarps) units = 2;
+    const int threads = eights <= 16 ? 16 : 32 * (int)((wide + units - 1) / units);
+    const int per = few ? 1 : std::max(1, 256 / threads);
+    // (a block of at least a warp)
+    const dim3 block(threads, threads == 16 ? std::max(per, 2) : per);
+    const int64_t blocks = (a.rows + block.y - 1) / block.y;
+    if (loop) {
+        const dim3 grid((unsigned)std::min<int64_t>(blocks, (int64_t)num_sms() * std::max(1, 1024 / (threads * per))));
+        if constexpr (T::kBytes == 2 && VEC)
+            return launch_pdl(units == 4 ? rms_norm_kernel<T, VEC, 4, true> : rms_norm_kernel<T, VEC, 2, true>, grid, block, 0,
+                              s, a);
+    }
+    return launch_pdl(units == 1 ? rms_norm_kernel<T, VEC, 1, false> : rms_norm_kernel<T, VEC, 2, false>,
+                      dim3((unsigned)blocks), block, 0, s, a);
 }
 
 template <typename T>

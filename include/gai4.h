@@ -559,9 +559,11 @@ gai4_status gai4_rope(const void* q, int64_t q_token_stride, void* q_out, int64_
  *   residual_out [rows, cols] T or NULL: h, rounded
  *   out [rows, cols] T or NULL: y, rounded
  *   codes [rows, cols] and scales [rows, ceil(cols / 128)], or both NULL: y as
- *         activations in e4m3 (not rounded to T in between)
- * h, the sum and y are binary32; a sum of squares beyond it (|h| above 1e19)
- * counts as infinite. Any cols >= 1. out or residual_out (not both) may be x or
+ *         activations in e4m3 (not rounded to T in between; codes are those of
+ *         h * gain, nearest to its binary32 product with 448 / a, a of its
+ *         blocks, and scales are a / (448 sqrt(...)))
+ * h, the sum, h * gain and y are binary32; a sum of squares beyond it (|h| above
+ * 1e19) counts as infinite, and squares below it as zero. Any cols >= 1. out or residual_out (not both) may be x or
  * residual where those are contiguous; outputs must not overlap the inputs or
  * each other otherwise.
  */
