@@ -11,8 +11,8 @@
 // An angle of a far position does not fit binary32. inv_freq (a double, in
 // radians) is turned into a 64-bit fraction of a turn by integer arithmetic;
 // position * fraction modulo 2^64 is then the exact rest of the turns, good to
-// 2^-33 of a turn at any 32-bit position, and its top bits are the argument of
-// a sine in half turns.
+// 2^-33 of a turn at any 32-bit position; it is the argument of a sine in half
+// turns, as the sum of two binary32 numbers.
 #include <algorithm>
 
 #include "common.cuh"
@@ -79,9 +79,79 @@ union Pack {
     typename T::storage e[W];
 };
 
-// Items of a block: (token, head, chunk). A chunk is W pairs (two accesses of
-// W elements each way) or, past them, W channels that are copied.
+// cos or sin of N neighbouring pairs
+template <int N>
+__device__ __forceinline__ void load_pairs(const float* p, float* v) {
+    if constexpr (N >= 4) {
+#pragma unroll
+        for (int j = 0; j < N; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(p + j);
+            v[j] = f.x; v[j + 1] = f.y; v[j + 2] = f.z; v[j + 3] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = p[j];
+    }
+}
+
+// Turns W pairs: halves (p[j], q[j]), or neighbours along p and then q. 16-bit
+// elements are taken and rounded two at a time.
 template <typename T, int W, bool INTERLEAVED>
+__device__ __forceinline__ void turn(Pack<T, W>& p, Pack<T, W>& q, const float (&c)[W], const float (&s)[W]) {
+    if constexpr (T::kBytes == 2 && W >= 2) {
+        constexpr int kWords = W / 2;
+        uint32_t* a = reinterpret_cast<uint32_t*>(&p);
+        uint32_t* b = reinterpret_cast<uint32_t*>(&q);
+        const auto low = [](uint32_t w) { return T::to_f32((uint16_t)(w & 0xffffu)); };
+        const auto high = [](uint32_t w) { return T::to_f32((uint16_t)(w >> 16)); };
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (INTERLEAVED) {
+                const float x = low(a[i]), y = high(a[i]), u = low(b[i]), v = high(b[i]);
+                const int j = kWords + i;
+                a[i] = pack16<T>(x * c[i] - y * s[i], y * c[i] + x * s[i]);
+                b[i] = pack16<T>(u * c[j] - v * s[j], v * c[j] + u * s[j]);
+            } else {
+                const float x = low(a[i]), u = high(a[i]), y = low(b[i]), v = high(b[i]);
+                const int j = 2 * i;
+                a[i] = pack16<T>(x * c[j] - y * s[j], u * c[j + 1] - v * s[j + 1]);
+                b[i] = pack16<T>(y * c[j] + x * s[j], v * c[j + 1] + u * s[j + 1]);
+            }
+        }
+    } else if constexpr (INTERLEAVED) {
+        typename T::storage e[2 * W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            e[j] = p.e[j];
+            e[W + j] = q.e[j];
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            const float x = T::to_f32(e[2 * j]), y = T::to_f32(e[2 * j + 1]);
+            e[2 * j] = T::from_f32(x * c[j] - y * s[j]);
+            e[2 * j + 1] = T::from_f32(y * c[j] + x * s[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            p.e[j] = e[j];
+            q.e[j] = e[W + j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            const float x = T::to_f32(p.e[j]), y = T::to_f32(q.e[j]);
+            p.e[j] = T::from_f32(x * c[j] - y * s[j]);
+            q.e[j] = T::from_f32(y * c[j] + x * s[j]);
+        }
+    }
+}
+
+// A chunk is W pairs of a head (two accesses of W elements each way, half of the
+// turned channels apart, so that neighbouring threads' lie side by side) or, past
+// them, W channels that are copied. A thread has one chunk of its block's rows
+// (token, head), kBatch rows at a time: their loads are under way while the
+// sines are computed.
+template <typename T, int W, bool INTERLEAVED, int kBatch>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
     using S = typename T::storage;
     using V = typename Vec<T, W>::type;
@@ -91,68 +161,86 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const int64_t t0 = (int64_t)(blockIdx.x / (unsigned)a.head_split) * a.per_block;
     const int part = (int)(blockIdx.x % (unsigned)a.head_split);
     const int tokens = (int)min((int64_t)a.per_block, a.tokens - t0);
-    for (int i = threadIdx.x; i < tokens * a.half; i += kThreads) {
+    const int all = a.heads[0] + a.heads[1];
+    const int h0 = (int)((int64_t)all * part / a.head_split), heads = (int)((int64_t)all * (part + 1) / a.head_split) - h0;
+    const int rows = tokens * heads;
+    const float per_head = 1.0f / (float)heads;   // rows are below 2^21: (r + 1/2) / heads is never taken across a whole number
+    const int turned = a.half / W, chunks = turned + (a.pass ? (a.d - 2 * a.half) / W : 0);
+    const int wide = chunks < kThreads ? kThreads / chunks : 1;   // rows that the block's threads take at a time
+    const int tid = threadIdx.x;
+    int chunk = chunks < kThreads ? tid % chunks : tid, r = chunks < kThreads ? tid / chunks : 0;
+    if (r >= wide) chunk = chunks;   // (threads left over)
+
+    S* to[kBatch];
+    int pairs[kBatch];   // first pair's place among the sines
+    Pack<T, W> p[kBatch], q[kBatch];
+    // (single elements of a neighbouring pair are next to each other)
+    constexpr bool kSingle = INTERLEAVED && W == 1;
+    const int next = kSingle ? 1 : a.half;
+    const auto load = [&]() {
+        const int at = chunk < turned ? (kSingle ? 2 : W) * chunk : 2 * a.half + (chunk - turned) * W;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int row = r + u * wide;
+            if (chunk >= chunks || row >= rows) continue;
+            const int t = (int)(((float)row + 0.5f) * per_head);
+            int head = h0 + row - t * heads;
+            const int which = head >= a.heads[0];
+            if (which) head -= a.heads[0];
+            const int64_t token = t0 + t;
+            const S* src = static_cast<const S*>(a.in[which]) + token * a.in_stride[which] + (int64_t)head * a.d + at;
+            to[u] = static_cast<S*>(a.out[which]) + token * a.out_stride[which] + (int64_t)head * a.d + at;
+            pairs[u] = t * a.half + chunk * (INTERLEAVED && W > 1 ? W / 2 : W);
+            p[u].v = *reinterpret_cast<const V*>(src);
+            if (chunk < turned) q[u].v = *reinterpret_cast<const V*>(src + next);
+        }
+    };
+    load();
+    for (int i = tid; i < tokens * a.half; i += kThreads) {
         const int t = i / a.half;
         const double f = a.inv_freq[i - t * a.half];
-        const uint64_t turns = (uint64_t)(int64_t)a.positions[t0 + t] * turn_fraction(f);
+        const int64_t turns = (int64_t)((uint64_t)(int64_t)a.positions[t0 + t] * turn_fraction(f));
+        // the angle in half turns as a sum of two: sine and cosine of the first, turned by the second
+        const float hi = (float)turns, lo = (float)(turns - (int64_t)hi) * (3.14159265f * 0x1p-63f);
         float s, c;
-        sincospif((float)(int64_t)turns * 0x1p-63f, &s, &c);
+        sincospif(hi * 0x1p-63f, &s, &c);
         const float m = isfinite(f) ? a.mscale : __uint_as_float(0x7fffffffu);
-        cs[0][i] = c * m;
-        cs[1][i] = s * m;
+        cs[0][i] = fmaf(-s, lo, c) * m;
+        cs[1][i] = fmaf(c, lo, s) * m;
     }
     __syncthreads();
-    const int heads = a.heads[0] + a.heads[1];
-    const int h0 = heads * part / a.head_split, h1 = heads * (part + 1) / a.head_split;
-    const int turned = a.half / W, chunks = turned + (a.pass ? (a.d - 2 * a.half) / W : 0);
-    const int items = tokens * (h1 - h0) * chunks;
-    for (int i = threadIdx.x; i < items; i += kThreads) {
-        const int r = i / chunks, chunk = i - r * chunks;
-        const int t = r / (h1 - h0);
-        int head = h0 + r - t * (h1 - h0);
-        const int which = head >= a.heads[0];
-        if (which) head -= a.heads[0];
-        const S* src = static_cast<const S*>(a.in[which]) + (t0 + t) * a.in_stride[which] + (int64_t)head * a.d;
-        S* dst = static_cast<S*>(a.out[which]) + (t0 + t) * a.out_stride[which] + (int64_t)head * a.d;
-        if (chunk >= turned) {
-            const int at = 2 * a.half + (chunk - turned) * W;
-            *reinterpret_cast<V*>(dst + at) = *reinterpret_cast<const V*>(src + at);
-            continue;
+    while (chunk < chunks) {
+        for (int first = r;;) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (first + u * wide >= rows) continue;
+                if (chunk < turned) {
+                    float c[W], s[W];
+                    if constexpr (INTERLEAVED && W > 1) {
+                        // half of the pairs in each access
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            load_pairs<W / 2>(cs[0] + pairs[u] + h * (a.half / 2), c + h * (W / 2));
+                            load_pairs<W / 2>(cs[1] + pairs[u] + h * (a.half / 2), s + h * (W / 2));
+                        }
+                    } else {
+                        load_pairs<W>(cs[0] + pairs[u], c);
+                        load_pairs<W>(cs[1] + pairs[u], s);
+                    }
+                    turn<T, W, INTERLEAVED>(p[u], q[u], c, s);
+                    *reinterpret_cast<V*>(to[u] + next) = q[u].v;
+                }
+                *reinterpret_cast<V*>(to[u]) = p[u].v;
+            }
+            r += kBatch * wide;
+            first = r;
+            if (r >= rows) break;
+            load();
         }
-        const int at = INTERLEAVED ? 2 * chunk * W : chunk * W, next = INTERLEAVED ? W : a.half;
-        Pack<T, W> p, q;
-        p.v = *reinterpret_cast<const V*>(src + at);
-        q.v = *reinterpret_cast<const V*>(src + at + next);
-        const float* c = cs[0] + t * a.half + chunk * W;
-        const float* s = cs[1] + t * a.half + chunk * W;
-        if constexpr (!INTERLEAVED) {
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                const float u = T::to_f32(p.e[j]), v = T::to_f32(q.e[j]);
-                p.e[j] = T::from_f32(u * c[j] - v * s[j]);
-                q.e[j] = T::from_f32(v * c[j] + u * s[j]);
-            }
-        } else {
-            S e[2 * W];
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                e[j] = p.e[j];
-                e[W + j] = q.e[j];
-            }
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                const float u = T::to_f32(e[2 * j]), v = T::to_f32(e[2 * j + 1]);
-                e[2 * j] = T::from_f32(u * c[j] - v * s[j]);
-                e[2 * j + 1] = T::from_f32(v * c[j] + u * s[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                p.e[j] = e[j];
-                q.e[j] = e[W + j];
-            }
-        }
-        *reinterpret_cast<V*>(dst + at) = p.v;
-        *reinterpret_cast<V*>(dst + at + next) = q.v;
+        if (chunks <= kThreads) break;
+        chunk += kThreads;   // (heads of more chunks than a block has threads)
+        r = 0;
+        if (chunk < chunks) load();
     }
 }
 
@@ -170,30 +258,38 @@ int width(const RopeArgs& a) {
     return 1;
 }
 
-template <typename T>
-cudaError_t rope_typed(RopeArgs a, bool interleaved, cudaStream_t s) {
-    const int w = width<T>(a);
+template <typename T, int W, bool INTERLEAVED>
+cudaError_t rope_launch(RopeArgs a, cudaStream_t s) {
+    // Many tokens: two rows a thread at a time, twice a block; but enough
+    // blocks to go round. In us, (rows, times) (1, 4), (2, 1), (2, 2): 20011 tokens
+    // of 40 heads of 128, bf16, 66, 87, 63; 4099 of 32 of 80, f32, 18, -, 17.
+    constexpr int kMany = 2, kTimes = 2;
     const int64_t heads = a.heads[0] + a.heads[1];
-    const int64_t per_token = heads * (a.half / w);   // items
-    // About four items a thread; while that leaves SMs idle, fewer tokens a
-    // block, then a token's heads on several blocks (which compute the same sines)
+    const int64_t per_token = heads * (a.half / W + (a.pass ? (a.d - 2 * a.half) / W : 0));   // chunks
     const int64_t sms = num_sms();
-    int64_t per = std::max<int64_t>(1, std::min<int64_t>(4 * kThreads / std::max<int64_t>(1, per_token), kMaxPairs / a.half));
-    per = std::max<int64_t>(1, std::min(per, a.tokens / (4 * sms)));
-    int64_t split = 1;
-    while (per == 1 && a.tokens * split < 2 * sms && per_token / split > kThreads && split * 2 <= heads) split *= 2;
+    int64_t per = 1, split = 1;
+    const bool many = a.tokens * per_token > 4 * sms * kThreads;
+    if (many)
+        per = std::max<int64_t>(1, std::min<int64_t>({kTimes * kMany * kThreads / per_token, kMaxPairs / a.half, a.tokens / (6 * sms)}));
+    else   // while SMs are idle, a token's heads go to several blocks, which compute the same sines
+        while (a.tokens * split < 2 * sms && per_token / split > kThreads && split * 2 <= heads) split *= 2;
     a.per_block = (int)per;
     a.head_split = (int)split;
     const int64_t blocks = (a.tokens + per - 1) / per * split;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    const dim3 grid((unsigned)blocks), block(kThreads);
-    if constexpr (T::kBytes == 2)
-        if (w == 8)
-            return launch_pdl(interleaved ? rope_kernel<T, 8, true> : rope_kernel<T, 8, false>, grid, block, 0, s, a);
-    switch (w) {
-    case 4: return launch_pdl(interleaved ? rope_kernel<T, 4, true> : rope_kernel<T, 4, false>, grid, block, 0, s, a);
-    case 2: return launch_pdl(interleaved ? rope_kernel<T, 2, true> : rope_kernel<T, 2, false>, grid, block, 0, s, a);
-    default: return launch_pdl(interleaved ? rope_kernel<T, 1, true> : rope_kernel<T, 1, false>, grid, block, 0, s, a);
+    return launch_pdl(many ? rope_kernel<T, W, INTERLEAVED, kMany> : rope_kernel<T, W, INTERLEAVED, 1>, dim3((unsigned)blocks),
+                      dim3(kThreads), 0, s, a);
+}
+
+template <typename T>
+cudaError_t rope_typed(const RopeArgs& a, bool interleaved, cudaStream_t s) {
+    switch (width<T>(a)) {
+    case 8:
+        if constexpr (T::kBytes == 2) return interleaved ? rope_launch<T, 8, true>(a, s) : rope_launch<T, 8, false>(a, s);
+        return cudaErrorInvalidValue;
+    case 4: return interleaved ? rope_launch<T, 4, true>(a, s) : rope_launch<T, 4, false>(a, s);
+    case 2: return interleaved ? rope_launch<T, 2, true>(a, s) : rope_launch<T, 2, false>(a, s);
+    default: return interleaved ? rope_launch<T, 1, true>(a, s) : rope_launch<T, 1, false>(a, s);
     }
 }
 
