@@ -561,29 +561,37 @@ static int clusters_at_once(int dev, int split) {
     return known[dev][split] = n;
 }
 
-// The split that should end first, and when, in units of 10 ns: 3 us for a start
-// and an end; 0.4 us (128 tokens: 0.52) a block of K of a CTA that has an SM to
-// itself, 0.56 us where two share one, and 1.3 us since the next call's CTAs then
-// find no room to load their weights early; or HBM at 6.2 TB/s. Measured in us,
-// split 1, 2, 3, 4, 6, 8:
+// The split that should end first, and when, in ns: a start and an end, which
+// grow with the tokens; a block of K of a CTA that has an SM to itself, 1.4 times
+// that where two share one, and 1.3 us more since the next call's CTAs then find
+// no room to load their weights early; or HBM at 6.2 TB/s. Measured in us, split
+// 1, 2, 3, 4, 6, 8 (16, 64, 16, 64, 64, 16 tokens at once):
 //   1 x 4096 x 4096     10.2   7.0   5.5   5.4   6.3   6.8
 //   64 x 2048 x 2048     9.0   6.9   6.0   5.2   4.8   6.4
 //   16 x 14336 x 5120   16.2  16.0  16.2  16.0  17.3  19.9
 //   33 x 5120 x 14336   42.7  24.6  18.7  20.3  16.9  21.0
 //   56 x 5120 x 17408   51.6  29.6  22.9  23.6  19.9  24.6
 //   16 x 256 x 16384    33.9  18.2  13.0  10.2   7.7   6.4
+// and 16, 32, 64, 128 tokens at once:
+//   128 x 361 x 256      2.7   3.3   4.3   6.5
+//   64 x 1024 x 1024     3.2   3.4   4.1   4.5
+//   40 x 4096 x 4096    10.3   8.2   7.3   8.0
+//   2000 x 300 x 512     6.8   5.2   4.9   7.5
 template <typename T, int MT>
 static int64_t few_plan(const Fp8MmLaunch& L, int* split) {
     using C = Few<MT>;
+    constexpr int64_t kBlockNs = MT == 16 ? 250 : MT == 32 ? 300 : MT == 64 ? 390 : 460;
     const int64_t clusters = (L.N + kTile - 1) / kTile * ((L.M + MT - 1) / MT);
-    const int64_t blocks = (L.K + kBlock - 1) / kBlock, hbm = L.N * L.K / 62000;
+    const int64_t blocks = (L.K + kBlock - 1) / kBlock, hbm = L.N * L.K / 6200;
+    const int64_t ends = 2300 + 25 * std::min<int64_t>(L.M, MT);
     int64_t best = -1;
     for (int n : kSplits) {
         if (n > blocks) break;
         const int64_t alone = clusters_at_once<T, MT>(L.device, n), each = (blocks + n - 1) / n;
-        const int64_t rounds = (clusters + alone * C::kPerSm - 1) / (alone * C::kPerSm);
-        const int64_t cost = clusters <= alone ? 300 + std::max((MT == 128 ? 52 : 40) * each, hbm)
-                                               : 430 * rounds + std::max((MT == 128 ? 52 : 56) * each * rounds, hbm);
+        const int64_t at_once = alone * C::kPerSm, rounds = (clusters + at_once - 1) / at_once;
+        const int64_t cost = clusters <= alone
+                                 ? ends + std::max(kBlockNs * each, hbm)
+                                 : (ends + 1300) * rounds + std::max(kBlockNs * (C::kPerSm > 1 ? 14 : 10) / 10 * each * rounds, hbm);
         if (best < 0 || cost < best) {
             best = cost;
             *split = n;
@@ -593,15 +601,13 @@ static int64_t few_plan(const Fp8MmLaunch& L, int* split) {
 }
 
 template <typename T, int MT>
-static cudaError_t few_launch(const Fp8MmLaunch& L, cudaStream_t s) {
+static cudaError_t few_launch(const Fp8MmLaunch& L, int split, cudaStream_t s) {
     using C = Few<MT>;
     CUtensorMap w_map, x_map;
     if (!make_map(&w_map, L.w, L.N, L.K, kTile) || !make_map(&x_map, L.x, L.M, L.K, MT)) return cudaErrorInvalidValue;
     static bool done[64];
     cudaError_t e = allow_smem_once(few_kernel<T, MT>, C::kSmem, done, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
-    int split = 1;
-    few_plan<T, MT>(L, &split);
     const int64_t tiles = (L.N + kTile - 1) / kTile, chunks = (L.M + MT - 1) / MT;
     if (tiles * chunks * split > 0x7fffffff) return cudaErrorInvalidConfiguration;
     const FewArgs a{L.w_scales, L.x_scales, L.out, L.M, L.N, (int)((L.K + kBlock - 1) / kBlock), (int)chunks, split,
@@ -711,6 +717,12 @@ __device__ __forceinline__ void arrive_at(uint32_t cluster_bar) {
 template <int NT>
 __device__ __forceinline__ int column(int half, int c) {
     return c / (NT / 4) * (NT / 2) + half * (NT / 4) + c % (NT / 4);
+}
+
+// place of byte `b` of row r in a box of stored rows
+template <int kBytes>
+__device__ __forceinline__ uint32_t boxed(int r, int b) {
+    return r * kBytes + (kBytes == 128 ? ((b >> 4 ^ (r & 7)) << 4 | (b & 15)) : b);
 }
 
 __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, int x, int y) {
@@ -948,42 +960,48 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
             if (!ok) break;
             const int64_t m0 = (int64_t)tm * kPairRows + rank * kTile + (warp & 3) * 32;
             if (m0 >= a.M) continue;
-            if (a.aligned) {
-                // 128 (96) bytes of the warp's rows at a time through shared memory;
-                // what lies beyond the matrix is cut off by the store. Rows of 128
-                // bytes are swizzled, those of 96 spread over the banks as they are.
-                constexpr int kEach = C::kOutBytes / T::kBytes;
+            // 128 (96) bytes of the warp's rows at a time through shared memory: by
+            // a TMA store, which cuts off what lies beyond the matrix, or where rows
+            // are not aligned for that, row after row. Rows of 128 bytes are
+            // swizzled, those of 96 spread over the banks as they are.
+            constexpr int kEach = C::kOutBytes / T::kBytes;
+            const int rows = (int)min((int64_t)32, a.M - m0);
 #pragma unroll
-                for (int c = 0; c < C::kCols; c += kEach) {
-                    const int64_t n = (int64_t)tn * NT + column<NT>(half, c);
-                    if (n >= a.N) continue;
-                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                    __syncwarp();
+            for (int c = 0; c < C::kCols; c += kEach) {
+                const int64_t n = (int64_t)tn * NT + column<NT>(half, c);
+                if (n >= a.N) continue;
+                if (a.aligned && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < C::kOutBytes / 16; ++i) {
-                        uint32_t w[4];
+                for (int i = 0; i < C::kOutBytes / 16; ++i) {
+                    uint32_t w[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if constexpr (T::kBytes == 4)
-                                w[j] = __float_as_uint(sum[c + 4 * i + j]);
-                            else
-                                w[j] = pack16<T>(sum[c + 8 * i + 2 * j], sum[c + 8 * i + 2 * j + 1]);
-                        }
-                        const int piece = C::kOutBytes == 128 ? i ^ (lane & 7) : i;
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + lane * C::kOutBytes + (piece << 4)),
-                                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                                     : "memory");
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (T::kBytes == 4)
+                            w[j] = __float_as_uint(sum[c + 4 * i + j]);
+                        else
+                            w[j] = pack16<T>(sum[c + 8 * i + 2 * j], sum[c + 8 * i + 2 * j + 1]);
                     }
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(box + boxed<C::kOutBytes>(lane, 16 * i)),
+                                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                 : "memory");
+                }
+                if (a.aligned) {
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) store_box(&out_map, box, (int)n, (int)m0);
+                    continue;
                 }
-            } else if (m0 + lane < a.M) {
+                __syncwarp();
+                const uint8_t* from = ring + C::kStages * C::kStage + (warp - 4) * kOutBox;
+                const int cols = (int)min((int64_t)kEach, a.N - n);
+                S* out = static_cast<S*>(a.out) + m0 * a.N + n;
+#pragma unroll 4
+                for (int r = 0; r < rows; ++r, out += a.N)
 #pragma unroll
-                for (int c = 0; c < C::kCols; ++c) {
-                    const int64_t n = (int64_t)tn * NT + column<NT>(half, c);
-                    if (n < a.N) static_cast<S*>(a.out)[(m0 + lane) * a.N + n] = T::from_f32(sum[c]);
-                }
+                    for (int e = 0; e < kEach; e += 32)
+                        if (e + lane < cols)
+                            out[e + lane] = *reinterpret_cast<const S*>(from + boxed<C::kOutBytes>(r, (e + lane) * T::kBytes));
             }
         }
         __syncwarp();
@@ -1030,25 +1048,40 @@ static cudaError_t many_launch(const Fp8MmLaunch& L, cudaStream_t s) {
     return launch_cluster(many_kernel<T, NT>, 2 * (unsigned)pairs, kPairThreads, C::kSmem, 2, s, w_map, x_map, out_map, a);
 }
 
-// The pairs take 3.5 us and 0.455 us a block of K and round of tiles with 256
+// The pairs take 5.5 us and 0.455 us a block of K and round of tiles with 256
 // weight rows, 0.42 us with 192 (8192 x 14336 x 5120: 24 rounds in 437 us, 32 in
-// 539; 1111 x 5000 x 14416: 2 rounds in 110, 2 in 101). They are taken from 65
-// tokens on where that is less than few_plan's time for 128 at once; few / many
-// in us: 128 x 4096 x 4096 10.3 / 17.8, 256 x 4096 x 4096 14.0 / 18.0, 512 x 4096
-// x 4096 19.8 / 18.3, 256 x 14336 x 5120 48 / 24, 512 x 1024 x 8192 13.5 / 31.
+// 539; 1111 x 5000 x 14416: 2 rounds in 110, 2 in 101). Whatever should end
+// first is taken; few / many in us: 128 x 4096 x 4096 10.3 / 17.8, 256 x 4096 x
+// 4096 14.0 / 18.0, 512 x 4096 x 4096 19.8 / 18.3, 256 x 14336 x 5120 48 / 24,
+// 512 x 1024 x 8192 13.5 / 31.
 template <typename T>
 static cudaError_t typed(const Fp8MmLaunch& L, cudaStream_t s) {
-    if (L.M <= 16) return few_launch<T, 16>(L, s);
-    if (L.M <= 32) return few_launch<T, 32>(L, s);
-    if (L.M <= 64) return few_launch<T, 64>(L, s);
-    const int64_t tm = (L.M + kPairRows - 1) / kPairRows, pairs = num_sms() / 2, blocks = (L.K + kBlock - 1) / kBlock;
-    const auto cost = [&](int nt, int64_t each) {
-        return 3500 + (tm * ((L.N + nt - 1) / nt) + pairs - 1) / pairs * blocks * each;   // ns
+    int split[4] = {1, 1, 1, 1};
+    int64_t least = few_plan<T, 16>(L, &split[0]);
+    int choice = 0;
+    const auto offer = [&](int c, int64_t cost) {
+        if (cost < least) {
+            least = cost;
+            choice = c;
+        }
     };
-    const int64_t wide = cost(256, 455), narrow = cost(192, 420);
-    int split;
-    if (10 * few_plan<T, 128>(L, &split) <= std::min(wide, narrow)) return few_launch<T, 128>(L, s);
-    return narrow < wide ? many_launch<T, 192>(L, s) : many_launch<T, 256>(L, s);
+    if (L.M > 16) offer(1, few_plan<T, 32>(L, &split[1]));
+    if (L.M > 32) offer(2, few_plan<T, 64>(L, &split[2]));
+    if (L.M > 64) {
+        offer(3, few_plan<T, 128>(L, &split[3]));
+        const int64_t tm = (L.M + kPairRows - 1) / kPairRows, pairs = num_sms() / 2, blocks = (L.K + kBlock - 1) / kBlock;
+        const auto rounds = [&](int nt) { return (tm * ((L.N + nt - 1) / nt) + pairs - 1) / pairs; };
+        offer(4, 5500 + 420 * blocks * rounds(192));
+        offer(5, 5500 + 455 * blocks * rounds(256));
+    }
+    switch (choice) {
+    case 0: return few_launch<T, 16>(L, split[0], s);
+    case 1: return few_launch<T, 32>(L, split[1], s);
+    case 2: return few_launch<T, 64>(L, split[2], s);
+    case 3: return few_launch<T, 128>(L, split[3], s);
+    case 4: return many_launch<T, 192>(L, s);
+    default: return many_launch<T, 256>(L, s);
+    }
 }
 
 }  // namespace fp8mm
