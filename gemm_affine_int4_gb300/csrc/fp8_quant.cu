@@ -15,9 +15,8 @@ using namespace fp8;
 
 constexpr int kThreads = 256;
 
-// 16 lanes hold a group, 8 elements each. A thread takes kUnits such eights, a
-// block's width apart, all of them loaded before the first is used. `units`:
-// eights of a row, rounded up to whole groups.
+// A thread takes kUnits eights, a block's width apart, all of them loaded before
+// the first is used. `units`: eights of a row, rounded up to whole groups.
 template <typename T, bool VEC, int kUnits>
 __global__ void __launch_bounds__(kThreads) quantize_x_fp8_kernel(const typename T::storage* __restrict__ x,
                                                                   int64_t x_stride, uint8_t* __restrict__ codes,
@@ -33,7 +32,7 @@ __global__ void __launch_bounds__(kThreads) quantize_x_fp8_kernel(const typename
     for (int j = 0; j < kUnits; ++j) {
         const int64_t u = first + j * kThreads;
         row[j] = u < 0x7fffffff ? (int64_t)((uint32_t)u / (uint32_t)units) : u / units;
-        col[j] = (u - row[j] * units) * 8;
+        col[j] = column_of<VEC>((int)(u - row[j] * units));
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
         if (u < total && col[j] < cols) load8<T, VEC>(x + row[j] * x_stride + col[j], cols - col[j], v[j]);
@@ -47,8 +46,8 @@ __global__ void __launch_bounds__(kThreads) quantize_x_fp8_kernel(const typename
     }
 }
 
-// One block of 128 x 128 a CTA: thread t holds columns 8 (t % 16) on of the
-// rows t / 16 + 16 j, in registers from the maximum to the codes.
+// One block of 128 x 128 a CTA: thread t holds eights t % 16 of the rows
+// t / 16 + 16 j, in registers from the maximum to the codes.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(const typename T::storage* __restrict__ w,
                                                                 uint8_t* __restrict__ codes,
@@ -56,7 +55,7 @@ __global__ void __launch_bounds__(kThreads) quantize_fp8_kernel(const typename T
     // no programmatic launch: what this kernel writes may be read as weights
     pdl_wait();
     __shared__ float part[kThreads / 32];
-    const int64_t k = (int64_t)blockIdx.x * kGroup + (threadIdx.x & 15) * 8;
+    const int64_t k = (int64_t)blockIdx.x * kGroup + column_of<VEC>(threadIdx.x & 15);
     const int64_t n0 = (int64_t)blockIdx.y * kGroup + (threadIdx.x >> 4);
     float v[8][8];
 #pragma unroll

@@ -68,9 +68,17 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], const Scale& s) {
 }
 
 // ---------------------------------------------------------------------------
-// 8 consecutive elements of a row: 16-byte accesses, or one by one with the
-// row's end at `left` elements (VEC false)
+// A thread's eight elements of a group of 128 that 16 threads hold. VEC: eight
+// neighbours, in 16-byte accesses. Otherwise every 16th, so that the single
+// accesses of the threads lie side by side. `left`: from the first of them to the
+// row's end.
 // ---------------------------------------------------------------------------
+template <bool VEC>
+__device__ __forceinline__ int column_of(int thread) {   // thread of the row
+    return VEC ? thread * 8 : (thread >> 4) * kGroup + (thread & 15);
+}
+constexpr int kApart = 16;
+
 template <typename T, bool VEC>
 struct Eight {
     // as loaded: 16 bytes of 16-bit elements, or values
@@ -87,7 +95,7 @@ struct Eight {
             v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i < left ? T::to_f32(p[i]) : 0.f;
+            for (int i = 0; i < 8; ++i) v[i] = kApart * i < left ? T::to_f32(p[kApart * i]) : 0.f;
         }
     }
     __device__ __forceinline__ void zero() {
@@ -135,7 +143,7 @@ __device__ __forceinline__ void store8(typename T::storage* p, int64_t left, con
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < left) p[i] = T::from_f32(v[i]);
+            if (kApart * i < left) p[kApart * i] = T::from_f32(v[i]);
     }
 }
 
@@ -146,7 +154,7 @@ __device__ __forceinline__ void store_codes8(uint8_t* p, int64_t left, uint2 c) 
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < left) p[i] = (uint8_t)((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
+            if (kApart * i < left) p[kApart * i] = (uint8_t)((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
     }
 }
 

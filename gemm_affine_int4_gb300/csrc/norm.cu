@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kUnits == 4 ? 512 : 1024) rms_norm_kernel(cons
     __shared__ float part[2][16][kMaxWarps];
     Inputs<T, VEC> in[kUnits];
     Eight<T, VEC> gain[kUnits];
-    const int col0 = threadIdx.x * 8, step = blockDim.x * 8;
+    const int col0 = column_of<VEC>(threadIdx.x), step = blockDim.x * 8;
     int64_t first = (int64_t)blockIdx.x * blockDim.y;   // row of the block's first threads
 #pragma unroll
     for (int j = 0; j < kUnits; ++j) in[j].load(a, first + threadIdx.y, col0 + j * step);
@@ -185,14 +185,14 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const __grid_consta
     Inputs<T, VEC> in;
     Eight<T, VEC> gain;
     float p[8], amax = 0.f, s = 0.f;
-    for (int64_t col = (int64_t)threadIdx.x * 8; col < a.cols; col += (int64_t)blockDim.x * 8) {
+    for (int64_t col = column_of<VEC>(threadIdx.x); col < a.cols; col += (int64_t)blockDim.x * 8) {
         in.load(a, row, col);
         load_gain<T, VEC>(a, col, gain);
         s += begin8<T, VEC>(a, in, gain, row, col, false, p, amax);
     }
     const float inv = inverse_root(row_sum(s, part), a);
     for (int64_t at = 0; at < a.cols; at += (int64_t)blockDim.x * 8) {
-        const int64_t col = at + (int64_t)threadIdx.x * 8;
+        const int64_t col = at + column_of<VEC>(threadIdx.x);
         in.load(a, row, col);
         load_gain<T, VEC>(a, col, gain);
         begin8<T, VEC>(a, in, gain, row, col, true, p, amax);

@@ -105,7 +105,8 @@ def test_rope_keeps_infinities_and_nan_to_their_pairs():
 # ---------------------------------------------------------------- norm
 
 SHAPES = [(1, 1), (1, 4096), (3, 7), (64, 4096), (5, 8200), (700, 128), (701, 129), (1000, 5120), (33, 1000), (2, 32768),
-          (3, 32776), (2, 100001), (400, 17), (350, 12288)]
+          (3, 32776), (2, 100001), (400, 17), (350, 12288), (5000, 100),
+          (1003, 16384), (320, 16392), (900, 511)]
 
 
 def check_codes(codes, scales, y, rel):
@@ -152,7 +153,9 @@ def test_norm_strided_rows_in_place_and_without_gain():
             a, b = x.clone(), r.clone()
             again = g4.gai4_rms_norm(a, eps=0.0, residual=b, out=a, residual_out=b)
             assert again.out is a and again.residual is b
-            assert torch.equal(a, got.out) and torch.equal(b, got.residual)
+            # (rows of another alignment may be summed in another order)
+            within(a, y, y.abs() * (rel + U[dt]) + TINY[dt], f"in place {cols} {off}")
+            assert torch.equal(b, got.residual)
 
 
 def test_norm_rows_of_zeros_and_of_no_numbers():
@@ -174,7 +177,7 @@ def test_norm_rows_of_zeros_and_of_no_numbers():
 
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 16), (7, 130), (33, 14336), (129, 128), (300, 1000), (2000, 2056),
-                                       (128, 8), (127, 4097)])
+                                       (128, 8), (127, 4097), (1500, 1001), (3000, 24)])
 def test_quantize(dt, rows, cols):
     x = rand(rows, cols, seed=3, dtype=T[dt]) * 2 ** torch.randint(-3, 4, (rows, 1), device="cuda").to(T[dt])
     for fn, block in ((g4.gai4_quantize_x_fp8, 1), (g4.gai4_quantize_fp8, 128)):
@@ -241,7 +244,8 @@ def problem(M, N, K, seed=0):
 @pytest.mark.parametrize("M,N,K", [
     (1, 1, 16), (1, 4096, 4096), (2, 129, 272), (15, 1000, 2048), (16, 128, 128), (17, 640, 1040), (32, 5120, 896),
     (33, 300, 5136), (56, 2048, 2048), (64, 512, 14336), (65, 200, 384), (100, 1111, 1616), (128, 256, 256),
-    (129, 257, 144), (200, 700, 3088), (300, 1024, 2064), (513, 384, 640), (1111, 500, 1424), (2048, 1024, 512)])
+    (129, 257, 144), (200, 700, 3088), (300, 1024, 2064), (513, 384, 640), (1111, 500, 1424), (2048, 1024, 512),
+    (1500, 1600, 512), (1500, 1601, 528), (1537, 1540, 144), (2304, 2048, 384), (2300, 2041, 272), (700, 5000, 2064)])
 def test_mm(dt, M, N, K):
     p = problem(M, N, K)
     out = g4.gai4_fp8_mm_t(*p, dtype=T[dt])
@@ -251,33 +255,33 @@ def test_mm(dt, M, N, K):
     assert torch.equal(out, g4.gai4_fp8_mm_t(*p, dtype=T[dt]))       # bit for bit
 
 
-@pytest.mark.parametrize("M", [1, 40, 128, 400])
-def test_mm_every_block_has_its_scales(M):
+@pytest.mark.parametrize("M,N", [(1, 400), (40, 400), (128, 400), (400, 400), (1500, 1700), (2304, 2048)])
+def test_mm_every_block_has_its_scales(M, N):
     """Scales that differ by powers of two from block to block, of rows and of columns: a wrong one is out by half."""
-    N, K = 400, 1200
+    K = 1200
     g = torch.Generator(device="cuda").manual_seed(9)
     wc, _, xc, _ = problem(M, N, K)
-    ws = 2.0 ** torch.randint(-6, 7, (4, 10), generator=g, device="cuda")
+    ws = 2.0 ** torch.randint(-6, 7, (-(-N // 128), 10), generator=g, device="cuda")
     xs = 2.0 ** torch.randint(-6, 7, (M, 10), generator=g, device="cuda")
     out = g4.gai4_fp8_mm_t(wc, ws, xc, xs, dtype=torch.float32)
     within(out, *mm64(wc, ws, xc, xs, torch.float32), "scales")
 
 
-@pytest.mark.parametrize("M", [3, 50, 120, 700])
-def test_mm_exact_small_integers(M):
+@pytest.mark.parametrize("M,N", [(3, 300), (50, 300), (120, 300), (700, 300), (1500, 1700), (2304, 2048)])
+def test_mm_exact_small_integers(M, N):
     """Codes of small integers and scales of one: every sum is a whole number, exactly."""
-    N, K = 300, 1136
+    K = 1136
     g = torch.Generator(device="cuda").manual_seed(4)
     x = torch.randint(-8, 9, (M, K), generator=g, device="cuda").float()
     w = torch.randint(-8, 9, (N, K), generator=g, device="cuda").float()
     ones = lambda r: torch.ones(r, 9, device="cuda")  # noqa: E731
-    out = g4.gai4_fp8_mm_t(w.to(E4M3), ones(3), x.to(E4M3), ones(M), dtype=torch.float32)
+    out = g4.gai4_fp8_mm_t(w.to(E4M3), ones(-(-N // 128)), x.to(E4M3), ones(M), dtype=torch.float32)
     assert torch.equal(out.double(), x.double() @ w.double().t())
 
 
-@pytest.mark.parametrize("M", [5, 300])
-def test_mm_not_a_number_stays_in_its_row_and_column(M):
-    N, K = 200, 512
+@pytest.mark.parametrize("M,N", [(5, 200), (300, 200), (1500, 1700), (2304, 2048)])
+def test_mm_not_a_number_stays_in_its_row_and_column(M, N):
+    K = 512
     wc, ws, xc, xs = problem(M, N, K)
     clean = g4.gai4_fp8_mm_t(wc, ws, xc, xs)
     wc.view(torch.uint8)[7, 300] = 0x7F
@@ -288,9 +292,9 @@ def test_mm_not_a_number_stays_in_its_row_and_column(M):
     assert torch.equal(out.isnan(), bad) and torch.equal(out[~bad], clean[~bad])
 
 
-@pytest.mark.parametrize("M", [1, 60, 128, 333])
-def test_mm_writes_its_rows_only(M):
-    N, K = 333, 256
+@pytest.mark.parametrize("M,N", [(1, 333), (60, 333), (128, 336), (333, 333), (1500, 1701), (1500, 1704), (2300, 2048)])
+def test_mm_writes_its_rows_only(M, N):
+    K = 256
     p = problem(M, N, K)
     room = torch.full((M + 2, N), 7.0, dtype=torch.bfloat16, device="cuda")
     g4.gai4_fp8_mm_t(*p, out=room[1:M + 1])
@@ -388,7 +392,7 @@ def test_a_layer_on_a_stream_and_in_a_graph():
 
 def test_two_streams_at_once():
     """Products of both kernels side by side: neither waits for the other's tensor memory for good."""
-    small, large = problem(9, 2000, 4096), problem(600, 1500, 2048, seed=7)
+    small, large = problem(9, 2000, 4096), problem(1500, 1700, 2048, seed=7)
     want = [g4.gai4_fp8_mm_t(*p) for p in (small, large)]
     streams = [torch.cuda.Stream() for _ in range(2)]
     torch.cuda.synchronize()
