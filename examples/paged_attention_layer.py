@@ -48,7 +48,7 @@ class Layer:
         plan = g4.gai4_kv_plan(self.lens, q_lens, self.table, self.free, self.free_count, PAGE, x.shape[0])
         qkv = self._project(self.w_qkv, x).view(x.shape[0], Q_HEADS + 2 * KV_HEADS, HEAD)
         q, k, v = qkv.split([Q_HEADS, KV_HEADS, KV_HEADS], 1)      # strided views: no copies
-        # (positions for rotary embeddings of q and k would be plan.positions)
+        # (for rotary positions, gai4_rope takes plan.positions here: fp8_decoder_layer.py)
         g4.gai4_kv_append(k, v, plan.slots, self.k_cache, self.v_cache, group_size=GROUP)
         o = g4.gai4_kv_attention(q, self.k_cache, self.v_cache, self.table, plan.kv_lens, plan.cu_q, group_size=GROUP,
                                  max_q_len=max_q_len, workspace=self.workspace)

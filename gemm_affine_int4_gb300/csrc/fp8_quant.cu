@@ -4,6 +4,8 @@
 // scale for each block of 128 rows x 128 columns. Both read every value once
 // and write a byte for it: bound by HBM (16-bit inputs 3 bytes a value, binary32
 // 5), for a few rows by the launch.
+#include <algorithm>
+
 #include "fp8_quant.cuh"
 #include "internal.h"
 
@@ -15,34 +17,38 @@ using namespace fp8;
 
 constexpr int kThreads = 256;
 
-// A thread takes kUnits eights, a block's width apart, all of them loaded before
-// the first is used. `units`: eights of a row, rounded up to whole groups.
-template <typename T, bool VEC, int kUnits>
+// A block takes blockDim.x eights of kRows * blockDim.y rows, a thread one eight
+// of kRows of them, all loaded before the first is used; `across` blocks take a
+// row.
+template <typename T, bool VEC, int kRows>
 __global__ void __launch_bounds__(kThreads) quantize_x_fp8_kernel(const typename T::storage* __restrict__ x,
                                                                   int64_t x_stride, uint8_t* __restrict__ codes,
                                                                   float* __restrict__ scales, int64_t rows,
-                                                                  int64_t cols, int64_t units) {
+                                                                  int64_t cols, unsigned across) {
     pdl_launch_dependents();
     pdl_wait();   // the kernels before this one are complete: global memory may be read
-    const int64_t total = rows * units;
-    const int64_t first = (int64_t)blockIdx.x * (kThreads * kUnits) + threadIdx.x;
-    float v[kUnits][8];
-    int64_t row[kUnits], col[kUnits];
+    const unsigned down = blockIdx.x / across;
+    const int64_t col = (int64_t)(blockIdx.x - down * across) * blockDim.x * 8 + column_of<VEC>(threadIdx.x);
+    const int64_t row = (int64_t)down * blockDim.y * kRows + threadIdx.y;
+    Eight<T, VEC> in[kRows];
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-        const int64_t u = first + j * kThreads;
-        row[j] = u < 0x7fffffff ? (int64_t)((uint32_t)u / (uint32_t)units) : u / units;
-        col[j] = column_of<VEC>((int)(u - row[j] * units));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
-        if (u < total && col[j] < cols) load8<T, VEC>(x + row[j] * x_stride + col[j], cols - col[j], v[j]);
+    for (int j = 0; j < kRows; ++j) {
+        const int64_t r = row + j * blockDim.y;
+        if (r < rows && col < cols)
+            in[j].load(x + r * x_stride + col, cols - col);
+        else
+            in[j].zero();
     }
+    const int64_t blocks = (cols + kGroup - 1) / kGroup;
 #pragma unroll
-    for (int j = 0; j < kUnits; ++j) {
-        const Scale s = scale_of(group_max(amax8(v[j])));
-        if (first + j * kThreads >= total) continue;
-        if (col[j] < cols) store_codes8<VEC>(codes + row[j] * cols + col[j], cols - col[j], codes8(v[j], s));
-        if ((threadIdx.x & 15) == 0) scales[row[j] * (units / 16) + col[j] / kGroup] = scale_value(s);
+    for (int j = 0; j < kRows; ++j) {
+        const int64_t r = row + j * blockDim.y;
+        float v[8];
+        in[j].values(v);
+        const Scale s = scale_of(group_max(amax8(v)));
+        if (r >= rows || col >= cols) continue;
+        store_codes8<VEC>(codes + r * cols + col, cols - col, codes8(v, s));
+        if ((threadIdx.x & 15) == 0) scales[r * blocks + col / kGroup] = scale_value(s);
     }
 }
 
@@ -88,18 +94,17 @@ template <typename T>
 cudaError_t x_launch(const void* x, int64_t x_stride, uint8_t* codes, float* scales, int64_t rows, int64_t cols,
                      cudaStream_t s) {
     const auto* p = static_cast<const typename T::storage*>(x);
-    const int64_t units = (cols + kGroup - 1) / kGroup * 16, total = rows * units;
+    const int64_t eights = (cols + kGroup - 1) / kGroup * 16;
     const bool vec = vec_ok(x, x_stride, cols, T::kBytes, codes);
     // few values: one eight a thread, on as many SMs as there are
-    if (total <= (int64_t)num_sms() * 4 * kThreads) {
-        const dim3 grid((unsigned)((total + kThreads - 1) / kThreads));
-        return launch_pdl(vec ? quantize_x_fp8_kernel<T, true, 1> : quantize_x_fp8_kernel<T, false, 1>, grid,
-                          dim3(kThreads), 0, s, p, x_stride, codes, scales, rows, cols, units);
-    }
-    const int64_t blocks = (total + 4 * kThreads - 1) / (4 * kThreads);
-    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    return launch_pdl(vec ? quantize_x_fp8_kernel<T, true, 4> : quantize_x_fp8_kernel<T, false, 4>,
-                      dim3((unsigned)blocks), dim3(kThreads), 0, s, p, x_stride, codes, scales, rows, cols, units);
+    const bool few = rows * eights <= (int64_t)num_sms() * 4 * kThreads;
+    const int tx = (int)std::min<int64_t>(eights, 128), ty = tx % 32 ? kThreads / tx & ~1 : kThreads / tx;   // whole warps
+    const int64_t across = (eights + tx - 1) / tx, down = (rows + ty * (few ? 1 : 4) - 1) / (ty * (few ? 1 : 4));
+    if (across * down > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    auto* k = few ? (vec ? quantize_x_fp8_kernel<T, true, 1> : quantize_x_fp8_kernel<T, false, 1>)
+                  : (vec ? quantize_x_fp8_kernel<T, true, 4> : quantize_x_fp8_kernel<T, false, 4>);
+    return launch_pdl(k, dim3((unsigned)(across * down)), dim3(tx, ty), 0, s, p, x_stride, codes, scales, rows, cols,
+                      (unsigned)across);
 }
 
 template <typename T>

@@ -177,7 +177,8 @@ def test_norm_rows_of_zeros_and_of_no_numbers():
 
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 16), (7, 130), (33, 14336), (129, 128), (300, 1000), (2000, 2056),
-                                       (128, 8), (127, 4097), (1500, 1001), (3000, 24)])
+                                       (128, 8), (127, 4097), (1500, 1001), (3000, 24), (77, 300),
+                                       (2500, 384), (9000, 80)])
 def test_quantize(dt, rows, cols):
     x = rand(rows, cols, seed=3, dtype=T[dt]) * 2 ** torch.randint(-3, 4, (rows, 1), device="cuda").to(T[dt])
     for fn, block in ((g4.gai4_quantize_x_fp8, 1), (g4.gai4_quantize_fp8, 128)):
