@@ -19,7 +19,9 @@ uintptr_t elem_bytes(int dtype) { return dtype == GAI4_F32 ? 4 : 2; }
 gai4_status done(cudaError_t e) { return e == cudaSuccess ? GAI4_OK : GAI4_ERR_CUDA; }
 
 constexpr int64_t kMost = 0x7fffffff;
-constexpr int64_t kMostSize = 1ll << 40;   // elements or strides of a tensor: products stay in 64 bits
+
+// rows of `row` elements, `stride` apart: byte offsets stay in 64 bits
+bool strided(int64_t stride, int64_t row, int64_t rows) { return stride >= row && stride <= (1ll << 60) / rows; }
 
 // Whether rows that are written lie apart from rows that are read (or, for
 // rows of one width, in their very place).
@@ -90,8 +92,7 @@ gai4_status gai4_rope(const void* q, int64_t q_token_stride, void* q_out, int64_
     for (int i = 0; i < 2; ++i) {
         if (L.heads[i] == 0) continue;
         const int64_t row = (int64_t)L.heads[i] * head_dim;
-        if (!L.in[i] || !L.out[i] || L.in_stride[i] < row || L.out_stride[i] < row || L.in_stride[i] > kMostSize ||
-            L.out_stride[i] > kMostSize)
+        if (!L.in[i] || !L.out[i] || !strided(L.in_stride[i], row, num_tokens) || !strided(L.out_stride[i], row, num_tokens))
             return GAI4_ERR_INVALID_ARG;
         if (!aligned_to(L.in[i], e) || !aligned_to(L.out[i], e)) return GAI4_ERR_MISALIGNED;
     }
@@ -117,8 +118,7 @@ gai4_status gai4_rms_norm(const void* x, int64_t x_row_stride, const void* resid
         return GAI4_ERR_INVALID_ARG;
     if (rows == 0) return GAI4_OK;
     if (!x || (!out && !residual_out && !codes) || (codes == nullptr) != (scales == nullptr)) return GAI4_ERR_INVALID_ARG;
-    if (x_row_stride < cols || x_row_stride > kMostSize ||
-        (residual && (residual_row_stride < cols || residual_row_stride > kMostSize)))
+    if (!strided(x_row_stride, cols, rows) || (residual && !strided(residual_row_stride, cols, rows)))
         return GAI4_ERR_INVALID_ARG;
     const uintptr_t e = elem_bytes(dtype);
     for (const void* p : {x, residual, gain, (const void*)out, (const void*)residual_out})
@@ -136,9 +136,9 @@ gai4_status gai4_rms_norm(const void* x, int64_t x_row_stride, const void* resid
 gai4_status gai4_quantize_x_fp8(const void* x, int64_t x_row_stride, uint8_t* codes, float* scales, gai4_dtype dtype,
                                 int64_t M, int64_t K, void* stream) {
     if (!known(dtype)) return GAI4_ERR_UNSUPPORTED;
-    if (M < 0 || M > kMost || K < 1 || K > kMost || x_row_stride < K || x_row_stride > kMostSize)
-        return GAI4_ERR_INVALID_ARG;
+    if (M < 0 || M > kMost || K < 1 || K > kMost) return GAI4_ERR_INVALID_ARG;
     if (M == 0) return GAI4_OK;
+    if (!strided(x_row_stride, K, M)) return GAI4_ERR_INVALID_ARG;
     if (!x || !codes || !scales) return GAI4_ERR_INVALID_ARG;
     if (!aligned_to(x, elem_bytes(dtype)) || !aligned_to(scales, 4)) return GAI4_ERR_MISALIGNED;
     return done(launch_quantize_x_fp8(x, x_row_stride, codes, scales, dtype, M, K, (cudaStream_t)stream));

@@ -81,7 +81,7 @@ def rope(**c):
 
 @pytest.mark.parametrize("change,status", [
     (dict(q=None), 1), (dict(qo=None), 1), (dict(k=None), 1), (dict(ko=None), 1), (dict(pos=None), 1), (dict(f=None), 1),
-    (dict(qs=1023), 1), (dict(qos=0), 1), (dict(ks=255), 1), (dict(kos=-1), 1), (dict(qs=1 << 50), 1), (dict(n=-1), 1),
+    (dict(qs=1023), 1), (dict(qos=0), 1), (dict(ks=255), 1), (dict(kos=-1), 1), (dict(qs=1 << 59), 1), (dict(n=(1 << 31) - 1, qs=1 << 40), 1), (dict(n=-1), 1),
     (dict(n=1 << 31), 1), (dict(hq=0, hkv=0), 1), (dict(hq=-1), 1), (dict(hkv=1 << 20), 1), (dict(rot=0), 1),
     (dict(rot=63), 1), (dict(rot=130), 1), (dict(d=0), 1), (dict(d=2048, qs=1 << 20, qos=1 << 20), 2), (dict(dt=3), 2),
     (dict(q=P(0x100000001)), 3), (dict(dt=0, ko=P(0x400000002)), 3), (dict(pos=P(0x10002)), 3), (dict(f=P(0x10004)), 3),
@@ -105,14 +105,14 @@ def norm(**c):
     (dict(xs=511), 1), (dict(rs=1), 1), (dict(rows=-1), 1), (dict(rows=1 << 31), 1), (dict(cols=0), 1),
     (dict(cols=1 << 31), 1), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1),
     (dict(dt=9), 2), (dict(x=P(0x100000001)), 3), (dict(dt=0, g=P(0x300000002)), 3), (dict(scales=P(0x700000002)), 3),
-    (dict(out=D, ro=D), 1), (dict(out=P(0x100000000 + 64)), 1), (dict(ro=B, rs=600), 1), (dict(rows=0), 0),
+    (dict(rows=1 << 30, xs=1 << 31), 1), (dict(out=D, ro=D), 1), (dict(out=P(0x100000000 + 64)), 1), (dict(ro=B, rs=600), 1), (dict(rows=0), 0),
     (dict(rows=0, x=None), 0)])
 def test_norm_refusals(change, status):
     assert norm(**change) == status
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(x=None), 1), (dict(c=None), 1), (dict(s=None), 1), (dict(xs=255), 1), (dict(M=-1), 1), (dict(K=0), 1),
+    (dict(x=None), 1), (dict(c=None), 1), (dict(s=None), 1), (dict(xs=255), 1), (dict(xs=1 << 60), 1), (dict(M=-1), 1), (dict(K=0), 1),
     (dict(dt=-1), 2), (dict(x=P(0x100000001)), 3), (dict(s=P(0x10001)), 3), (dict(M=0), 0)])
 def test_quantize_x_refusals(change, status):
     a = dict(x=A, xs=256, c=B, s=C, dt=1, M=3, K=256)
