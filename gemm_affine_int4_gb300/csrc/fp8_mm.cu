@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
         }
     } else if (warp == 1) {
         give_registers<MT>();
+        pdl_wait();   // (before every first wait with a limit: a kernel ahead may run for long)
         const bool ready = warp_wait(&tmem_ready, 0, ctl);
         fence_after();
         const uint32_t tmem = tmem_slot, from = smem_u32(ring);
@@ -373,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
         if constexpr (MT == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int row = threadIdx.x & 127;
         const int64_t n = n0 + row;
+        pdl_wait();
         bool ok = warp_wait(&tmem_ready, 0, ctl);
         fence_after();
         const uint32_t lanes = tmem_slot + ((uint32_t)(warp & 3) << 21);
@@ -424,7 +426,6 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
         fence_before();
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&tmem_done);
-        pdl_wait();   // (every thread that writes outputs)
         if (a.split == 1) {
             if (n < a.N) {
 #pragma unroll
@@ -537,12 +538,34 @@ static bool make_out_map(CUtensorMap* map, const void* p, int64_t rows, int64_t 
                   bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+// Shared memory of a kernel that hands registers over, on the current device.
+// setmaxnreg.inc waits until it finds what it asks for, so the kernel must have
+// been launched with `regs` registers a thread (the shares add up to that).
+template <typename Kernel>
+static cudaError_t prepare(Kernel kernel, size_t smem, bool (&done)[64], int dev, int regs, int carveout = -1) {
+    if (done[dev]) return cudaSuccess;
+    if (regs > 0) {
+        cudaFuncAttributes f;
+        const cudaError_t e = cudaFuncGetAttributes(&f, kernel);
+        if (e != cudaSuccess) return e;
+        if ((f.numRegs + 7) / 8 * 8 != regs) return cudaErrorInvalidDeviceFunction;
+    }
+    return allow_smem_once(kernel, smem, done, carveout);
+}
+
+template <typename T, int MT>
+static cudaError_t few_prepare(int dev) {
+    static bool done[64];
+    return prepare(few_kernel<T, MT>, Few<MT>::kSmem, done, dev, MT == 128 ? 128 : 0, cudaSharedmemCarveoutMaxShared);
+}
+
 // How many clusters of a size find SMs of their own (a cluster lies within a part
 // of the GPU, so not every SM takes part in large ones).
 template <typename T, int MT>
 static int clusters_at_once(int dev, int split) {
     static int known[64][kMostSplit + 1];
     if (known[dev][split] > 0) return known[dev][split];
+    if (few_prepare<T, MT>(dev) != cudaSuccess) return std::max(1, num_sms() / split);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)split);
     cfg.blockDim = dim3(kThreads);
@@ -605,8 +628,7 @@ static cudaError_t few_launch(const Fp8MmLaunch& L, int split, cudaStream_t s) {
     using C = Few<MT>;
     CUtensorMap w_map, x_map;
     if (!make_map(&w_map, L.w, L.N, L.K, kTile) || !make_map(&x_map, L.x, L.M, L.K, MT)) return cudaErrorInvalidValue;
-    static bool done[64];
-    cudaError_t e = allow_smem_once(few_kernel<T, MT>, C::kSmem, done, cudaSharedmemCarveoutMaxShared);
+    const cudaError_t e = few_prepare<T, MT>(L.device);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (L.N + kTile - 1) / kTile, chunks = (L.M + MT - 1) / MT;
     if (tiles * chunks * split > 0x7fffffff) return cudaErrorInvalidConfiguration;
@@ -640,7 +662,8 @@ constexpr int kPairThreads = 32 * (4 + kSumWarps);
 constexpr int kPairRows = 256;
 constexpr int kBatch = 8;
 // 384 threads x 168 registers = 128 x 72 + 256 x 216
-constexpr int kControlRegs = 72, kSumRegs = 216;
+constexpr int kLaunchRegs = 168, kControlRegs = 72, kSumRegs = 216;
+static_assert(kPairThreads * kLaunchRegs == 128 * kControlRegs + 32 * kSumWarps * kSumRegs, "");
 
 constexpr int kOutBox = 32 * 128;   // bytes of a warp: 32 rows of 128
 
@@ -803,6 +826,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
                 tile_at(a, t, tm, tn);
                 const int n = tn * NT + rank * (NT / 2);
                 for (int kb = 0; kb < a.blocks; ++kb, ++g) {
+                    if (g == C::kStages) pdl_wait();   // (as in few_kernel)
                     if (g >= C::kStages && !(ok = warp_wait(&empty[slot], phase, ctl))) break;
                     if (rank == 0) expect_warp(smem_u32(&full[slot]), 2 * C::kStage);
                     pair_load(to + slot * C::kStage, &w_map, lead + 8 * slot, kb * kBlock, n);
@@ -852,6 +876,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
                 __syncwarp();
             }
             if (rank == 0) {
+                pdl_wait();
                 bool ok = warp_wait(&tmem_ready, 0, ctl);
                 fence_after();
                 const uint32_t tmem = tmem_slot, from = smem_u32(ring);
@@ -887,13 +912,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
         constexpr int kPart = C::kPart, kChunk = 16;
         const int half = (warp - 4) >> 2;
         const int row = (warp & 3) * 32 + lane;
+        pdl_wait();
         bool ok = warp_wait(&tmem_ready, 0, ctl);
         fence_after();
         const uint32_t mine = tmem_slot + ((uint32_t)(warp & 3) << 21) + half * C::kCols;
         const uint32_t sx_at = smem_u32(&sx[0][0][row]), sw_at = smem_u32(&sw[0][0][0]);
         const uint32_t filled = smem_u32(&d_full[half][0]), released = mapa(smem_u32(&d_empty[half][0]), 0);
         const uint32_t box = smem_u32(ring) + C::kStages * C::kStage + (warp - 4) * kOutBox;
-        pdl_wait();   // (every thread that writes outputs)
         int buf = 0, batch = 0;
         uint32_t d_phase = 0, s_phase = 0;
         bool ready = false;   // the next buffer is known to be filled
@@ -1038,11 +1063,13 @@ static cudaError_t many_launch(const Fp8MmLaunch& L, cudaStream_t s) {
         (aligned && !make_out_map<T>(&out_map, L.out, L.M, L.N, C::kOutBytes)))
         return cudaErrorInvalidValue;
     static bool done[64];
-    cudaError_t e = allow_smem_once(many_kernel<T, NT>, C::kSmem, done);
+    const cudaError_t e = prepare(many_kernel<T, NT>, C::kSmem, done, L.device, kLaunchRegs);
     if (e != cudaSuccess) return e;
     const int64_t tm = (L.M + kPairRows - 1) / kPairRows, tn = (L.N + NT - 1) / NT;
-    if (tm * tn > 0x7fffffff - 4096) return cudaErrorInvalidConfiguration;
     const int pairs = (int)std::min<int64_t>(tm * tn, num_sms() / 2);
+    // (a pair counts its blocks of K in 32 bits)
+    if (tm * tn > 0x7fffffff - 4096 || (tm * tn + pairs - 1) / pairs * ((L.K + kBlock - 1) / kBlock) > 0x7fffffff)
+        return cudaErrorInvalidConfiguration;
     const ManyArgs a{L.w_scales, L.x_scales, L.out, L.M, L.N, (int)((L.K + kBlock - 1) / kBlock), (int)tm, (int)tn, pairs,
                      aligned, L.status, L.spin_limit};
     return launch_cluster(many_kernel<T, NT>, 2 * (unsigned)pairs, kPairThreads, C::kSmem, 2, s, w_map, x_map, out_map, a);

@@ -13,9 +13,9 @@
  *    gai4_qmm_t_noalloc, both static __device__ variables.
  *  - Kernels are launched with programmatic dependent launch: a call may
  *    start while the kernel before it in the stream finishes, if that kernel
- *    allows it (this library's kernels do, but for those of gai4_quantize and
- *    gai4_kv_append, which write weights; a kernel that does not signal it is
- *    waited for in full, as usual). The packed weights, scales, biases and
+ *    allows it (this library's kernels do, but for those of gai4_quantize,
+ *    gai4_quantize_fp8 and gai4_kv_append, which write weights; a kernel that
+ *    does not signal it is waited for in full, as usual). The packed weights, scales, biases and
  *    quantized blocks may be read from the start of the call; activations are
  *    read, and outputs and workspaces written, only after the preceding
  *    kernels have completed. So a kernel that writes weights must not signal
@@ -592,6 +592,9 @@ gai4_status gai4_quantize_fp8(const void* w, uint8_t* codes, float* scales, gai4
  *   out[m, n] = sum_b x_scales[m, b] w_scales[n / 128, b] sum_{k in block b} x[m, k] w[n, k]
  *   w_codes [N, K], x_codes [M, K] (16-byte aligned), scales as above (finite,
  *   the products of a row's and a column's scales within binary32's range);
+ *   w_codes may be read from the start of the call: the kernel before it may
+ *   have written them if it is gai4_quantize_fp8's or signals no programmatic
+ *   launch, not if it is gai4_quantize_x_fp8's or gai4_rms_norm's;
  *   out [M, N] T. Any M >= 0 and N >= 1; K a multiple of 16 (UNSUPPORTED
  *   otherwise). Codes of a NaN make the outputs that read them NaN.
  * Sums within a block are the tensor cores' (products exact), sums over blocks
