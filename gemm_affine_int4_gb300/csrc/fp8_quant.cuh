@@ -95,7 +95,13 @@ struct Eight {
             v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = kApart * i < left ? T::to_f32(p[kApart * i]) : 0.f;
+            for (int i = 0; i < 8; ++i) {
+                typename T::storage raw = 0;
+                if (kApart * i < left) raw = p[kApart * i];
+                // (the zero is not converted apart, behind a branch: the loads are issued together)
+                if constexpr (T::kBytes == 2) asm("" : "+h"(raw));
+                v[i] = T::to_f32(raw);
+            }
         }
     }
     __device__ __forceinline__ void zero() {
@@ -105,6 +111,10 @@ struct Eight {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = 0.f;
         }
+    }
+    // from here on the values are made anew (not kept as binary32 from before)
+    __device__ __forceinline__ void keep() {
+        if constexpr (kPacked) asm("" : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w));
     }
     __device__ __forceinline__ void values(float (&to)[8]) const {
         if constexpr (kPacked) {
@@ -120,13 +130,6 @@ struct Eight {
         }
     }
 };
-
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const typename T::storage* p, int64_t left, float (&v)[8]) {
-    Eight<T, VEC> e;
-    e.load(p, left);
-    e.values(v);
-}
 
 template <typename T, bool VEC>
 __device__ __forceinline__ void store8(typename T::storage* p, int64_t left, const float (&v)[8]) {
