@@ -420,3 +420,70 @@ def test_stream_argument():
     assert torch.equal(y, g4.gai4_fp8_mm_t(wc, ws, c, s)) and torch.equal(c.view(torch.uint8), g4.gai4_quantize_x_fp8(x)[0].view(torch.uint8))
     assert torch.equal(n.scales, g4.gai4_rms_norm(x, fp8=True).scales)
     assert torch.equal(q, g4.gai4_rope(x.view(40, 16, 64), None, torch.arange(40, dtype=torch.int32, device="cuda"), f)[0])
+
+
+def test_beside_products_of_4_bit_weights():
+    """On two streams, in turn with kernels that take tensor memory too (4-bit weights, 16 and 300 rows)."""
+    products = [problem(M, 1024, 2048, seed=M) for M in (1, 20, 50, 120, 1500)]
+    w4 = g4.gai4_quantize(rand(4096, 2048) * 0.02, 4, 64, torch.bfloat16)
+    rows = [rand(M, 2048, seed=M, dtype=torch.bfloat16) for M in (16, 300)]
+
+    def step(i, stream=None):
+        p, x = products[i % len(products)], rows[i % 2]
+        return g4.gai4_fp8_mm_t(*p, stream=stream), g4.gai4_qmm_t(*w4, x, stream=stream)
+
+    want = [step(i) for i in range(10)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [(i % 10, step(i % 10, streams[(i // 3) % 2])) for i in range(120)]
+    torch.cuda.synchronize()
+    assert g4.gai4_last_device_status() == 0
+    assert all(torch.equal(a, b) for i, y in got for a, b in zip(want[i], y))
+
+
+def inside(shape, dtype, before):
+    """A contiguous tensor within a buffer of bytes 0x5a, and a check of what lies around it."""
+    size = torch.empty(0, dtype=dtype).element_size()
+    n = math.prod(shape) * size
+    room = torch.full((before + n + 256,), 0x5a, dtype=torch.uint8, device="cuda")
+    t = room[before:before + n].view(dtype).view(shape)
+    return t, lambda: bool((room[:before] == 0x5a).all()) and bool((room[before + n:] == 0x5a).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("before", [64, 12])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 129), (5, 1000), (700, 1000), (700, 777), (2, 17001), (300, 64)])
+def test_nothing_is_written_around_the_outputs(dt, before, rows, cols):
+    x, r = rand(rows, cols, seed=1, dtype=T[dt]), rand(rows, cols, seed=2, dtype=T[dt])
+    blocks = (cols + 127) // 128
+    made = [inside((rows, cols), T[dt], before), inside((rows, cols), T[dt], before), inside((rows, cols), E4M3, before),
+            inside((rows, blocks), torch.float32, before)]
+    out, h, codes, scales = (t for t, _ in made)
+    want = g4.gai4_rms_norm(x, residual=r, fp8=True, out=torch.empty_like(x))
+    g4.gai4_rms_norm(x, residual=r, fp8=True, out=out, residual_out=h, codes=codes, scales=scales)
+    assert all(check() for _, check in made)
+    assert same(h, want.residual)
+    g4.gai4_quantize_x_fp8(x, codes=codes, scales=scales)
+    assert all(check() for _, check in made)
+    c, s = g4.gai4_quantize_x_fp8(x)
+    assert same(codes, c) and same(scales, s)
+    ws, wcheck = inside(((rows + 127) // 128, blocks), torch.float32, before)
+    g4.gai4_quantize_fp8(x, codes=codes, scales=ws)
+    assert wcheck() and all(check() for _, check in made)
+    c, s = g4.gai4_quantize_fp8(x)
+    assert same(codes, c) and same(ws, s)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("before", [64, 12])
+@pytest.mark.parametrize("n,hq,hkv,d,rot", [(1, 1, 1, 2, 2), (3, 3, 1, 33, 32), (1000, 5, 2, 80, 40), (9, 2, 1, 1024, 6)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_writes_its_rows_only(dt, before, n, hq, hkv, d, rot, interleaved):
+    q, k = rand(n, hq, d, seed=3, dtype=T[dt]), rand(n, hkv, d, seed=4, dtype=T[dt])
+    f, _ = g4.gai4_rope_inv_freq(rot)
+    p = positions(n, 1000)
+    (qo, qcheck), (ko, kcheck) = inside((n, hq, d), T[dt], before), inside((n, hkv, d), T[dt], before)
+    g4.gai4_rope(q, k, p, f, interleaved=interleaved, q_out=qo, k_out=ko)
+    assert qcheck() and kcheck()
+    want = g4.gai4_rope(q, k, p, f, interleaved=interleaved)
+    assert same(qo, want[0]) and same(ko, want[1])
