@@ -200,15 +200,98 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const __grid_consta
     }
 }
 
+// Many rows into e4m3 alone: a warp goes through its row, a step of 256 behind its
+// loads, without a barrier. Codes and the new residual are written on the way, and
+// of the row no more is kept than its groups' maxima (in shared memory), for the
+// scales. One step ahead and 36 warps an SM; two steps and 24 take 141 us instead of
+// 114 (20011 x 5120, bf16, residual). y in T would be written in a second pass: 107
+// us, rms_norm_kernel 80.
+constexpr int kRowWarps = 4;
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(32 * kRowWarps, 6) rms_norm_codes_kernel(const __grid_constant__ NormArgs a) {
+    using S = typename T::storage;
+    pdl_launch_dependents();
+    pdl_wait();   // the kernels before this one are complete: global memory may be read
+    extern __shared__ float maxima[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = (int64_t)blockIdx.x * kRowWarps + warp;
+    if (row >= a.rows) return;
+    const int cols = (int)a.cols, groups = (cols + kGroup - 1) / kGroup;
+    float* maximum = maxima + warp * groups;
+    const int col0 = column_of<VEC>(lane);
+    const S* x = static_cast<const S*>(a.x) + row * a.x_stride + col0;
+    const S* r = a.residual ? static_cast<const S*>(a.residual) + row * a.r_stride + col0 : nullptr;
+    const S* g = a.gain ? static_cast<const S*>(a.gain) + col0 : nullptr;
+    S* h = a.residual_out ? static_cast<S*>(a.residual_out) + row * a.cols + col0 : nullptr;
+    uint8_t* codes = a.codes + row * a.cols + col0;
+    Eight<T, VEC> in, res, gain;
+    const auto load = [&](int left) {
+        if (left > 0) {
+            in.load(x, left);
+            if (r) res.load(r, left);
+            if (g) gain.load(g, left);
+        } else {
+            in.zero();
+            res.zero();
+            gain.zero();
+        }
+    };
+    load(cols - col0);
+    float sum = 0.f;
+    for (int at = 0, left = cols - col0; at < cols; at += 256, left -= 256) {
+        float p[8], q[8];
+        in.values(p);
+        if (r) {
+            res.values(q);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] += q[i];
+        }
+        if (h && left > 0) store8<T, VEC>(h + at, left, p);
+        float squares = 0.f;   // (of the step: so the row's sum has few roundings)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) squares = fmaf(p[i], p[i], squares);
+        sum += squares;
+        if (g) {
+            gain.values(q);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] *= q[i];
+        }
+        x += 256;
+        if (r) r += 256;
+        if (g) g += 256;
+        load(left - 256);
+        const float amax = max_abs(group_max(amax8(p)), kLeastMax), f = __fdiv_rn(448.0f, amax);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = p[i] * f;
+        if (left > 0) {
+            store_codes8<VEC>(codes + at, left, codes8(q));
+            if ((lane & 15) == 0) maximum[at / kGroup + (lane >> 4)] = amax;
+        }
+    }
+    const float inv = inverse_root(warp_sum(sum), a);
+    __syncwarp();
+    for (int i = lane; i < groups; i += 32) a.scales[row * groups + i] = __fdiv_rn(inv * maximum[i], 448.0f);
+}
+
 template <typename T, bool VEC>
 cudaError_t norm_launch(const NormArgs& a, cudaStream_t s) {
     const int64_t eights = (a.cols + 7) / 8;
     const int64_t wide = (eights + 31) / 32;   // warps that take the row at one eight a thread
-    if (wide > kMaxWarps * 2)
+    // Into e4m3 alone, a warp a row: in us, and with the kernels below, bf16 with a
+    // residual 20011 x 5120 114, 125; 20011 x 1000 27, 28; 3000 x 28672 118, 175; without
+    // one 20011 x 5120 72, 104; f32 without one 10000 x 5120 53, 59. Not for rows that do
+    // not go round among 36 warps an SM (6000 x 2048 20, 18; 700 x 40000 112, 57), short
+    // ones (30000 x 512 21, 20), and f32 with a residual (10000 x 5120 101, 95).
+    const bool long_rows = wide > kMaxWarps * 2;
+    if (a.codes && !a.out && a.cols > 512 && a.cols <= 262144 && a.rows >= (long_rows ? 8 : 64) * num_sms() &&
+        (long_rows || T::kBytes == 2 || !a.residual))
+        return launch_pdl(rms_norm_codes_kernel<T, VEC>, dim3((unsigned)((a.rows + kRowWarps - 1) / kRowWarps)),
+                          dim3(32 * kRowWarps), (size_t)((a.cols + kGroup - 1) / kGroup * 4 * kRowWarps), s, a);
+    if (long_rows)
         return launch_pdl(rms_norm_long_kernel<T, VEC>, dim3((unsigned)a.rows), dim3(1024), 0, s, a);
     // Few rows: as many threads a row as it has eights. Many rows: two eights a
     // thread, so that more is on its way (20011 x 5120, bf16, residual and codes:
-    // 158 us with one, 130 with two), and blocks that take row after row (122 us).
+    // 158 us with one, 130 with two), and blocks that take row after row (125 us).
     // Those pay off for 16-bit rows only: 10000 x 5120 in f32 takes 96 us without,
     // 134 with, as registers run out. Without a residual half as much is read at a
     // time: four eights (80 us, two 87).

@@ -37,15 +37,17 @@ def rope64(x, positions, inv_freq, mscale, interleaved):
     return y, bound * (1 + U[x.dtype]) + turned * (U[x.dtype] * y.abs() + TINY[x.dtype])
 
 
-def norm64(x, gain, eps, residual):
+def norm64(x, gain, eps, residual, a_warp_a_row=False):
     """(h, y, relative bound of y before its last rounding). The sum of squares goes through at most 8 + 4 + 10 additions
     (8 + cols / 8192 + 10 for long rows) and counts half in y; x + residual, the mean, eps, the root and two products
-    round once each, h in the sum and in y."""
+    round once each, h in the sum and in y. A warp that takes a row in steps of 256 adds 8 squares a lane, a step at a
+    time, and 32 lanes: 8 + cols / 256 + 5."""
     h = x.double() if residual is None else x.double() + residual.double()
     y = h / torch.sqrt((h * h).mean(1, keepdim=True) + eps)
     if gain is not None:
         y = y * gain.double()
-    return h, y, u * (22 + h.shape[1] / 8192) / 2 + 8 * u
+    additions = 14 + h.shape[1] / 256 if a_warp_a_row else 22 + h.shape[1] / 8192
+    return h, y, u * additions / 2 + 8 * u
 
 
 def quantize_ref(x, block_rows):

@@ -109,11 +109,13 @@ SHAPES = [(1, 1), (1, 4096), (3, 7), (64, 4096), (5, 8200), (700, 128), (701, 12
           (1003, 16384), (320, 16392), (900, 511)]
 
 
-def check_codes(codes, scales, y, rel):
+def check_codes(codes, scales, y, rel, root=None):
     """e4m3 rows against y in 64 bits: the scale is off by y's own bound and two roundings, a value by half a step of
-    e4m3 (2^-4 of it, 2^-10 of the scale near zero) and by y's bound."""
+    e4m3 (2^-4 of it, 2^-10 of the scale near zero) and by y's bound. `root` [R, 1], where rows are zero: a block's
+    least maximum, 2^-100, is one of y * root."""
     R, C = y.shape
-    a = torch.nn.functional.pad(y.abs(), (0, -C % 128)).unflatten(1, (-1, 128)).amax(-1).clamp(min=2.0 ** -100)
+    a = torch.nn.functional.pad(y.abs(), (0, -C % 128)).unflatten(1, (-1, 128)).amax(-1)
+    a = torch.maximum(a, 2.0 ** -100 / root) if root is not None else a.clamp(min=2.0 ** -100)
     within(scales, a / 448, a / 448 * (rel + 3 * 2.0 ** -24), "scales")
     s = scales.double().repeat_interleave(128, 1)[:, :C]
     got = codes.double() * s
@@ -139,6 +141,27 @@ def test_norm(dt, rows, cols):
         check_codes(only.codes, only.scales, y, rel)
         assert torch.equal(both.out, plain.out) and torch.equal(both.scales, only.scales)
         assert torch.equal(both.codes.view(torch.uint8), only.codes.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(9728, 520), (10001, 1024), (12345, 777), (1217, 16392), (1300, 17001)])
+def test_norm_of_many_rows_into_codes(dt, rows, cols):
+    """Rows enough for a warp a row: with and without residual and gain, strided, in place."""
+    x, r = rand(rows, cols + 8, dtype=T[dt])[:, :cols], rand(rows, cols, seed=1, dtype=T[dt])
+    x[:, cols // 2] *= 30
+    x[3] = 0
+    gain = rand(cols, seed=2, dtype=T[dt])
+    for residual, g in ((None, gain), (r, gain), (r, None)):
+        h, y, rel = norm64(x, g, 1e-5, residual, a_warp_a_row=True)
+        inputs = None if residual is None else residual.clone()
+        got = g4.gai4_rms_norm(x, g, eps=1e-5, residual=inputs, fp8=True, residual_out=inputs)
+        check_codes(got.codes, got.scales, y, rel, root=torch.sqrt((h * h).mean(1, keepdim=True) + 1e-5))
+        if residual is not None:
+            assert got.residual is inputs and torch.equal(inputs, (x.float() + r.float()).to(T[dt]))
+    x[5, 7], x[6, cols - 1] = nan, inf
+    got = g4.gai4_rms_norm(x, gain, eps=1e-5, fp8=True)
+    v = values(got.codes[:8], got.scales[:8], 1)
+    assert bool(v[5].isnan().all()) and bool(v[6, cols - 1].isnan()) and not bool(v[[0, 3, 4, 7]].isnan().any())
 
 
 def test_norm_strided_rows_in_place_and_without_gain():
