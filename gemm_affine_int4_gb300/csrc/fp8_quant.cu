@@ -4,7 +4,7 @@
 // scale for each block of 128 rows x 128 columns. Both read every value once
 // and write a byte for it: bound by HBM (16-bit inputs 3 bytes a value, binary32
 // 5), for a few rows by the launch. 5000 x 5001, whose elements are read and written
-// singly, in us: weights bf16 34, f32 26; activations 32, 28 (floors 11, 18).
+// singly, in us: weights bf16 34, f32 26; activations 25, 25 (floors 11, 18).
 #include <algorithm>
 
 #include "fp8_quant.cuh"
@@ -108,13 +108,14 @@ cudaError_t x_launch(const void* x, int64_t x_stride, uint8_t* codes, float* sca
     const auto* p = static_cast<const typename T::storage*>(x);
     const int64_t eights = (cols + kGroup - 1) / kGroup * 16;
     const bool vec = vec_ok(x, x_stride, cols, T::kBytes, codes);
-    // few values: one eight a thread, on as many SMs as there are
-    const bool few = rows * eights <= (int64_t)num_sms() * 4 * kThreads;
+    // few values: one eight a thread, on as many SMs as there are. Single elements too:
+    // an eight of those is eight loads (5000 x 5001, bf16: 25 us, 32 with four rows a
+    // thread; 14336 x 5120 in 16-byte accesses: 55, and 42).
+    const bool few = !vec || rows * eights <= (int64_t)num_sms() * 4 * kThreads;
     const int tx = (int)std::min<int64_t>(eights, 128), ty = tx % 32 ? kThreads / tx & ~1 : kThreads / tx;   // whole warps
     const int64_t across = (eights + tx - 1) / tx, down = (rows + ty * (few ? 1 : 4) - 1) / (ty * (few ? 1 : 4));
     if (across * down > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    auto* k = few ? (vec ? quantize_x_fp8_kernel<T, true, 1> : quantize_x_fp8_kernel<T, false, 1>)
-                  : (vec ? quantize_x_fp8_kernel<T, true, 4> : quantize_x_fp8_kernel<T, false, 4>);
+    auto* k = !vec ? quantize_x_fp8_kernel<T, false, 1> : few ? quantize_x_fp8_kernel<T, true, 1> : quantize_x_fp8_kernel<T, true, 4>;
     return launch_pdl(k, dim3((unsigned)(across * down)), dim3(tx, ty), 0, s, p, x_stride, codes, scales, rows, cols,
                       (unsigned)across);
 }
