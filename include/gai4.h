@@ -595,7 +595,7 @@ gai4_status gai4_quantize_fp8(const void* w, uint8_t* codes, float* scales, gai4
  *   w_codes may be read from the start of the call: the kernel before it may
  *   have written them if it is gai4_quantize_fp8's or signals no programmatic
  *   launch, not if it is gai4_quantize_x_fp8's or gai4_rms_norm's;
- *   out [M, N] T. Any M >= 0 and N >= 1; K a multiple of 16 (UNSUPPORTED
+ *   out [M, N] T, apart from the inputs. Any M >= 0 and N >= 1; K a multiple of 16 (UNSUPPORTED
  *   otherwise). Codes of a NaN make the outputs that read them NaN.
  * Sums within a block are the tensor cores' (products exact), sums over blocks
  * binary32; one rounding to T at the end. Results repeat bit for bit; those of

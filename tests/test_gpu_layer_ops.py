@@ -510,3 +510,55 @@ def test_rope_writes_its_rows_only(dt, before, n, hq, hkv, d, rot, interleaved):
     assert qcheck() and kcheck()
     want = g4.gai4_rope(q, k, p, f, interleaved=interleaved)
     assert same(qo, want[0]) and same(ko, want[1])
+
+
+def test_offsets_beyond_32_bits():
+    """Tensors of 2254 million elements: the last rows are those of a call on them alone."""
+    rows, cols, tail = 550400, 4096, 12800
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-tail:] = rand(tail, cols, dtype=torch.bfloat16)
+    last = x[-tail:].clone()
+    for kw in (dict(fp8=True), dict(fp8=False), dict(fp8=True, out=True)):
+        big, small = (g4.gai4_rms_norm(t, residual=t, fp8=kw["fp8"], out=torch.empty_like(t) if kw.get("out") else None)
+                      for t in (x, last))
+        for a, b in zip(big, small):
+            assert (a is None) == (b is None)
+            assert a is None or same(a[-tail:], b)
+        del big, small, a, b
+    p = torch.arange(rows, dtype=torch.int32, device="cuda")
+    f, _ = g4.gai4_rope_inv_freq(128)
+    q, k = x.view(rows, 32, 128).split([28, 4], 1)
+    qo, ko = g4.gai4_rope(q, k, p, f)
+    want = g4.gai4_rope(*last.view(tail, 32, 128).split([28, 4], 1), p[-tail:].clone(), f)
+    assert same(qo[-tail:], want[0]) and same(ko[-tail:], want[1])
+    del qo, ko, want
+    wc, ws = g4.gai4_quantize_fp8(x)
+    c, s = g4.gai4_quantize_fp8(last)
+    assert same(wc[-tail:], c) and same(ws[-tail // 128:], s)
+    del wc
+    xc, xs = g4.gai4_quantize_x_fp8(x)
+    c, s = g4.gai4_quantize_x_fp8(last)
+    assert same(xc[-tail:], c) and same(xs[-tail:], s)
+    del x
+    for n in (4096, 4097):   # (rows of outputs on 16-byte boundaries, and not)
+        w = g4.gai4_quantize_fp8(rand(n, cols, seed=n) * 0.02)
+        y = g4.gai4_fp8_mm_t(*w, xc, xs)
+        assert same(y[-tail:], g4.gai4_fp8_mm_t(*w, c, s))
+        del y
+
+
+@pytest.mark.parametrize("M", [1, 100, 300])
+def test_weights_beyond_32_bits(M):
+    """Small integers, so that every order of additions gives the same."""
+    N, K, tail = 550400, 4096, 1280
+
+    def ints(n, seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        return torch.randint(-2, 3, (n, K), generator=g, device="cuda").to(E4M3)
+
+    w = torch.zeros(N, K, dtype=E4M3, device="cuda")
+    w[-tail:] = ints(tail, 1)
+    ws = torch.ones(N // 128, K // 128, device="cuda")
+    x, xs = ints(M, 2), torch.ones(M, K // 128, device="cuda")
+    y = g4.gai4_fp8_mm_t(w, ws, x, xs, dtype=torch.float32)
+    assert torch.equal(y[:, -tail:], x.float() @ w[-tail:].float().t()) and not bool(y[:, :-tail].any())
