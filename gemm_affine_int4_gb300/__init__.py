@@ -559,38 +559,24 @@ def gai4_kv_attention(q, k_cache, v_cache, block_table, kv_lens, cu_q, group_siz
 # float32 scales, [M, ceil(K / 128)] for activations and
 # [ceil(N / 128), ceil(K / 128)] for weights.
 # ---------------------------------------------------------------------------
-# The calls are short on the GPU, so the checks are one expression each, and
-# messages are made only where one fails.
-_E4M3 = torch.float8_e4m3fn
-_CODES = {torch.float8_e4m3fn, torch.uint8}
-_F32 = torch.float32
+# Checks, allocation and the call itself are csrc/torch_calls.cpp: the kernels
+# are short, and Python takes longer than they do.
 _ROPE_SCALING = {None: 0, "linear": 1, "ntk": 2, "yarn": 3, "smooth": 4}
-_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_bound = None
 
 
-def _launch(name: str, fn, device: int, stream, *args):
-    """Calls `fn` with the tensors' device current and the stream as its last argument."""
-    if stream is not None:
-        handle = stream.cuda_stream
-    elif _raw_stream is not None:
-        handle = _raw_stream(device)
-    else:
-        handle = torch.cuda.current_stream(device).cuda_stream
-    if device == _get_device():
-        st = fn(*args, handle)
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, handle)
-    if st != GAI4_OK:
-        raise Gai4Error(name, st)
-
-
-def _refuse(what: str):
-    raise ValueError("gai4: " + what)
-
-
-def _off_device():
-    _refuse("tensors must live on one CUDA device, and be contiguous where they have no stride argument")
+def _bind():
+    """Load _calls.so, which calls the library's entries on the current stream."""
+    global _bound
+    if _bound is None:
+        lib()
+        try:
+            from . import _calls
+        except ImportError as e:
+            raise RuntimeError("_calls.so is not built; run `python -m gemm_affine_int4_gb300.build`") from e
+        _calls.set_error(Gai4Error)
+        _bound = _calls
+    return _bound
 
 
 def gai4_rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -598,7 +584,7 @@ def gai4_rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: str | None 
     """(inv_freq float64 [rot_dim / 2], mscale) for gai4_rope. scaling: None,
     "linear", "ntk", "yarn" or "smooth"; high defaults to 32 (yarn) or 4."""
     if scaling not in _ROPE_SCALING:
-        _refuse(f"unknown scaling {scaling!r}")
+        raise ValueError(f"gai4: unknown scaling {scaling!r}")
     host = torch.empty(max(rot_dim // 2, 1), dtype=torch.float64)
     mscale = ctypes.c_float()
     if high is None:
@@ -606,17 +592,6 @@ def gai4_rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: str | None 
     _check("gai4_rope_inv_freq", lib().gai4_rope_inv_freq(host.data_ptr(), ctypes.addressof(mscale), rot_dim, base,
                                                           _ROPE_SCALING[scaling], factor, original_len, low, high))
     return host.to(device), mscale.value
-
-
-def _head_rows(t, n: int, d: int, dtype, device: int, what: str):
-    """(heads, token stride, address) of [n, heads, d] rows with contiguous heads."""
-    m, h, e = t.shape
-    s0, s1, s2 = t.stride()
-    if m != n or e != d or t.dtype is not dtype or (s2 != 1 and d > 1) or (s1 != d and h > 1):
-        _refuse(f"{what} must be [tokens, heads, head_dim] of q's type, heads contiguous within a token")
-    if t.get_device() != device or device < 0:
-        _off_device()
-    return h, s0 if n > 1 else h * d, t.data_ptr()
 
 
 def gai4_rope(q, k, positions, inv_freq, interleaved: bool = False, mscale: float = 1.0, q_out=None, k_out=None,
@@ -627,40 +602,10 @@ def gai4_rope(q, k, positions, inv_freq, interleaved: bool = False, mscale: floa
     positions[token] * inv_freq[pair]. positions int32 [tokens], inv_freq
     float64. New tensors unless q_out, k_out are given; q and k themselves are
     allowed. Returns (q_out, k_out)."""
-    n, hq, d = q.shape
-    T = q.dtype
-    dev = q.get_device()
-    if positions.shape != (n,) or positions.dtype is not torch.int32 or inv_freq.dim() != 1 or \
-            inv_freq.dtype is not torch.float64:
-        _refuse("positions must be int32 [tokens], inv_freq float64 [rot_dim / 2]")
-    if positions.get_device() != dev or inv_freq.get_device() != dev or dev < 0 or not positions.is_contiguous() or \
-            not inv_freq.is_contiguous():
-        _off_device()
-    _, qs, qp = _head_rows(q, n, d, T, dev, "q")
-    if q_out is None:
-        q_out = _empty((n, hq, d), T, q.device, stream)
-        qo, qop = hq * d, q_out.data_ptr()
-    elif q_out is q:
-        qo, qop = qs, qp
-    else:
-        h, qo, qop = _head_rows(q_out, n, d, T, dev, "q_out")
-        if h != hq:
-            _refuse("q_out must have q's shape")
-    hk = ks = kp = ko = kop = 0
-    if k is not None:
-        hk, ks, kp = _head_rows(k, n, d, T, dev, "k")
-        if k_out is None:
-            k_out = _empty((n, hk, d), T, q.device, stream)
-            ko, kop = hk * d, k_out.data_ptr()
-        elif k_out is k:
-            ko, kop = ks, kp
-        else:
-            h, ko, kop = _head_rows(k_out, n, d, T, dev, "k_out")
-            if h != hk:
-                _refuse("k_out must have k's shape")
-    _launch("gai4_rope", lib().gai4_rope, dev, stream, qp, qs, qop, qo, kp, ks, kop, ko, positions.data_ptr(),
-            inv_freq.data_ptr(), mscale, _dtype(q), n, hq, hk, d, 2 * inv_freq.shape[0], 1 if interleaved else 0)
-    return q_out, k_out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gai4_rope(q, k, positions, inv_freq, interleaved, mscale, q_out, k_out)
+    return (_bound or _bind()).rope(q, k, positions, inv_freq, interleaved, mscale, q_out, k_out)
 
 
 class Normed(NamedTuple):
@@ -671,122 +616,43 @@ class Normed(NamedTuple):
     scales: torch.Tensor | None     # float32 [rows, ceil(cols / 128)]
 
 
-def _matrix(t, shape, dtype, device: int, what: str) -> int:
-    """Address of a contiguous output or operand."""
-    if t.shape != shape or t.dtype is not dtype:
-        _refuse(f"{what} must be {dtype} of shape {tuple(shape)}")
-    if t.get_device() != device or device < 0 or not t.is_contiguous():
-        _off_device()
-    return t.data_ptr()
-
-
-def _row_stride(t, device: int, what: str) -> int:
-    """Row stride of [rows, cols] with contiguous columns."""
-    s0, s1 = t.stride()
-    rows, cols = t.shape
-    if s1 != 1 and cols > 1:
-        _refuse(f"{what}: columns must be contiguous")
-    if t.get_device() != device or device < 0:
-        _off_device()
-    return s0 if rows > 1 else cols
-
-
-def _fp8_outputs(codes, scales, rows: int, cols: int, scale_rows: int, x, dev: int, stream):
-    """(codes, their address, scales, their address), made where they are None."""
-    blocks = (cols + 127) >> 7
-    if codes is None:
-        codes = _empty((rows, cols), _E4M3, x.device, stream)
-    elif codes.dtype not in _CODES or codes.shape != (rows, cols) or not codes.is_contiguous() or codes.get_device() != dev:
-        _refuse("codes must be float8_e4m3fn (or uint8) [rows, cols], contiguous, on x's device")
-    if scales is None:
-        scales = _empty((scale_rows, blocks), _F32, x.device, stream)
-        sp = scales.data_ptr()
-    else:
-        sp = _matrix(scales, (scale_rows, blocks), _F32, dev, "scales")
-    return codes, codes.data_ptr(), scales, sp
-
-
 def gai4_rms_norm(x, gain=None, eps: float = 1e-6, residual=None, fp8: bool = False, out=None, residual_out=None,
                   codes=None, scales=None, stream=None) -> Normed:
     """h = x + residual, y = h / sqrt(mean(h^2) + eps) * gain for rows x
     [rows, cols] (any row stride). With residual the sum h comes back too. With
     fp8 y comes back as e4m3 codes and scales, and in x's type only where `out`
     is given; residual_out may be `residual` itself."""
-    rows, cols = shape = x.shape
-    T = x.dtype
-    dev = x.get_device()
-    xs = _row_stride(x, dev, "x")
-    rp = rs = gp = op = rop = cp = sp = 0
-    if residual is not None:
-        if residual.shape != shape or residual.dtype is not T:
-            _refuse("residual must have x's shape and type")
-        rp, rs = residual.data_ptr(), _row_stride(residual, dev, "residual")
-        if residual_out is None:
-            residual_out = _empty(shape, T, x.device, stream)
-            rop = residual_out.data_ptr()
-    if residual_out is not None and not rop:
-        rop = _matrix(residual_out, shape, T, dev, "residual_out")
-    if gain is not None:
-        gp = _matrix(gain, (cols,), T, dev, "gain")
-    if out is not None:
-        op = _matrix(out, shape, T, dev, "out")
-    elif not fp8:
-        out = _empty(shape, T, x.device, stream)
-        op = out.data_ptr()
-    if fp8:
-        codes, cp, scales, sp = _fp8_outputs(codes, scales, rows, cols, rows, x, dev, stream)
-    elif codes is not None or scales is not None:
-        _refuse("codes and scales are outputs of fp8=True")
-    _launch("gai4_rms_norm", lib().gai4_rms_norm, dev, stream, x.data_ptr(), xs, rp, rs, gp, op, rop, cp, sp, _dtype(x),
-            rows, cols, eps)
-    return Normed(out, residual_out, codes, scales)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gai4_rms_norm(x, gain, eps, residual, fp8, out, residual_out, codes, scales)
+    return Normed(*(_bound or _bind()).rms_norm(x, gain, eps, residual, fp8, out, residual_out, codes, scales))
 
 
 def gai4_quantize_x_fp8(x, codes=None, scales=None, stream=None):
     """Activations x [M, K] (any row stride) -> (codes e4m3 [M, K], scales
     float32 [M, ceil(K / 128)])."""
-    M, K = x.shape
-    dev = x.get_device()
-    xs = _row_stride(x, dev, "x")
-    codes, cp, scales, sp = _fp8_outputs(codes, scales, M, K, M, x, dev, stream)
-    _launch("gai4_quantize_x_fp8", lib().gai4_quantize_x_fp8, dev, stream, x.data_ptr(), xs, cp, sp, _dtype(x), M, K)
-    return codes, scales
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gai4_quantize_x_fp8(x, codes, scales)
+    return (_bound or _bind()).quantize_x_fp8(x, codes, scales)
 
 
 def gai4_quantize_fp8(w, codes=None, scales=None, stream=None):
     """Weights w [N, K] -> (codes e4m3 [N, K], scales float32 [ceil(N / 128),
     ceil(K / 128)])."""
-    N, K = w.shape
-    dev = w.get_device()
-    if dev < 0 or not w.is_contiguous():
-        _off_device()
-    codes, cp, scales, sp = _fp8_outputs(codes, scales, N, K, (N + 127) >> 7, w, dev, stream)
-    _launch("gai4_quantize_fp8", lib().gai4_quantize_fp8, dev, stream, w.data_ptr(), cp, sp, _dtype(w), N, K)
-    return codes, scales
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gai4_quantize_fp8(w, codes, scales)
+    return (_bound or _bind()).quantize_fp8(w, codes, scales)
 
 
 def gai4_fp8_mm_t(w_codes, w_scales, x_codes, x_scales, out=None, dtype=torch.bfloat16, stream=None):
     """out[m, n] = sum_k (x_codes x_scales)[m, k] (w_codes w_scales)[n, k] in
     `dtype` (or out's type); K a multiple of 16."""
-    N, K = w_codes.shape
-    M, K2 = x_codes.shape
-    B = (K + 127) >> 7
-    if K2 != K or x_scales.shape != (M, B) or w_scales.shape != ((N + 127) >> 7, B) or x_scales.dtype is not _F32 or \
-            w_scales.dtype is not _F32 or w_codes.dtype not in _CODES or x_codes.dtype not in _CODES:
-        _refuse("codes e4m3 [N, K] and [M, K], scales float32 [ceil(N / 128), ceil(K / 128)] and [M, ceil(K / 128)]")
-    dev = x_codes.get_device()
-    if dev < 0 or w_codes.get_device() != dev or w_scales.get_device() != dev or x_scales.get_device() != dev or \
-            not (w_codes.is_contiguous() and w_scales.is_contiguous() and x_codes.is_contiguous() and
-                 x_scales.is_contiguous()):
-        _off_device()
-    if out is None:
-        out = _empty((M, N), dtype, x_codes.device, stream)
-        op = out.data_ptr()
-    else:
-        op = _matrix(out, (M, N), out.dtype, dev, "out")
-    _launch("gai4_fp8_mm_t", lib().gai4_fp8_mm_t, dev, stream, w_codes.data_ptr(), w_scales.data_ptr(),
-            x_codes.data_ptr(), x_scales.data_ptr(), op, _dtype(out), M, N, K)
-    return out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gai4_fp8_mm_t(w_codes, w_scales, x_codes, x_scales, out, dtype)
+    return (_bound or _bind()).fp8_mm_t(w_codes, w_scales, x_codes, x_scales, out, dtype)
 
 
 def gai4_last_device_status(stream=None) -> int:
