@@ -2,8 +2,11 @@
 // module `_calls`. Each function checks its tensors, allocates the outputs that
 // were not given on the current stream, and calls the C entry on that stream. The
 // kernels of a decoding step take 2 to 5 us; the same in Python and ctypes took 9
-// to 15 us a call, this takes 4 to 7.
+// to 15 us a call, this takes 3 to 6.
 #include <Python.h>
+
+#include <algorithm>
+#include <cstdint>
 
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -57,7 +60,17 @@ Tensor fresh(at::IntArrayRef shape, ScalarType type, const Tensor& like) {
 
 void* stream_of(int device) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream(); }
 
-void done(const char* name, gai4_status status) {
+// without the interpreter's lock: a full launch queue blocks a call
+struct Unlocked {
+    PyThreadState* thread = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(thread); }
+};
+template <typename F>
+void call(const char* name, F entry) {
+    const gai4_status status = [&] {
+        const Unlocked unlocked;
+        return entry();
+    }();
     if (status == GAI4_OK) return;
     PyObject* e = PyObject_CallFunction(error_class, "si", name, (int)status);
     if (e) {
@@ -160,12 +173,17 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t count) {
         k_to = head_rows(k_out, n, d, type, device, "k_out");
         GAI4_CHECK(k_to.heads == k_from.heads, "k_out must have k's shape");
     }
+    const float mscale = (float)number(a[5]);
+    const bool interleaved = truth(a[4]);
+    const gai4_dtype dtype = dtype_of(type);
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
-    done("gai4_rope",
-         gai4_rope(from.data, from.stride, to.data, to.stride, k_from.data, k_from.stride, k_to.data, k_to.stride,
-                   static_cast<const int32_t*>(positions.data_ptr()), static_cast<const double*>(inv_freq.data_ptr()),
-                   (float)number(a[5]), dtype_of(type), n, from.heads, k_from.heads, (int)std::min<int64_t>(d, INT32_MAX),
-                   (int)std::min<int64_t>(2 * inv_freq.size(0), INT32_MAX), truth(a[4]), stream_of(device)));
+    call("gai4_rope", [&] {
+        return gai4_rope(from.data, from.stride, to.data, to.stride, k_from.data, k_from.stride, k_to.data, k_to.stride,
+                         static_cast<const int32_t*>(positions.data_ptr()),
+                         static_cast<const double*>(inv_freq.data_ptr()), mscale, dtype, n, from.heads, k_from.heads,
+                         (int)std::min<int64_t>(d, INT32_MAX), (int)std::min<int64_t>(2 * inv_freq.size(0), INT32_MAX),
+                         interleaved, stream_of(device));
+    });
     return tuple(q_out, k_out);
     END_HANDLE_TH_ERRORS
 }
@@ -191,7 +209,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t count) {
     if (given(a[6])) {
         residual_out = tensor(a[6]);
         whole(residual_out, x.sizes(), type, device, "residual_out");
-    } else if (residual || given(a[3])) {
+    } else if (given(a[3])) {
         residual_out = fresh(x.sizes(), type, x);
     }
     if (given(a[5])) {
@@ -204,12 +222,15 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t count) {
         fp8_outputs(a[7], a[8], x, rows, device, codes, scales);
     else
         GAI4_CHECK(!given(a[7]) && !given(a[8]), "codes and scales are outputs of fp8=True");
+    const float eps = (float)number(a[2]);
+    const gai4_dtype dtype = dtype_of(type);
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
     const auto data = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
-    done("gai4_rms_norm",
-         gai4_rms_norm(x.data_ptr(), x_stride, residual, r_stride, gain, data(out), data(residual_out),
-                       static_cast<uint8_t*>(data(codes)), static_cast<float*>(data(scales)), dtype_of(type), rows, cols,
-                       (float)number(a[2]), stream_of(device)));
+    call("gai4_rms_norm", [&] {
+        return gai4_rms_norm(x.data_ptr(), x_stride, residual, r_stride, gain, data(out), data(residual_out),
+                             static_cast<uint8_t*>(data(codes)), static_cast<float*>(data(scales)), dtype, rows, cols, eps,
+                             stream_of(device));
+    });
     return tuple(out, residual_out, codes, scales);
     END_HANDLE_TH_ERRORS
 }
@@ -222,11 +243,13 @@ PyObject* quantize_x_fp8(PyObject*, PyObject* const* a, Py_ssize_t count) {
     const int64_t stride = row_stride(x, device, "x");
     Tensor codes, scales;
     fp8_outputs(a[1], a[2], x, x.size(0), device, codes, scales);
+    const gai4_dtype dtype = dtype_of(x.scalar_type());
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
-    done("gai4_quantize_x_fp8",
-         gai4_quantize_x_fp8(x.data_ptr(), stride, static_cast<uint8_t*>(codes.data_ptr()),
-                             static_cast<float*>(scales.data_ptr()), dtype_of(x.scalar_type()), x.size(0), x.size(1),
-                             stream_of(device)));
+    call("gai4_quantize_x_fp8", [&] {
+        return gai4_quantize_x_fp8(x.data_ptr(), stride, static_cast<uint8_t*>(codes.data_ptr()),
+                                   static_cast<float*>(scales.data_ptr()), dtype, x.size(0), x.size(1),
+                                   stream_of(device));
+    });
     return tuple(codes, scales);
     END_HANDLE_TH_ERRORS
 }
@@ -241,10 +264,12 @@ PyObject* quantize_fp8(PyObject*, PyObject* const* a, Py_ssize_t count) {
     GAI4_CHECK(w.is_contiguous(), kOffDevice);
     Tensor codes, scales;
     fp8_outputs(a[1], a[2], w, (w.size(0) + 127) / 128, device, codes, scales);
+    const gai4_dtype dtype = dtype_of(w.scalar_type());
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
-    done("gai4_quantize_fp8",
-         gai4_quantize_fp8(w.data_ptr(), static_cast<uint8_t*>(codes.data_ptr()), static_cast<float*>(scales.data_ptr()),
-                           dtype_of(w.scalar_type()), w.size(0), w.size(1), stream_of(device)));
+    call("gai4_quantize_fp8", [&] {
+        return gai4_quantize_fp8(w.data_ptr(), static_cast<uint8_t*>(codes.data_ptr()),
+                                 static_cast<float*>(scales.data_ptr()), dtype, w.size(0), w.size(1), stream_of(device));
+    });
     return tuple(codes, scales);
     END_HANDLE_TH_ERRORS
 }
@@ -274,11 +299,13 @@ PyObject* fp8_mm_t(PyObject*, PyObject* const* a, Py_ssize_t count) {
         dtype_of(type);
         out = fresh({M, N}, type, x);
     }
+    const gai4_dtype dtype = dtype_of(out.scalar_type());
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
-    done("gai4_fp8_mm_t",
-         gai4_fp8_mm_t(static_cast<const uint8_t*>(w.data_ptr()), static_cast<const float*>(ws.data_ptr()),
-                       static_cast<const uint8_t*>(x.data_ptr()), static_cast<const float*>(xs.data_ptr()), out.data_ptr(),
-                       dtype_of(out.scalar_type()), M, N, w.size(1), stream_of(device)));
+    call("gai4_fp8_mm_t", [&] {
+        return gai4_fp8_mm_t(static_cast<const uint8_t*>(w.data_ptr()), static_cast<const float*>(ws.data_ptr()),
+                             static_cast<const uint8_t*>(x.data_ptr()), static_cast<const float*>(xs.data_ptr()),
+                             out.data_ptr(), dtype, M, N, w.size(1), stream_of(device));
+    });
     return wrapped(out);
     END_HANDLE_TH_ERRORS
 }

@@ -562,3 +562,55 @@ def test_weights_beyond_32_bits(M):
     x, xs = ints(M, 2), torch.ones(M, K // 128, device="cuda")
     y = g4.gai4_fp8_mm_t(w, ws, x, xs, dtype=torch.float32)
     assert torch.equal(y[:, -tail:], x.float() @ w[-tail:].float().t()) and not bool(y[:, :-tail].any())
+
+
+def test_refused_on_the_gpu():
+    """What only the library's entry refuses, its types, and outputs that do not fit; the next call works."""
+    x = rand(6, 256, dtype=torch.bfloat16)
+    c, s = g4.gai4_quantize_x_fp8(x)
+    w = g4.gai4_quantize_fp8(rand(128, 256))
+    f, _ = g4.gai4_rope_inv_freq(64)
+    p = torch.arange(6, dtype=torch.int32, device="cuda")
+    q = x.view(6, 4, 64)
+    with pytest.raises(g4.Gai4Error, match="gai4_rms_norm"):
+        g4.gai4_rms_norm(x, eps=-1.0)
+    with pytest.raises(g4.Gai4Error, match="gai4_rope"):
+        g4.gai4_rope(q, q[:, :2], p, f, q_out=q, k_out=q[:, 2:])     # k's rows where q's are written
+    with pytest.raises(g4.Gai4Error, match="gai4_fp8_mm_t"):
+        narrow = g4.gai4_quantize_fp8(rand(128, 200)), g4.gai4_quantize_x_fp8(x[:, :200])
+        g4.gai4_fp8_mm_t(*narrow[0], *narrow[1])                      # K a multiple of 16
+    for bad in (lambda: g4.gai4_rms_norm(x.double()), lambda: g4.gai4_quantize_x_fp8(x.int()),
+                lambda: g4.gai4_fp8_mm_t(*w, c, s, dtype=torch.float64),
+                lambda: g4.gai4_fp8_mm_t(*w, c, s, out=torch.empty(6, 127, device="cuda")),
+                lambda: g4.gai4_fp8_mm_t(*w, c, s.cpu()), lambda: g4.gai4_rope(q, None, p.cpu(), f),
+                lambda: g4.gai4_rms_norm(x, out=torch.empty(6, 512, device="cuda", dtype=x.dtype)[:, ::2]),
+                lambda: g4.gai4_rms_norm(x, fp8=True, codes=torch.empty(6, 256, device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(TypeError):
+        g4.gai4_rms_norm(x, eps="small")
+    assert same(g4.gai4_quantize_x_fp8(x.clone().requires_grad_())[0], c)
+    assert same(g4.gai4_fp8_mm_t(w[0].view(torch.uint8), w[1], c.view(torch.uint8), s), g4.gai4_fp8_mm_t(*w, c, s))
+
+
+def test_calls_from_several_threads():
+    import threading
+    x = rand(48, 4096, dtype=torch.bfloat16)
+    w = g4.gai4_quantize_fp8(rand(512, 4096) * 0.02)
+    want = g4.gai4_fp8_mm_t(*w, *g4.gai4_quantize_x_fp8(x))
+    torch.cuda.synchronize()
+    got, streams = [], [torch.cuda.Stream() for _ in range(4)]
+
+    def work(stream):
+        with torch.cuda.stream(stream):
+            for _ in range(200):
+                y = g4.gai4_fp8_mm_t(*w, *g4.gai4_quantize_x_fp8(x))
+            stream.synchronize()
+            got.append(y)
+
+    threads = [threading.Thread(target=work, args=(s,)) for s in streams]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(got) == 4 and all(torch.equal(y, want) for y in got)

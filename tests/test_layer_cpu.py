@@ -167,3 +167,14 @@ def test_binding_refuses_wrong_shapes():
 def test_a_refused_call_raises_the_librarys_error():
     with pytest.raises(g4.Gai4Error):
         g4.gai4_rope_inv_freq(64, base=0.5, device="cpu")
+
+
+def test_binding_names_what_it_was_given():
+    with pytest.raises(TypeError):
+        g4.gai4_quantize_x_fp8(None)
+    with pytest.raises(TypeError):
+        g4.gai4_fp8_mm_t(3, 4, 5, 6)
+    with pytest.raises(ValueError, match="one CUDA device"):
+        g4.gai4_rms_norm(torch.zeros(2, 3))
+    with pytest.raises(ValueError, match="columns contiguous"):
+        g4.gai4_rms_norm(torch.zeros(2, 3, 4))
