@@ -1052,8 +1052,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
         __syncwarp();
     }
 
-    // What was issued lands before the CTAs leave; without a time-out it has.
+    // What was issued lands before the CTAs leave; without a time-out it has. (After
+    // one, a load of tokens may have been issued whose stage no load of weights has
+    // counted: no barrier tells when it lands, so it is given far more than its time.)
     __syncthreads();
+    if (abort_flag && threadIdx.x == 0)
+        for (int i = 0; i < 100; ++i) __nanosleep(1000);
     if (abort_flag && rank == 0 && threadIdx.x == 0) {
         for (int i = 0; i < min(loads, C::kStages); ++i)
             mbar_wait_drain(&full[i], (uint32_t)((loads - 1 - i) / C::kStages) & 1u, a.spin_limit, a.status);

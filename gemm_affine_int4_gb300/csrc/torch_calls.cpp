@@ -88,6 +88,7 @@ template <typename... Ts>
 PyObject* tuple(const Ts&... ts) {
     PyObject* all[] = {wrapped(ts)...};
     PyObject* r = PyTuple_New(sizeof...(Ts));
+    if (!r) throw python_error();
     for (size_t i = 0; i < sizeof...(Ts); ++i) PyTuple_SET_ITEM(r, (Py_ssize_t)i, all[i]);
     return r;
 }
