@@ -6,7 +6,7 @@
 // Every row is read and written once: bound by HBM, for a few tokens by the
 // launch. A block computes the sines of its tokens' angles once, in shared
 // memory, and turns all heads with them; no table over positions is kept or
-// read. 20011 tokens of 40 heads of 128, 16 bits: 63 to 66 us (92 to 96% of the
+// read. 20011 tokens of 40 heads of 128, 16 bits: 62 to 65 us (93 to 97% of the
 // measured HBM rate); 64 tokens: 2.3 us.
 //
 // An angle of a far position does not fit binary32. inv_freq (a double, in
@@ -95,6 +95,10 @@ __device__ __forceinline__ void load_pairs(const float* p, float* v) {
     }
 }
 
+// One pair; written out, so that the widths of access round alike.
+__device__ __forceinline__ float first(float x, float y, float c, float s) { return fmaf(x, c, -(y * s)); }
+__device__ __forceinline__ float second(float x, float y, float c, float s) { return fmaf(x, s, y * c); }
+
 // Turns W pairs: halves (p[j], q[j]), or neighbours along p and then q. 16-bit
 // elements are taken and rounded two at a time.
 template <typename T, int W, bool INTERLEAVED>
@@ -110,13 +114,13 @@ __device__ __forceinline__ void turn(Pack<T, W>& p, Pack<T, W>& q, const float (
             if constexpr (INTERLEAVED) {
                 const float x = low(a[i]), y = high(a[i]), u = low(b[i]), v = high(b[i]);
                 const int j = kWords + i;
-                a[i] = pack16<T>(x * c[i] - y * s[i], y * c[i] + x * s[i]);
-                b[i] = pack16<T>(u * c[j] - v * s[j], v * c[j] + u * s[j]);
+                a[i] = pack16<T>(first(x, y, c[i], s[i]), second(x, y, c[i], s[i]));
+                b[i] = pack16<T>(first(u, v, c[j], s[j]), second(u, v, c[j], s[j]));
             } else {
                 const float x = low(a[i]), u = high(a[i]), y = low(b[i]), v = high(b[i]);
                 const int j = 2 * i;
-                a[i] = pack16<T>(x * c[j] - y * s[j], u * c[j + 1] - v * s[j + 1]);
-                b[i] = pack16<T>(y * c[j] + x * s[j], v * c[j + 1] + u * s[j + 1]);
+                a[i] = pack16<T>(first(x, y, c[j], s[j]), first(u, v, c[j + 1], s[j + 1]));
+                b[i] = pack16<T>(second(x, y, c[j], s[j]), second(u, v, c[j + 1], s[j + 1]));
             }
         }
     } else if constexpr (INTERLEAVED) {
@@ -129,8 +133,8 @@ __device__ __forceinline__ void turn(Pack<T, W>& p, Pack<T, W>& q, const float (
 #pragma unroll
         for (int j = 0; j < W; ++j) {
             const float x = T::to_f32(e[2 * j]), y = T::to_f32(e[2 * j + 1]);
-            e[2 * j] = T::from_f32(x * c[j] - y * s[j]);
-            e[2 * j + 1] = T::from_f32(y * c[j] + x * s[j]);
+            e[2 * j] = T::from_f32(first(x, y, c[j], s[j]));
+            e[2 * j + 1] = T::from_f32(second(x, y, c[j], s[j]));
         }
 #pragma unroll
         for (int j = 0; j < W; ++j) {
@@ -141,18 +145,18 @@ __device__ __forceinline__ void turn(Pack<T, W>& p, Pack<T, W>& q, const float (
 #pragma unroll
         for (int j = 0; j < W; ++j) {
             const float x = T::to_f32(p.e[j]), y = T::to_f32(q.e[j]);
-            p.e[j] = T::from_f32(x * c[j] - y * s[j]);
-            q.e[j] = T::from_f32(y * c[j] + x * s[j]);
+            p.e[j] = T::from_f32(first(x, y, c[j], s[j]));
+            q.e[j] = T::from_f32(second(x, y, c[j], s[j]));
         }
     }
 }
 
 // A chunk is W pairs of a head (two accesses of W elements each way, half of the
 // turned channels apart, so that neighbouring threads' lie side by side) or, past
-// them, W channels that are copied. A thread has one chunk of its block's rows
+// them, two accesses that are copied. A thread has one chunk of its block's rows
 // (token, head), kBatch rows at a time: their loads are under way while the
 // sines are computed.
-template <typename T, int W, bool INTERLEAVED, int kBatch>
+template <typename T, int W, bool INTERLEAVED, bool PASS, int kBatch>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
     using S = typename T::storage;
     using V = typename Vec<T, W>::type;
@@ -166,7 +170,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const int h0 = (int)((int64_t)all * part / a.head_split), heads = (int)((int64_t)all * (part + 1) / a.head_split) - h0;
     const int rows = tokens * heads;
     const float per_head = 1.0f / (float)heads;   // rows are below 2^21: (r + 1/2) / heads is never taken across a whole number
-    const int turned = a.half / W, chunks = turned + (a.pass ? (a.d - 2 * a.half) / W : 0);
+    // (copied accesses: the second of a chunk half of them apart, none for the last if they are odd)
+    const int turned = a.half / W, copied = PASS ? (a.d - 2 * a.half) / W : 0, apart = (copied + 1) / 2;
+    const int chunks = turned + apart;
     const int wide = chunks < kThreads ? kThreads / chunks : 1;   // rows that the block's threads take at a time
     const int tid = threadIdx.x;
     int chunk = chunks < kThreads ? tid % chunks : tid, r = chunks < kThreads ? tid / chunks : 0;
@@ -177,9 +183,16 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     Pack<T, W> p[kBatch], q[kBatch];
     // (single elements of a neighbouring pair are next to each other)
     constexpr bool kSingle = INTERLEAVED && W == 1;
-    const int next = kSingle ? 1 : a.half;
+    int next = kSingle ? 1 : a.half;   // from the first access to the second
+    bool two = true;
     const auto load = [&]() {
-        const int at = chunk < turned ? (kSingle ? 2 : W) * chunk : 2 * a.half + (chunk - turned) * W;
+        int at = (kSingle ? 2 : W) * chunk;
+        if constexpr (PASS) {
+            const bool turn = chunk < turned;
+            next = turn ? (kSingle ? 1 : a.half) : apart * W;
+            two = turn || chunk - turned + apart < copied;
+            if (!turn) at = 2 * a.half + (chunk - turned) * W;
+        }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int row = r + u * wide;
@@ -193,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
             to[u] = static_cast<S*>(a.out[which]) + token * a.out_stride[which] + (int64_t)head * a.d + at;
             pairs[u] = t * a.half + chunk * (INTERLEAVED && W > 1 ? W / 2 : W);
             p[u].v = *reinterpret_cast<const V*>(src);
-            if (chunk < turned) q[u].v = *reinterpret_cast<const V*>(src + next);
+            if (two) q[u].v = *reinterpret_cast<const V*>(src + next);
         }
     };
     load();
@@ -215,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 if (first + u * wide >= rows) continue;
-                if (chunk < turned) {
+                if (!PASS || chunk < turned) {
                     float c[W], s[W];
                     if constexpr (INTERLEAVED && W > 1) {
                         // half of the pairs in each access
@@ -229,9 +242,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                         load_pairs<W>(cs[1] + pairs[u], s);
                     }
                     turn<T, W, INTERLEAVED>(p[u], q[u], c, s);
-                    *reinterpret_cast<V*>(to[u] + next) = q[u].v;
                 }
                 *reinterpret_cast<V*>(to[u]) = p[u].v;
+                if (two) *reinterpret_cast<V*>(to[u] + next) = q[u].v;
             }
             r += kBatch * wide;
             first = r;
@@ -261,12 +274,15 @@ int width(const RopeArgs& a) {
 
 template <typename T, int W, bool INTERLEAVED>
 cudaError_t rope_launch(RopeArgs a, cudaStream_t s) {
-    // Many tokens: two rows a thread at a time, twice a block; but enough
-    // blocks to go round. In us, (rows, times) (1, 4), (2, 1), (2, 2): 20011 tokens
-    // of 40 heads of 128, bf16, 66, 87, 63; 4099 of 32 of 80, f32, 18, -, 17.
-    constexpr int kMany = 2, kTimes = 2;
+    // Many tokens, 16 bits: two rows a thread at a time, twice a block; f32: one, four
+    // times; but enough blocks to go round. In us, (rows, times) (2, 2), (1, 2), (1, 4):
+    // 20011 tokens of 40 heads of 128, bf16, 62, 80, 65; 3000 of them 13.1, 15.3, 14.1;
+    // f32: 4099 of 40 of 128 31, 29, 29, 4099 of 32 of 80, 32 channels turned, 17.8, 21.8,
+    // 16.8.
+    constexpr int kMany = T::kBytes == 2 ? 2 : 1, kTimes = T::kBytes == 2 ? 2 : 4;
     const int64_t heads = a.heads[0] + a.heads[1];
-    const int64_t per_token = heads * (a.half / W + (a.pass ? (a.d - 2 * a.half) / W : 0));   // chunks
+    const bool pass = a.pass && a.d > 2 * a.half;
+    const int64_t per_token = heads * (a.half / W + (pass ? ((a.d - 2 * a.half) / W + 1) / 2 : 0));   // chunks
     const int64_t sms = num_sms();
     int64_t per = 1, split = 1;
     const bool many = a.tokens * per_token > 4 * sms * kThreads;
@@ -278,8 +294,12 @@ cudaError_t rope_launch(RopeArgs a, cudaStream_t s) {
     a.head_split = (int)split;
     const int64_t blocks = (a.tokens + per - 1) / per * split;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    return launch_pdl(many ? rope_kernel<T, W, INTERLEAVED, kMany> : rope_kernel<T, W, INTERLEAVED, 1>, dim3((unsigned)blocks),
-                      dim3(kThreads), 0, s, a);
+    const dim3 grid((unsigned)blocks), block(kThreads);
+    if (pass)
+        return launch_pdl(many ? rope_kernel<T, W, INTERLEAVED, true, kMany> : rope_kernel<T, W, INTERLEAVED, true, 1>, grid,
+                          block, 0, s, a);
+    return launch_pdl(many ? rope_kernel<T, W, INTERLEAVED, false, kMany> : rope_kernel<T, W, INTERLEAVED, false, 1>, grid, block,
+                      0, s, a);
 }
 
 template <typename T>

@@ -34,7 +34,8 @@ def positions(n, far, seed=1):
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("n,hq,hkv,d,rot,far", [
     (1, 1, 1, 64, 64, 8), (64, 32, 8, 128, 128, 131072), (777, 7, 1, 80, 20, 4000), (5, 3, 2, 96, 24, 2 ** 31 - 1),
-    (130, 16, 16, 256, 64, 10 ** 6), (33, 2, 0, 6, 2, 100), (9, 40, 8, 1024, 1024, 5000), (2000, 1, 1, 34, 34, 70000)])
+    (130, 16, 16, 256, 64, 10 ** 6), (33, 2, 0, 6, 2, 100), (9, 40, 8, 1024, 1024, 5000), (2000, 1, 1, 34, 34, 70000),
+    (3000, 5, 2, 72, 48, 9000), (21, 4, 1, 1000, 40, 9000)])
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_rope(dt, n, hq, hkv, d, rot, far, interleaved):
     qkv = rand(n, hq + 2 * hkv, d, dtype=T[dt])
