@@ -176,6 +176,67 @@ __global__ void __launch_bounds__(kUnits == 4 ? 512 : 1024) rms_norm_kernel(cons
     } while (LOOP && first < a.rows);
 }
 
+// y in T alone, without a residual, many 16-bit rows: as the kernel above with LOOP,
+// but a row stays as it was loaded until its root is known, half of the registers
+// of its values.
+template <typename T, int kUnits>
+__global__ void __launch_bounds__(512, 2) rms_norm_plain_kernel(const __grid_constant__ NormArgs a) {
+    using S = typename T::storage;
+    pdl_launch_dependents();
+    pdl_wait();   // the kernels before this one are complete: global memory may be read
+    __shared__ float part[2][16][kMaxWarps];
+    Eight<T, true> x[kUnits], next[kUnits], gain[kUnits];
+    const int col0 = threadIdx.x * 8, step = blockDim.x * 8;
+    int64_t first = (int64_t)blockIdx.x * blockDim.y;   // row of the block's first threads
+    const auto load = [&](int64_t row) {
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j) {
+            const int col = col0 + j * step;
+            if (row < a.rows && col < a.cols)
+                next[j].load(static_cast<const S*>(a.x) + row * a.x_stride + col, 8);
+            else
+                next[j].zero();
+        }
+    };
+    load(first + threadIdx.y);
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j) load_gain<T, true>(a, col0 + j * step, gain[j]);
+    int turn = 0;
+    do {
+        const int64_t row = first + threadIdx.y;
+        first += (int64_t)gridDim.x * blockDim.y;
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j) {
+            float v[8];
+            next[j].values(v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s = fmaf(v[i], v[i], s);
+            x[j] = next[j];
+        }
+        load(first + threadIdx.y);
+        const float inv = inverse_root(row_sum(s, part[turn]), a);
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j) {
+            const int col = col0 + j * step;
+            if (row >= a.rows || col >= a.cols) continue;
+            x[j].keep();
+            float v[8], g[8];
+            x[j].values(v);
+            if (a.gain) {
+                gain[j].keep();
+                gain[j].values(g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] *= g[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= inv;
+            store8<T, true>(static_cast<S*>(a.out) + row * a.cols + col, 8, v);
+        }
+        turn ^= 1;
+    } while (first < a.rows);
+}
+
 // rows of any length, one a block, read twice (nothing is written in between:
 // outputs may lie on inputs)
 template <typename T, bool VEC>
@@ -296,7 +357,7 @@ cudaError_t norm_launch(const NormArgs& a, cudaStream_t s) {
     // 158 us with one, 130 with two), and blocks that take row after row (125 us).
     // Those pay off for 16-bit rows only: 10000 x 5120 in f32 takes 96 us without,
     // 134 with, as registers run out. Without a residual half as much is read at a
-    // time: four eights (80 us, two 87).
+    // time: four eights (y alone, before it had a kernel of its own: 80 us, two 87).
     const bool few = a.rows <= 2 * num_sms();
     const bool loop = !few && T::kBytes == 2 && VEC && wide > 1;
     int units = few || wide == 1 ? 1 : loop && !a.residual && wide > 4 ? 4 : 2;
@@ -306,6 +367,16 @@ cudaError_t norm_launch(const NormArgs& a, cudaStream_t s) {
     // (a block of at least a warp)
     const dim3 block(threads, threads == 16 ? std::max(per, 2) : per);
     const int64_t blocks = (a.rows + block.y - 1) / block.y;
+    if (loop && a.out && !a.codes && !a.residual && !a.residual_out) {
+        // In us, and with the kernel above: bf16 20011 x 5120 69, 80; 10000 x 4096 28, 34;
+        // 30000 x 1024 21, 27; 4000 x 14336 39, 51.
+        if constexpr (T::kBytes == 2 && VEC) {
+            units = wide >= 4 ? 4 : 2;
+            const int tx = 32 * (int)((wide + units - 1) / units), ty = std::max(1, 256 / tx);
+            const dim3 grid((unsigned)std::min<int64_t>((a.rows + ty - 1) / ty, (int64_t)num_sms() * (1024 / (tx * ty))));
+            return launch_pdl(units == 4 ? rms_norm_plain_kernel<T, 4> : rms_norm_plain_kernel<T, 2>, grid, dim3(tx, ty), 0, s, a);
+        }
+    }
     if (loop) {
         const dim3 grid((unsigned)std::min<int64_t>(blocks, (int64_t)num_sms() * std::max(1, 1024 / (threads * per))));
         if constexpr (T::kBytes == 2 && VEC)

@@ -107,7 +107,7 @@ def test_rope_keeps_infinities_and_nan_to_their_pairs():
 
 SHAPES = [(1, 1), (1, 4096), (3, 7), (64, 4096), (5, 8200), (700, 128), (701, 129), (1000, 5120), (33, 1000), (2, 32768),
           (3, 32776), (2, 100001), (400, 17), (350, 12288), (5000, 100),
-          (1003, 16384), (320, 16392), (900, 511)]
+          (1003, 16384), (320, 16392), (900, 511), (400, 264), (777, 1032), (1500, 5120), (3001, 520)]
 
 
 def check_codes(codes, scales, y, rel, root=None):
@@ -140,7 +140,8 @@ def test_norm(dt, rows, cols):
             assert torch.equal(plain.residual, (x.float() + r.float()).to(T[dt]))
             assert torch.equal(plain.residual, only.residual) and torch.equal(plain.residual, both.residual)
         check_codes(only.codes, only.scales, y, rel)
-        assert torch.equal(both.out, plain.out) and torch.equal(both.scales, only.scales)
+        within(both.out, y, y.abs() * (rel + U[T[dt]]) + TINY[T[dt]], "norm beside codes")
+        assert torch.equal(both.scales, only.scales)
         assert torch.equal(both.codes.view(torch.uint8), only.codes.view(torch.uint8))
 
 
@@ -180,6 +181,19 @@ def test_norm_strided_rows_in_place_and_without_gain():
             # (rows of another alignment may be summed in another order)
             within(a, y, y.abs() * (rel + U[dt]) + TINY[dt], f"in place {cols} {off}")
             assert torch.equal(b, got.residual)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(400, 264), (1000, 2048), (500, 16384), (700, 1001), (310, 20000)])
+def test_norm_of_many_rows_in_place(dt, rows, cols):
+    x, r, gain = rand(rows, cols, dtype=T[dt]), rand(rows, cols, seed=1, dtype=T[dt]), rand(cols, seed=2, dtype=T[dt])
+    for residual in (None, r):
+        h, y, rel = norm64(x, gain, 1e-6, residual)
+        a, b = x.clone(), None if residual is None else residual.clone()
+        got = g4.gai4_rms_norm(a, gain, residual=b, out=a, residual_out=b)
+        assert got.out is a
+        within(a, y, y.abs() * (rel + U[T[dt]]) + TINY[T[dt]], "in place")
+        assert b is None or torch.equal(b, (x.float() + r.float()).to(T[dt]))
 
 
 def test_norm_rows_of_zeros_and_of_no_numbers():
