@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads) quantize_x_fp8_kernel(const typename
 
 // One block of 128 x 128 a CTA: thread t holds eights t % 16 of the rows
 // t / 16 + 16 j, in registers from the maximum to the codes: as loaded, so that 16-bit
-// inputs leave room for five CTAs an SM (14336 x 5120: bf16 37 us, 46 with the values
+// inputs leave room for five CTAs an SM (14336 x 5120: bf16 34 us; 46 with the values
 // kept in binary32 and three CTAs; f32 55 us, 98% of the measured HBM rate).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads, VEC && T::kBytes == 2 ? 5 : 3) quantize_fp8_kernel(const typename T::storage* __restrict__ w,

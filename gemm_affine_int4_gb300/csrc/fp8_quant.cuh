@@ -5,8 +5,8 @@
 // largest e4m3 value. Quotients of 16-bit inputs lie on the border between two
 // codes now and then (448 x / a has few bits), so the quotient is rounded
 // correctly to binary32 before the conversion: an exact tie stays one. A
-// product with 448 / a or with the scale's reciprocal would break such ties at
-// random.
+// product with 448 / a as one number, or with the scale's reciprocal, would break
+// such ties at random.
 #pragma once
 
 #include "common.cuh"
@@ -25,26 +25,22 @@ __device__ __forceinline__ float max_abs(float a, float b) {
 }
 
 struct Scale {
-    float part;   // amax / 512, amax at least 2^-100 (infinite or NaN if the group holds such a value)
-    float rcp;
+    float amax;      // at least 2^-100 (infinite or NaN if the group holds such a value)
+    float f, rest;   // 448 / amax as a sum of two
 };
 __device__ __forceinline__ Scale scale_of(float amax) {
     Scale s;
-    s.part = max_abs(amax, kLeastMax) * 0x1p-9f;
-    s.rcp = __frcp_rn(s.part);
+    s.amax = max_abs(amax, kLeastMax);
+    s.f = __fdiv_rn(448.0f, s.amax);
+    s.rest = fmaf(-s.f, s.amax, 448.0f) * (s.f * (1.0f / 448.0f));   // the residual is exact
     return s;
 }
-__device__ __forceinline__ float scale_value(const Scale& s) { return __fdiv_rn(s.part, 0.875f); }
+__device__ __forceinline__ float scale_value(const Scale& s) { return __fdiv_rn(s.amax, 448.0f); }
 
-// 448 x / amax, rounded to nearest: c = 448 x 2^-9 (exact for 16-bit x, no
-// overflow), a first quotient by amax 2^-9 from its correctly rounded
-// reciprocal, and one correction by the exact residual. If amax is infinite or
-// NaN the residual is NaN, and with it every code of the group.
-__device__ __forceinline__ float quotient(float x, const Scale& s) {
-    const float c = x * 0.875f;
-    const float t = c * s.rcp;
-    return fmaf(fmaf(-t, s.part, c), s.rcp, t);
-}
+// 448 x / amax, good to 2^-46 before its one rounding, so that what is exact in
+// binary32 stays exact. If amax is infinite or NaN the residual is NaN, and with it
+// every code of the group.
+__device__ __forceinline__ float quotient(float x, const Scale& s) { return fmaf(x, s.f, x * s.rest); }
 
 // two codes, `lo` in the low byte
 __device__ __forceinline__ uint32_t codes2(float lo, float hi) {

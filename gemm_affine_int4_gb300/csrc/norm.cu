@@ -93,12 +93,9 @@ __device__ __forceinline__ float begin8(const NormArgs& a, const Inputs<T, VEC>&
         for (int i = 0; i < 8; ++i) p[i] *= g[i];
     }
     if (write && a.codes) {   // (uniform)
-        amax = max_abs(group_max(amax8(p)), kLeastMax);
-        const float f = __fdiv_rn(448.0f, amax);
-        float q[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = p[i] * f;
-        if (in) store_codes8<VEC>(a.codes + at, left, codes8(q));
+        const Scale scale = scale_of(group_max(amax8(p)));
+        amax = scale.amax;
+        if (in) store_codes8<VEC>(a.codes + at, left, codes8(p, scale));
     }
     return sum;
 }
@@ -323,12 +320,10 @@ __global__ void __launch_bounds__(32 * kRowWarps, 6) rms_norm_codes_kernel(const
         if (r) r += 256;
         if (g) g += 256;
         load(left - 256);
-        const float amax = max_abs(group_max(amax8(p)), kLeastMax), f = __fdiv_rn(448.0f, amax);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = p[i] * f;
+        const Scale scale = scale_of(group_max(amax8(p)));
         if (left > 0) {
-            store_codes8<VEC>(codes + at, left, codes8(q));
-            if ((lane & 15) == 0) maximum[at / kGroup + (lane >> 4)] = amax;
+            store_codes8<VEC>(codes + at, left, codes8(p, scale));
+            if ((lane & 15) == 0) maximum[at / kGroup + (lane >> 4)] = scale.amax;
         }
     }
     const float inv = inverse_root(warp_sum(sum), a);

@@ -502,9 +502,8 @@ size_t gai4_kv_attention_workspace_bytes(int64_t q_heads, int64_t kv_heads, int 
  * The represented value is code * scale. Quantization takes, of the block's
  * values v,
  *   a = max(max |v|, 2^-100),  scale = RN(a / 448),
- *   code = the e4m3 value nearest to q, ties to even, q = RN(448 v / a)
- * (for float inputs 448 v is rounded first). A block that holds an infinity or
- * a NaN represents NaN throughout.
+ *   code = the e4m3 value nearest to q, ties to even, q = RN(448 v / a).
+ * A block that holds an infinity or a NaN represents NaN throughout.
  * (No counterpart on the pages; an addition of this library.)
  * ======================================================================== */
 
@@ -560,8 +559,7 @@ gai4_status gai4_rope(const void* q, int64_t q_token_stride, void* q_out, int64_
  *   out [rows, cols] T or NULL: y, rounded
  *   codes [rows, cols] and scales [rows, ceil(cols / 128)], or both NULL: y as
  *         activations in e4m3 (not rounded to T in between; codes are those of
- *         h * gain, nearest to its binary32 product with 448 / a, a of its
- *         blocks, and scales are a / (448 sqrt(...)))
+ *         h * gain, a of its blocks, and scales are a / (448 sqrt(...)))
  * h, the sum, h * gain and y are binary32; a sum of squares beyond it (|h| above
  * 1e19) counts as infinite, and squares below it as zero. Any cols >= 1. out or residual_out (not both) may be x or
  * residual where those are contiguous; outputs must not overlap the inputs or

@@ -56,8 +56,7 @@ def quantize_ref(x, block_rows):
     p = torch.nn.functional.pad(x.float(), (0, -C % 128, 0, -R % block_rows))
     b = p.unflatten(0, (-1, block_rows)).unflatten(2, (-1, 128))
     a = b.abs().amax((1, 3), keepdim=True).clamp(min=2.0 ** -100)
-    # binary32's own division: 448 v / a with the power of two taken out
-    q = (b * 0.875) / a * 512
+    q = (b.double() * 448 / a.double()).float()
     q = q.flatten(2).flatten(0, 1)[:R, :C]
     return q.to(E4M3), (a / torch.full_like(a, 448.0))[:, 0, :, 0]
 
