@@ -205,7 +205,8 @@ struct FewArgs {
     long long spin_limit;
 };
 
-// a share of the registers of warps 0-3 goes to warps 4-7: 128 x 56 + 128 x 200 = 256 x 128
+// A share of the registers of warps 0-3 goes to warps 4-7: 128 x 56 + 128 x 200 = 256 x 128.
+// The four warps of a warpgroup execute this one instruction, ahead of their roles.
 template <int MT>
 __device__ __forceinline__ void give_registers() {
     if constexpr (MT == 128) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -267,115 +268,114 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     S* out = static_cast<S*>(a.out);
     bool freed = false;   // (of warp 3)
 
-    if (warp == 0) {
+    if (warp < 4) {
         give_registers<MT>();
-        // the first stages' weights before the kernels ahead of this one have finished
-        const uint32_t to = smem_u32(ring);
-        const int first = min(count, C::kStages);
-        for (int i = 0; i < first; ++i) {
-            expect_warp(smem_u32(&full[i]), C::kStage);
-            load_warp(to + i * C::kStage, &w_map, smem_u32(&full[i]), (b0 + i) * kBlock, (int)n0);
-        }
-        pdl_wait();
-        if (lane == 0) loads = first;
-        for (int i = 0; i < first; ++i)
-            load_warp(to + i * C::kStage + kTile * kBlock, &x_map, smem_u32(&full[i]), (b0 + i) * kBlock, (int)m0);
-        int slot = 0;
-        uint32_t phase = 0;
-        for (int i = first; i < count; ++i) {
-            if (!warp_wait(&empty[slot], phase, ctl)) break;
-            const uint32_t st = to + slot * C::kStage;
-            expect_warp(smem_u32(&full[slot]), C::kStage);
-            load_warp(st, &w_map, smem_u32(&full[slot]), (b0 + i) * kBlock, (int)n0);
-            load_warp(st + kTile * kBlock, &x_map, smem_u32(&full[slot]), (b0 + i) * kBlock, (int)m0);
-            if (lane == 0) loads = i + 1;
-            if (++slot == C::kStages) {
-                slot = 0;
-                phase ^= 1u;
+        if (warp == 0) {
+            // the first stages' weights before the kernels ahead of this one have finished
+            const uint32_t to = smem_u32(ring);
+            const int first = min(count, C::kStages);
+            for (int i = 0; i < first; ++i) {
+                expect_warp(smem_u32(&full[i]), C::kStage);
+                load_warp(to + i * C::kStage, &w_map, smem_u32(&full[i]), (b0 + i) * kBlock, (int)n0);
             }
-        }
-    } else if (warp == 1) {
-        give_registers<MT>();
-        pdl_wait();   // (before every first wait with a limit: a kernel ahead may run for long)
-        const bool ready = warp_wait(&tmem_ready, 0, ctl);
-        fence_after();
-        const uint32_t tmem = tmem_slot, from = smem_u32(ring);
-        int slot = 0, buf = 0;
-        uint32_t phase = 0, d_phase = 1;   // (the first round finds every buffer free)
-        for (int i = 0; ready && i < count; ++i) {
-            if (!__all_sync(0xffffffffu, both_ready(smem_u32(&full[slot]), phase, smem_u32(&d_empty[buf]), d_phase)) &&
-                !(warp_wait(&full[slot], phase, ctl) && warp_wait(&d_empty[buf], d_phase, ctl)))
-                break;
+            pdl_wait();
+            if (lane == 0) loads = first;
+            for (int i = 0; i < first; ++i)
+                load_warp(to + i * C::kStage + kTile * kBlock, &x_map, smem_u32(&full[i]), (b0 + i) * kBlock, (int)m0);
+            int slot = 0;
+            uint32_t phase = 0;
+            for (int i = first; i < count; ++i) {
+                if (!warp_wait(&empty[slot], phase, ctl)) break;
+                const uint32_t st = to + slot * C::kStage;
+                expect_warp(smem_u32(&full[slot]), C::kStage);
+                load_warp(st, &w_map, smem_u32(&full[slot]), (b0 + i) * kBlock, (int)n0);
+                load_warp(st + kTile * kBlock, &x_map, smem_u32(&full[slot]), (b0 + i) * kBlock, (int)m0);
+                if (lane == 0) loads = i + 1;
+                if (++slot == C::kStages) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
+            }
+        } else if (warp == 1) {
+            pdl_wait();   // (before every first wait with a limit: a kernel ahead may run for long)
+            const bool ready = warp_wait(&tmem_ready, 0, ctl);
             fence_after();
-            const uint32_t st = desc_lo(from + slot * C::kStage);
-            block_products(tmem + buf * MT, st, st + (kTile * kBlock >> 4), idesc(kTile, MT), &empty[slot], &d_full[buf]);
-            if (lane == 0) products = i + 1;
-            if (++slot == C::kStages) {
-                slot = 0;
-                phase ^= 1u;
-            }
-            if (++buf == C::kBufs) {
-                buf = 0;
-                d_phase ^= 1u;
-            }
-        }
-    } else if (warp == 2) {
-        give_registers<MT>();
-        pdl_wait();
-        // Lanes: 4 blocks of K by 8 tokens. A batch is copied while the one before
-        // it lands and is multiplied in place.
-        const int k = lane & 3, i0 = lane >> 2;
-        const int batches = (count + kFewBatch - 1) / kFewBatch;
-        const float* sw = a.w_scales + (int64_t)tile * a.blocks + b0 + k;
-        const float* sx = a.x_scales + (m0 + i0) * a.blocks + b0 + k;
-        const auto start = [&](int j) {
-            const bool in = j * kFewBatch + k < count;
-            float* to = &scales[j % kFewBatches][k][i0];
-#pragma unroll 4
-            for (int t = 0; t < MT; t += 8) {
-                const bool there = in && t + i0 < live;
-                copy4(to + t, there ? sx + (int64_t)t * a.blocks + j * kFewBatch : a.x_scales, there);
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            return in ? sw[j * kFewBatch] : 0.f;
-        };
-        float w = start(0);
-        for (int j = 0; j < batches; ++j) {
-            float next = 0.f;
-            if (j + 1 < batches) {
-                const int n = j + 1;
-                if (n >= kFewBatches &&
-                    !warp_wait(&s_empty[n % kFewBatches], (uint32_t)(n / kFewBatches - 1) & 1u, ctl))
+            const uint32_t tmem = tmem_slot, from = smem_u32(ring);
+            int slot = 0, buf = 0;
+            uint32_t phase = 0, d_phase = 1;   // (the first round finds every buffer free)
+            for (int i = 0; ready && i < count; ++i) {
+                if (!__all_sync(0xffffffffu, both_ready(smem_u32(&full[slot]), phase, smem_u32(&d_empty[buf]), d_phase)) &&
+                    !(warp_wait(&full[slot], phase, ctl) && warp_wait(&d_empty[buf], d_phase, ctl)))
                     break;
-                next = start(n);
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-            } else {
-                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                fence_after();
+                const uint32_t st = desc_lo(from + slot * C::kStage);
+                block_products(tmem + buf * MT, st, st + (kTile * kBlock >> 4), idesc(kTile, MT), &empty[slot], &d_full[buf]);
+                if (lane == 0) products = i + 1;
+                if (++slot == C::kStages) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
+                if (++buf == C::kBufs) {
+                    buf = 0;
+                    d_phase ^= 1u;
+                }
             }
-            float* mine = &scales[j % kFewBatches][k][i0];
+        } else if (warp == 2) {
+            pdl_wait();
+            // Lanes: 4 blocks of K by 8 tokens. A batch is copied while the one before
+            // it lands and is multiplied in place.
+            const int k = lane & 3, i0 = lane >> 2;
+            const int batches = (count + kFewBatch - 1) / kFewBatch;
+            const float* sw = a.w_scales + (int64_t)tile * a.blocks + b0 + k;
+            const float* sx = a.x_scales + (m0 + i0) * a.blocks + b0 + k;
+            const auto start = [&](int j) {
+                const bool in = j * kFewBatch + k < count;
+                float* to = &scales[j % kFewBatches][k][i0];
 #pragma unroll 4
-            for (int t = 0; t < MT; t += 8) mine[t] *= w;
-            mbar_arrive(&s_full[j % kFewBatches]);
-            w = next;
-        }
-    } else if (warp == 3) {
-        give_registers<MT>();
-        // Tensor memory is taken after the kernels before this one have finished,
-        // and the next one may start after it is taken; and it is free again
-        // before the cluster's CTAs wait for each other's sums. So no CTA holds
-        // columns while it waits for one that may need them.
-        pdl_wait();
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
-                     "r"(C::kCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-        fence_before();
-        pdl_launch_dependents();
-        if (lane == 0) mbar_arrive(&tmem_ready);
-        if (warp_wait(&tmem_done, 0, ctl)) {
-            fence_after();
-            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_slot), "r"(C::kCols) : "memory");
-            freed = true;
+                for (int t = 0; t < MT; t += 8) {
+                    const bool there = in && t + i0 < live;
+                    copy4(to + t, there ? sx + (int64_t)t * a.blocks + j * kFewBatch : a.x_scales, there);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                return in ? sw[j * kFewBatch] : 0.f;
+            };
+            float w = start(0);
+            for (int j = 0; j < batches; ++j) {
+                float next = 0.f;
+                if (j + 1 < batches) {
+                    const int n = j + 1;
+                    if (n >= kFewBatches &&
+                        !warp_wait(&s_empty[n % kFewBatches], (uint32_t)(n / kFewBatches - 1) & 1u, ctl))
+                        break;
+                    next = start(n);
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");
+                } else {
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                }
+                float* mine = &scales[j % kFewBatches][k][i0];
+#pragma unroll 4
+                for (int t = 0; t < MT; t += 8) mine[t] *= w;
+                mbar_arrive(&s_full[j % kFewBatches]);
+                w = next;
+            }
+        } else if (warp == 3) {
+            // Tensor memory is taken after the kernels before this one have finished,
+            // and the next one may start after it is taken; and it is free again
+            // before the cluster's CTAs wait for each other's sums. So no CTA holds
+            // columns while it waits for one that may need them.
+            pdl_wait();
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                         "r"(C::kCols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+            fence_before();
+            pdl_launch_dependents();
+            if (lane == 0) mbar_arrive(&tmem_ready);
+            if (warp_wait(&tmem_done, 0, ctl)) {
+                fence_after();
+                asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_slot), "r"(C::kCols) : "memory");
+                freed = true;
+            }
         }
     } else {
         if constexpr (MT == 128) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
