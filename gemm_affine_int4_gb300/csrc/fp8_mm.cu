@@ -482,11 +482,15 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
         }
     }
 
-    // What was issued lands before the CTA leaves; without a time-out it has: the
-    // commit of the last products was waited for above, and so were the sums sent
-    // to this CTA.
+    // What was issued lands before the CTA leaves. Without a time-out it has but for
+    // the other commits of the last products, which nobody had to wait for yet: a
+    // thread each does.
     __syncthreads();
-    if (!abort_flag) return;
+    if (!abort_flag) {
+        if (threadIdx.x < min(count, C::kStages))
+            mbar_wait_drain(&empty[threadIdx.x], (uint32_t)((count - 1 - (int)threadIdx.x) / C::kStages) & 1u, a.spin_limit, a.status);
+        return;
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < min(loads, C::kStages); ++i)
             mbar_wait_drain(&full[i], (uint32_t)((loads - 1 - i) / C::kStages) & 1u, a.spin_limit, a.status);
@@ -1052,10 +1056,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
         __syncwarp();
     }
 
-    // What was issued lands before the CTAs leave; without a time-out it has. (After
+    // What was issued lands before the CTAs leave. Without a time-out it has but for
+    // the other commits of the last products, as in few_kernel. (After
     // one, a load of tokens may have been issued whose stage no load of weights has
     // counted: no barrier tells when it lands, so it is given far more than its time.)
     __syncthreads();
+    const int fills = (tiles - pair + a.pairs - 1) / a.pairs * a.blocks;
+    if (!abort_flag && threadIdx.x < min(fills, C::kStages))
+        mbar_wait_drain(&empty[threadIdx.x], (uint32_t)((fills - 1 - (int)threadIdx.x) / C::kStages) & 1u, a.spin_limit, a.status);
     if (abort_flag && threadIdx.x == 0)
         for (int i = 0; i < 100; ++i) __nanosleep(1000);
     if (abort_flag && rank == 0 && threadIdx.x == 0) {
