@@ -73,6 +73,7 @@ SIGNATURES = {
     "gai4_quantize_x_fp8": ([_P, _I64, _P, _P, _I, _I64, _I64, _P], _I),
     "gai4_quantize_fp8": ([_P, _P, _P, _I, _I64, _I64, _P], _I),
     "gai4_fp8_mm_t": ([_P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _P], _I),
+    "gai4_check_fp8_mm_wait": ([_P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I, _I, _I64, _P, _P], _I),
 }
 
 
@@ -670,4 +671,22 @@ def gai4_check_bounded_wait(arrive: bool, limit_cycles: int, status: torch.Tenso
     _check("gai4_check_bounded_wait", lib().gai4_check_bounded_wait(1 if arrive else 0, int(limit_cycles),
                                                                    _ptr(status), _stream(stream)))
     (stream if stream is not None else torch.cuda.current_stream()).synchronize()
+    return int(status.item())
+
+
+def gai4_check_fp8_mm_wait(w_codes, w_scales, x_codes, x_scales, out, withheld: int, blocks: int, limit_cycles: int) -> int:
+    """gai4_fp8_mm_t on the current stream with some loads withheld from block
+    `blocks` of K on (bits 0 to 3 of `withheld`, see gai4.h); returns the kernel's
+    status word after the stream has finished: 0, or GAI4_ERR_TIMEOUT, and `out`
+    is then undefined."""
+    (M, K), N, blocks_k = x_codes.shape, w_codes.shape[0], -(-x_codes.shape[1] // 128)
+    if (tuple(w_codes.shape) != (N, K) or tuple(x_scales.shape) != (M, blocks_k) or tuple(out.shape) != (M, N)
+            or tuple(w_scales.shape) != (-(-N // 128), blocks_k) or w_codes.element_size() != 1 or x_codes.element_size() != 1
+            or w_scales.dtype != torch.float32 or x_scales.dtype != torch.float32):
+        raise ValueError("gai4: operands as gai4_fp8_mm_t takes them, out [M, N]")
+    status = torch.zeros(1, dtype=torch.int32, device=out.device)
+    _check("gai4_check_fp8_mm_wait", lib().gai4_check_fp8_mm_wait(
+        _ptr(w_codes), _ptr(w_scales), _ptr(x_codes), _ptr(x_scales), _ptr(out), _dtype(out), M, N, K, int(withheld),
+        int(blocks), int(limit_cycles), _ptr(status), _stream(None)))
+    torch.cuda.current_stream().synchronize()
     return int(status.item())

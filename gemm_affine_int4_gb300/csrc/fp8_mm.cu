@@ -91,6 +91,24 @@ __device__ __forceinline__ uint32_t mapa(uint32_t a, uint32_t rank) {
     return r;
 }
 
+__device__ __forceinline__ void store_at(uint32_t cluster_addr, int v) {
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ int load_at(uint32_t cluster_addr) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
+// How often the i-th of `of` places has been used by `count` uses in turn, and
+// the parity of the last use (of one at least)
+__device__ __forceinline__ int rounds(int count, int of, int i) { return count > i ? (count - 1 - i) / of + 1 : 0; }
+__device__ __forceinline__ uint32_t last_phase(int count, int of, int i) { return (uint32_t)(rounds(count, of, i) - 1) & 1u; }
+// bytes that were announced and will not come
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
 // Issued by a converged warp, one lane of which is elected: a barrier's bytes
 // to come, and a load that reports to it.
 __device__ __forceinline__ void expect_warp(uint32_t bar, uint32_t bytes) {
@@ -201,6 +219,7 @@ struct FewArgs {
     int blocks;      // of K
     int m_chunks;
     int split;       // cluster size
+    int until[2];    // loads of CTAs of even and odd rank end before this block
     int* status;
     long long spin_limit;
 };
@@ -273,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
         if (warp == 0) {
             // the first stages' weights before the kernels ahead of this one have finished
             const uint32_t to = smem_u32(ring);
-            const int first = min(count, C::kStages);
+            const int bring = min(count, a.until[rank & 1]), first = min(bring, C::kStages);
             for (int i = 0; i < first; ++i) {
                 expect_warp(smem_u32(&full[i]), C::kStage);
                 load_warp(to + i * C::kStage, &w_map, smem_u32(&full[i]), (b0 + i) * kBlock, (int)n0);
@@ -284,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
                 load_warp(to + i * C::kStage + kTile * kBlock, &x_map, smem_u32(&full[i]), (b0 + i) * kBlock, (int)m0);
             int slot = 0;
             uint32_t phase = 0;
-            for (int i = first; i < count; ++i) {
+            for (int i = first; i < bring; ++i) {
                 if (!warp_wait(&empty[slot], phase, ctl)) break;
                 const uint32_t st = to + slot * C::kStage;
                 expect_warp(smem_u32(&full[slot]), C::kStage);
@@ -488,14 +507,14 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     __syncthreads();
     if (!abort_flag) {
         if (threadIdx.x < min(count, C::kStages))
-            mbar_wait_drain(&empty[threadIdx.x], (uint32_t)((count - 1 - (int)threadIdx.x) / C::kStages) & 1u, a.spin_limit, a.status);
+            mbar_wait_drain(&empty[threadIdx.x], last_phase(count, C::kStages, threadIdx.x), a.spin_limit, a.status);
         return;
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < min(loads, C::kStages); ++i)
-            mbar_wait_drain(&full[i], (uint32_t)((loads - 1 - i) / C::kStages) & 1u, a.spin_limit, a.status);
+            mbar_wait_drain(&full[i], last_phase(loads, C::kStages, i), a.spin_limit, a.status);
         for (int i = 0; i < min(products, C::kBufs); ++i)
-            mbar_wait_drain(&d_full[i], (uint32_t)((products - 1 - i) / C::kBufs) & 1u, a.spin_limit, a.status);
+            mbar_wait_drain(&d_full[i], last_phase(products, C::kBufs, i), a.spin_limit, a.status);
     }
     fence_before();
     __syncthreads();
@@ -647,7 +666,7 @@ static cudaError_t few_launch(const Fp8MmLaunch& L, int split, cudaStream_t s) {
     const int64_t tiles = (L.N + kTile - 1) / kTile, chunks = (L.M + MT - 1) / MT;
     if (tiles * chunks * split > 0x7fffffff) return cudaErrorInvalidConfiguration;
     const FewArgs a{L.w_scales, L.x_scales, L.out, L.M, L.N, (int)((L.K + kBlock - 1) / kBlock), (int)chunks, split,
-                    L.status, L.spin_limit};
+                    {std::min(L.until[0][0], L.until[0][1]), std::min(L.until[1][0], L.until[1][1])}, L.status, L.spin_limit};
     return launch_cluster(few_kernel<T, MT>, (unsigned)(tiles * chunks * split), kThreads, C::kSmem, (unsigned)split, s,
                           w_map, x_map, a);
 }
@@ -710,6 +729,7 @@ struct ManyArgs {
     int tiles_m, tiles_n;
     int pairs;
     int aligned;                // rows of out start on 16-byte boundaries: out_map is there
+    int until[2][2];            // loads of a CTA's weights and tokens end before this block
     int* status;
     long long spin_limit;
 };
@@ -793,6 +813,13 @@ __device__ __forceinline__ void copy_scales(const ManyArgs& a, int m, int wr, in
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// what a CTA has issued, blocks of K or batches of scales
+struct Issued {
+    int loads[2];      // of weights, of tokens
+    int products[2];   // of the halves
+    int batches;
+};
+
 template <typename T, int NT>
 __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_constant__ CUtensorMap w_map,
                                                                const __grid_constant__ CUtensorMap x_map,
@@ -806,7 +833,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
     __shared__ float sx[2][kBatch][kTile + 4], sw[2][kBatch][2];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
-    __shared__ int loads, products[2];   // issued
+    __shared__ Issued issued;
+    __shared__ int gave_up;   // one of the two CTAs
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -828,7 +856,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
             mbar_init(&s_empty[i], kSumWarps);
         }
         mbar_init(&tmem_ready, 2);
-        abort_flag = loads = products[0] = products[1] = 0;
+        abort_flag = gave_up = 0;
+        issued = Issued{};
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -840,6 +869,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
         const uint32_t lead = mapa(smem_u32(full), 0);   // the first CTA's barriers
         if (warp == 0) {
             const uint32_t to = smem_u32(ring) + kTile * kBlock;
+            const int until = a.until[rank][0];
             int slot = 0, g = 0;
             uint32_t phase = 1;   // (the first round finds every slot free)
             bool ok = true;
@@ -847,21 +877,24 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
                 int tm, tn;
                 tile_at(a, t, tm, tn);
                 const int n = tn * NT + rank * (NT / 2);
-                for (int kb = 0; kb < a.blocks; ++kb, ++g) {
+                const int end = min(a.blocks, until - g);
+                for (int kb = 0; kb < end; ++kb, ++g) {
                     if (g == C::kStages) pdl_wait();   // (as in few_kernel)
                     if (g >= C::kStages && !(ok = warp_wait(&empty[slot], phase, ctl))) break;
                     if (rank == 0) expect_warp(smem_u32(&full[slot]), 2 * C::kStage);
                     pair_load(to + slot * C::kStage, &w_map, lead + 8 * slot, kb * kBlock, n);
-                    if (lane == 0) loads = g + 1;
                     if (++slot == C::kStages) {
                         slot = 0;
                         phase ^= 1u;
                     }
                 }
+                if (end < a.blocks) break;
             }
+            if (lane == 0) issued.loads[0] = g;
         } else if (warp == 2) {
             pdl_wait();
             const uint32_t to = smem_u32(ring);
+            const int until = a.until[rank][1];
             const int w_rows = (int)((a.N + kBlock - 1) / kBlock);
             int slot = 0, g = 0, j = 0;
             uint32_t phase = 1;
@@ -870,7 +903,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
                 int tm, tn;
                 tile_at(a, t, tm, tn);
                 const int m = tm * kPairRows + rank * kTile;
-                for (int kb = 0; kb < a.blocks; ++kb, ++g) {
+                const int end = min(a.blocks, until - g);
+                for (int kb = 0; kb < end; ++kb, ++g) {
                     if (kb % kBatch == 0) {
                         if (j >= 2 && !(ok = warp_wait(&s_empty[j & 1], (uint32_t)(j / 2 - 1) & 1u, ctl))) break;
                         copy_scales(a, m, (int)((int64_t)tn * NT / kBlock), w_rows, kb, sx[j & 1], sw[j & 1], &s_full[j & 1]);
@@ -883,6 +917,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
                         phase ^= 1u;
                     }
                 }
+                if (end < a.blocks) break;
+            }
+            if (lane == 0) {
+                issued.loads[1] = g;
+                issued.batches = j;
             }
         } else {
             if (warp == 3) {
@@ -905,9 +944,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
                 // warp 1 takes the first half of both CTAs' weight rows, warp 3 the second
                 const int half = warp >> 1;
                 const int total = (tiles - pair + a.pairs - 1) / a.pairs * a.blocks;
-                int slot = 0, buf = 0;
+                int slot = 0, buf = 0, g = 0;
                 uint32_t phase = 0, d_phase = 1;
-                for (int g = 0; ok && g < total; ++g) {
+                for (; ok && g < total; ++g) {
                     // (the first round finds every buffer free: a barrier's phase before its first is over)
                     if (!__all_sync(0xffffffffu, both_ready(smem_u32(&full[slot]), phase, smem_u32(&d_empty[half][buf]), d_phase)) &&
                         !(ok = warp_wait(&full[slot], phase, ctl) && warp_wait(&d_empty[half][buf], d_phase, ctl)))
@@ -916,7 +955,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
                     const uint32_t st = desc_lo(from + slot * C::kStage);
                     pair_products(tmem + (2 * buf + half) * C::kCols, st, st + (kTile * kBlock + half * C::kPart * kBlock >> 4),
                                   idesc(kPairRows, C::kCols), &empty[slot], &d_full[half][buf]);
-                    if (lane == 0) products[half] = g + 1;
                     if (++slot == C::kStages) {
                         slot = 0;
                         phase ^= 1u;
@@ -926,6 +964,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
                         d_phase ^= 1u;
                     }
                 }
+                if (lane == 0) issued.products[half] = g;
             }
         }
     } else {
@@ -1057,26 +1096,60 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
     }
 
     // What was issued lands before the CTAs leave. Without a time-out it has but for
-    // the other commits of the last products, as in few_kernel. (After
-    // one, a load of tokens may have been issued whose stage no load of weights has
-    // counted: no barrier tells when it lands, so it is given far more than its time.)
+    // the other commits of the last products, as in few_kernel. After one, both CTAs
+    // learn of it, and of how much each of them has issued.
     __syncthreads();
-    const int fills = (tiles - pair + a.pairs - 1) / a.pairs * a.blocks;
-    if (!abort_flag && threadIdx.x < min(fills, C::kStages))
-        mbar_wait_drain(&empty[threadIdx.x], (uint32_t)((fills - 1 - (int)threadIdx.x) / C::kStages) & 1u, a.spin_limit, a.status);
-    if (abort_flag && threadIdx.x == 0)
-        for (int i = 0; i < 100; ++i) __nanosleep(1000);
-    if (abort_flag && rank == 0 && threadIdx.x == 0) {
-        for (int i = 0; i < min(loads, C::kStages); ++i)
-            mbar_wait_drain(&full[i], (uint32_t)((loads - 1 - i) / C::kStages) & 1u, a.spin_limit, a.status);
-        for (int h = 0; h < 2; ++h)
-            for (int i = 0; i < min(products[h], C::kBufs); ++i)
-                mbar_wait_drain(&d_full[h][i], (uint32_t)((products[h] - 1 - i) / C::kBufs) & 1u, a.spin_limit, a.status);
+    if (abort_flag) {
+        if (threadIdx.x < 2) store_at(mapa(smem_u32(&gave_up), threadIdx.x), 1);
+    } else {
+        const int fills = (tiles - pair + a.pairs - 1) / a.pairs * a.blocks;
+        if (threadIdx.x < min(fills, C::kStages))
+            mbar_wait_drain(&empty[threadIdx.x], last_phase(fills, C::kStages, threadIdx.x), a.spin_limit, a.status);
     }
     fence_before();
     __syncthreads();
     cluster_arrive();
     cluster_wait();
+    if (gave_up) {
+        if (threadIdx.x == 0) {
+            int loads[2][2], products[2];
+            for (int i = 0; i < 2; ++i) {
+                for (int r = 0; r < 2; ++r) loads[r][i] = load_at(mapa(smem_u32(&issued.loads[i]), r));
+                products[i] = load_at(mapa(smem_u32(&issued.products[i]), 0));
+            }
+            for (int i = 0; rank == 0 && i < C::kStages; ++i) {
+                // Of the stage's last round, the loads that were not issued are counted as
+                // having landed; or, if it was the weights' load that announces the bytes, the
+                // others are announced.
+                constexpr int kBytes[2] = {NT / 2 * kBlock, kTile * kBlock};
+                int round = 0, bytes = 0;
+                for (int l = 0; l < 4; ++l) round = max(round, rounds(loads[l >> 1][l & 1], C::kStages, i));
+                if (round == 0) continue;
+                for (int l = 0; l < 4; ++l)
+                    bytes += rounds(loads[l >> 1][l & 1], C::kStages, i) == round ? kBytes[l & 1] : 0;
+                if (rounds(loads[0][0], C::kStages, i) < round)
+                    mbar_arrive_expect_tx(&full[i], (uint32_t)bytes);
+                else if (bytes < 2 * C::kStage)
+                    mbar_complete_tx(&full[i], (uint32_t)(2 * C::kStage - bytes));
+                mbar_wait_drain(&full[i], (uint32_t)(round - 1) & 1u, a.spin_limit, a.status);
+            }
+            for (int i = 0; i < C::kStages; ++i) {   // (the same for the two halves' products)
+                const int r0 = rounds(products[0], C::kStages, i), r1 = rounds(products[1], C::kStages, i);
+                if (max(r0, r1) == 0) continue;
+                if (r0 != r1) mbar_arrive(&empty[i]);
+                mbar_wait_drain(&empty[i], (uint32_t)(max(r0, r1) - 1) & 1u, a.spin_limit, a.status);
+            }
+            for (int i = 0; i < 2 * C::kBufs; ++i) {
+                const int n = products[i / C::kBufs], b = i % C::kBufs;
+                if (n > b) mbar_wait_drain(&d_full[i / C::kBufs][b], last_phase(n, C::kBufs, b), a.spin_limit, a.status);
+            }
+            for (int i = 0; i < min(issued.batches, 2); ++i)
+                mbar_wait_drain(&s_full[i], last_phase(issued.batches, 2, i), a.spin_limit, a.status);
+        }
+        __syncthreads();
+        cluster_arrive();
+        cluster_wait();
+    }
     fence_after();
     if (warp == 3)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem_slot) : "memory");
@@ -1101,7 +1174,7 @@ static cudaError_t many_launch(const Fp8MmLaunch& L, cudaStream_t s) {
     if (tm * tn > 0x7fffffff - 4096 || (tm * tn + pairs - 1) / pairs * ((L.K + kBlock - 1) / kBlock) > 0x7fffffff)
         return cudaErrorInvalidConfiguration;
     const ManyArgs a{L.w_scales, L.x_scales, L.out, L.M, L.N, (int)((L.K + kBlock - 1) / kBlock), (int)tm, (int)tn, pairs,
-                     aligned, L.status, L.spin_limit};
+                     aligned, {{L.until[0][0], L.until[0][1]}, {L.until[1][0], L.until[1][1]}}, L.status, L.spin_limit};
     return launch_cluster(many_kernel<T, NT>, 2 * (unsigned)pairs, kPairThreads, C::kSmem, 2, s, w_map, x_map, out_map, a);
 }
 

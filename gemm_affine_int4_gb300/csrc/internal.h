@@ -221,6 +221,9 @@ struct Fp8MmLaunch {
     int* status;
     long long spin_limit;
     int device;              // the current one, below 64
+    // loads of weights and of tokens end before this block of K, in CTAs of even
+    // and odd rank of a cluster (the diagnostic of time-outs)
+    int until[2][2] = {{INT32_MAX, INT32_MAX}, {INT32_MAX, INT32_MAX}};
 };
 cudaError_t launch_fp8_mm(const Fp8MmLaunch& L, int dtype, cudaStream_t s);
 

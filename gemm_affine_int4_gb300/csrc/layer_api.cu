@@ -38,6 +38,22 @@ bool apart(const void* in, int64_t in_stride, int64_t in_row, const void* out, i
     return off >= (uintptr_t)(in_row * e) && off + (uintptr_t)(out_row * e) <= pitch;
 }
 
+// L.status NULL: the library's own
+gai4_status fp8_mm(Fp8MmLaunch& L, gai4_dtype dtype, void* stream) {
+    if (!known(dtype)) return GAI4_ERR_UNSUPPORTED;
+    if (L.M < 0 || L.M > kMost - 512 || L.N < 1 || L.N > kMost - 512 || L.K < 1 || L.K > kMost - 512)
+        return GAI4_ERR_INVALID_ARG;
+    if (L.K % 16 != 0) return GAI4_ERR_UNSUPPORTED;
+    if (L.M == 0) return GAI4_OK;
+    if (!L.w || !L.w_scales || !L.x || !L.x_scales || !L.out) return GAI4_ERR_INVALID_ARG;
+    if (!aligned_to(L.w, 16) || !aligned_to(L.x, 16) || !aligned_to(L.w_scales, 4) || !aligned_to(L.x_scales, 4) ||
+        !aligned_to(L.out, elem_bytes(dtype)))
+        return GAI4_ERR_MISALIGNED;
+    if (!L.status) L.status = status_ptr();
+    if (!L.status || cudaGetDevice(&L.device) != cudaSuccess || L.device >= 64) return GAI4_ERR_CUDA;
+    return done(launch_fp8_mm(L, dtype, (cudaStream_t)stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -155,17 +171,20 @@ gai4_status gai4_quantize_fp8(const void* w, uint8_t* codes, float* scales, gai4
 
 gai4_status gai4_fp8_mm_t(const uint8_t* w_codes, const float* w_scales, const uint8_t* x_codes, const float* x_scales,
                           void* out, gai4_dtype dtype, int64_t M, int64_t N, int64_t K, void* stream) {
-    if (!known(dtype)) return GAI4_ERR_UNSUPPORTED;
-    if (M < 0 || M > kMost - 512 || N < 1 || N > kMost - 512 || K < 1 || K > kMost - 512) return GAI4_ERR_INVALID_ARG;
-    if (K % 16 != 0) return GAI4_ERR_UNSUPPORTED;
-    if (M == 0) return GAI4_OK;
-    if (!w_codes || !w_scales || !x_codes || !x_scales || !out) return GAI4_ERR_INVALID_ARG;
-    if (!aligned_to(w_codes, 16) || !aligned_to(x_codes, 16) || !aligned_to(w_scales, 4) || !aligned_to(x_scales, 4) ||
-        !aligned_to(out, elem_bytes(dtype)))
-        return GAI4_ERR_MISALIGNED;
-    Fp8MmLaunch L{w_codes, w_scales, x_codes, x_scales, out, M, N, K, status_ptr(), 2000000000LL, 0};   // ~1 s a wait
-    if (!L.status || cudaGetDevice(&L.device) != cudaSuccess || L.device >= 64) return GAI4_ERR_CUDA;
-    return done(launch_fp8_mm(L, dtype, (cudaStream_t)stream));
+    Fp8MmLaunch L{w_codes, w_scales, x_codes, x_scales, out, M, N, K, nullptr, 2000000000LL, 0};   // ~1 s a wait
+    return fp8_mm(L, dtype, stream);
+}
+
+gai4_status gai4_check_fp8_mm_wait(const uint8_t* w_codes, const float* w_scales, const uint8_t* x_codes,
+                                   const float* x_scales, void* out, gai4_dtype dtype, int64_t M, int64_t N, int64_t K,
+                                   int withheld, int blocks, int64_t limit_cycles, int* status, void* stream) {
+    if (!status || withheld < 0 || withheld > 15 || blocks < 0 || limit_cycles <= 0 || limit_cycles > 4000000000LL)
+        return GAI4_ERR_INVALID_ARG;
+    if (!aligned_to(status, 4)) return GAI4_ERR_MISALIGNED;
+    Fp8MmLaunch L{w_codes, w_scales, x_codes, x_scales, out, M, N, K, status, limit_cycles, 0};
+    for (int i = 0; i < 4; ++i)
+        if (withheld >> i & 1) L.until[i >> 1][i & 1] = blocks;
+    return fp8_mm(L, dtype, stream);
 }
 
 }  // extern "C"

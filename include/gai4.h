@@ -602,6 +602,23 @@ gai4_status gai4_quantize_fp8(const void* w, uint8_t* codes, float* scales, gai4
 gai4_status gai4_fp8_mm_t(const uint8_t* w_codes, const float* w_scales, const uint8_t* x_codes, const float* x_scales,
                           void* out, gai4_dtype dtype, int64_t M, int64_t N, int64_t K, void* stream);
 
+/*
+ * gai4_check_fp8_mm_wait -- diagnostic of that kernel's time-out path, as
+ * gai4_check_bounded_wait is of the wait by itself: the same call, but some
+ * loads end before block `blocks` (of 128) of each CTA's way, as if they had
+ * been lost. What waits for them gives up after limit_cycles (1 .. 4e9) SM
+ * clock cycles a wait, the kernel takes back what it has in flight and returns
+ * with *status = GAI4_ERR_TIMEOUT (device int, 4-byte aligned, caller-owned)
+ * and `out` undefined. Nothing is left behind: the next call is as any other.
+ *   withheld  bits 0 and 1: weights and tokens of CTAs of even rank of their
+ *         cluster; bits 2 and 3: of odd rank. (A few-token kernel, which loads
+ *         both together, withholds both for either.) 0, or `blocks` beyond a
+ *         CTA's last: the call is gai4_fp8_mm_t.
+ */
+gai4_status gai4_check_fp8_mm_wait(const uint8_t* w_codes, const float* w_scales, const uint8_t* x_codes,
+                                   const float* x_scales, void* out, gai4_dtype dtype, int64_t M, int64_t N, int64_t K,
+                                   int withheld, int blocks, int64_t limit_cycles, int* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

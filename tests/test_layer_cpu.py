@@ -178,3 +178,12 @@ def test_binding_names_what_it_was_given():
         g4.gai4_rms_norm(torch.zeros(2, 3))
     with pytest.raises(ValueError, match="columns contiguous"):
         g4.gai4_rms_norm(torch.zeros(2, 3, 4))
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(status=None), 1), (dict(withheld=-1), 1), (dict(withheld=16), 1), (dict(blocks=-1), 1), (dict(limit=0), 1),
+    (dict(limit=4000000001), 1), (dict(status=P(0x10002)), 3), (dict(w=None), 1), (dict(K=24), 2), (dict(M=0), 0)])
+def test_withheld_loads_refusals(change, status):
+    a = dict(w=A, ws=A, x=A, xs=A, out=A, dt=2, M=3, N=64, K=256, withheld=1, blocks=0, limit=1000, status=A)
+    a.update(change)
+    assert g4.lib().gai4_check_fp8_mm_wait(*a.values(), None) == status
