@@ -298,38 +298,36 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
                 load_warp(to + i * C::kStage, &w_map, smem_u32(&full[i]), (b0 + i) * kBlock, (int)n0);
             }
             pdl_wait();
-            if (lane == 0) loads = first;
             for (int i = 0; i < first; ++i)
                 load_warp(to + i * C::kStage + kTile * kBlock, &x_map, smem_u32(&full[i]), (b0 + i) * kBlock, (int)m0);
-            int slot = 0;
+            int slot = 0, i = first;
             uint32_t phase = 0;
-            for (int i = first; i < bring; ++i) {
+            for (; i < bring; ++i) {
                 if (!warp_wait(&empty[slot], phase, ctl)) break;
                 const uint32_t st = to + slot * C::kStage;
                 expect_warp(smem_u32(&full[slot]), C::kStage);
                 load_warp(st, &w_map, smem_u32(&full[slot]), (b0 + i) * kBlock, (int)n0);
                 load_warp(st + kTile * kBlock, &x_map, smem_u32(&full[slot]), (b0 + i) * kBlock, (int)m0);
-                if (lane == 0) loads = i + 1;
                 if (++slot == C::kStages) {
                     slot = 0;
                     phase ^= 1u;
                 }
             }
+            if (lane == 0) loads = i;
         } else if (warp == 1) {
             pdl_wait();   // (before every first wait with a limit: a kernel ahead may run for long)
             const bool ready = warp_wait(&tmem_ready, 0, ctl);
             fence_after();
             const uint32_t tmem = tmem_slot, from = smem_u32(ring);
-            int slot = 0, buf = 0;
+            int slot = 0, buf = 0, i = 0;
             uint32_t phase = 0, d_phase = 1;   // (the first round finds every buffer free)
-            for (int i = 0; ready && i < count; ++i) {
+            for (; ready && i < count; ++i) {
                 if (!__all_sync(0xffffffffu, both_ready(smem_u32(&full[slot]), phase, smem_u32(&d_empty[buf]), d_phase)) &&
                     !(warp_wait(&full[slot], phase, ctl) && warp_wait(&d_empty[buf], d_phase, ctl)))
                     break;
                 fence_after();
                 const uint32_t st = desc_lo(from + slot * C::kStage);
                 block_products(tmem + buf * MT, st, st + (kTile * kBlock >> 4), idesc(kTile, MT), &empty[slot], &d_full[buf]);
-                if (lane == 0) products = i + 1;
                 if (++slot == C::kStages) {
                     slot = 0;
                     phase ^= 1u;
@@ -339,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
                     d_phase ^= 1u;
                 }
             }
+            if (lane == 0) products = i;
         } else if (warp == 2) {
             pdl_wait();
             // Lanes: 4 blocks of K by 8 tokens. A batch is copied while the one before
@@ -377,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
                 mbar_arrive(&s_full[j % kFewBatches]);
                 w = next;
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");   // (after a time-out, the next batch's)
         } else if (warp == 3) {
             // Tensor memory is taken after the kernels before this one have finished,
             // and the next one may start after it is taken; and it is free again
@@ -394,6 +394,9 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
                 fence_after();
                 asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_slot), "r"(C::kCols) : "memory");
                 freed = true;
+                // The other commits of the last products arrive before the CTA leaves.
+                if (lane < min(count, C::kStages)) mbar_wait(&empty[lane], last_phase(count, C::kStages, lane), ctl);
+                __syncwarp();
             }
         }
     } else {
@@ -501,18 +504,16 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
         }
     }
 
-    // What was issued lands before the CTA leaves. Without a time-out it has but for
-    // the other commits of the last products, which nobody had to wait for yet: a
-    // thread each does.
+    // What was issued lands before the CTA leaves; without a time-out it has: both
+    // commits of the last products were waited for above, and so were the sums sent
+    // to this CTA.
     __syncthreads();
-    if (!abort_flag) {
-        if (threadIdx.x < min(count, C::kStages))
-            mbar_wait_drain(&empty[threadIdx.x], last_phase(count, C::kStages, threadIdx.x), a.spin_limit, a.status);
-        return;
-    }
+    if (!abort_flag) return;
     if (threadIdx.x == 0) {
         for (int i = 0; i < min(loads, C::kStages); ++i)
             mbar_wait_drain(&full[i], last_phase(loads, C::kStages, i), a.spin_limit, a.status);
+        for (int i = 0; i < min(products, C::kStages); ++i)
+            mbar_wait_drain(&empty[i], last_phase(products, C::kStages, i), a.spin_limit, a.status);
         for (int i = 0; i < min(products, C::kBufs); ++i)
             mbar_wait_drain(&d_full[i], last_phase(products, C::kBufs, i), a.spin_limit, a.status);
     }
@@ -521,10 +522,14 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     fence_after();
     if (warp == 3 && !freed)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_slot), "r"(C::kCols) : "memory");
-    if (a.split > 1) {   // sums may still be on their way here: until the others have sent theirs, or left
+    if (a.split > 1) {
+        // Every CTA sends its sums, whether they are whole or not. Those for this one may
+        // still be on their way: after the others have sent theirs, or left, the barrier
+        // that counts their bytes is waited for.
         if (warp < 4) cluster_wait();
         cluster_arrive();
         cluster_wait();
+        if (threadIdx.x == 0 && own > 0) mbar_wait_drain(&joined, 0, a.spin_limit, a.status);
     }
 }
 
@@ -1096,8 +1101,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) many_kernel(const __grid_cons
     }
 
     // What was issued lands before the CTAs leave. Without a time-out it has but for
-    // the other commits of the last products, as in few_kernel. After one, both CTAs
-    // learn of it, and of how much each of them has issued.
+    // the other commits of the last products, which a thread each waits for. After one,
+    // both CTAs learn of it, and of how much each of them has issued.
     __syncthreads();
     if (abort_flag) {
         if (threadIdx.x < 2) store_at(mapa(smem_u32(&gave_up), threadIdx.x), 1);

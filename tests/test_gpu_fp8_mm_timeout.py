@@ -32,3 +32,20 @@ def give_up(shape, cases):
 @pytest.mark.parametrize("shape", MANY)
 def test_pairs_of_ctas(shape, withheld):
     give_up(shape, [(withheld, blocks) for blocks in (0, 1, 3, 4, 6, 8)])
+
+
+# few tokens: 16 to 128 at once, clusters of 1 to 8 CTAs; blocks that each CTA has at least
+FEW = [((1, 4096, 4096), 8), ((64, 2048, 2048), 2), ((56, 5120, 17408), 17), ((128, 4096, 4096), 8), ((256, 4096, 4096), 8),
+       ((16, 256, 16384), 16), ((40, 4096, 4096), 5), ((33, 300, 5136), 5), ((9, 20000, 2048), 2)]
+
+
+@pytest.mark.parametrize("withheld", [3, 1, 2, 15])
+@pytest.mark.parametrize("shape,least", FEW)
+def test_few_tokens(shape, least, withheld):
+    give_up(shape, [(withheld, blocks) for blocks in (0, 1, 2, 3, 4, 5, 6, 7, 12) if blocks < least])
+
+
+@pytest.mark.parametrize("shape,least", FEW[:1] + FEW[2:4] + FEW[5:6])
+def test_few_tokens_one_half_of_a_cluster(shape, least):
+    """CTAs that have all of their loads beside CTAs that do not."""
+    give_up(shape, [(withheld, blocks) for withheld in (4, 12, 3) for blocks in range(least)])
