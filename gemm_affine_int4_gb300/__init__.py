@@ -73,6 +73,7 @@ SIGNATURES = {
     "gai4_quantize_x_fp8": ([_P, _I64, _P, _P, _I, _I64, _I64, _P], _I),
     "gai4_quantize_fp8": ([_P, _P, _P, _I, _I64, _I64, _P], _I),
     "gai4_fp8_mm_t": ([_P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _P], _I),
+    "gai4_fp8_mm_t_plan": ([_I64, _I64, _I64, _I, ctypes.POINTER(_I), ctypes.POINTER(_I), ctypes.POINTER(_I)], _I),
     "gai4_check_fp8_mm_wait": ([_P, _P, _P, _P, _P, _I, _I64, _I64, _I64, _I, _I, _I64, _P, _P], _I),
 }
 
@@ -654,6 +655,14 @@ def gai4_fp8_mm_t(w_codes, w_scales, x_codes, x_scales, out=None, dtype=torch.bf
         with torch.cuda.stream(stream):
             return gai4_fp8_mm_t(w_codes, w_scales, x_codes, x_scales, out, dtype)
     return (_bound or _bind()).fp8_mm_t(w_codes, w_scales, x_codes, x_scales, out, dtype)
+
+
+def gai4_fp8_mm_t_plan(M: int, N: int, K: int, dtype=torch.bfloat16) -> tuple[int, int, int]:
+    """(tokens, weight rows) of gai4_fp8_mm_t's tile for these sizes and the CTAs that share one."""
+    tokens, rows, ctas = _I(0), _I(0), _I(0)
+    _check("gai4_fp8_mm_t_plan", lib().gai4_fp8_mm_t_plan(M, N, K, _DTYPE[dtype], ctypes.byref(tokens), ctypes.byref(rows),
+                                                          ctypes.byref(ctas)))
+    return tokens.value, rows.value, ctas.value
 
 
 def gai4_last_device_status(stream=None) -> int:

@@ -1189,9 +1189,15 @@ static cudaError_t many_launch(const Fp8MmLaunch& L, cudaStream_t s) {
 // first is taken; few / many in us: 128 x 4096 x 4096 10.3 / 17.8, 256 x 4096 x
 // 4096 14.0 / 18.0, 512 x 4096 x 4096 19.8 / 18.3, 256 x 14336 x 5120 48 / 24,
 // 512 x 1024 x 8192 13.5 / 31.
+struct Form {
+    int which;   // of kTiles
+    int ctas;    // that share a tile
+};
+constexpr int kTiles[][2] = {{16, 128}, {32, 128}, {64, 128}, {128, 128}, {256, 192}, {256, 256}};   // tokens, weight rows
+
 template <typename T>
-static cudaError_t typed(const Fp8MmLaunch& L, cudaStream_t s) {
-    int split[4] = {1, 1, 1, 1};
+static Form choose(const Fp8MmLaunch& L) {
+    int split[] = {1, 1, 1, 1, 2, 2};
     int64_t least = few_plan<T, 16>(L, &split[0]);
     int choice = 0;
     const auto offer = [&](int c, int64_t cost) {
@@ -1209,11 +1215,17 @@ static cudaError_t typed(const Fp8MmLaunch& L, cudaStream_t s) {
         offer(4, 5500 + 420 * blocks * rounds(192));
         offer(5, 5500 + 455 * blocks * rounds(256));
     }
-    switch (choice) {
-    case 0: return few_launch<T, 16>(L, split[0], s);
-    case 1: return few_launch<T, 32>(L, split[1], s);
-    case 2: return few_launch<T, 64>(L, split[2], s);
-    case 3: return few_launch<T, 128>(L, split[3], s);
+    return {choice, split[choice]};
+}
+
+template <typename T>
+static cudaError_t typed(const Fp8MmLaunch& L, cudaStream_t s) {
+    const Form f = choose<T>(L);
+    switch (f.which) {
+    case 0: return few_launch<T, 16>(L, f.ctas, s);
+    case 1: return few_launch<T, 32>(L, f.ctas, s);
+    case 2: return few_launch<T, 64>(L, f.ctas, s);
+    case 3: return few_launch<T, 128>(L, f.ctas, s);
     case 4: return many_launch<T, 192>(L, s);
     default: return many_launch<T, 256>(L, s);
     }
@@ -1227,6 +1239,15 @@ cudaError_t launch_fp8_mm(const Fp8MmLaunch& L, int dtype, cudaStream_t s) {
     case GAI4_F32: return fp8mm::typed<F32>(L, s);
     default: return fp8mm::typed<BF16>(L, s);
     }
+}
+
+void plan_fp8_mm(const Fp8MmLaunch& L, int dtype, int* tokens, int* weight_rows, int* ctas) {
+    const fp8mm::Form f = dtype == GAI4_F16   ? fp8mm::choose<F16>(L)
+                          : dtype == GAI4_F32 ? fp8mm::choose<F32>(L)
+                                              : fp8mm::choose<BF16>(L);
+    *tokens = fp8mm::kTiles[f.which][0];
+    *weight_rows = fp8mm::kTiles[f.which][1];
+    *ctas = f.ctas;
 }
 
 }  // namespace gai4

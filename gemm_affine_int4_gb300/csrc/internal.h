@@ -226,6 +226,8 @@ struct Fp8MmLaunch {
     int until[2][2] = {{INT32_MAX, INT32_MAX}, {INT32_MAX, INT32_MAX}};
 };
 cudaError_t launch_fp8_mm(const Fp8MmLaunch& L, int dtype, cudaStream_t s);
+// the tile that launch_fp8_mm would take, and the CTAs that share one (sizes and device of L)
+void plan_fp8_mm(const Fp8MmLaunch& L, int dtype, int* tokens, int* weight_rows, int* ctas);
 
 int* status_ptr();  // device status word of the current device
 int num_sms();  // SM count of the current device (cached)

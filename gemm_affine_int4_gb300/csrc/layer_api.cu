@@ -38,12 +38,16 @@ bool apart(const void* in, int64_t in_stride, int64_t in_row, const void* out, i
     return off >= (uintptr_t)(in_row * e) && off + (uintptr_t)(out_row * e) <= pitch;
 }
 
+gai4_status fp8_mm_sizes(gai4_dtype dtype, int64_t M, int64_t N, int64_t K) {
+    if (!known(dtype)) return GAI4_ERR_UNSUPPORTED;
+    if (M < 0 || M > kMost - 512 || N < 1 || N > kMost - 512 || K < 1 || K > kMost - 512) return GAI4_ERR_INVALID_ARG;
+    return K % 16 != 0 ? GAI4_ERR_UNSUPPORTED : GAI4_OK;
+}
+
 // L.status NULL: the library's own
 gai4_status fp8_mm(Fp8MmLaunch& L, gai4_dtype dtype, void* stream) {
-    if (!known(dtype)) return GAI4_ERR_UNSUPPORTED;
-    if (L.M < 0 || L.M > kMost - 512 || L.N < 1 || L.N > kMost - 512 || L.K < 1 || L.K > kMost - 512)
-        return GAI4_ERR_INVALID_ARG;
-    if (L.K % 16 != 0) return GAI4_ERR_UNSUPPORTED;
+    const gai4_status sizes = fp8_mm_sizes(dtype, L.M, L.N, L.K);
+    if (sizes != GAI4_OK) return sizes;
     if (L.M == 0) return GAI4_OK;
     if (!L.w || !L.w_scales || !L.x || !L.x_scales || !L.out) return GAI4_ERR_INVALID_ARG;
     if (!aligned_to(L.w, 16) || !aligned_to(L.x, 16) || !aligned_to(L.w_scales, 4) || !aligned_to(L.x_scales, 4) ||
@@ -173,6 +177,17 @@ gai4_status gai4_fp8_mm_t(const uint8_t* w_codes, const float* w_scales, const u
                           void* out, gai4_dtype dtype, int64_t M, int64_t N, int64_t K, void* stream) {
     Fp8MmLaunch L{w_codes, w_scales, x_codes, x_scales, out, M, N, K, nullptr, 2000000000LL, 0};   // ~1 s a wait
     return fp8_mm(L, dtype, stream);
+}
+
+gai4_status gai4_fp8_mm_t_plan(int64_t M, int64_t N, int64_t K, gai4_dtype dtype, int* tokens, int* weight_rows, int* ctas) {
+    if (!tokens || !weight_rows || !ctas) return GAI4_ERR_INVALID_ARG;
+    const gai4_status sizes = fp8_mm_sizes(dtype, M, N, K);
+    if (sizes != GAI4_OK) return sizes;
+    if (M == 0) return GAI4_ERR_INVALID_ARG;
+    Fp8MmLaunch L{nullptr, nullptr, nullptr, nullptr, nullptr, M, N, K, nullptr, 0, 0};
+    if (cudaGetDevice(&L.device) != cudaSuccess || L.device >= 64) return GAI4_ERR_CUDA;
+    plan_fp8_mm(L, dtype, tokens, weight_rows, ctas);
+    return GAI4_OK;
 }
 
 gai4_status gai4_check_fp8_mm_wait(const uint8_t* w_codes, const float* w_scales, const uint8_t* x_codes,

@@ -602,6 +602,12 @@ gai4_status gai4_quantize_fp8(const void* w, uint8_t* codes, float* scales, gai4
 gai4_status gai4_fp8_mm_t(const uint8_t* w_codes, const float* w_scales, const uint8_t* x_codes, const float* x_scales,
                           void* out, gai4_dtype dtype, int64_t M, int64_t N, int64_t K, void* stream);
 
+/* The plan gai4_fp8_mm_t runs on the current device: the tokens and weight rows
+ * of a tile (16, 32, 64 or 128 x 128, or 256 x 192 or 256), and the CTAs that
+ * share one (parts of K, or 2 with half of the tile each). M >= 1. Host memory;
+ * nothing runs on the device. */
+gai4_status gai4_fp8_mm_t_plan(int64_t M, int64_t N, int64_t K, gai4_dtype dtype, int* tokens, int* weight_rows, int* ctas);
+
 /*
  * gai4_check_fp8_mm_wait -- diagnostic of that kernel's time-out path, as
  * gai4_check_bounded_wait is of the wait by itself: the same call, but some

@@ -187,3 +187,12 @@ def test_withheld_loads_refusals(change, status):
     a = dict(w=A, ws=A, x=A, xs=A, out=A, dt=2, M=3, N=64, K=256, withheld=1, blocks=0, limit=1000, status=A)
     a.update(change)
     assert g4.lib().gai4_check_fp8_mm_wait(*a.values(), None) == status
+
+
+@pytest.mark.parametrize("change,status", [(dict(M=0), 1), (dict(N=0), 1), (dict(K=24), 2), (dict(dt=3), 2), (dict(a=None), 1),
+                                           (dict(b=None), 1), (dict(c=None), 1), (dict(M=1 << 31), 1)])
+def test_product_plan_refusals(change, status):
+    i, j, k = ctypes.c_int(), ctypes.c_int(), ctypes.c_int()
+    a = dict(M=3, N=64, K=256, dt=2, a=ctypes.byref(i), b=ctypes.byref(j), c=ctypes.byref(k))
+    a.update(change)
+    assert g4.lib().gai4_fp8_mm_t_plan(*a.values()) == status
