@@ -12,7 +12,7 @@
 // An angle of a far position does not fit binary32. inv_freq (a double, in
 // radians) is turned into a 64-bit fraction of a turn by integer arithmetic;
 // position * fraction modulo 2^64 is then the exact rest of the turns, good to
-// 2^-33 of a turn at any 32-bit position; it is the argument of a sine in half
+// 2^-32 of a turn at any 32-bit position; it is the argument of a sine in half
 // turns, as the sum of two binary32 numbers.
 #include <algorithm>
 
@@ -41,24 +41,20 @@ struct RopeArgs {
     int pass;            // 1: channels from 2 * half on are copied (outputs elsewhere)
 };
 
-// radians -> turns modulo 1, in units of 2^-64. 1 / (2 pi) = C 2^-66; the
-// product of the 53-bit significand with C is shifted to the binary point.
-// Infinite and NaN frequencies are left to the caller.
+// radians -> turns modulo 1, in units of 2^-64. 1 / (2 pi) = C 2^-130 with 128 bits;
+// the product of the 53-bit significand with C, but for its last 64 bits, is shifted
+// to the binary point. Frequencies of 2^53 and more, whose neighbours are 2 radians
+// apart, and those that are no numbers are left to the caller.
 __device__ __forceinline__ uint64_t turn_fraction(double f) {
     const uint64_t b = (uint64_t)__double_as_longlong(f);
     const int be = (int)(b >> 52) & 0x7ff;
     const uint64_t m = (b & 0xfffffffffffffull) | (be ? 1ull << 52 : 0ull);
-    constexpr uint64_t C = 0xa2f9836e4e441529ull;
-    const uint64_t lo = m * C, hi = __umul64hi(m, C);
+    constexpr uint64_t C1 = 0xa2f9836e4e441529ull, C0 = 0xfc2757d1f534ddc0ull;
+    const uint64_t low = m * C1, lo = low + __umul64hi(m, C0), hi = __umul64hi(m, C1) + (lo < low);
     // f = m 2^(e - 52), e = be - 1023: turns 2^64 = (hi : lo) 2^(e - 54)
-    const int shift = 54 + 1023 - (be ? be : 1);
-    uint64_t t;
-    if (shift <= 0)
-        t = -shift < 64 ? lo << -shift : 0;
-    else if (shift < 64)
-        t = (hi << (64 - shift)) | (lo >> shift);
-    else
-        t = shift < 128 ? hi >> (shift - 64) : 0;
+    const int shift = 54 + 1023 - (be ? be : 1);   // (2 or more)
+    const uint64_t l = shift < 64 ? lo : hi, h = shift < 64 ? hi : 0;
+    const uint64_t t = shift < 128 ? l >> (shift & 63) | h << 1 << (~shift & 63) : 0;
     return (int64_t)b < 0 ? 0 - t : t;
 }
 
@@ -218,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         const float hi = (float)turns, lo = (float)(turns - (int64_t)hi) * (3.14159265f * 0x1p-63f);
         float s, c;
         sincospif(hi * 0x1p-63f, &s, &c);
-        const float m = isfinite(f) ? a.mscale : __uint_as_float(0x7fffffffu);
+        const float m = fabs(f) < 0x1p53 ? a.mscale : __uint_as_float(0x7fffffffu);
         cs[0][i] = fmaf(-s, lo, c) * m;
         cs[1][i] = fmaf(c, lo, s) * m;
     }

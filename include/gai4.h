@@ -538,9 +538,10 @@ gai4_status gai4_rope_inv_freq(double* inv_freq, float* mscale, int rot_dim, dou
  *   q_out, k_out  likewise; they may be q and k themselves (same stride), and
  *         must not overlap the inputs or each other otherwise
  *   positions [num_tokens] i32, any value: a negative one turns back
- *   inv_freq [rot_dim / 2] double (device, 8-byte aligned): any value. The
- *         angle's whole turns are taken off exactly, so far positions lose
- *         nothing.
+ *   inv_freq [rot_dim / 2] double (device, 8-byte aligned): any value below 2^53
+ *         in magnitude (from there on a double does not tell an angle: such a
+ *         pair becomes NaN, as for an infinity or a NaN). The angle's whole turns
+ *         are taken off exactly, and 2^-32 of a turn is left at any position.
  * rot_dim even, 2 .. head_dim; head_dim up to 1024. Every row is turned, those
  * behind a step's last token (position 0 in gai4_kv_plan's positions) too.
  */
