@@ -2,7 +2,8 @@
 with nvcc, then linked into one shared library next to this file (the CUDA
 runtime is linked statically, so the library loads on hosts without a GPU
 driver too), and _calls.so, the module that reaches some of its entries from
-Python without ctypes (csrc/torch_calls.cpp, g++ against PyTorch's headers).
+Python without ctypes (csrc/torch_calls.cpp, g++ against PyTorch's headers; left
+out where there is no PyTorch for CUDA: the library needs none).
 Usage: python -m gemm_affine_int4_gb300.build [--verbose]."""
 from __future__ import annotations
 
@@ -41,9 +42,20 @@ def _deps():
                   [os.path.join(os.path.dirname(HERE), "include", "gai4.h")])
 
 
-def _calls_command(nvcc: str, obj: str):
+def _torch():
+    """(folder, text of its version file) of a PyTorch for CUDA, or None."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    folder = os.path.dirname(spec.origin)
+    if not glob.glob(os.path.join(folder, "lib", "libtorch_cuda.so*")):
+        return None
+    with open(os.path.join(folder, "version.py")) as f:
+        return folder, f.read()
+
+
+def _calls_command(nvcc: str, torch: str, obj: str):
     """(compile, link) of torch_calls.cpp; the module finds libgai4.so beside itself."""
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
     include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include"),
                sysconfig.get_paths()["include"]]
@@ -53,6 +65,18 @@ def _calls_command(nvcc: str, obj: str):
     link = ["g++", "-shared", obj, "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
             "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
     return compile_, link
+
+
+def _calls_key(version: str, commands) -> str:
+    """What _calls.so is made for, beside its sources: layouts of PyTorch's and Python's objects."""
+    return "\n".join([version, sys.version, str(sysconfig.get_config_var("EXT_SUFFIX"))] + [" ".join(c) for c in commands])
+
+
+def _made_for(stamp: str, key: str) -> bool:
+    if not os.path.exists(stamp):
+        return False
+    with open(stamp) as f:
+        return f.read() == key
 
 
 def _stale(target: str, inputs) -> bool:
@@ -75,24 +99,33 @@ def build(verbose: bool = False, force: bool = False) -> str:
             cmd = [nvcc] + NVCC_FLAGS + (["-Xptxas", "-v"] if verbose else []) + ["-c", src, "-o", obj]
             jobs.append((src, cmd))
 
-    calls_obj = os.path.join(BUILD, "torch_calls.o")
-    compile_calls, link_calls = _calls_command(nvcc, calls_obj)
-    calls_src = compile_calls[compile_calls.index("-c") + 1]
-    if force or _stale(calls_obj, [calls_src] + deps):
-        jobs.insert(0, (calls_src, compile_calls))
+    torch = _torch()
+    calls_src = os.path.join(CSRC, "torch_calls.cpp")
+    calls_obj, stamp = os.path.join(BUILD, "torch_calls.o"), os.path.join(BUILD, "torch_calls.key")
+    if torch is None:
+        print("no PyTorch for CUDA: libgai4.so is built without _calls.so, which calls some of its entries from Python",
+              file=sys.stderr)
+    else:
+        commands = _calls_command(nvcc, torch[0], calls_obj)
+        key = _calls_key(torch[1], commands)
+        if force or _stale(calls_obj, [calls_src] + deps) or not _made_for(stamp, key):
+            if os.path.exists(stamp):
+                os.remove(stamp)
+            jobs.insert(0, (calls_src, commands[0]))
 
     def run(job):
         src, cmd = job
         p = subprocess.run(cmd, capture_output=True, text=True)
         return src, p.returncode, p.stdout + p.stderr
 
+    failed = []
     if jobs:
-        with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
+        with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             for src, rc, log in ex.map(run, jobs):
                 if verbose or rc != 0:
                     sys.stderr.write(log)
                 if rc != 0:
-                    raise RuntimeError(f"compiling {os.path.basename(src)} failed")
+                    failed.append(src)
 
     def link(target, cmd):
         tmp = target + ".tmp%d" % os.getpid()
@@ -102,10 +135,15 @@ def build(verbose: bool = False, force: bool = False) -> str:
             raise RuntimeError(f"linking {os.path.basename(target)} failed")
         os.replace(tmp, target)
 
-    if force or jobs or _stale(LIB, objs):
+    # (the library first: it does not need the module)
+    if not set(failed) - {calls_src} and (force or jobs or _stale(LIB, objs)):
         link(LIB, [nvcc] + ARCH + ["-shared"] + objs)
-    if force or jobs or _stale(CALLS, [calls_obj]):
-        link(CALLS, link_calls)
+    if failed:
+        raise RuntimeError("compiling " + ", ".join(os.path.basename(f) for f in failed) + " failed")
+    if torch is not None and (force or jobs or _stale(CALLS, [calls_obj]) or not _made_for(stamp, key)):
+        link(CALLS, commands[1])
+        with open(stamp, "w") as f:
+            f.write(key)
     return LIB
 
 
