@@ -575,7 +575,7 @@ def _bind():
         try:
             from . import _calls
         except ImportError as e:
-            raise RuntimeError("_calls.so is not built; run `python -m gemm_affine_int4_gb300.build`") from e
+            raise RuntimeError(f"_calls.so does not load ({e}); run `python -m gemm_affine_int4_gb300.build`") from e
         _calls.set_error(Gai4Error)
         _bound = _calls
     return _bound

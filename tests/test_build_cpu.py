@@ -1,11 +1,14 @@
 """What the build makes anew: the module that calls the library from Python is bound to PyTorch and Python, the library
 to neither."""
 import os
+import subprocess
 import sys
 
 import pytest
 
 from gemm_affine_int4_gb300 import build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture
@@ -90,3 +93,12 @@ def test_where_pytorch_is_not(monkeypatch, tmp_path):
     assert build._torch() is None
     (tmp_path / "lib" / "libtorch_cuda.so").write_text("")
     assert build._torch() == (str(tmp_path), "cuda = None\n")
+
+
+def test_why_the_module_does_not_load_is_told():
+    program = ("import sys, gemm_affine_int4_gb300 as g4\n"
+               "sys.modules['gemm_affine_int4_gb300._calls'] = None\n"
+               "try:\n    g4._bind()\nexcept RuntimeError as e:\n    print(e, '|', e.__cause__)\n")
+    done = subprocess.run([sys.executable, "-c", program], cwd=ROOT, capture_output=True, text=True, timeout=120)
+    told, cause = done.stdout.strip().split(" | ")
+    assert cause and cause in told, done.stdout + done.stderr
