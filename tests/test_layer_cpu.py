@@ -56,6 +56,25 @@ def test_scaled_frequencies():
     assert freqs(2, scaling="ntk", factor=4.0) == ([1.0], 1.0)
 
 
+@pytest.mark.parametrize("rot,base,factor,length,low,high", [
+    (64, 5e5, 8.0, 8192, 1.0, 32.0), (128, 1e4, 4.0, 4096, 1.0, 32.0), (32, 1e4, 40.0, 4096, 2.0, 17.5), (128, 1e6, 2.0, 32768, 0.5, 64.0),
+    (20, 150.0, 16.0, 300, 1.0, 8.0), (64, 1e4, 8.0, 20, 1.0, 32.0), (64, 100.0, 8.0, 1e6, 1.0, 32.0)])
+def test_yarn_between_the_ends_of_its_ramp(rot, base, factor, length, low, high):
+    """The ramp is linear in the pair's number, from the last pair of at least `high` turns (the first at least) to the
+    first of at most `low` (or rot - 1), as if there were that many pairs."""
+    f, _ = freqs(rot, base=base, scaling="yarn", factor=factor, original_len=length, low=low, high=high)
+    turns = [length * base ** (-2 * i / rot) / (2 * math.pi) for i in range(rot)]
+    first = max([i for i in range(rot) if turns[i] >= high], default=0)
+    last = min([i for i in range(rot) if turns[i] <= low], default=rot - 1)
+    inside = 0
+    for i, x in enumerate(f):
+        divided = min(max((i - first) / (last - first), 0.0), 1.0) if last > first else float(i > first)
+        inside += 0 < divided < 1
+        plain = base ** (-2 * i / rot)
+        assert math.isclose(x, plain / factor * divided + plain * (1 - divided), rel_tol=1e-12), i
+    assert inside > 0 or length == 1e6
+
+
 @pytest.mark.parametrize("change,status", [
     (dict(f=None), 1), (dict(m=None), 1), (dict(rot=0), 1), (dict(rot=63), 1), (dict(base=1.0), 1),
     (dict(base=float("nan")), 1), (dict(base=float("inf")), 1), (dict(how=5), 2), (dict(how=-1), 2),
