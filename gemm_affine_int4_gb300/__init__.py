@@ -650,7 +650,11 @@ def gai4_quantize_fp8(w, codes=None, scales=None, stream=None):
 
 def gai4_fp8_mm_t(w_codes, w_scales, x_codes, x_scales, out=None, dtype=torch.bfloat16, stream=None):
     """out[m, n] = sum_k (x_codes x_scales)[m, k] (w_codes w_scales)[n, k] in
-    `dtype` (or out's type); K a multiple of 16."""
+    `dtype` (or out's type); K a multiple of 16. w_codes may be read before the
+    kernel ahead in the stream has ended, where that kernel signals programmatic
+    launch: gai4_quantize_fp8's and PyTorch's elementwise ones do not; a kernel of
+    your own that writes w_codes must not, and gai4_quantize_x_fp8 or gai4_rms_norm, which do,
+    cannot have written them right before."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return gai4_fp8_mm_t(w_codes, w_scales, x_codes, x_scales, out, dtype)

@@ -176,9 +176,9 @@ __device__ __forceinline__ void send4(uint32_t to, uint32_t bar, float x, float 
 //   warps 4-7  thread = weight row: sum[m] += D[m] * scale[m]; join
 //
 // Bound by HBM where the weights are many, by the start, a block's chain and the
-// join where they are few: 56 x 5120 x 17408 takes 20.2 us (4.5 TB/s, 66% of the
-// measured rate: 240 CTAs on 152 SMs, so 88 of them have two), 1 x 4096 x 4096 4.6 us,
-// of which 2.5 are the weights' time. A block takes 230 ns (16 tokens) to 460 (128),
+// join where they are few: 56 x 5120 x 17408 takes 20.2 to 20.5 us (4.5 TB/s, 66% of the
+// measured rate: 240 CTAs on 152 SMs, so 88 of them have two), 1 x 4096 x 4096 4.6 us
+// (8 blocks a CTA), of which 2.5 are the weights' time. A block takes 230 ns (16 tokens) to 460 (128),
 // and rings of 7 to 11 stages, a second producer and scales read earlier change that
 // by 3% at most: an SM takes in 63 to 80 bytes a ns, whatever the tokens.
 // ---------------------------------------------------------------------------
@@ -627,17 +627,17 @@ static int clusters_at_once(int dev, int split) {
 // that where two share one, and 1.3 us more since the next call's CTAs then find
 // no room to load their weights early; or HBM at 6.2 TB/s. Measured in us, split
 // 1, 2, 3, 4, 6, 8 (16, 64, 16, 64, 64, 16 tokens at once):
-//   1 x 4096 x 4096     10.2   7.0   5.5   5.4   6.3   6.8
-//   64 x 2048 x 2048     9.0   6.9   6.0   5.2   4.8   6.4
-//   16 x 14336 x 5120   16.2  16.0  16.2  16.0  17.3  19.9
-//   33 x 5120 x 14336   42.7  24.6  18.7  20.3  16.9  21.0
-//   56 x 5120 x 17408   51.6  29.6  22.9  23.6  19.9  24.6
-//   16 x 256 x 16384    33.9  18.2  13.0  10.2   7.7   6.4
-// and 16, 32, 64, 128 tokens at once:
-//   128 x 361 x 256      2.7   3.3   4.3   6.5
-//   64 x 1024 x 1024     3.2   3.4   4.1   4.5
-//   40 x 4096 x 4096    10.3   8.2   7.3   8.0
-//   2000 x 300 x 512     6.8   5.2   4.9   7.5
+//   1 x 4096 x 4096     10.1   7.0   5.5   4.6   6.2   6.7
+//   64 x 2048 x 2048     9.2   7.0   6.1   5.2   4.7   6.3
+//   16 x 14336 x 5120   16.6  16.6  17.3  16.9  18.1  20.5
+//   33 x 5120 x 14336   43.0  24.6  19.1  20.4  17.3  21.3
+//   56 x 5120 x 17408   52.0  29.8  23.1  23.7  20.5  25.3
+//   16 x 256 x 16384    33.3  18.1  13.0  10.3   7.9   6.4
+// and 16, 32, 64, 128 tokens at once, each with its best split:
+//   128 x 361 x 256      2.3   2.8   3.9   6.3
+//   64 x 1024 x 1024     2.7   3.1   3.7   4.2
+//   40 x 4096 x 4096    10.0   8.1   6.9   7.9
+//   2000 x 300 x 512     6.7   5.2   4.8   7.2
 template <typename T, int MT>
 static int64_t few_plan(const Fp8MmLaunch& L, int* split) {
     using C = Few<MT>;
@@ -695,7 +695,7 @@ static cudaError_t few_launch(const Fp8MmLaunch& L, int split, cudaStream_t s) {
 // Two producers and two issuers, since a block of K is 512 cycles of products,
 // and waits, a load and an issue take a warp some 150 to 250 cycles each.
 //
-// 8192 x 14336 x 5120 takes 437 us at full clocks (2.75 PFLOP/s; 473 to 488 where the
+// 8192 x 14336 x 5120 takes 437 us at full clocks (2.75 PFLOP/s; 471 to 498 where the
 // power limit lowers them): 850 cycles a block of K. Without the multiplications
 // they are 730, so most of the rest is a tensor memory buffer's round trip (commit,
 // wait, read, arrivals from both CTAs, wait): with two of each half the 512 columns
@@ -1183,12 +1183,12 @@ static cudaError_t many_launch(const Fp8MmLaunch& L, cudaStream_t s) {
     return launch_cluster(many_kernel<T, NT>, 2 * (unsigned)pairs, kPairThreads, C::kSmem, 2, s, w_map, x_map, out_map, a);
 }
 
-// The pairs take 5.5 us and 0.455 us a block of K and round of tiles with 256
-// weight rows, 0.42 us with 192 (8192 x 14336 x 5120: 24 rounds in 437 us, 32 in
-// 539; 1111 x 5000 x 14416: 2 rounds in 110, 2 in 101). Whatever should end
-// first is taken; few / many in us: 128 x 4096 x 4096 10.3 / 17.8, 256 x 4096 x
-// 4096 14.0 / 18.0, 512 x 4096 x 4096 19.8 / 18.3, 256 x 14336 x 5120 48 / 24,
-// 512 x 1024 x 8192 13.5 / 31.
+// The pairs are taken to need 5.5 us and 0.455 us a block of K and round of tiles
+// with 256 weight rows, 0.42 us with 192 (8192 x 14336 x 5120: 24 rounds in 471 us,
+// 32 in 510; 1111 x 5000 x 14416: 2 rounds in 110, 2 in 94, so that 192 rows need 0.39
+// to 0.40). Whatever should end first is taken; few / many in us: 128 x 4096 x 4096
+// 10.3 / 16.5, 256 x 4096 x 4096 13.9 / 16.7, 512 x 4096 x 4096 20.3 / 17.0, 256 x 14336
+// x 5120 41 / 24, 512 x 1024 x 8192 13.4 / 28.
 struct Form {
     int which;   // of kTiles
     int ctas;    // that share a tile

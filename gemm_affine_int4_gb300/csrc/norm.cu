@@ -14,8 +14,8 @@
 // row belongs to some warps; a thread takes kUnits eights of it, a row's width of
 // threads apart (16 lanes hold a group of 128), and keeps p for y in T. Rows too
 // long for that are read a second time. Many rows into e4m3 alone are a warp's each.
-// 20011 x 5120, bf16, residual: codes 114 us (93% of the measured HBM rate), y 136
-// (89%); 64 x 4096, codes: 2.1 us.
+// 20011 x 5120, bf16, residual: codes 114 us (93% of the measured HBM rate), y 136 to 140
+// (86 to 89%); without one: codes 72 to 74 (62 to 64%), y 69 (88%); 64 x 4096, codes: 2.1 us.
 #include <algorithm>
 
 #include "fp8_quant.cuh"
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(512, 2) rms_norm_plain_kernel(const __grid_con
 }
 
 // rows of any length, one a block, read twice (nothing is written in between:
-// outputs may lie on inputs)
+// outputs may lie on inputs): 700 x 40000, bf16, residual 56 to 59 us, at 59% of HBM once
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const __grid_constant__ NormArgs a) {
     pdl_launch_dependents();
@@ -264,8 +264,10 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const __grid_consta
 // loads, without a barrier. Codes and the new residual are written on the way, and
 // of the row no more is kept than its groups' maxima (in shared memory), for the
 // scales. One step ahead and 36 warps an SM; two steps and 24 take 141 us instead of
-// 114 (20011 x 5120, bf16, residual). y in T would be written in a second pass: 107
-// us, rms_norm_kernel 80.
+// 114 (20011 x 5120, bf16, residual). Without a residual half as much is on its way, 18 KB
+// an SM, and bounds it: 72 to 74 us for 46 of HBM; and so it is for fewer rows than those 36
+// warps an SM (3000 x 28672 with a residual 118, for 89). y in T would be written in a second
+// pass: 107 us, rms_norm_kernel 80.
 constexpr int kRowWarps = 4;
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(32 * kRowWarps, 6) rms_norm_codes_kernel(const __grid_constant__ NormArgs a) {

@@ -562,9 +562,9 @@ gai4_status gai4_rope(const void* q, int64_t q_token_stride, void* q_out, int64_
  *         activations in e4m3 (not rounded to T in between; codes are those of
  *         h * gain, a of its blocks, and scales are a / (448 sqrt(...)))
  * h, the sum, h * gain and y are binary32; a sum of squares beyond it (|h| above
- * 1e19) counts as infinite, and squares below it as zero. Any cols >= 1. out or residual_out (not both) may be x or
- * residual where those are contiguous; outputs must not overlap the inputs or
- * each other otherwise.
+ * 1e19) counts as infinite, and squares below it as zero. Any cols >= 1. out and
+ * residual_out may each be x or residual where those are contiguous (not both the
+ * same one); outputs must not overlap the inputs or each other otherwise.
  */
 gai4_status gai4_rms_norm(const void* x, int64_t x_row_stride, const void* residual, int64_t residual_row_stride,
                           const void* gain, void* out, void* residual_out, uint8_t* codes, float* scales,
