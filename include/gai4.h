@@ -620,7 +620,7 @@ gai4_status gai4_fp8_mm_t_plan(int64_t M, int64_t N, int64_t K, gai4_dtype dtype
  *   withheld  bits 0 and 1: weights and tokens of CTAs of even rank of their
  *         cluster; bits 2 and 3: of odd rank. (A few-token kernel, which loads
  *         both together, withholds both for either.) 0, or `blocks` beyond a
- *         CTA's last: the call is gai4_fp8_mm_t.
+ *         CTA's last: the call is gai4_fp8_mm_t, with that limit a wait.
  */
 gai4_status gai4_check_fp8_mm_wait(const uint8_t* w_codes, const float* w_scales, const uint8_t* x_codes,
                                    const float* x_scales, void* out, gai4_dtype dtype, int64_t M, int64_t N, int64_t K,
